@@ -27,8 +27,16 @@ MOE_ERR_CUDA = 5
 MOE_ERR_WORKSPACE = 6
 MOE_BF16 = 0
 MOE_FP16 = 1
+MOE_FP32 = 2
+MOE_INT32 = 3
+MOE_SIGMOID = 0
+MOE_SOFTMAX = 1
 
 _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16}
+_ANY_DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16,
+              torch.float32: MOE_FP32, torch.int32: MOE_INT32}
+_SCORE = {"sigmoid": MOE_SIGMOID, "softmax": MOE_SOFTMAX,
+          MOE_SIGMOID: MOE_SIGMOID, MOE_SOFTMAX: MOE_SOFTMAX}
 
 
 class moe_shape(ctypes.Structure):
@@ -93,6 +101,14 @@ def _load():
                                       vp]
     L.moe_swiglu_quant_grouped_bf16.argtypes = [vp, i64, ctypes.c_int32, vp, vp,
                                                 ctypes.c_int32, vp, i64, vp, vp, vp, vp]
+    i32, f32 = ctypes.c_int32, ctypes.c_float
+    L.moe_route.argtypes = [vp, i32, i64, i32, i64, vp, i32, i32, i32, i32, i32, i32, f32,
+                            vp, vp, vp, vp]
+    L.moe_route_backward.argtypes = [vp, i32, i64, i32, i64, i32, i32, i32, f32, vp, vp, vp,
+                                     vp, vp]
+    L.moe_combine_backward.argtypes = [sp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.moe_linear_i8.argtypes = [vp, i64, i64, vp, i64, i32, i32, i32, vp, vp, vp, i64, vp,
+                                vp, i32, vp, vp]
     for name in ("moe_dispatch_layout", "moe_notify_dispatch", "moe_dispatch",
                  "moe_combine", "moe_combine_quant", "moe_token_layout",
                  "moe_dispatch_fused", "moe_swiglu_quant", "moe_group_offsets",
@@ -101,7 +117,9 @@ def _load():
                  "moe_grouped_gemm_i8_dequant", "moe_combine_f32",
                  "moe_dispatch_expand", "moe_swiglu_quant_grouped_bf16",
                  "moe_grouped_gemm_i8_swiglu", "moe_interleave_gate_up",
-                 "moe_quant_rows_bf16", "moe_dispatch_layout_static"):
+                 "moe_quant_rows_bf16", "moe_dispatch_layout_static",
+                 "moe_route", "moe_route_backward", "moe_combine_backward",
+                 "moe_linear_i8"):
         getattr(L, name).restype = ctypes.c_int
     return L
 
@@ -579,6 +597,122 @@ def moe_quant_rows_bf16(h, group_off, codes, inv_scale, stream=None):
         int(G), _ptr(codes, torch.bfloat16, M * I, "codes"),
         _ptr(inv_scale, torch.float32, M, "inv_scale"), _stream(stream))
     return _check(st, "moe_quant_rows_bf16")
+
+
+def _rows(t, name, dtypes):
+    """(pointer, row stride in elements) of a CUDA matrix whose rows are
+    contiguous but may lie apart (a column slice of a wider matrix)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must have dtype %s, got %s" % (name, tuple(dtypes), t.dtype))
+    if t.dim() != 2 or (t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1):
+        raise ValueError("%s must be a matrix with contiguous rows" % name)
+    stride = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    if stride < t.shape[1]:
+        raise ValueError("%s: rows overlap" % name)
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+_LOGITS = (torch.float32, torch.bfloat16, torch.float16)
+
+
+def _score(score):
+    if score not in _SCORE:
+        raise ValueError("score must be 'sigmoid' or 'softmax', got %r" % (score,))
+    return _SCORE[score]
+
+
+def moe_route(logits, bias, score, k, topk_idx, topk_weights, dev_status, n_group=1,
+              topk_group=1, group_top=1, renormalise=True, scale=1.0, stream=None):
+    """Routing: the k expert ids int32 [T, k] and gate weights fp32 [T, k] of
+    every token from its logits [T, E] (fp32, bf16 or fp16; rows may lie
+    apart).  score 'sigmoid' or 'softmax'; bias fp32 [E] or None shifts the
+    choice, not the weights; of n_group groups the topk_group with the best
+    sums of their group_top best choices stay; renormalise divides the weights
+    by their sum; scale multiplies them."""
+    p, stride = _rows(logits, "logits", _LOGITS)
+    T, E = logits.shape
+    if T == 0:
+        return MOE_OK
+    st = _lib.moe_route(
+        p, _ANY_DTYPE[logits.dtype], T, E, stride, _ptr(bias, torch.float32, E, "bias"),
+        _score(score), int(n_group), int(topk_group), int(group_top), int(k),
+        int(bool(renormalise)), float(scale), _ptr(topk_idx, torch.int32, T * k, "topk_idx"),
+        _ptr(topk_weights, torch.float32, T * k, "topk_weights"),
+        _ptr(dev_status, torch.int32, 1, "dev_status"), _stream(stream))
+    return _check(st, "moe_route")
+
+
+def moe_route_backward(logits, topk_idx, d_weights, score, d_logits, dev_status,
+                       renormalise=True, scale=1.0, stream=None):
+    """Gradient of moe_route's weights: d_logits [T, E] (the logits' dtype)
+    from topk_idx [T, k] and d_weights fp32 [T, k]."""
+    p, stride = _rows(logits, "logits", _LOGITS)
+    T, E = logits.shape
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, k]")
+    k = topk_idx.shape[1]
+    if T == 0:
+        return MOE_OK
+    st = _lib.moe_route_backward(
+        p, _ANY_DTYPE[logits.dtype], T, E, stride, _score(score), k, int(bool(renormalise)),
+        float(scale), _ptr(topk_idx, torch.int32, T * k, "topk_idx"),
+        _ptr(d_weights, torch.float32, T * k, "d_weights"),
+        _ptr(d_logits, logits.dtype, T * E, "d_logits"),
+        _ptr(dev_status, torch.int32, 1, "dev_status"), _stream(stream))
+    return _check(st, "moe_route_backward")
+
+
+def moe_combine_backward(shape, d_out, expert_out, topk_idx, topk_weights, send_idx,
+                         put_offset, rank_recv_base, d_expert_out, d_weights, dev_status,
+                         stream=None):
+    """Gradient of moe_combine: d_expert_out [rows, H] = weight x d_out[token]
+    and d_weights [T, k] = <d_out[token], expert_out[row]>."""
+    T, k, H = shape.R * shape.bs, shape.k, shape.H
+    E = shape.R * shape.experts_per_rank
+    rows = expert_out.shape[0]
+    dt = torch.bfloat16 if shape.dtype == MOE_BF16 else torch.float16
+    st = _lib.moe_combine_backward(
+        ctypes.byref(shape), _ptr(d_out, dt, T * H, "d_out"),
+        _ptr(expert_out, dt, rows * H, "expert_out"), rows,
+        _ptr(topk_idx, torch.int32, T * k, "topk_idx"),
+        _ptr(topk_weights, torch.float32, T * k, "topk_weights"),
+        _ptr(send_idx, torch.int32, T * k, "send_idx"),
+        _ptr(put_offset, torch.int32, E * shape.R, "put_offset"),
+        _ptr(rank_recv_base, torch.int64, shape.R + 1, "rank_recv_base"),
+        _ptr(d_expert_out, dt, rows * H, "d_expert_out"),
+        _ptr(d_weights, torch.float32, T * k, "d_weights"),
+        _ptr(dev_status, torch.int32, 1, "dev_status"), _stream(stream))
+    return _check(st, "moe_combine_backward")
+
+
+def moe_linear_i8(a, w, K, group_rows, col_scale, row_scale, bias, c, dev_status,
+                  stream=None):
+    """c [rows, N] (bf16, fp16, fp32, or int32 for the accumulators) = int8
+    rows a [rows, stride] x int8 weights w [G, N, stride]^T over K codes, times
+    col_scale [G, N] and the row's scale, plus bias [G, N].  a may hold row
+    images (uint8) as dispatch writes them; row_scale is (tensor, byte_offset,
+    byte_stride); group_rows int32 [G] (None with G = 1: every row)."""
+    i8 = (torch.int8, torch.uint8)
+    ap, a_stride = _rows(a, "a", i8)
+    if w.dim() != 3 or w.shape[2] < K or a.shape[1] < K:
+        raise ValueError("a must be [rows, >= K] and w [G, N, >= K]")
+    rows, (G, N, w_stride) = a.shape[0], w.shape
+    if rows == 0:
+        return MOE_OK
+    if c.shape != (rows, N) or c.dtype not in _ANY_DTYPE:
+        raise ValueError("c must be [rows, N] in bf16, fp16, fp32 or int32")
+    if group_rows is not None and group_rows.numel() != G:
+        raise ValueError("group_rows must have G entries")
+    rp, rstride = (None, 4) if row_scale is None else _strided(row_scale, rows, "row_scale")
+    st = _lib.moe_linear_i8(
+        ap, rows, a_stride, _ptr(w, i8, None, "w"), w_stride, G, N, int(K),
+        _ptr(group_rows, torch.int32, G, "group_rows"),
+        _ptr(col_scale, torch.float32, G * N, "col_scale"), rp, rstride,
+        _ptr(bias, torch.float32, G * N, "bias"), _ptr(c, None, None, "c"),
+        _ANY_DTYPE[c.dtype], _ptr(dev_status, torch.int32, 1, "dev_status"), _stream(stream))
+    return _check(st, "moe_linear_i8")
 
 
 # the size queries and the status names under the C entry points' own names

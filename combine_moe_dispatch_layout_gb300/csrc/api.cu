@@ -11,6 +11,10 @@ namespace {
 
 using moe_ep::Shape;
 
+// Row strides beyond any buffer this GPU can hold (a bound for 64-bit
+// offsets: rows < 2^31, so row * stride stays below 2^63).
+constexpr int64_t kMaxStride = int64_t(1) << 32;
+
 bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
@@ -28,6 +32,17 @@ bool valid_shape(const moe_shape* sh, Shape* out) {
   if (sh->dtype != MOE_BF16 && sh->dtype != MOE_FP16) return false;
   *out = Shape{int(R), int(bs), int(k), int(epr), int(H), int(sh->dtype)};
   return true;
+}
+
+// Limits of moe_route and moe_route_backward (scale: finite).
+bool valid_routing(int32_t dtype, int64_t T, int32_t E, int64_t stride, int32_t score,
+                   int32_t k, float scale) {
+  if (dtype != MOE_BF16 && dtype != MOE_FP16 && dtype != MOE_FP32) return false;
+  if (E < 1 || E > MOE_EP_MAX_EXPERTS || k < 1 || k > MOE_EP_MAX_TOPK || k > E) return false;
+  if (T < 0 || T >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31)) return false;
+  if (stride < E || stride >= kMaxStride) return false;
+  if (score != MOE_SIGMOID && score != MOE_SOFTMAX) return false;
+  return scale - scale == 0.0f;
 }
 
 moe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -482,6 +497,96 @@ moe_status moe_deq_combine(const moe_shape* shape, const int32_t* expert_acc,
       s, expert_acc, expert_rows, weight_scale, row_scale, row_scale_stride, topk_idx,
       topk_weights, send_idx, put_offset, rank_recv_base, out, dev_status,
       static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_route(const void* logits, int32_t logits_dtype, int64_t T, int32_t E,
+                     int64_t logits_stride, const float* bias, int32_t score,
+                     int32_t n_group, int32_t topk_group, int32_t group_top, int32_t k,
+                     int32_t renormalise, float scale, int32_t* topk_idx,
+                     float* topk_weights, int32_t* dev_status, void* stream) {
+  if (!valid_routing(logits_dtype, T, E, logits_stride, score, k, scale) || !dev_status ||
+      n_group < 1 || n_group > E || E % n_group != 0 || topk_group < 1 ||
+      topk_group > n_group || group_top < 1 || group_top > 2)
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_weights ||
+      !aligned(logits, logits_dtype == MOE_FP32 ? 4 : 2) || !aligned(bias, 4) ||
+      !aligned(topk_idx, 4) || !aligned(topk_weights, 4) || !aligned(dev_status, 4))
+    return MOE_ERR_INVALID_ARG;
+  const moe_ep::RouteArgs r{logits, logits_dtype, T, logits_stride, E, k, score, n_group,
+                            topk_group, group_top, renormalise != 0, scale, bias};
+  return from_cuda(moe_ep::launch_route(r, topk_idx, topk_weights, dev_status,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_route_backward(const void* logits, int32_t logits_dtype, int64_t T, int32_t E,
+                              int64_t logits_stride, int32_t score, int32_t k,
+                              int32_t renormalise, float scale, const int32_t* topk_idx,
+                              const float* d_weights, void* d_logits, int32_t* dev_status,
+                              void* stream) {
+  if (!valid_routing(logits_dtype, T, E, logits_stride, score, k, scale) || !dev_status)
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !d_weights || !d_logits ||
+      !aligned(logits, logits_dtype == MOE_FP32 ? 4 : 2) || !aligned(topk_idx, 4) ||
+      !aligned(d_weights, 4) || !aligned(d_logits, 16) || !aligned(dev_status, 4))
+    return MOE_ERR_INVALID_ARG;
+  const moe_ep::RouteArgs r{logits, logits_dtype, T, logits_stride, E, k, score, 1,
+                            1, 1, renormalise != 0, scale, nullptr};
+  return from_cuda(moe_ep::launch_route_backward(r, topk_idx, d_weights, d_logits, dev_status,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_combine_backward(const moe_shape* shape, const void* d_out,
+                                const void* expert_out, int64_t expert_out_rows,
+                                const int32_t* topk_idx, const float* topk_weights,
+                                const int32_t* send_idx, const int32_t* put_offset,
+                                const int64_t* rank_recv_base, void* d_expert_out,
+                                float* d_weights, int32_t* dev_status, void* stream) {
+  Shape s;
+  if (!valid_shape(shape, &s)) return MOE_ERR_INVALID_ARG;
+  if (expert_out_rows < 0 || !dev_status) return MOE_ERR_INVALID_ARG;
+  if (s.T() == 0) return MOE_OK;
+  if (!d_out || (expert_out_rows > 0 && (!expert_out || !d_expert_out)) || !topk_idx ||
+      !topk_weights || !send_idx || !put_offset || !rank_recv_base || !d_weights)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(d_out, 16) || !aligned(expert_out, 16) || !aligned(d_expert_out, 16) ||
+      !aligned(topk_idx, 4) || !aligned(topk_weights, 4) || !aligned(send_idx, 4) ||
+      !aligned(put_offset, 4) || !aligned(rank_recv_base, 8) || !aligned(d_weights, 4) ||
+      !aligned(dev_status, 4))
+    return MOE_ERR_INVALID_ARG;
+  return from_cuda(moe_ep::launch_combine_backward(
+      s, d_out, expert_out, expert_out_rows, topk_idx, topk_weights, send_idx, put_offset,
+      rank_recv_base, d_expert_out, d_weights, dev_status,
+      static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_linear_i8(const void* a, int64_t a_rows, int64_t a_stride, const void* w,
+                         int64_t w_stride, int32_t G, int32_t N, int32_t K,
+                         const int32_t* group_rows, const float* col_scale,
+                         const void* row_scale, int64_t row_scale_stride,
+                         const float* bias, void* c, int32_t c_dtype,
+                         int32_t* dev_status, void* stream) {
+  if (a_rows < 0 || a_rows > INT32_MAX || K < 1 || K > MOE_EP_MAX_HIDDEN || N < 1 ||
+      N > MOE_EP_MAX_HIDDEN || G < 1 || G > MOE_EP_MAX_EXPERTS || a_stride < K ||
+      a_stride % 16 != 0 || w_stride < K || w_stride % 16 != 0 || a_stride >= kMaxStride ||
+      w_stride >= kMaxStride || c_dtype < MOE_BF16 || c_dtype > MOE_INT32 || !dev_status)
+    return MOE_ERR_INVALID_ARG;
+  const bool scaled = c_dtype != MOE_INT32;
+  if (scaled ? row_scale_stride < 4 || row_scale_stride % 4 != 0 || row_scale_stride >= kMaxStride
+             : bias != nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (a_rows == 0) return MOE_OK;
+  if (!a || !w || !c || (!group_rows && G != 1) || (scaled && (!col_scale || !row_scale)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(c, 16) || !aligned(group_rows, 4) ||
+      !aligned(bias, 4) || !aligned(dev_status, 4) ||
+      (scaled && (!aligned(col_scale, 4) || !aligned(row_scale, 4))))
+    return MOE_ERR_INVALID_ARG;
+  const moe_ep::LinearArgs p{a, a_rows, a_stride, w, w_stride, G, N, K, group_rows, col_scale,
+                             static_cast<const unsigned char*>(row_scale), row_scale_stride,
+                             bias, c, c_dtype};
+  return from_cuda(moe_ep::launch_linear_i8(p, dev_status, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,147 @@
+// combine_backward.cu -- gradient of the combine (include/moe_ep.h,
+// moe_combine_backward).
+//
+// Mathematics.  out[g] = sum_k w[g][k] y[row(g,k)], so the gradient of row
+// (g, k) is w[g][k] d_out[g] and that of the weight is <d_out[g], y[row]>.
+// Both take one pass: each expert row is read once and its gradient row
+// written once, P*H elements each way, and d_out[g] stays in registers for
+// the token's k rows.  Memory-bound: (T + 2P) rows of 2H bytes.
+//
+// A persistent grid walks the tokens.  The last warp resolves the next
+// token's rows and weights into the other half of a double-buffered table
+// while the compute warps work on this one; each compute thread owns 16-byte
+// chunks of the hidden dimension, issues the loads of up to kBatch rows
+// before using them, writes the gradient rows and adds up its part of the k
+// dot products.  Dot products go over a warp by shuffles and over the CTA
+// through shared memory, warps in ascending order: a fixed order.
+#include <algorithm>
+
+#include "moe_ep_internal.cuh"
+
+namespace moe_ep {
+namespace {
+
+constexpr int kBatch = 8;
+constexpr int kMaxThreads = 512;
+constexpr unsigned kAll = 0xffffffffu;
+
+template <int DT>
+__global__ void __launch_bounds__(kMaxThreads)
+combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict__ y,
+                        int64_t y_rows, const int32_t* __restrict__ topk_idx,
+                        const float* __restrict__ weights,
+                        const int32_t* __restrict__ send_idx,
+                        const int32_t* __restrict__ put_offset,
+                        const int64_t* __restrict__ rank_recv_base, int R, int bs, int k,
+                        int epr, int H, int64_t T, uint4* __restrict__ d_y,
+                        float* __restrict__ d_weights, int32_t* dev_status) {
+  __shared__ int64_t s_rows[2][MOE_EP_MAX_TOPK];
+  __shared__ float s_w[2][MOE_EP_MAX_TOPK];
+  __shared__ float s_dot[kMaxThreads / 32][MOE_EP_MAX_TOPK];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ncomp = blockDim.x - 32, nwarps = ncomp >> 5;
+  const bool producer = tid >= ncomp;
+  const int nch = H / 8;
+
+  int64_t g = blockIdx.x;
+  if (producer)
+    resolve_token(g, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k, epr,
+                  y_rows, s_rows[0], s_w[0], dev_status, lane);
+  __syncthreads();
+
+  for (int it = 0; g < T; ++it, g += gridDim.x) {
+    const int buf = it & 1;
+    if (producer) {
+      const int64_t gn = g + gridDim.x;
+      if (gn < T)
+        resolve_token(gn, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k,
+                      epr, y_rows, s_rows[buf ^ 1], s_w[buf ^ 1], dev_status, lane);
+    } else {
+      for (int k0 = 0; k0 < k; k0 += kBatch) {
+        float dot[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) dot[b] = 0.0f;
+        for (int c = tid; c < nch; c += ncomp) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int64_t row = k0 + b < k ? s_rows[buf][k0 + b] : -1;
+            v[b] = row >= 0 ? ld_stream_16(y + row * nch + c) : make_uint4(0u, 0u, 0u, 0u);
+          }
+          float d[8];
+          unpack8<DT>(__ldg(d_out + g * nch + c), d);
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int64_t row = k0 + b < k ? s_rows[buf][k0 + b] : -1;
+            if (row >= 0) {
+              const float w = s_w[buf][k0 + b];
+              float f[8], o[8];
+              unpack8<DT>(v[b], f);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                dot[b] = __fmaf_rn(d[j], f[j], dot[b]);
+                o[j] = __fmul_rn(w, d[j]);
+              }
+              d_y[row * nch + c] = pack8<DT>(o);
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+          for (int s = 16; s; s >>= 1)
+            dot[b] = __fadd_rn(dot[b], __shfl_xor_sync(kAll, dot[b], s));
+          if (lane == 0 && k0 + b < k) s_dot[warp][k0 + b] = dot[b];
+        }
+      }
+    }
+    __syncthreads();   // dots are in; this token's table is free, the next is ready
+    if (!producer && tid < k) {
+      float sum = 0.0f;
+      for (int w = 0; w < nwarps; ++w) sum = __fadd_rn(sum, s_dot[w][tid]);
+      d_weights[g * k + tid] = sum;
+    }
+    // a warp may write the next token's dots once all have read these
+    __syncthreads();
+  }
+}
+
+template <int DT>
+cudaError_t launch_t(const Shape& s, const void* d_out, const void* y, int64_t y_rows,
+                     const int32_t* topk_idx, const float* weights, const int32_t* send_idx,
+                     const int32_t* put_offset, const int64_t* rank_recv_base, void* d_y,
+                     float* d_weights, int32_t* dev_status, cudaStream_t st) {
+  const int nch = s.H / 8;
+  // at least k compute threads: thread j finishes slot j's dot product
+  int threads = std::max((nch + 1) / 2, s.k);
+  threads = std::min(kMaxThreads - 32, (threads + 31) / 32 * 32) + 32;
+  auto kernel = combine_backward_kernel<DT>;
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = current_device_sms(&dev, &sms);
+  if (e == cudaSuccess)
+    e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), threads, 0, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>(s.T(), int64_t(std::max(1, per_sm)) * sms);
+  kernel<<<static_cast<unsigned>(grid), threads, 0, st>>>(
+      static_cast<const uint4*>(d_out), static_cast<const uint4*>(y), y_rows, topk_idx,
+      weights, send_idx, put_offset, rank_recv_base, s.R, s.bs, s.k, s.epr, s.H, s.T(),
+      static_cast<uint4*>(d_y), d_weights, dev_status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_combine_backward(const Shape& s, const void* d_out, const void* y,
+                                    int64_t y_rows, const int32_t* topk_idx,
+                                    const float* weights, const int32_t* send_idx,
+                                    const int32_t* put_offset, const int64_t* rank_recv_base,
+                                    void* d_y, float* d_weights, int32_t* dev_status,
+                                    cudaStream_t st) {
+  if (s.dtype == MOE_BF16)
+    return launch_t<MOE_BF16>(s, d_out, y, y_rows, topk_idx, weights, send_idx, put_offset,
+                              rank_recv_base, d_y, d_weights, dev_status, st);
+  return launch_t<MOE_FP16>(s, d_out, y, y_rows, topk_idx, weights, send_idx, put_offset,
+                            rank_recv_base, d_y, d_weights, dev_status, st);
+}
+
+}  // namespace moe_ep

@@ -454,4 +454,48 @@ cudaError_t launch_combine(const Shape& s, const void* y, int64_t y_rows,
                            const int64_t* rank_recv_base, void* out,
                            int32_t* dev_status, cudaStream_t st);
 
+// Routing arguments shared by the forward and the backward kernel.
+struct RouteArgs {
+  const void* logits;
+  int dtype;             // MOE_BF16, MOE_FP16 or MOE_FP32
+  int64_t T, stride;     // tokens; elements between rows
+  int E, k;
+  int score;             // MOE_SIGMOID or MOE_SOFTMAX
+  int n_group, topk_group, group_top;
+  bool renormalise;
+  float scale;
+  const float* bias;     // [E] or nullptr
+};
+
+cudaError_t launch_route(const RouteArgs& r, int32_t* topk_idx, float* topk_weights,
+                         int32_t* dev_status, cudaStream_t st);
+
+cudaError_t launch_route_backward(const RouteArgs& r, const int32_t* topk_idx,
+                                  const float* d_weights, void* d_logits,
+                                  int32_t* dev_status, cudaStream_t st);
+
+cudaError_t launch_combine_backward(const Shape& s, const void* d_out, const void* y,
+                                    int64_t y_rows, const int32_t* topk_idx,
+                                    const float* weights, const int32_t* send_idx,
+                                    const int32_t* put_offset, const int64_t* rank_recv_base,
+                                    void* d_y, float* d_weights, int32_t* dev_status,
+                                    cudaStream_t st);
+
+struct LinearArgs {
+  const void* a;
+  int64_t a_rows, a_stride;
+  const void* w;
+  int64_t w_stride;
+  int G, N, K;
+  const int32_t* group_rows;        // [G] or nullptr (one group of a_rows rows)
+  const float* col_scale;           // [G][N]
+  const unsigned char* row_scale;
+  int64_t row_scale_stride;         // bytes
+  const float* bias;                // [G][N] or nullptr
+  void* c;
+  int c_dtype;                      // moe_dtype
+};
+
+cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st);
+
 }  // namespace moe_ep

@@ -1,0 +1,465 @@
+// route.cu -- routing: logits -> the k expert ids and gate weights of every
+// token (include/moe_ep.h, moe_route).
+//
+// Mathematics.  Every expert e gets a ranking key: without a bias the logit
+// itself (sigmoid and softmax are increasing, so it orders experts as their
+// scores do), with a bias the choice s[e] + b[e].  A float maps to an unsigned
+// key with the same order (sign bit flipped for positive values, all bits for
+// negative ones); key 0 means "not available".  The k best keys are taken one
+// after another; weights are then recomputed for the k chosen logits alone,
+// in full precision, one per lane.  Softmax weights that are renormalised are
+// exp(l - max of the chosen) over their sum: the sum over all experts cancels,
+// so it is not computed.
+//
+// Warp kernel (E <= 1024): one warp per token, lane L holding VPT neighbouring
+// experts, so the lowest lane and the lowest position inside it are the lowest
+// id and ties need no index compares.  Each lane keeps its two best keys
+// sorted; a round is one warp maximum, one ballot and a pop in the winning
+// lane, which looks through its keys again only when it has won twice (rare:
+// the k winners spread over the lanes).
+#include <algorithm>
+
+#include "moe_ep_internal.cuh"
+
+namespace moe_ep {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kMaxF = 3.402823466e38f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+template <int DT>
+struct Elem { using T = uint16_t; };
+template <>
+struct Elem<MOE_FP32> { using T = float; };
+
+template <int DT>
+__device__ __forceinline__ float load_logit(const typename Elem<DT>::T* p) {
+  if constexpr (DT == MOE_FP32) return __ldg(p);
+  else return widen<DT>(__ldg(p));
+}
+
+// Order-preserving key of a float; -0 reads as +0.  Keys of numbers above
+// -inf are never 0.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f));
+  return b ^ ((b & 0x80000000u) ? 0xffffffffu : 0x80000000u);
+}
+
+// e^x to about 2 ulp for the ranking of scores: x log2(e) in two parts, the
+// second one (with |part| < 2^-16) to first order.  Clamped where e^x is 0 or
+// inf in fp32 anyway.
+__device__ __forceinline__ float exp_rank(float x) {
+  x = fminf(fmaxf(x, -120.0f), 120.0f);
+  constexpr float kL2e = 1.44269502f, kL2eLo = 1.92596299e-8f, kLn2 = 0.693147181f;
+  const float t = __fmul_rn(x, kL2e);
+  const float r = __fmaf_rn(x, kL2eLo, __fmaf_rn(x, kL2e, -t));
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return __fmaf_rn(e, __fmul_rn(r, kLn2), e);
+}
+__device__ __forceinline__ float sigmoid_rank(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, exp_rank(-x))));
+  return r;
+}
+// The score in full precision (the weights).
+__device__ __forceinline__ float sigmoid_full(float x) {
+  return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+
+// Ids and weights of one token from the chosen experts: slot j = lane or
+// lane + 32 (sel[.] = -1: no expert).  m and inv_sum: the softmax's maximum
+// and 1 / sum (plain softmax only).
+template <int DT>
+__device__ __forceinline__ void write_token(const RouteArgs& r,
+                                            const typename Elem<DT>::T* row, int64_t t,
+                                            const int (&sel)[2], float m, float sum, int lane,
+                                            int32_t* idx, float* weights) {
+  float l[2], s[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    l[h] = sel[h] >= 0 ? fminf(load_logit<DT>(row + sel[h]), kMaxF) : kNegInf;
+  if (r.score == MOE_SOFTMAX) {
+    if (r.renormalise) m = warp_max(fmaxf(l[0], l[1]));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = sel[h] >= 0 ? expf(__fsub_rn(l[h], m)) : 0.0f;
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = sel[h] >= 0 ? sigmoid_full(l[h]) : 0.0f;
+  }
+  float d = 1.0f;
+  if (r.renormalise) {
+    d = warp_sum(__fadd_rn(s[0], s[1]));
+    if (d == 0.0f) d = 1.0f;
+  } else if (r.score == MOE_SOFTMAX) {
+    d = sum;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = lane + 32 * h;
+    if (j < r.k) {
+      idx[t * r.k + j] = sel[h];
+      weights[t * r.k + j] = sel[h] >= 0 ? __fmul_rn(__fdiv_rn(s[h], d), r.scale) : 0.0f;
+    }
+  }
+}
+
+constexpr int kWarps = 4;   // tokens per CTA of the warp kernel
+
+// vec: row starts and the lanes' chunks are 16-byte aligned.
+template <int DT, int VPT>
+__global__ void __launch_bounds__(kWarps * 32)
+route_warp_kernel(const RouteArgs r, bool vec, int lanes_per_group,
+                  int32_t* __restrict__ idx, float* __restrict__ weights,
+                  int32_t* dev_status) {
+  using T = typename Elem<DT>::T;
+  constexpr int kPer16 = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= r.T) return;
+  const T* row = static_cast<const T*>(r.logits) + t * r.stride;
+  const int e0 = lane * VPT;
+
+  // ---- logits ------------------------------------------------------------------
+  float l[VPT];
+  if (VPT % kPer16 == 0 && vec && e0 + VPT <= r.E) {
+#pragma unroll
+    for (int c = 0; c < VPT / kPer16; ++c) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
+      if constexpr (DT == MOE_FP32) {
+        l[4 * c] = __uint_as_float(v.x);
+        l[4 * c + 1] = __uint_as_float(v.y);
+        l[4 * c + 2] = __uint_as_float(v.z);
+        l[4 * c + 3] = __uint_as_float(v.w);
+      } else {
+        float f[8];
+        unpack8<DT>(v, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[8 * c + i] = f[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      l[i] = e0 + i < r.E ? load_logit<DT>(row + e0 + i) : kNegInf;
+  }
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    nan |= l[i] != l[i];
+    l[i] = l[i] != l[i] ? kNegInf : fminf(l[i], kMaxF);
+  }
+  if (nan) set_status(dev_status, MOE_ERR_INVALID_ARG);
+
+  // ---- the softmax's maximum and sum, where a weight or a choice needs them --------
+  const bool grouped = r.topk_group < r.n_group;
+  float m = 0.0f, sum = 1.0f;
+  if (r.score == MOE_SOFTMAX && (!r.renormalise || r.bias || grouped)) {
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) m = fmaxf(m, l[i]);
+    m = fmaxf(warp_max(m), -kMaxF);
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      sum = __fadd_rn(sum, l[i] > kNegInf ? exp_rank(__fsub_rn(l[i], m)) : 0.0f);
+    sum = warp_sum(sum);
+    if (sum == 0.0f) sum = 1.0f;
+  }
+  const float inv_sum = __fdiv_rn(1.0f, sum);
+  auto score = [&](float x) {
+    return r.score == MOE_SOFTMAX ? __fmul_rn(exp_rank(__fsub_rn(x, m)), inv_sum)
+                                  : sigmoid_rank(x);
+  };
+
+  // ---- ranking keys (l becomes the ranked value), the lane's two best ---------------
+  if (r.bias) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (e0 + i < r.E) {
+        const float c = __fadd_rn(score(l[i]), __ldg(r.bias + e0 + i));
+        l[i] = l[i] > kNegInf && c > kNegInf ? c : kNegInf;
+      }
+  }
+  uint32_t key[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) key[i] = l[i] > kNegInf ? order_key(l[i]) : 0u;
+  uint32_t k1 = 0, k2 = 0, taken = 0;
+  int i1 = 0, i2 = 0;
+  auto scan = [&]() {
+    k1 = k2 = 0;
+    i1 = i2 = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const uint32_t v = (taken >> i) & 1u ? 0u : key[i];
+      if (v > k1) {
+        k2 = k1;
+        i2 = i1;
+        k1 = v;
+        i1 = i;
+      } else if (v > k2) {
+        k2 = v;
+        i2 = i;
+      }
+    }
+  };
+  scan();
+
+  // ---- groups: a lane's experts are all of one group, lanes_per_group lanes each --------
+  if (grouped) {
+    auto choice = [&](uint32_t k) {      // the choice behind a key
+      if (k == 0) return kNegInf;
+      const float f = __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+      return r.bias ? f : score(f);
+    };
+    float a1 = choice(k1), a2 = choice(k2);
+    for (int d = 1; d < lanes_per_group; d <<= 1) {
+      const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+      a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+      a1 = fmaxf(a1, b1);
+    }
+    const float gs = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
+    const int mine = lane / lanes_per_group;
+    int better = 0;
+    for (int g = 0; g < r.n_group; ++g) {
+      const float o = __shfl_sync(kAll, gs, g * lanes_per_group);
+      better += o > gs || (o == gs && g < mine);
+    }
+    if (better >= r.topk_group) {
+      k1 = k2 = 0;
+      taken = kAll;
+    }
+  }
+
+  // ---- the k best -----------------------------------------------------------------------
+  int sel[2] = {-1, -1};
+  int held = 2;                       // sorted keys left in this lane
+  for (int j = 0; j < r.k; ++j) {
+    if (VPT > 2 && __any_sync(kAll, held == 0)) {
+      if (held == 0) {
+        scan();
+        held = 2;
+      }
+    }
+    const uint32_t best = __reduce_max_sync(kAll, k1);
+    if (best == 0) break;
+    const int win = __ffs(__ballot_sync(kAll, k1 == best)) - 1;
+    const int e = __shfl_sync(kAll, i1, win) + win * VPT;
+    if (lane == (j & 31)) {
+      if (j < 32) sel[0] = e;
+      else sel[1] = e;
+    }
+    if (lane == win) {
+      taken |= 1u << i1;
+      k1 = k2;
+      i1 = i2;
+      k2 = 0;
+      --held;
+    }
+  }
+  write_token<DT>(r, row, t, sel, m, sum, lane, idx, weights);
+}
+
+// Any E up to MOE_EP_MAX_EXPERTS and any groups: one CTA per token (persistent
+// grid), ranking keys and choices in shared memory, a block-wide maximum of
+// (key, lowest id) per chosen expert.
+constexpr int kWideThreads = 128;
+
+template <int DT>
+__global__ void __launch_bounds__(kWideThreads)
+route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restrict__ weights,
+                  int32_t* dev_status) {
+  using T = typename Elem<DT>::T;
+  extern __shared__ uint32_t s_dyn[];
+  uint32_t* key = s_dyn;                                       // [E]
+  float* choice = reinterpret_cast<float*>(s_dyn + r.E);       // [E]
+  float* gscore = choice + r.E;                                // [n_group]
+  __shared__ float s_red[kWideThreads / 32];
+  __shared__ uint64_t s_best[2][kWideThreads / 32];
+  __shared__ int s_sel[MOE_EP_MAX_TOPK];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool grouped = r.topk_group < r.n_group;
+  const int per = r.E / r.n_group;
+
+  for (int64_t t = blockIdx.x; t < r.T; t += gridDim.x) {
+    const T* row = static_cast<const T*>(r.logits) + t * r.stride;
+    auto logit = [&](int e) {
+      const float l = load_logit<DT>(row + e);
+      return l != l ? kNegInf : fminf(l, kMaxF);
+    };
+    float m = kNegInf, sum = 0.0f;
+    bool nan = false;
+    for (int e = tid; e < r.E; e += kWideThreads) {
+      const float l = load_logit<DT>(row + e);
+      nan |= l != l;
+      m = fmaxf(m, logit(e));
+    }
+    if (nan) set_status(dev_status, MOE_ERR_INVALID_ARG);
+    if (r.score == MOE_SOFTMAX) {
+      m = warp_max(m);
+      if (lane == 0) s_red[warp] = m;
+      __syncthreads();
+      m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+      m = fmaxf(m, -kMaxF);
+      __syncthreads();
+      for (int e = tid; e < r.E; e += kWideThreads) {
+        const float l = logit(e);
+        sum = __fadd_rn(sum, l > kNegInf ? exp_rank(__fsub_rn(l, m)) : 0.0f);
+      }
+      sum = warp_sum(sum);
+      if (lane == 0) s_red[warp] = sum;
+      __syncthreads();
+      sum = __fadd_rn(__fadd_rn(s_red[0], s_red[1]), __fadd_rn(s_red[2], s_red[3]));
+    }
+    if (sum == 0.0f) sum = 1.0f;
+    const float inv_sum = __fdiv_rn(1.0f, sum);
+    for (int e = tid; e < r.E; e += kWideThreads) {
+      const float l = logit(e);
+      float c = r.score == MOE_SOFTMAX ? __fmul_rn(exp_rank(__fsub_rn(l, m)), inv_sum)
+                                       : sigmoid_rank(l);
+      if (r.bias) c = __fadd_rn(c, __ldg(r.bias + e));
+      const bool on = l > kNegInf && c > kNegInf;
+      key[e] = on ? order_key(r.bias ? c : l) : 0u;
+      choice[e] = on ? c : kNegInf;
+    }
+    __syncthreads();
+    if (grouped) {
+      for (int g = tid; g < r.n_group; g += kWideThreads) {
+        float a1 = kNegInf, a2 = kNegInf;
+        for (int i = 0; i < per; ++i) {
+          const float c = choice[g * per + i];
+          a2 = fmaxf(fminf(a1, c), a2);
+          a1 = fmaxf(a1, c);
+        }
+        gscore[g] = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
+      }
+      __syncthreads();
+      for (int g = tid; g < r.n_group; g += kWideThreads) {
+        const float gs = gscore[g];
+        int better = 0;
+        for (int o = 0; o < r.n_group; ++o)
+          better += gscore[o] > gs || (gscore[o] == gs && o < g);
+        if (better >= r.topk_group)
+          for (int i = 0; i < per; ++i) key[g * per + i] = 0u;
+      }
+      __syncthreads();
+    }
+    // (key, ~id): the larger key, then the lower id.  Every thread keeps the
+    // best of its experts and looks again when it loses it.
+    auto own_best = [&]() {
+      uint64_t b = 0;
+      for (int e = tid; e < r.E; e += kWideThreads) {
+        const uint64_t v = uint64_t(key[e]) << 32 | uint32_t(~e);
+        if (key[e] != 0 && v > b) b = v;
+      }
+      return b;
+    };
+    uint64_t own = own_best();
+    int n = 0;
+    for (; n < r.k; ++n) {
+      uint64_t b = own;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) {
+        const uint64_t o = __shfl_xor_sync(kAll, b, d);
+        b = o > b ? o : b;
+      }
+      if (lane == 0) s_best[n & 1][warp] = b;
+      __syncthreads();
+      b = s_best[n & 1][0];
+      for (int i = 1; i < kWideThreads / 32; ++i)
+        b = s_best[n & 1][i] > b ? s_best[n & 1][i] : b;
+      if (b == 0) break;
+      const int e = static_cast<int>(~uint32_t(b));
+      if (tid == 0) s_sel[n] = e;
+      if (b == own) {
+        key[e] = 0u;
+        own = own_best();
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int sel[2] = {lane < n ? s_sel[lane] : -1, lane + 32 < n ? s_sel[lane + 32] : -1};
+      write_token<DT>(r, row, t, sel, m, sum, lane, idx, weights);
+    }
+    __syncthreads();
+  }
+}
+
+template <int DT, int VPT>
+cudaError_t launch_warp(const RouteArgs& r, int lanes_per_group, int32_t* idx, float* weights,
+                        int32_t* dev_status, cudaStream_t st) {
+  const size_t el = DT == MOE_FP32 ? 4 : 2;
+  const bool vec = reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 && r.stride * el % 16 == 0;
+  const int64_t grid = (r.T + kWarps - 1) / kWarps;
+  route_warp_kernel<DT, VPT><<<static_cast<unsigned>(grid), kWarps * 32, 0, st>>>(
+      r, vec, lanes_per_group, idx, weights, dev_status);
+  return cudaGetLastError();
+}
+
+// The warp kernel's experts per lane: the smallest of its sizes that holds E
+// and, with groups in play, cuts no group (a power of two of lanes each, for
+// the butterfly that joins their best choices); 0 where there is none.
+int experts_per_lane(const RouteArgs& r, int* lanes_per_group) {
+  *lanes_per_group = 32;
+  for (const int v : {1, 2, 4, 8, 16, 24, 32}) {
+    if (v * 32 < r.E) continue;
+    if (r.topk_group == r.n_group) return v;
+    const int per = r.E / r.n_group, lanes = per / v;
+    if (per % v == 0 && (lanes & (lanes - 1)) == 0) {
+      *lanes_per_group = lanes;
+      return v;
+    }
+  }
+  return 0;
+}
+
+template <int DT>
+cudaError_t launch_t(const RouteArgs& r, int32_t* idx, float* weights, int32_t* dev_status,
+                     cudaStream_t st) {
+  int lpg = 32;
+  switch (experts_per_lane(r, &lpg)) {
+    case 1: return launch_warp<DT, 1>(r, lpg, idx, weights, dev_status, st);
+    case 2: return launch_warp<DT, 2>(r, lpg, idx, weights, dev_status, st);
+    case 4: return launch_warp<DT, 4>(r, lpg, idx, weights, dev_status, st);
+    case 8: return launch_warp<DT, 8>(r, lpg, idx, weights, dev_status, st);
+    case 16: return launch_warp<DT, 16>(r, lpg, idx, weights, dev_status, st);
+    case 24: return launch_warp<DT, 24>(r, lpg, idx, weights, dev_status, st);
+    case 32: return launch_warp<DT, 32>(r, lpg, idx, weights, dev_status, st);
+    default: break;
+  }
+  const size_t smem = (2 * size_t(r.E) + r.n_group) * 4;
+  const void* fn = reinterpret_cast<const void*>(route_wide_kernel<DT>);
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = current_device_sms(&dev, &sms);
+  if (e == cudaSuccess) e = kernel_blocks_per_sm(fn, kWideThreads, smem, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>(r.T, int64_t(std::max(1, per_sm)) * sms);
+  route_wide_kernel<DT><<<static_cast<unsigned>(grid), kWideThreads, smem, st>>>(
+      r, idx, weights, dev_status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& r, int32_t* topk_idx, float* topk_weights,
+                         int32_t* dev_status, cudaStream_t st) {
+  switch (r.dtype) {
+    case MOE_BF16: return launch_t<MOE_BF16>(r, topk_idx, topk_weights, dev_status, st);
+    case MOE_FP16: return launch_t<MOE_FP16>(r, topk_idx, topk_weights, dev_status, st);
+    default: return launch_t<MOE_FP32>(r, topk_idx, topk_weights, dev_status, st);
+  }
+}
+
+}  // namespace moe_ep

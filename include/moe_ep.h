@@ -17,7 +17,10 @@
  * notify and dispatch in one launch -- and moe_combine_quant,
  * moe_token_layout); and the fused deep MoE of section 4 (moe_dispatch_expand,
  * moe_group_offsets, the grouped INT8 GEMMs on the tensor cores, the GMM1
- * epilogue moe_swiglu_quant*, moe_combine_f32 / moe_deq_combine).
+ * epilogue moe_swiglu_quant*, moe_combine_f32 / moe_deq_combine); and what
+ * stands around them: routing (moe_route), the gradients of routing and
+ * combine (moe_route_backward, moe_combine_backward), and the INT8 product
+ * that reads 8-bit operands (moe_linear_i8).
  *
  * Notation: R ranks, epr experts per rank, E = R*epr experts, bs tokens per
  * rank, T = R*bs tokens, k experts per token, P = T*k (token, k) pairs,
@@ -66,7 +69,12 @@ typedef enum {
                               before first use, or overlapping calls share it */
 } moe_status;
 
-typedef enum { MOE_BF16 = 0, MOE_FP16 = 1 } moe_dtype;
+/* Element types.  A shape's dtype (tokens, expert outputs) is MOE_BF16 or
+ * MOE_FP16; the wider types are for the arguments that name them. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_INT32 = 3 } moe_dtype;
+
+/* Score function of moe_route. */
+typedef enum { MOE_SIGMOID = 0, MOE_SOFTMAX = 1 } moe_score;
 
 /* Limits.  R <= 384 is CAM_MAX_RANK_SIZE (comm_args.h, section 2.2.1). */
 #define MOE_EP_MAX_RANKS 384
@@ -471,6 +479,124 @@ moe_status moe_deq_combine(const moe_shape* shape, const int32_t* expert_acc,
                            const int32_t* send_idx, const int32_t* put_offset,
                            const int64_t* rank_recv_base, void* out, int32_t* dev_status,
                            void* stream);
+
+/* ---- routing and the pipeline's gradients (no counterpart in the page, which
+ * takes topk_idx and topk_weights as given) ----------------------------------- */
+
+/* Routing: the ids and gate weights that the pipeline takes.  For a token
+ * with logits l[0..E-1] (read as fp32):
+ *   score     s[e] = 1 / (1 + exp(-l[e]))             (MOE_SIGMOID)
+ *             s[e] = exp(l[e]) / sum_i exp(l[i])      (MOE_SOFTMAX)
+ *   choice    c[e] = s[e] + bias[e]; without a bias c = s
+ *   groups    the experts form n_group groups of E / n_group neighbours; a
+ *             group's score is the sum of its group_top (1 or 2) highest
+ *             choices, and only the topk_group groups with the highest scores
+ *             stay (ties: the lower group)
+ *   ids       the k experts of those groups with the highest choice, in
+ *             descending order, ties to the lower id.  Without a bias the
+ *             order is taken on the logits, which order experts as their
+ *             scores do but never tie by rounding
+ *   weights   s of the chosen experts (never c); renormalise != 0 divides them
+ *             by their sum; then times scale
+ * An expert whose logit is -inf, or whose choice is -inf or NaN (a bias of
+ * -inf, say), is not available: it is never chosen and counts for no group.
+ * Slots left over when fewer than k experts are available get id -1 and
+ * weight 0 (moe_dispatch_layout does not count such a pair, gives it send
+ * index -1 and reports MOE_ERR_EXPERT_ID).  A NaN logit is read as -inf and
+ * sets MOE_ERR_INVALID_ARG in *dev_status; +inf is read as the largest
+ * finite number.  Renormalised weights of scores that sum to 0 are 0.
+ *   logits        [T] rows of E values, logits_stride elements apart, in
+ *                 logits_dtype (MOE_BF16, MOE_FP16 or MOE_FP32), aligned to
+ *                 their element
+ *   bias          fp32 [E] or NULL
+ *   topk_idx      int32 [T][k]
+ *   topk_weights  fp32 [T][k]
+ * 0 <= T, T*k < 2^31, 1 <= E <= MOE_EP_MAX_EXPERTS, logits_stride >= E,
+ * 1 <= k <= min(E, MOE_EP_MAX_TOPK), 1 <= topk_group <= n_group, E % n_group
+ * == 0, group_top 1 or 2, scale finite.  Choices are fp32 within a few ulp of
+ * the definition; weights are computed from the chosen logits alone where the
+ * definition allows it.  One launch. */
+moe_status moe_route(const void* logits, int32_t logits_dtype, int64_t T, int32_t E,
+                     int64_t logits_stride, const float* bias, int32_t score,
+                     int32_t n_group, int32_t topk_group, int32_t group_top, int32_t k,
+                     int32_t renormalise, float scale, int32_t* topk_idx,
+                     float* topk_weights, int32_t* dev_status, void* stream);
+
+/* Gradient of moe_route's weights with respect to the logits (the choice of
+ * the experts, and so the bias, has none).  With g[j] = d_weights[j] * scale
+ * over the slots j of a token that hold an expert, s and w[j] = s[j] / sum s:
+ *   renormalised, sigmoid   d[e_j] = w[j] (1 - s[j]) (g[j] - sum_i w[i] g[i])
+ *   renormalised, softmax   d[e_j] = w[j] (g[j] - sum_i w[i] g[i])
+ *   plain sigmoid           d[e_j] = s[j] (1 - s[j]) g[j]
+ *   plain softmax           d[e] = s[e] (g[j] if e = e_j, else 0, minus
+ *                           sum_i s[i] g[i]), for every expert
+ * and 0 for the other experts.  Slots with id -1 take no part; an id outside
+ * [-1, E) takes no part and sets MOE_ERR_EXPERT_ID; a token's ids are
+ * distinct, as moe_route gives them (a repeated id gets the sum of its slots).
+ *   logits, logits_dtype, T, E, logits_stride, score, k, renormalise, scale
+ *               as in the moe_route call (NaN logits: as there, no status)
+ *   topk_idx    int32 [T][k] (read)
+ *   d_weights   fp32 [T][k] (read)
+ *   d_logits    [T][E] in logits_dtype, rows E apart, 16-byte aligned
+ * One launch. */
+moe_status moe_route_backward(const void* logits, int32_t logits_dtype, int64_t T, int32_t E,
+                              int64_t logits_stride, int32_t score, int32_t k,
+                              int32_t renormalise, float scale, const int32_t* topk_idx,
+                              const float* d_weights, void* d_logits, int32_t* dev_status,
+                              void* stream);
+
+/* Gradient of moe_combine: for every pair (g, k) with receive row r,
+ *   d_expert_out[r][h] = topk_weights[g][k] * d_out[g][h]   (one fp32 rounding,
+ *                        then rounded to nearest even in the token dtype)
+ *   d_weights[g][k]    = sum_h d_out[g][h] * expert_out[r][h]   (fp32)
+ * Rows no pair maps to are left untouched.  A pair with a bad id or a row
+ * outside expert_out_rows gets d_weights 0, writes no row and sets the
+ * matching status.  The sum's order is fixed by H alone.  (The gradient of a
+ * verbatim moe_dispatch needs no entry point of its own: it is moe_combine of
+ * the rows' gradients with weights of 1.)
+ *   d_out         [T][H] in the token dtype, 16-byte aligned (read)
+ *   expert_out    [expert_out_rows][H], 16-byte aligned (read)
+ *   d_expert_out  [expert_out_rows][H], 16-byte aligned
+ *   d_weights     fp32 [T][k]
+ *   other arguments as moe_combine.  One launch. */
+moe_status moe_combine_backward(const moe_shape* shape, const void* d_out,
+                                const void* expert_out, int64_t expert_out_rows,
+                                const int32_t* topk_idx, const float* topk_weights,
+                                const int32_t* send_idx, const int32_t* put_offset,
+                                const int64_t* rank_recv_base, void* d_expert_out,
+                                float* d_weights, int32_t* dev_status, void* stream);
+
+/* Matrix product of 8-bit codes with a scale per row (token) and per output
+ * column (channel), the rows grouped by expert: for row m of group g
+ *   acc[m][n] = sum_{j<K} a[m][j] * w[g][n][j]                 (exact int32)
+ *   c[m][n]   = fp32(acc) * col_scale[g][n] * row_scale(m) (+ bias[g][n])
+ * each product and the sum rounded to nearest even in fp32, then c rounded to
+ * c_dtype; c_dtype MOE_INT32 stores acc itself and reads no scale (what
+ * moe_swiglu_quant_grouped takes).  Both operands stay 8-bit in memory, so a
+ * few rows cost one pass over the weights' bytes; group 0 alone with
+ * group_rows NULL is a plain product (a shared expert, a projection).
+ *   a           int8 [a_rows], rows a_stride bytes apart: packed codes, or the
+ *               row images of moe_dispatch (a_stride = moe_recv_row_bytes)
+ *   w           int8 [G][N], rows w_stride bytes apart (w[g] N rows after
+ *               w[g-1]); codes -128..127 in both
+ *   group_rows  int32 [G] device; NULL only with G == 1: all a_rows rows
+ *   col_scale   fp32 [G][N] (not read with MOE_INT32)
+ *   row_scale   row m's fp32 at byte m * row_scale_stride (not read with
+ *               MOE_INT32)
+ *   bias        fp32 [G][N] or NULL (NULL with MOE_INT32)
+ *   c           [a_rows][N] in c_dtype (MOE_BF16, MOE_FP16, MOE_FP32 or
+ *               MOE_INT32); rows past the groups' total are not written
+ * a, w and c are 16-byte aligned; a_stride and w_stride are multiples of 16 and
+ * at least K (bytes past K in a row are never used);
+ * 1 <= K, N <= MOE_EP_MAX_HIDDEN, 0 <= a_rows <= 2^31 - 1,
+ * 1 <= G <= MOE_EP_MAX_EXPERTS; row_scale_stride >= 4, a multiple of 4.
+ * Errors found on the device as moe_grouped_gemm_i8.  One launch. */
+moe_status moe_linear_i8(const void* a, int64_t a_rows, int64_t a_stride, const void* w,
+                         int64_t w_stride, int32_t G, int32_t N, int32_t K,
+                         const int32_t* group_rows, const float* col_scale,
+                         const void* row_scale, int64_t row_scale_stride,
+                         const float* bias, void* c, int32_t c_dtype,
+                         int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }
