@@ -3,125 +3,688 @@
 //
 // Mathematics.  acc[m][n] = sum_j a[m][j] w[g][n][j] in int32 (K <= 65536, so
 // |acc| <= 2^30: exact), then c = ((fp32(acc) * col) * row) + bias, one
-// rounding each, then one rounding to the output type.
+// rounding each, then one rounding to the output type.  sm_103a has no INT8
+// tensor-core product, so the codes are widened to fp16 inside the kernel
+// (exact, |code| <= 128) and multiplied with fp32 accumulation in chunks of
+// 1024 products: a chunk's partial sums are integers of at most 1024 * 2^14 =
+// 2^24, all exact in fp32; chunks are added in int32.
 //
-// 64 x 64 output tile per CTA, K in steps of 64 bytes through shared memory,
-// four-way integer dot products.
+// Widening costs no memory traffic: both operands travel as bytes from HBM to
+// shared memory.  A code byte b, xor 0x80, put under the high byte 0x64 is the
+// fp16 number 1024 + (b + 128); subtracting 1152 leaves b: five instructions
+// for four codes.
+//
+// Tile: 128 output channels (the MMA's M, TMEM lanes) x up to NT tokens (the
+// MMA's N), so few tokens make narrow, cheap instructions while every weight
+// is still read once.  Warps of a CTA (one CTA per SM, persistent):
+//   warp 0        copies 128 weight rows and up to NT token rows, 128 bytes of
+//                 each, into a ring of byte stages (tensor copies, 128-byte swizzle)
+//   warp 1        issues tcgen05.mma (K = 16) from fp16 stages into one of two
+//                 TMEM accumulators, alternating per chunk
+//   warps 4-11    widen byte stages into fp16 stages (64 codes, 128-byte swizzle)
+//   warps 12-19   drain finished chunks into int32 registers (one channel per
+//                 thread), then scale and store: a warp's stores for one token
+//                 are 32 neighbouring channels
+// When a plain product has fewer tiles than the GPU has SMs, a cluster of up to
+// 8 CTAs splits K; the partial sums (integers, so any order gives the same
+// result) meet in shared memory across the cluster, each CTA finishing its
+// share of the tile's tokens.
+// Every wait is bounded: a timeout sets MOE_ERR_TIMEOUT, the CTA stops issuing
+// work and drains what is in flight.
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "moe_ep_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace moe_ep {
-namespace {
 
-constexpr int BM = 64, BN = 64, BK = 64, kThreads = 256;
-
-// 16 bytes at column j of a row of K codes; zeros past K.
-__device__ __forceinline__ uint4 load_codes(const uint8_t* row, int j, int K) {
-  if (j + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row + j));
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (j + i < K) w[i >> 2] |= uint32_t(__ldg(row + j + i)) << (8 * (i & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+cudaError_t encode_bytes_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
+                            int64_t stride, uint32_t box_rows) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                   cudaEnableDefault, &q);
+  if (e != cudaSuccess) return e;
+  if (q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(stride)};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = reinterpret_cast<Encode>(fn)(
+      map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-__global__ void __launch_bounds__(kThreads)
-linear_i8_kernel(const LinearArgs p, int32_t* dev_status) {
-  __shared__ uint32_t sa[BM][BK / 4 + 1], sw[BN][BK / 4 + 1];
-  __shared__ int64_t s_row0, s_rows;
-  __shared__ int s_g, s_n0;
-  const int tid = threadIdx.x;
+namespace {
+
+constexpr int BM = 128;              // output channels per tile
+constexpr int BK = 64;               // codes per fp16 stage: one 128-byte row
+constexpr int kHalves = 2;           // fp16 stages per byte stage (128-byte rows both)
+constexpr int BKB = kHalves * BK;
+constexpr int kChunk = 1024 / BKB;   // byte stages per chunk: 1024 products, exact in fp32
+constexpr int kRasterTokens = 8;     // token blocks per raster band (weights reused from L2)
+constexpr int kConvWarps = 8, kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * (kConvWarps + kEpiWarps);
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kAccCols = 256;   // column offset of the second accumulator
+constexpr uint32_t kSpin = kGemmSpin;
+constexpr int kMaxByteStages = 12;
+
+// Registers per thread: 96 at launch (640 threads).  With 256-token tiles an
+// epilogue thread holds 128 sums, so they are handed out again by role:
+// 256 x 160 + 256 x 56 + 128 x 40 = 60416 <= 640 x 96.
+constexpr int kEpiRegs = 160, kConvRegs = 56, kCtrlRegs = 40;
+
+// LT: token rows that one CTA holds (a pair of CTAs shares the tile's tokens).
+template <int LT>
+struct Stages {
+  static constexpr int kF16 = LT > 128 ? 2 : 3;                  // fp16 stages
+  static constexpr uint32_t kF16Bytes = (BM + LT) * BK * 2;
+  static constexpr uint32_t kByteBytes = (BM + LT) * BKB;
+  static constexpr uint32_t kOffBytes = kF16 * kF16Bytes;
+  // barriers and flags, then the group tables, follow the byte stages
+  static constexpr uint32_t kBarBytes = 512;
+  static size_t bytes(int nbyte, int G) {
+    return 1024 + kOffBytes + size_t(nbyte) * kByteBytes + kBarBytes + size_t(G + 1) * 8;
+  }
+};
+
+struct Tile {
+  int g;           // group
+  int n0;          // first output channel
+  int row0;        // first token row
+  int rows;        // tokens stored
+  int cols;        // tokens computed: rows rounded up to the MMA's step
+};
+
+__device__ __forceinline__ int group_count(const LinearArgs& p, int g, int32_t* dev_status) {
+  if (!p.group_rows) return static_cast<int>(p.a_rows);
+  const int c = __ldg(p.group_rows + g);
+  if (c < 0 && dev_status) set_status(dev_status, MOE_ERR_INVALID_ARG);
+  return c < 0 ? 0 : c;
+}
+
+// A group of cnt tokens is cut into equal blocks of at most `block` tokens.
+__device__ __forceinline__ int token_blocks(int cnt, int block) {
+  return static_cast<int>((int64_t(cnt) + block - 1) / block);
+}
+
+// CG CTAs share a tile of CG * BM channels; token counts are multiples of
+// 16 * CG (the MMA's step).
+template <int CG>
+__device__ __forceinline__ Tile decode_tile(int t, const int* goff, const int* tpre, int G,
+                                            int ntn, int block) {
+  int lo = 0, hi = G;                 // largest g with tpre[g] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tpre[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int cnt = goff[lo + 1] - goff[lo];
+  const int blocks = token_blocks(cnt, block);
+  constexpr int kStep = 16 * CG;
+  const int per = ((cnt + blocks - 1) / blocks + kStep - 1) / kStep * kStep;
+  // bands of kRasterTokens token blocks (the last band takes the remainder);
+  // inside a band the token block is fastest, so the CTAs in flight share
+  // weight tiles and a bounded number of token blocks
+  const int nband = max(blocks / kRasterTokens, 1);
+  const int local = t - tpre[lo];
+  const int per_band = kRasterTokens * ntn;
+  const int band = min(local / per_band, nband - 1);
+  const int width = band < nband - 1 ? kRasterTokens : blocks - band * kRasterTokens;
+  const int r = local - band * per_band;
+  Tile tl;
+  tl.g = lo;
+  tl.n0 = r / width * (CG * BM);
+  const int first = (band * kRasterTokens + r % width) * per;
+  tl.row0 = goff[lo] + first;
+  tl.rows = max(0, min(per, cnt - first));
+  tl.cols = max(kStep, (tl.rows + kStep - 1) / kStep * kStep);
+  return tl;
+}
+
+// 16 codes -> 16 fp16 numbers (exact), low to high.
+__device__ __forceinline__ void widen16(const uint4& v, uint4 (&o)[2]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = w[i] ^ 0x80808080u;
+    const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140);   // 0x64b1 64b0
+    const uint32_t hi = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[2 * i]) : "r"(lo), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[2 * i + 1]) : "r"(hi), "r"(0x64806480u));
+  }
+  o[0] = make_uint4(r[0], r[1], r[2], r[3]);
+  o[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w) : "memory");
+}
+
+// Stores c[m][n] from the accumulator: OUT is the output type.
+template <int OUT>
+__device__ __forceinline__ void store_out(void* c, int64_t at, int32_t acc, float col, float row,
+                                          float bias, bool has_bias) {
+  if constexpr (OUT == MOE_INT32) {
+    static_cast<int32_t*>(c)[at] = acc;
+  } else {
+    float v = __fmul_rn(__fmul_rn(__int2float_rn(acc), col), row);
+    if (has_bias) v = __fadd_rn(v, bias);
+    if constexpr (OUT == MOE_FP32) static_cast<float*>(c)[at] = v;
+    else static_cast<uint16_t*>(c)[at] = static_cast<uint16_t>(narrow_rn<OUT>(v));
+  }
+}
+
+// NT: tokens per tile at most; CG: CTAs per tile (1, or a pair that shares its
+// operands and runs one MMA of 256 channels).  With CG = 1 a larger cluster
+// splits K.
+template <int NT, int CG, int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ CUtensorMap map_a, const LinearArgs p, int block,
+                      int box_rows, int nbyte, int32_t* dev_status) {
+  constexpr int LT = NT / CG;
+  using St = Stages<LT>;
+  constexpr int NF = St::kF16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + St::kOffBytes + nbyte * St::kByteBytes);
+  uint64_t* bfull = bars;                       // byte stage filled
+  uint64_t* bempty = bfull + kMaxByteStages;    // byte stage widened
+  uint64_t* ffull = bempty + kMaxByteStages;    // fp16 stage written
+  uint64_t* fempty = ffull + 4;                 // fp16 stage multiplied
+  uint64_t* tfull = fempty + 4;                 // accumulator final
+  uint64_t* tempty = tfull + 2;                 // accumulator drained
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+  int* goff = reinterpret_cast<int*>(smem + St::kOffBytes + nbyte * St::kByteBytes +
+                                     St::kBarBytes);
+  int* tpre = goff + p.G + 1;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ntn = (p.N + CG * BM - 1) / (CG * BM);
+  const int rank = CG > 1 ? static_cast<int>(cluster_rank()) : 0;    // in the pair
+  const int split = CG > 1 ? 1 : static_cast<int>(cluster_size());
+  const int part = CG > 1 ? 0 : static_cast<int>(cluster_rank());
+
+  // ---- group tables: row offsets and tile prefix -----------------------------------
+  {
+    const int per = (p.G + kThreads - 1) / kThreads;
+    const int g0 = min(tid * per, p.G), g1 = min(g0 + per, p.G);
+    int64_t rsum = 0;
+    int tsum = 0;
+    for (int g = g0; g < g1; ++g) {
+      const int c = group_count(p, g, dev_status);
+      rsum += c;
+      tsum += token_blocks(c, block) * ntn;
+    }
+    int64_t* s_r = reinterpret_cast<int64_t*>(smem);              // [kThreads] (stages: unused yet)
+    int* s_t = reinterpret_cast<int*>(s_r + kThreads);
+    s_r[tid] = rsum;
+    s_t[tid] = tsum;
+    __syncthreads();
+    if (warp == 0) {          // exclusive scan of the threads' sums
+      constexpr int kPer = kThreads / 32;
+      int64_t r = 0;
+      int tt = 0;
+      for (int i = 0; i < kPer; ++i) {
+        r += s_r[lane * kPer + i];
+        tt += s_t[lane * kPer + i];
+      }
+      int64_t ri = r;
+      int ti = tt;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, ri, d);
+        const int b = __shfl_up_sync(0xffffffffu, ti, d);
+        if (lane >= d) {
+          ri += a;
+          ti += b;
+        }
+      }
+      int64_t re = ri - r;
+      int te = ti - tt;
+      for (int i = 0; i < kPer; ++i) {
+        const int64_t a = s_r[lane * kPer + i];
+        const int b = s_t[lane * kPer + i];
+        s_r[lane * kPer + i] = re;
+        s_t[lane * kPer + i] = te;
+        re += a;
+        te += b;
+      }
+      if (lane == 31) {
+        // more rows than the buffer holds: no tile at all
+        const bool over = re > p.a_rows;
+        if (over) set_status(dev_status, MOE_ERR_CAPACITY);
+        goff[p.G] = over ? 0 : static_cast<int>(re);
+        tpre[p.G] = over ? 0 : te;
+      }
+    }
+    __syncthreads();
+    int64_t r = s_r[tid];
+    int tt = s_t[tid];
+    for (int g = g0; g < g1; ++g) {
+      goff[g] = static_cast<int>(min(r, p.a_rows));
+      tpre[g] = tt;
+      const int c = group_count(p, g, nullptr);
+      r += c;
+      tt += token_blocks(c, block) * ntn;
+    }
+  }
   if (tid == 0) {
-    const int64_t ntn = (p.N + BN - 1) / BN;
-    int64_t t = blockIdx.x, off = 0;
-    s_g = -1;
-    for (int g = 0; g < p.G; ++g) {
-      int64_t n = p.group_rows ? __ldg(p.group_rows + g) : p.a_rows;
-      if (n < 0) {
-        set_status(dev_status, MOE_ERR_INVALID_ARG);
-        n = 0;
-      }
-      const int64_t tiles = (n + BM - 1) / BM * ntn;
-      if (s_g < 0 && t < tiles) {
-        s_g = g;
-        s_row0 = off + t / ntn * BM;
-        s_rows = min(int64_t(BM), n - t / ntn * BM);
-        s_n0 = static_cast<int>(t % ntn) * BN;
-      }
-      t -= tiles;
-      off += n;
+    for (int s = 0; s < nbyte; ++s) {
+      mbar_init(bfull + s, 1);
+      mbar_init(bempty + s, kConvWarps);
     }
-    if (off > p.a_rows) {
-      set_status(dev_status, MOE_ERR_CAPACITY);
-      s_g = -1;
+    for (int s = 0; s < NF; ++s) {
+      mbar_init(ffull + s, CG * kConvWarps / kHalves);
+      mbar_init(fempty + s, 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull + b, 1);
+      mbar_init(tempty + b, CG * kEpiWarps);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tensor_map_prefetch(&map_w);
+    tensor_map_prefetch(&map_a);
   }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc<CG>(tmem_slot, kTmemCols);
+  }
+  tc_fence_before();
   __syncthreads();
-  const int g = s_g;
-  if (g < 0) return;
-  const int64_t row0 = s_row0;
-  const int rows = static_cast<int>(s_rows), n0 = s_n0;
-  const uint8_t* a = static_cast<const uint8_t*>(p.a) + row0 * p.a_stride;
-  const uint8_t* w = static_cast<const uint8_t*>(p.w) + (int64_t(g) * p.N + n0) * p.w_stride;
-  const int lr = tid >> 2, lc = (tid & 3) * 16;      // this thread's 16 bytes of a tile
-  const int ty = tid >> 4, tx = tid & 15;
-  int acc[4][4] = {};
-  for (int j = 0; j < p.K; j += BK) {
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    const uint4 va = lr < rows && j + lc < p.K ? load_codes(a + lr * p.a_stride, j + lc, p.K) : z;
-    const uint4 vw = n0 + lr < p.N && j + lc < p.K
-                         ? load_codes(w + lr * p.w_stride, j + lc, p.K) : z;
-    __syncthreads();
-    const uint32_t ua[4] = {va.x, va.y, va.z, va.w}, uw[4] = {vw.x, vw.y, vw.z, vw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sa[lr][lc / 4 + i] = ua[i];
-      sw[lr][lc / 4 + i] = uw[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < BK / 4; ++c)
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          acc[y][x] = __dp4a(static_cast<int>(sa[ty + 16 * y][c]),
-                             static_cast<int>(sw[tx + 16 * x][c]), acc[y][x]);
-  }
-#pragma unroll
-  for (int y = 0; y < 4; ++y) {
-    const int r = ty + 16 * y;
-    if (r >= rows) continue;
-    const int64_t m = row0 + r;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int n = n0 + tx + 16 * x;
-      if (n >= p.N) continue;
-      const int64_t at = m * p.N + n, gn = int64_t(g) * p.N + n;
-      if (p.c_dtype == MOE_INT32) {
-        static_cast<int32_t*>(p.c)[at] = acc[y][x];
-        continue;
+  if constexpr (CG > 1) cluster_sync();      // the peer's barriers are ready too
+  tc_fence_after();
+
+  const uint32_t tmem = *tmem_slot;
+  const int tiles = tpre[p.G];
+  const int nkb = (p.K + BKB - 1) / BKB;     // byte stages (zeros past K)
+  const int kb0 = nkb * part / split, kb1 = nkb * (part + 1) / split;   // this CTA's
+  const int nk = kb1 - kb0;
+  const int nchunks = (nk + kChunk - 1) / kChunk;
+  const int first = blockIdx.x / (CG * split), step = gridDim.x / (CG * split);
+
+  if (warp < 4) {
+    if constexpr (NT > 64) regs_fewer<kCtrlRegs>();
+    if (warp == 0) {
+      // ---- copies -------------------------------------------------------------------
+      const bool issue = elect_one();
+      int s = 0;
+      uint32_t phase = 0, nload = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += step) {
+        const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
+        const int rows = tl.cols / CG;                   // this CTA's token rows
+        const int boxes = (rows + box_rows - 1) / box_rows;
+        const int wrow = tl.g * p.N + tl.n0 + rank * BM;
+        const int arow = tl.row0 + rank * rows;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_bounded(bempty + s, phase ^ 1u, kSpin)) {
+            ok = false;
+            break;
+          }
+          if (issue) {
+            const uint32_t dst = sbase + St::kOffBytes + s * St::kByteBytes;
+            mbar_arrive_expect_tx(bfull + s, (BM + boxes * box_rows) * BKB);
+            tensor_load_2d(dst, &map_w, kb * BKB, wrow, bfull + s);
+            for (int b = 0; b < boxes; ++b)
+              tensor_load_2d(dst + (BM + b * box_rows) * BKB, &map_a, kb * BKB,
+                             arow + b * box_rows, bfull + s);
+          }
+          ++nload;
+          if (++s == nbyte) { s = 0; phase ^= 1u; }
+        }
+        ok = ok && !*abort_flag;
       }
-      const float ts = __ldg(reinterpret_cast<const float*>(p.row_scale + m * p.row_scale_stride));
-      float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[y][x]), __ldg(p.col_scale + gn)), ts);
-      if (p.bias) v = __fadd_rn(v, __ldg(p.bias + gn));
-      if (p.c_dtype == MOE_FP32) static_cast<float*>(p.c)[at] = v;
-      else
-        static_cast<uint16_t*>(p.c)[at] = static_cast<uint16_t>(
-            p.c_dtype == MOE_BF16 ? narrow_rn<MOE_BF16>(v) : narrow_rn<MOE_FP16>(v));
+      if (!ok) {      // after a timeout, no copy may land once the CTA has gone
+        if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        for (uint32_t i = nload > uint32_t(nbyte) ? nload - nbyte : 0; i < nload; ++i)
+          mbar_wait_bounded(bfull + i % nbyte, (i / nbyte) & 1u, kSpin);
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---- products (of the pair, by its first CTA) -----------------------------------
+      const bool issue = elect_one();
+      int f = 0;
+      uint32_t phase = 0, chunk = 0, ncommit = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += step) {
+        const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
+        const uint32_t idesc = f16_mma_desc(CG * BM, tl.cols);
+        for (int c = 0; ok && c < nchunks; ++c, ++chunk) {
+          const uint32_t b = chunk & 1u, use = (chunk >> 1) & 1u;
+          if (!mbar_wait_bounded(tempty + b, use ^ 1u, kSpin) || *abort_flag) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + b * kAccCols;
+          const int n = min(kChunk, nk - c * kChunk) * kHalves;
+          for (int kb = 0; kb < n; ++kb) {
+            if (!mbar_wait_bounded(ffull + f, phase, kSpin)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (issue) {
+              const uint32_t st = sbase + f * St::kF16Bytes;
+              const uint64_t da = operand_desc(st), db = operand_desc(st + BM * BK * 2);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)     // + 32 bytes along K per step
+                mma_f16<CG>(d, da + 2 * kk, db + 2 * kk, idesc, kb != 0 || kk != 0);
+              mma_commit_to<CG>(fempty + f);
+            }
+            ++ncommit;
+            if (++f == NF) { f = 0; phase ^= 1u; }
+          }
+          if (!ok) break;
+          if (issue) mma_commit_to<CG>(tfull + b);
+        }
+      }
+      if (!ok) {
+        if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // every commit has arrived (the last one of each barrier) before the CTA
+      // may go, also after a timeout
+      for (uint32_t i = ncommit > uint32_t(NF) ? ncommit - NF : 0; i < ncommit; ++i)
+        if (!mbar_wait_bounded(fempty + i % NF, (i / NF) & 1u, kSpin))
+          set_status(dev_status, MOE_ERR_TIMEOUT);
+      for (uint32_t i = chunk > 2 ? chunk - 2 : 0; i < chunk; ++i)
+        if (!mbar_wait_bounded(tfull + (i & 1u), (i >> 1) & 1u, kSpin))
+          set_status(dev_status, MOE_ERR_TIMEOUT);
+    } else if (CG > 1 && warp == 1) {
+      // the leader's last commits reach this CTA's barriers before it may go
+      const uint32_t ntile = first < tiles ? (tiles - first + step - 1) / step : 0;
+      const uint32_t ncommit = ntile * nk * kHalves;
+      for (uint32_t i = ncommit > uint32_t(NF) ? ncommit - NF : 0; i < ncommit; ++i)
+        for (uint32_t k = 0; k < kSpin && !*abort_flag; ++k)
+          if (mbar_try_wait(fempty + i % NF, (i / NF) & 1u)) break;
     }
+    __syncwarp();
+    if (split > 1) {
+      cluster_sync();
+      cluster_sync();
+    }
+  } else if (warp < 4 + kConvWarps) {
+    // ---- bytes -> fp16 ------------------------------------------------------------------
+    if constexpr (NT > 64) regs_fewer<kConvRegs>();
+    // two groups of four warps, one for each 64-code half of a byte stage: one
+    // group's waits and fences overlap the other's widening.  A thread takes 16
+    // codes (quarter uc of the half) of one row in 32.  Eight neighbouring
+    // threads read rows r and r + 4, whose swizzled quarters lie in different
+    // halves of the banks; their two 16-byte fp16 pieces are stored in
+    // opposite order, so that the eight stores, too, use all banks once.
+    constexpr int kGroupThreads = 32 * kConvWarps / kHalves;
+    constexpr int kRows = kGroupThreads / 4;            // rows per pass: a multiple of 8, so
+    constexpr int kPasses = (BM + LT) / kRows;          // every pass has one swizzle key
+    constexpr int kBatch = kPasses % 4 == 0 ? 4 : 3;    // passes loaded before widening
+    const int half = (tid - 128) / kGroupThreads, u = (tid - 128) % kGroupThreads;
+    const int uq = u >> 2, uc = u & 3;
+    const int ur = (uq >> 3) * 8 + ((uq >> 1) & 3) + (uq & 1) * 4;
+    const uint32_t in = ur * BKB + (((half * 4 + uc) ^ (ur & 7)) << 4);
+    const uint32_t second = uq & 1;                     // which piece goes first
+    const uint32_t out0 = ur * (BK * 2) + (((2 * uc + second) ^ (ur & 7)) << 4);
+    const uint32_t out1 = ur * (BK * 2) + (((2 * uc + 1 - second) ^ (ur & 7)) << 4);
+    int s = 0, f = half;
+    uint32_t bphase = 0, fphase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += step) {
+      const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
+      const int rows = BM + tl.cols / CG;               // weight rows, then token rows
+      for (int kb = 0; kb < nk; ++kb) {
+        const bool got = mbar_wait_bounded(bfull + s, bphase, kSpin) &&
+                         mbar_wait_bounded(fempty + f, fphase ^ 1u, kSpin);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        const uint32_t src = sbase + St::kOffBytes + s * St::kByteBytes + in;
+        const uint32_t dst = sbase + f * St::kF16Bytes;
+#pragma unroll
+        for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if ((i0 + i) * kRows + ur < rows) v[i] = lds128(src + (i0 + i) * kRows * BKB);
+          if (i0 + kBatch >= kPasses) {                 // this half of the stage is read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bempty + s);
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if ((i0 + i) * kRows + ur < rows) {
+              uint4 o[2];
+              widen16(second ? make_uint4(v[i].z, v[i].w, v[i].x, v[i].y) : v[i], o);
+              sts128(dst + (i0 + i) * kRows * BK * 2 + out0, o[0]);
+              sts128(dst + (i0 + i) * kRows * BK * 2 + out1, o[1]);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG > 1) cluster_arrive(cluster_addr(smem_addr(ffull + f), 0));
+          else mbar_arrive(ffull + f);
+        }
+        if (++s == nbyte) { s = 0; bphase ^= 1u; }
+        f += kHalves;
+        if (f >= NF) { f -= NF; fphase ^= 1u; }
+      }
+      ok = ok && !*abort_flag;
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (!ok) {
+      if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (split > 1) {
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    // ---- chunk sums -> int32, scales, stores ----------------------------------------------
+    if constexpr (NT > 64) regs_more<kEpiRegs>();
+    constexpr int kCols = NT / 2;            // accumulator columns per thread
+    const int q = warp & 3;                  // TMEM lanes 32 q ..
+    const int half = (warp - 4 - kConvWarps) >> 2;
+    const int eth = tid - 128 - 32 * kConvWarps;   // epilogue thread
+    uint32_t chunk = 0;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += step) {
+      const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
+      const int n = tl.n0 + rank * BM + q * 32 + lane;
+      int32_t acc[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) acc[j] = 0;
+      for (int c = 0; c < nchunks; ++c, ++chunk) {
+        const uint32_t b = chunk & 1u, use = (chunk >> 1) & 1u;
+        const bool got = mbar_wait_bounded(tfull + b, use, kSpin) && !*abort_flag;
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t base = tmem + (uint32_t(q * 32) << 16) + b * kAccCols + half * kCols;
+#pragma unroll
+        for (int cb = 0; cb < kCols / 16; ++cb)
+          if (half * kCols + cb * 16 < tl.cols) {
+            uint32_t v[16];
+            tmem_load16(base + cb * 16, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[cb * 16 + j] += __float2int_rn(__uint_as_float(v[j]));
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG > 1) cluster_arrive(cluster_addr(smem_addr(tempty + b), 0));
+          else mbar_arrive(tempty + b);
+        }
+      }
+      if (!ok) {
+        if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+      const bool chan = n < p.N;
+      const int64_t gn = int64_t(tl.g) * p.N + n;
+      const float col = OUT != MOE_INT32 && chan ? __ldg(p.col_scale + gn) : 0.0f;
+      const float bias = OUT != MOE_INT32 && p.bias && chan ? __ldg(p.bias + gn) : 0.0f;
+      auto row_scale = [&](int j) {         // of the tile's token j (0 past the tile)
+        return OUT != MOE_INT32 && j < tl.rows
+                   ? __ldg(reinterpret_cast<const float*>(
+                         p.row_scale + int64_t(tl.row0 + j) * p.row_scale_stride))
+                   : 0.0f;
+      };
+      if (split == 1) {
+#pragma unroll
+        for (int jb = 0; jb < kCols; jb += 32) {
+          const int j0 = half * kCols + jb;
+          if (j0 >= tl.rows) break;
+          const float rs = row_scale(j0 + lane);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float row = __shfl_sync(0xffffffffu, rs, j);
+            if (j0 + j < tl.rows && chan)
+              store_out<OUT>(p.c, int64_t(tl.row0 + j0 + j) * p.N + n, acc[jb + j], col, row,
+                             bias, p.bias != nullptr);
+          }
+        }
+      } else {
+        // rank d finishes columns [d, d+1) * kCols / split of each half
+        cluster_sync();                     // every CTA is done with its stages
+        const int share = kCols / split;
+        const uint32_t mine = sbase + ((part * share) * 256 + eth) * 4;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          const int d = j / share, jj = j - d * share;
+          cluster_store(cluster_addr(mine + jj * 1024, d), static_cast<uint32_t>(acc[j]));
+        }
+        cluster_sync();
+        for (int jj = 0; jj < share; ++jj) {
+          int32_t sum = 0;
+          for (int r = 0; r < split; ++r)
+            sum += *reinterpret_cast<volatile int32_t*>(smem + ((r * share + jj) * 256 + eth) * 4);
+          const int j = half * kCols + part * share + jj;
+          if (j < tl.rows && chan)
+            store_out<OUT>(p.c, int64_t(tl.row0 + j) * p.N + n, sum, col, row_scale(j), bias,
+                           p.bias != nullptr);
+        }
+      }
+    }
+    if (split > 1 && (first >= tiles || !ok)) {   // no tile, or a timeout: the peers still wait
+      cluster_sync();
+      cluster_sync();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // no CTA of a pair goes while the other may still arrive on its barriers
+  if constexpr (CG > 1) cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free<CG>(tmem, kTmemCols);
+  }
+}
+
+template <int NT, int CG, int OUT>
+cudaError_t launch_out(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
+                       int block, int box_rows, int clusters, int split, int32_t* dev_status,
+                       int optin, cudaStream_t st) {
+  using S = Stages<NT / CG>;
+  int nbyte = kMaxByteStages;
+  while (nbyte > 2 && S::bytes(nbyte, p.G) > size_t(optin)) --nbyte;
+  const size_t smem = S::bytes(nbyte, p.G);
+  auto kernel = linear_i8_tile_kernel<NT, CG, OUT>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * CG * split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(CG * split);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, block, box_rows, nbyte, dev_status);
+}
+
+template <int NT, int CG>
+cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
+                      int block, int box_rows, int clusters, int split, int32_t* dev_status,
+                      int optin, cudaStream_t st) {
+  switch (p.c_dtype) {
+    case MOE_BF16:
+      return launch_out<NT, CG, MOE_BF16>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
+    case MOE_FP16:
+      return launch_out<NT, CG, MOE_FP16>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
+    case MOE_FP32:
+      return launch_out<NT, CG, MOE_FP32>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
+    default:
+      return launch_out<NT, CG, MOE_INT32>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
-  const int64_t ntn = (p.N + BN - 1) / BN;
-  const int64_t tiles = (p.a_rows / BM + p.G) * ntn;   // at least the groups' tiles
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  linear_i8_kernel<<<static_cast<unsigned>(tiles), kThreads, 0, st>>>(p, dev_status);
-  return cudaGetLastError();
+  int dev = 0, sms = 0, optin = 0;
+  cudaError_t e = current_device_sms(&dev, &sms);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e != cudaSuccess) return e;
+  // Pairs of CTAs on 256 x 256 tiles where groups are large enough to fill
+  // them and there are tiles for most SMs; else one CTA on 128 x 64.
+  const bool big = p.a_rows / p.G > 128 &&
+                   (p.a_rows / 256 + 1) * ((p.N + 255) / 256) * 2 >= sms;
+  const int nt = big ? 256 : 64, cg = big ? 2 : 1;
+  const int64_t ntn = (p.N + cg * BM - 1) / (cg * BM);
+  // at most this many tiles, for any group sizes
+  const int64_t most = (p.a_rows / nt + std::min<int64_t>(p.G, p.a_rows)) * ntn;
+  if (most > INT32_MAX) return cudaErrorInvalidValue;
+  int clusters = static_cast<int>(std::min<int64_t>(most, sms / cg));
+  int block = nt, split = 1;
+  if (p.G == 1 && !big) {
+    const int64_t tiles = (p.a_rows + nt - 1) / nt * ntn;
+    const int nkb = (p.K + BKB - 1) / BKB;
+    while (split < 8 && tiles * split * 2 <= sms && nkb >= split * 2 * 2) split *= 2;
+    if (split > 1) clusters = static_cast<int>(tiles);   // one tile per cluster
+  }
+  CUtensorMap mw, ma;
+  // token rows per copy: few copies for full tiles, few useless rows for small groups
+  const int64_t mean = (p.a_rows + p.G - 1) / p.G;
+  const int box_rows = big || mean > 32 ? 64 : mean > 16 ? 32 : 16;
+  e = encode_bytes_2d(&mw, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, BM);
+  if (e == cudaSuccess)
+    e = encode_bytes_2d(&ma, p.a, p.a_rows, p.K, p.a_stride, box_rows);
+  if (e != cudaSuccess) return e;
+  return big ? launch_nt<256, 2>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st)
+             : launch_nt<64, 1>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
 }
 
 }  // namespace moe_ep
