@@ -21,8 +21,8 @@
 //                 each, into a ring of byte stages (tensor copies, 128-byte swizzle)
 //   warp 1        issues tcgen05.mma (K = 16) from fp16 stages into one of two
 //                 TMEM accumulators, alternating per chunk
-//   warps 4-11    widen byte stages into fp16 stages (64 codes, 128-byte swizzle)
-//   warps 12-19   drain finished chunks into int32 registers (one channel per
+//   8 or 16 warps widen byte stages into fp16 stages (64 codes, 128-byte swizzle)
+//   16 or 8 warps drain finished chunks into int32 registers (one channel per
 //                 thread), then scale and store: a warp's stores for one token
 //                 are 32 neighbouring channels
 // When a plain product has fewer tiles than the GPU has SMs, a cluster of up to
@@ -34,6 +34,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_ep_internal.cuh"
 #include "tcgen05.cuh"
@@ -71,22 +72,28 @@ constexpr int kHalves = 2;           // fp16 stages per byte stage (128-byte row
 constexpr int BKB = kHalves * BK;
 constexpr int kChunk = 1024 / BKB;   // byte stages per chunk: 1024 products, exact in fp32
 constexpr int kRasterTokens = 8;     // token blocks per raster band (weights reused from L2)
-constexpr int kConvWarps = 8, kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * (kConvWarps + kEpiWarps);
+// Warps that widen (in groups of four on different stages) and warps that drain
+// and store.  A pair's 256-token tiles have long MMAs and 256 accumulator
+// columns per lane: two groups keep up, and 16 warps hold 64 sums per thread.
+// Narrow tiles stream weights: four groups, 8 warps with 32 sums per thread.
+constexpr int kGroupWarps = 4;
+template <int CG>
+struct Roles {
+  static constexpr int kConvWarps = CG > 1 ? 8 : 16;
+  static constexpr int kEpiWarps = 24 - kConvWarps;
+};
+constexpr int kThreads = 128 + 32 * 24;
+// Registers per thread: 72 at launch (896 threads).  With pairs they are handed
+// out again by role: 512 x 96 + 256 x 40 + 128 x 40 = 64512 = 896 x 72.
+constexpr int kEpiRegs = 96, kConvRegs = 40, kCtrlRegs = 40;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAccCols = 256;   // column offset of the second accumulator
-constexpr uint32_t kSpin = kGemmSpin;
-constexpr int kMaxByteStages = 12;
-
-// Registers per thread: 96 at launch (640 threads).  With 256-token tiles an
-// epilogue thread holds 128 sums, so they are handed out again by role:
-// 256 x 160 + 256 x 56 + 128 x 40 = 60416 <= 640 x 96.
-constexpr int kEpiRegs = 160, kConvRegs = 56, kCtrlRegs = 40;
+constexpr int kMaxByteStages = 12, kMaxF16Stages = 6;
 
 // LT: token rows that one CTA holds (a pair of CTAs shares the tile's tokens).
 template <int LT>
 struct Stages {
-  static constexpr int kF16 = LT > 128 ? 2 : 3;                  // fp16 stages
+  static constexpr int kF16 = 4;                                  // fp16 stages
   static constexpr uint32_t kF16Bytes = (BM + LT) * BK * 2;
   static constexpr uint32_t kByteBytes = (BM + LT) * BKB;
   static constexpr uint32_t kOffBytes = kF16 * kF16Bytes;
@@ -120,14 +127,15 @@ __device__ __forceinline__ int token_blocks(int cnt, int block) {
 // CG CTAs share a tile of CG * BM channels; token counts are multiples of
 // 16 * CG (the MMA's step).
 template <int CG>
-__device__ __forceinline__ Tile decode_tile(int t, const int* goff, const int* tpre, int G,
+__device__ __forceinline__ Tile decode_tile(int t, uint32_t goff, uint32_t tpre, int G,
                                             int ntn, int block) {
   int lo = 0, hi = G;                 // largest g with tpre[g] <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (tpre[mid] <= t) lo = mid; else hi = mid;
+    if (smem_load(tpre + 4 * mid) <= t) lo = mid; else hi = mid;
   }
-  const int cnt = goff[lo + 1] - goff[lo];
+  const int off = smem_load(goff + 4 * lo);
+  const int cnt = smem_load(goff + 4 * lo + 4) - off;
   const int blocks = token_blocks(cnt, block);
   constexpr int kStep = 16 * CG;
   const int per = ((cnt + blocks - 1) / blocks + kStep - 1) / kStep * kStep;
@@ -135,7 +143,7 @@ __device__ __forceinline__ Tile decode_tile(int t, const int* goff, const int* t
   // inside a band the token block is fastest, so the CTAs in flight share
   // weight tiles and a bounded number of token blocks
   const int nband = max(blocks / kRasterTokens, 1);
-  const int local = t - tpre[lo];
+  const int local = t - smem_load(tpre + 4 * lo);
   const int per_band = kRasterTokens * ntn;
   const int band = min(local / per_band, nband - 1);
   const int width = band < nband - 1 ? kRasterTokens : blocks - band * kRasterTokens;
@@ -144,7 +152,7 @@ __device__ __forceinline__ Tile decode_tile(int t, const int* goff, const int* t
   tl.g = lo;
   tl.n0 = r / width * (CG * BM);
   const int first = (band * kRasterTokens + r % width) * per;
-  tl.row0 = goff[lo] + first;
+  tl.row0 = off + first;
   tl.rows = max(0, min(per, cnt - first));
   tl.cols = max(kStep, (tl.rows + kStep - 1) / kStep * kStep);
   return tl;
@@ -177,7 +185,7 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
                "r"(v.w) : "memory");
 }
 
-// Stores c[m][n] from the accumulator: OUT is the output type.
+// One output: its scales, its bias, its rounding.
 template <int OUT>
 __device__ __forceinline__ void store_out(void* c, int64_t at, int32_t acc, float col, float row,
                                           float bias, bool has_bias) {
@@ -191,6 +199,33 @@ __device__ __forceinline__ void store_out(void* c, int64_t at, int32_t acc, floa
   }
 }
 
+// Two tokens of one channel at once, N elements apart, by the same operations
+// (packed; nz is -0, see mul2_rn): the full tiles' way, half the instructions.
+template <int OUT, bool BIAS>
+__device__ __forceinline__ void store_pair(uint8_t* at, uint32_t pitch, int32_t a0, int32_t a1,
+                                           float col, float r0, float r1, float bias, float nz) {
+  if constexpr (OUT == MOE_INT32) {
+    *reinterpret_cast<int32_t*>(at) = a0;
+    *reinterpret_cast<int32_t*>(at + pitch) = a1;
+  } else {
+    float2 v = make_float2(__int2float_rn(a0), __int2float_rn(a1));
+    v = mul2_rn(mul2_rn(v, bcast2(col), nz), make_float2(r0, r1), nz);
+    if constexpr (BIAS) v = add2_rn(v, bcast2(bias));
+    if constexpr (OUT == MOE_FP32) {
+      *reinterpret_cast<float*>(at) = v.x;
+      *reinterpret_cast<float*>(at + pitch) = v.y;
+    } else {
+      uint32_t h;
+      if constexpr (OUT == MOE_BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v.y), "f"(v.x));
+      else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(v.y), "f"(v.x));
+      *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(h);
+      *reinterpret_cast<uint16_t*>(at + pitch) = static_cast<uint16_t>(h >> 16);
+    }
+  }
+}
+
 // NT: tokens per tile at most; CG: CTAs per tile (1, or a pair that shares its
 // operands and runs one MMA of 256 channels).  With CG = 1 a larger cluster
 // splits K.
@@ -198,26 +233,29 @@ template <int NT, int CG, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ CUtensorMap map_a, const LinearArgs p, int block,
-                      int box_rows, int nbyte, int32_t* dev_status) {
+                      int box_rows, int nbyte, float nz, int32_t* dev_status) {
   constexpr int LT = NT / CG;
   using St = Stages<LT>;
+  constexpr int kConvWarps = Roles<CG>::kConvWarps, kEpiWarps = Roles<CG>::kEpiWarps;
+  constexpr int kConvGroups = kConvWarps / kGroupWarps;
   constexpr int NF = St::kF16;
+  // every widening group starts on a stage of its own
+  static_assert(NF >= kConvGroups && NF <= kMaxF16Stages && kConvGroups % kHalves == 0, "stages");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + St::kOffBytes + nbyte * St::kByteBytes);
-  uint64_t* bfull = bars;                       // byte stage filled
-  uint64_t* bempty = bfull + kMaxByteStages;    // byte stage widened
-  uint64_t* ffull = bempty + kMaxByteStages;    // fp16 stage written
-  uint64_t* fempty = ffull + 4;                 // fp16 stage multiplied
-  uint64_t* tfull = fempty + 4;                 // accumulator final
-  uint64_t* tempty = tfull + 2;                 // accumulator drained
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
-  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-  int* goff = reinterpret_cast<int*>(smem + St::kOffBytes + nbyte * St::kByteBytes +
-                                     St::kBarBytes);
-  int* tpre = goff + p.G + 1;
+  const uint32_t bars = sbase + St::kOffBytes + nbyte * St::kByteBytes;
+  auto bfull = [&](int s) { return bars + 8 * s; };                        // byte stage filled
+  auto bempty = [&](int s) { return bars + 8 * (kMaxByteStages + s); };    // ... widened
+  constexpr int kF0 = 2 * kMaxByteStages, kT0 = kF0 + 2 * kMaxF16Stages;
+  auto ffull = [&](int f) { return bars + 8 * (kF0 + f); };                // fp16 stage written
+  auto fempty = [&](int f) { return bars + 8 * (kF0 + kMaxF16Stages + f); };  // ... multiplied
+  auto tfull = [&](int b) { return bars + 8 * (kT0 + b); };                // accumulator final
+  auto tempty = [&](int b) { return bars + 8 * (kT0 + 2 + b); };           // ... drained
+  const uint32_t tmem_slot = bars + 8 * (kT0 + 4), abort_flag = tmem_slot + 4;
+  static_assert(8 * (kT0 + 5) <= St::kBarBytes, "barriers fit");
+  const uint32_t goff = bars + St::kBarBytes, tpre = goff + 4 * (p.G + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntn = (p.N + CG * BM - 1) / (CG * BM);
@@ -274,16 +312,16 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         // more rows than the buffer holds: no tile at all
         const bool over = re > p.a_rows;
         if (over) set_status(dev_status, MOE_ERR_CAPACITY);
-        goff[p.G] = over ? 0 : static_cast<int>(re);
-        tpre[p.G] = over ? 0 : te;
+        smem_store(goff + 4 * p.G, over ? 0 : static_cast<int>(re));
+        smem_store(tpre + 4 * p.G, over ? 0 : te);
       }
     }
     __syncthreads();
     int64_t r = s_r[tid];
     int tt = s_t[tid];
     for (int g = g0; g < g1; ++g) {
-      goff[g] = static_cast<int>(min(r, p.a_rows));
-      tpre[g] = tt;
+      smem_store(goff + 4 * g, static_cast<int>(min(r, p.a_rows)));
+      smem_store(tpre + 4 * g, tt);
       const int c = group_count(p, g, nullptr);
       r += c;
       tt += token_blocks(c, block) * ntn;
@@ -291,18 +329,18 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   }
   if (tid == 0) {
     for (int s = 0; s < nbyte; ++s) {
-      mbar_init(bfull + s, 1);
-      mbar_init(bempty + s, kConvWarps);
+      bar_init(bfull(s), 1);
+      bar_init(bempty(s), kHalves * kGroupWarps);
     }
     for (int s = 0; s < NF; ++s) {
-      mbar_init(ffull + s, CG * kConvWarps / kHalves);
-      mbar_init(fempty + s, 1);
+      bar_init(ffull(s), CG * kGroupWarps);
+      bar_init(fempty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull + b, 1);
-      mbar_init(tempty + b, CG * kEpiWarps);
+      bar_init(tfull(b), 1);
+      bar_init(tempty(b), CG * kEpiWarps);
     }
-    *abort_flag = 0;
+    smem_store(abort_flag, 0);
     fence_mbar_init();
     tensor_map_prefetch(&map_w);
     tensor_map_prefetch(&map_a);
@@ -316,8 +354,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   if constexpr (CG > 1) cluster_sync();      // the peer's barriers are ready too
   tc_fence_after();
 
-  const uint32_t tmem = *tmem_slot;
-  const int tiles = tpre[p.G];
+  const uint32_t tmem = smem_load(tmem_slot);
+  const int tiles = smem_load(tpre + 4 * p.G);
   const int nkb = (p.K + BKB - 1) / BKB;     // byte stages (zeros past K)
   const int kb0 = nkb * part / split, kb1 = nkb * (part + 1) / split;   // this CTA's
   const int nk = kb1 - kb0;
@@ -325,7 +363,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   const int first = blockIdx.x / (CG * split), step = gridDim.x / (CG * split);
 
   if (warp < 4) {
-    if constexpr (NT > 64) regs_fewer<kCtrlRegs>();
+    if constexpr (CG > 1) regs_fewer<kCtrlRegs>();
     if (warp == 0) {
       // ---- copies -------------------------------------------------------------------
       const bool issue = elect_one();
@@ -339,28 +377,28 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         const int wrow = tl.g * p.N + tl.n0 + rank * BM;
         const int arow = tl.row0 + rank * rows;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_bounded(bempty + s, phase ^ 1u, kSpin)) {
+          if (!bar_wait(bempty(s), phase ^ 1u)) {
             ok = false;
             break;
           }
           if (issue) {
             const uint32_t dst = sbase + St::kOffBytes + s * St::kByteBytes;
-            mbar_arrive_expect_tx(bfull + s, (BM + boxes * box_rows) * BKB);
-            tensor_load_2d(dst, &map_w, kb * BKB, wrow, bfull + s);
+            bar_expect(bfull(s), (BM + boxes * box_rows) * BKB);
+            tensor_load_2d(dst, &map_w, kb * BKB, wrow, bfull(s));
             for (int b = 0; b < boxes; ++b)
               tensor_load_2d(dst + (BM + b * box_rows) * BKB, &map_a, kb * BKB,
-                             arow + b * box_rows, bfull + s);
+                             arow + b * box_rows, bfull(s));
           }
           ++nload;
           if (++s == nbyte) { s = 0; phase ^= 1u; }
         }
-        ok = ok && !*abort_flag;
+        ok = ok && !smem_load(abort_flag);
       }
       if (!ok) {      // after a timeout, no copy may land once the CTA has gone
         if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
-        *abort_flag = 1;
+        smem_store(abort_flag, 1);
         for (uint32_t i = nload > uint32_t(nbyte) ? nload - nbyte : 0; i < nload; ++i)
-          mbar_wait_bounded(bfull + i % nbyte, (i / nbyte) & 1u, kSpin);
+          bar_wait(bfull(i % nbyte), (i / nbyte) & 1u);
       }
     } else if (warp == 1 && rank == 0) {
       // ---- products (of the pair, by its first CTA) -----------------------------------
@@ -373,7 +411,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         const uint32_t idesc = f16_mma_desc(CG * BM, tl.cols);
         for (int c = 0; ok && c < nchunks; ++c, ++chunk) {
           const uint32_t b = chunk & 1u, use = (chunk >> 1) & 1u;
-          if (!mbar_wait_bounded(tempty + b, use ^ 1u, kSpin) || *abort_flag) {
+          if (!bar_wait(tempty(b), use ^ 1u) || smem_load(abort_flag)) {
             ok = false;
             break;
           }
@@ -381,7 +419,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           const uint32_t d = tmem + b * kAccCols;
           const int n = min(kChunk, nk - c * kChunk) * kHalves;
           for (int kb = 0; kb < n; ++kb) {
-            if (!mbar_wait_bounded(ffull + f, phase, kSpin)) {
+            if (!bar_wait(ffull(f), phase)) {
               ok = false;
               break;
             }
@@ -392,34 +430,34 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk)     // + 32 bytes along K per step
                 mma_f16<CG>(d, da + 2 * kk, db + 2 * kk, idesc, kb != 0 || kk != 0);
-              mma_commit_to<CG>(fempty + f);
+              mma_commit_to<CG>(fempty(f));
             }
             ++ncommit;
             if (++f == NF) { f = 0; phase ^= 1u; }
           }
           if (!ok) break;
-          if (issue) mma_commit_to<CG>(tfull + b);
+          if (issue) mma_commit_to<CG>(tfull(b));
         }
       }
       if (!ok) {
         if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
-        *abort_flag = 1;
+        smem_store(abort_flag, 1);
       }
       // every commit has arrived (the last one of each barrier) before the CTA
       // may go, also after a timeout
       for (uint32_t i = ncommit > uint32_t(NF) ? ncommit - NF : 0; i < ncommit; ++i)
-        if (!mbar_wait_bounded(fempty + i % NF, (i / NF) & 1u, kSpin))
+        if (!bar_wait(fempty(i % NF), (i / NF) & 1u))
           set_status(dev_status, MOE_ERR_TIMEOUT);
       for (uint32_t i = chunk > 2 ? chunk - 2 : 0; i < chunk; ++i)
-        if (!mbar_wait_bounded(tfull + (i & 1u), (i >> 1) & 1u, kSpin))
+        if (!bar_wait(tfull(i & 1u), (i >> 1) & 1u))
           set_status(dev_status, MOE_ERR_TIMEOUT);
     } else if (CG > 1 && warp == 1) {
       // the leader's last commits reach this CTA's barriers before it may go
       const uint32_t ntile = first < tiles ? (tiles - first + step - 1) / step : 0;
       const uint32_t ncommit = ntile * nk * kHalves;
       for (uint32_t i = ncommit > uint32_t(NF) ? ncommit - NF : 0; i < ncommit; ++i)
-        for (uint32_t k = 0; k < kSpin && !*abort_flag; ++k)
-          if (mbar_try_wait(fempty + i % NF, (i / NF) & 1u)) break;
+        for (uint32_t k = 0; k < kGemmSpin && !smem_load(abort_flag); ++k)
+          if (bar_poll(fempty(i % NF), (i / NF) & 1u)) break;
     }
     __syncwarp();
     if (split > 1) {
@@ -428,74 +466,85 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     }
   } else if (warp < 4 + kConvWarps) {
     // ---- bytes -> fp16 ------------------------------------------------------------------
-    if constexpr (NT > 64) regs_fewer<kConvRegs>();
-    // two groups of four warps, one for each 64-code half of a byte stage: one
-    // group's waits and fences overlap the other's widening.  A thread takes 16
-    // codes (quarter uc of the half) of one row in 32.  Eight neighbouring
-    // threads read rows r and r + 4, whose swizzled quarters lie in different
-    // halves of the banks; their two 16-byte fp16 pieces are stored in
-    // opposite order, so that the eight stores, too, use all banks once.
-    constexpr int kGroupThreads = 32 * kConvWarps / kHalves;
+    if constexpr (CG > 1) regs_fewer<kConvRegs>();
+    // groups of four warps, each on one 64-code half of every other byte stage:
+    // one group's waits and fences overlap the others' widening.  A thread takes
+    // 16 codes (quarter uc of the half) of one row in kRows.  Eight neighbouring
+    // threads share rows r and r ^ 5: their swizzled byte quarters lie in
+    // different halves of the banks (bit 2 of the row differs), and so do their
+    // fp16 pieces (even and odd ones: bit 0 differs), so loads and stores are
+    // free of bank conflicts.
+    constexpr int kGroupThreads = 32 * kGroupWarps;
     constexpr int kRows = kGroupThreads / 4;            // rows per pass: a multiple of 8, so
     constexpr int kPasses = (BM + LT) / kRows;          // every pass has one swizzle key
-    constexpr int kBatch = kPasses % 4 == 0 ? 4 : 3;    // passes loaded before widening
-    const int half = (tid - 128) / kGroupThreads, u = (tid - 128) % kGroupThreads;
+    constexpr int kBatch = kPasses % 3 == 0 ? 3 : 2;    // passes loaded before widening
+    const int grp = (tid - 128) / kGroupThreads, u = (tid - 128) % kGroupThreads;
+    const int half = grp % kHalves, turn = grp / kHalves;
+    constexpr int kTurns = kConvGroups / kHalves;
     const int uq = u >> 2, uc = u & 3;
-    const int ur = (uq >> 3) * 8 + ((uq >> 1) & 3) + (uq & 1) * 4;
+    const int ur = (uq & ~7) + (((uq >> 1) & 3) ^ ((uq & 1) * 5));
     const uint32_t in = ur * BKB + (((half * 4 + uc) ^ (ur & 7)) << 4);
-    const uint32_t second = uq & 1;                     // which piece goes first
-    const uint32_t out0 = ur * (BK * 2) + (((2 * uc + second) ^ (ur & 7)) << 4);
-    const uint32_t out1 = ur * (BK * 2) + (((2 * uc + 1 - second) ^ (ur & 7)) << 4);
-    int s = 0, f = half;
+    const uint32_t out0 = ur * (BK * 2) + (((2 * uc) ^ (ur & 7)) << 4);
+    const uint32_t out1 = ur * (BK * 2) + (((2 * uc + 1) ^ (ur & 7)) << 4);
+    int s = turn, f = grp;
     uint32_t bphase = 0, fphase = 0;
+    int skip = turn;                      // byte stages until this group's next one
     bool ok = true;
     for (int t = first; ok && t < tiles; t += step) {
       const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
       const int rows = BM + tl.cols / CG;               // weight rows, then token rows
-      for (int kb = 0; kb < nk; ++kb) {
-        const bool got = mbar_wait_bounded(bfull + s, bphase, kSpin) &&
-                         mbar_wait_bounded(fempty + f, fphase ^ 1u, kSpin);
+      int kb = skip;
+      for (; kb < nk; kb += kTurns) {
+        const bool got = bar_wait(bfull(s), bphase) &&
+                         bar_wait(fempty(f), fphase ^ 1u);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         const uint32_t src = sbase + St::kOffBytes + s * St::kByteBytes + in;
         const uint32_t dst = sbase + f * St::kF16Bytes;
+        auto widen = [&](auto full) {       // full: every token row of the tile is there
+          auto has = [&](int i) {
+            return decltype(full)::value || (i + 1) * kRows <= BM || i * kRows + ur < rows;
+          };
 #pragma unroll
-        for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
-          uint4 v[kBatch];
+          for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+            uint4 v[kBatch];
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if ((i0 + i) * kRows + ur < rows) v[i] = lds128(src + (i0 + i) * kRows * BKB);
-          if (i0 + kBatch >= kPasses) {                 // this half of the stage is read
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bempty + s);
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if ((i0 + i) * kRows + ur < rows) {
-              uint4 o[2];
-              widen16(second ? make_uint4(v[i].z, v[i].w, v[i].x, v[i].y) : v[i], o);
-              sts128(dst + (i0 + i) * kRows * BK * 2 + out0, o[0]);
-              sts128(dst + (i0 + i) * kRows * BK * 2 + out1, o[1]);
+            for (int i = 0; i < kBatch; ++i)
+              if (has(i0 + i)) v[i] = lds128(src + (i0 + i) * kRows * BKB);
+            if (i0 + kBatch >= kPasses) {               // this half of the stage is read
+              __syncwarp();
+              if (lane == 0) bar_arrive(bempty(s));
             }
-        }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              if (has(i0 + i)) {
+                uint4 o[2];
+                widen16(v[i], o);
+                sts128(dst + (i0 + i) * kRows * BK * 2 + out0, o[0]);
+                sts128(dst + (i0 + i) * kRows * BK * 2 + out1, o[1]);
+              }
+          }
+        };
+        if (rows == BM + LT) widen(std::true_type());
+        else widen(std::false_type());
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (CG > 1) cluster_arrive(cluster_addr(smem_addr(ffull + f), 0));
-          else mbar_arrive(ffull + f);
+          if constexpr (CG > 1) cluster_arrive(cluster_addr(ffull(f), 0));
+          else bar_arrive(ffull(f));
         }
-        if (++s == nbyte) { s = 0; bphase ^= 1u; }
-        f += kHalves;
-        if (f >= NF) { f -= NF; fphase ^= 1u; }
+        for (s += kTurns; s >= nbyte; s -= nbyte) bphase ^= 1u;
+        for (f += kConvGroups; f >= NF; f -= NF) fphase ^= 1u;
       }
-      ok = ok && !*abort_flag;
+      skip = kb - nk;
+      ok = ok && !smem_load(abort_flag);
       ok = __all_sync(0xffffffffu, ok);
     }
     if (!ok) {
       if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
-      *abort_flag = 1;
+      smem_store(abort_flag, 1);
     }
     if (split > 1) {
       cluster_sync();
@@ -503,92 +552,143 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     }
   } else {
     // ---- chunk sums -> int32, scales, stores ----------------------------------------------
-    if constexpr (NT > 64) regs_more<kEpiRegs>();
-    constexpr int kCols = NT / 2;            // accumulator columns per thread
+    if constexpr (CG > 1) regs_more<kEpiRegs>();
+    constexpr int kParts = kEpiWarps / 4, kCols = NT / kParts;   // columns per thread
     const int q = warp & 3;                  // TMEM lanes 32 q ..
-    const int half = (warp - 4 - kConvWarps) >> 2;
-    const int eth = tid - 128 - 32 * kConvWarps;   // epilogue thread
+    const int col0 = ((warp - 4 - kConvWarps) >> 2) * kCols;
+    const uint32_t base = tmem + (uint32_t(q * 32) << 16) + col0;
     uint32_t chunk = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += step) {
       const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
-      const int n = tl.n0 + rank * BM + q * 32 + lane;
-      int32_t acc[kCols];
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) acc[j] = 0;
-      for (int c = 0; c < nchunks; ++c, ++chunk) {
-        const uint32_t b = chunk & 1u, use = (chunk >> 1) & 1u;
-        const bool got = mbar_wait_bounded(tfull + b, use, kSpin) && !*abort_flag;
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
+      const int live = tl.cols - col0;       // columns of this thread that are computed
+      auto wait = [&]() {                    // for the next chunk
+        const bool got = bar_wait(tfull(chunk & 1u), (chunk >> 1) & 1u) &&
+                         !smem_load(abort_flag);
+        ok = __all_sync(0xffffffffu, got);
         tc_fence_after();
-        const uint32_t base = tmem + (uint32_t(q * 32) << 16) + b * kAccCols + half * kCols;
-#pragma unroll
-        for (int cb = 0; cb < kCols / 16; ++cb)
-          if (half * kCols + cb * 16 < tl.cols) {
-            uint32_t v[16];
-            tmem_load16(base + cb * 16, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[cb * 16 + j] += __float2int_rn(__uint_as_float(v[j]));
-          }
+        return ok;
+      };
+      auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (CG > 1) cluster_arrive(cluster_addr(smem_addr(tempty + b), 0));
-          else mbar_arrive(tempty + b);
+          if constexpr (CG > 1) cluster_arrive(cluster_addr(tempty(chunk & 1u), 0));
+          else bar_arrive(tempty(chunk & 1u));
         }
+        ++chunk;
+      };
+      // scales: into L1 now, into registers after the sums
+      if (OUT != MOE_INT32) {
+#pragma unroll
+        for (int i = 0; i < kCols; i += 32)
+          if (col0 + i + lane < tl.rows)
+            prefetch_l1(p.row_scale + int64_t(tl.row0 + col0 + i + lane) * p.row_scale_stride);
+        const int n = tl.n0 + rank * BM + q * 32 + lane;
+        if (n < p.N) prefetch_l1(p.col_scale + int64_t(tl.g) * p.N + n);
       }
-      if (!ok) {
-        if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
-        *abort_flag = 1;
-        break;
+      int32_t acc[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) acc[j] = 0;
+      // every chunk but the last: into the sums
+      for (int c = 1; c < nchunks; ++c) {
+        if (!wait()) break;
+#pragma unroll
+        for (int cb = 0; cb < kCols / 8; ++cb)
+          if (cb * 8 < live) {
+            uint32_t v[8];
+            tmem_load8(base + (chunk & 1u) * kAccCols + cb * 8, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[cb * 8 + j] += __float2int_rn(__uint_as_float(v[j]));
+          }
+        release();
       }
-      const bool chan = n < p.N;
+      // the last one: eight columns at a time through the scales to memory
+      const int n = tl.n0 + rank * BM + q * 32 + lane;
+      const int lim = n < p.N ? tl.rows - col0 : 0;    // tokens of this thread to store
       const int64_t gn = int64_t(tl.g) * p.N + n;
-      const float col = OUT != MOE_INT32 && chan ? __ldg(p.col_scale + gn) : 0.0f;
-      const float bias = OUT != MOE_INT32 && p.bias && chan ? __ldg(p.bias + gn) : 0.0f;
+      const float col = OUT != MOE_INT32 && n < p.N ? __ldg(p.col_scale + gn) : 0.0f;
+      const float bias = OUT != MOE_INT32 && p.bias && n < p.N ? __ldg(p.bias + gn) : 0.0f;
       auto row_scale = [&](int j) {         // of the tile's token j (0 past the tile)
         return OUT != MOE_INT32 && j < tl.rows
                    ? __ldg(reinterpret_cast<const float*>(
                          p.row_scale + int64_t(tl.row0 + j) * p.row_scale_stride))
                    : 0.0f;
       };
-      if (split == 1) {
+      if (!ok || !wait()) {
+        if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
+        smem_store(abort_flag, 1);
+        break;
+      }
+      auto drain = [&](auto&& emit) {
 #pragma unroll
-        for (int jb = 0; jb < kCols; jb += 32) {
-          const int j0 = half * kCols + jb;
-          if (j0 >= tl.rows) break;
-          const float rs = row_scale(j0 + lane);
+        for (int cb = 0; cb < kCols / 8; ++cb)
+          if (cb * 8 < live) {
+            uint32_t v[8];
+            int32_t sum[8];
+            tmem_load8(base + (chunk & 1u) * kAccCols + cb * 8, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float row = __shfl_sync(0xffffffffu, rs, j);
-            if (j0 + j < tl.rows && chan)
-              store_out<OUT>(p.c, int64_t(tl.row0 + j0 + j) * p.N + n, acc[jb + j], col, row,
-                             bias, p.bias != nullptr);
+            for (int j = 0; j < 8; ++j)
+              sum[j] = acc[cb * 8 + j] + __float2int_rn(__uint_as_float(v[j]));
+            emit(cb * 8, sum);
           }
-        }
-      } else {
-        // rank d finishes columns [d, d+1) * kCols / split of each half
-        cluster_sync();                     // every CTA is done with its stages
-        const int share = kCols / split;
-        const uint32_t mine = sbase + ((part * share) * 256 + eth) * 4;
+        release();
+      };
+      if (CG > 1 || split == 1) {
+        constexpr int kItem = OUT == MOE_BF16 || OUT == MOE_FP16 ? 2 : 4;
+        const uint32_t pitch = p.N * kItem;
+        uint8_t* at = static_cast<uint8_t*>(p.c) +
+                      (int64_t(tl.row0 + col0) * p.N + n) * kItem;
+        if (tl.rows == NT && tl.n0 + rank * BM + BM <= p.N) {
+          auto full = [&](auto has_bias) {
+            float rs = 0.0f;                // lane l: the scale of token l of 32
+            drain([&](int j0, const int32_t (&sum)[8]) {
+              if (j0 % 32 == 0) rs = row_scale(col0 + j0 + lane);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          const int d = j / share, jj = j - d * share;
-          cluster_store(cluster_addr(mine + jj * 1024, d), static_cast<uint32_t>(acc[j]));
+              for (int j = 0; j < 8; j += 2, at += 2 * pitch)
+                store_pair<OUT, decltype(has_bias)::value>(
+                    at, pitch, sum[j], sum[j + 1], col,
+                    __shfl_sync(0xffffffffu, rs, (j0 + j) % 32),
+                    __shfl_sync(0xffffffffu, rs, (j0 + j + 1) % 32), bias, nz);
+            });
+          };
+          if (p.bias) full(std::true_type());
+          else full(std::false_type());
+        } else {
+          float rs = 0.0f;
+          drain([&](int j0, const int32_t (&sum)[8]) {
+            if (j0 % 32 == 0) rs = row_scale(col0 + j0 + lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j, at += pitch) {
+              const float row = __shfl_sync(0xffffffffu, rs, (j0 + j) % 32);
+              if (j0 + j < lim)
+                store_out<OUT>(at, 0, sum[j], col, row, bias, p.bias != nullptr);
+            }
+          });
         }
+      } else if constexpr (CG == 1) {
+        // rank d finishes columns [d, d+1) * kCols / split of each thread
+        cluster_sync();                     // every CTA is done with its stages
+        const int eth = tid - 128 - 32 * kConvWarps;   // epilogue thread
+        const int share = kCols / split, shift = 31 - __clz(share);    // powers of two
+        const uint32_t mine = sbase + ((part * share) * 256 + eth) * 4;
+        drain([&](int j0, const int32_t (&sum)[8]) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int d = (j0 + j) >> shift, jj = (j0 + j) & (share - 1);
+            cluster_store(cluster_addr(mine + jj * 1024, d), static_cast<uint32_t>(sum[j]));
+          }
+        });
         cluster_sync();
         for (int jj = 0; jj < share; ++jj) {
+          const int j = col0 + part * share + jj;
+          if (j - col0 >= lim) continue;
           int32_t sum = 0;
           for (int r = 0; r < split; ++r)
             sum += *reinterpret_cast<volatile int32_t*>(smem + ((r * share + jj) * 256 + eth) * 4);
-          const int j = half * kCols + part * share + jj;
-          if (j < tl.rows && chan)
-            store_out<OUT>(p.c, int64_t(tl.row0 + j) * p.N + n, sum, col, row_scale(j), bias,
-                           p.bias != nullptr);
+          store_out<OUT>(p.c, int64_t(tl.row0 + j) * p.N + n, sum, col, row_scale(j), bias,
+                         p.bias != nullptr);
         }
       }
     }
@@ -614,7 +714,7 @@ cudaError_t launch_out(const CUtensorMap& mw, const CUtensorMap& ma, const Linea
                        int block, int box_rows, int clusters, int split, int32_t* dev_status,
                        int optin, cudaStream_t st) {
   using S = Stages<NT / CG>;
-  int nbyte = kMaxByteStages;
+  int nbyte = kMaxByteStages;    // at least kConvGroups / kHalves = 2
   while (nbyte > 2 && S::bytes(nbyte, p.G) > size_t(optin)) --nbyte;
   const size_t smem = S::bytes(nbyte, p.G);
   auto kernel = linear_i8_tile_kernel<NT, CG, OUT>;
@@ -631,7 +731,7 @@ cudaError_t launch_out(const CUtensorMap& mw, const CUtensorMap& ma, const Linea
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, block, box_rows, nbyte, dev_status);
+  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, block, box_rows, nbyte, -0.0f, dev_status);
 }
 
 template <int NT, int CG>
