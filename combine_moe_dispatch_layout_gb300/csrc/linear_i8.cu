@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "group_tiles.cuh"
 #include "moe_ep_internal.cuh"
 #include "tcgen05.cuh"
 
@@ -112,31 +113,15 @@ struct Tile {
   int cols;        // tokens computed: rows rounded up to the MMA's step
 };
 
-__device__ __forceinline__ int group_count(const LinearArgs& p, int g, int32_t* dev_status) {
-  if (!p.group_rows) return static_cast<int>(p.a_rows);
-  const int c = __ldg(p.group_rows + g);
-  if (c < 0 && dev_status) set_status(dev_status, MOE_ERR_INVALID_ARG);
-  return c < 0 ? 0 : c;
-}
-
-// A group of cnt tokens is cut into equal blocks of at most `block` tokens.
-__device__ __forceinline__ int token_blocks(int cnt, int block) {
-  return static_cast<int>((int64_t(cnt) + block - 1) / block);
-}
-
 // CG CTAs share a tile of CG * BM channels; token counts are multiples of
 // 16 * CG (the MMA's step).
 template <int CG>
 __device__ __forceinline__ Tile decode_tile(int t, uint32_t goff, uint32_t tpre, int G,
                                             int ntn, int block) {
-  int lo = 0, hi = G;                 // largest g with tpre[g] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (smem_load(tpre + 4 * mid) <= t) lo = mid; else hi = mid;
-  }
+  const int lo = group_of_tile(t, tpre, G);
   const int off = smem_load(goff + 4 * lo);
   const int cnt = smem_load(goff + 4 * lo + 4) - off;
-  const int blocks = token_blocks(cnt, block);
+  const int blocks = row_blocks(cnt, block);    // equal ones, of at most `block` tokens
   constexpr int kStep = 16 * CG;
   const int per = ((cnt + blocks - 1) / blocks + kStep - 1) / kStep * kStep;
   // bands of kRasterTokens token blocks (the last band takes the remainder);
@@ -263,70 +248,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   const int split = CG > 1 ? 1 : static_cast<int>(cluster_size());
   const int part = CG > 1 ? 0 : static_cast<int>(cluster_rank());
 
-  // ---- group tables: row offsets and tile prefix -----------------------------------
-  {
-    const int per = (p.G + kThreads - 1) / kThreads;
-    const int g0 = min(tid * per, p.G), g1 = min(g0 + per, p.G);
-    int64_t rsum = 0;
-    int tsum = 0;
-    for (int g = g0; g < g1; ++g) {
-      const int c = group_count(p, g, dev_status);
-      rsum += c;
-      tsum += token_blocks(c, block) * ntn;
-    }
-    int64_t* s_r = reinterpret_cast<int64_t*>(smem);              // [kThreads] (stages: unused yet)
-    int* s_t = reinterpret_cast<int*>(s_r + kThreads);
-    s_r[tid] = rsum;
-    s_t[tid] = tsum;
-    __syncthreads();
-    if (warp == 0) {          // exclusive scan of the threads' sums
-      constexpr int kPer = kThreads / 32;
-      int64_t r = 0;
-      int tt = 0;
-      for (int i = 0; i < kPer; ++i) {
-        r += s_r[lane * kPer + i];
-        tt += s_t[lane * kPer + i];
-      }
-      int64_t ri = r;
-      int ti = tt;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t a = __shfl_up_sync(0xffffffffu, ri, d);
-        const int b = __shfl_up_sync(0xffffffffu, ti, d);
-        if (lane >= d) {
-          ri += a;
-          ti += b;
-        }
-      }
-      int64_t re = ri - r;
-      int te = ti - tt;
-      for (int i = 0; i < kPer; ++i) {
-        const int64_t a = s_r[lane * kPer + i];
-        const int b = s_t[lane * kPer + i];
-        s_r[lane * kPer + i] = re;
-        s_t[lane * kPer + i] = te;
-        re += a;
-        te += b;
-      }
-      if (lane == 31) {
-        // more rows than the buffer holds: no tile at all
-        const bool over = re > p.a_rows;
-        if (over) set_status(dev_status, MOE_ERR_CAPACITY);
-        smem_store(goff + 4 * p.G, over ? 0 : static_cast<int>(re));
-        smem_store(tpre + 4 * p.G, over ? 0 : te);
-      }
-    }
-    __syncthreads();
-    int64_t r = s_r[tid];
-    int tt = s_t[tid];
-    for (int g = g0; g < g1; ++g) {
-      smem_store(goff + 4 * g, static_cast<int>(min(r, p.a_rows)));
-      smem_store(tpre + 4 * g, tt);
-      const int c = group_count(p, g, nullptr);
-      r += c;
-      tt += token_blocks(c, block) * ntn;
-    }
-  }
+  // (the scan borrows the stages, which are not in use yet)
+  build_group_tables<kThreads>(p, block, ntn, smem, goff, tpre, dev_status);
   if (tid == 0) {
     for (int s = 0; s < nbyte; ++s) {
       bar_init(bfull(s), 1);
@@ -750,9 +673,18 @@ cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const Linear
   }
 }
 
+// Up to this many rows, the kernel that streams weights through integer dot
+// products is the faster one: of a plain product (4 rows of 2048 -> 7168: 8.0
+// against 13.4 us; 8 rows of 7168 -> 4096: 17.3 against 17.6), and per group on
+// average (256 groups of 7168 -> 4096: mean 2 rows 1.09 against 1.30 ms, mean 3
+// level, mean 4 1.55 against 1.39).
+constexpr int64_t kFewPlain = 4, kFewGrouped = 3;
+
 }  // namespace
 
 cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
+  if (p.a_rows <= (p.G == 1 ? kFewPlain : kFewGrouped * p.G))
+    return launch_linear_i8_few(p, dev_status, st);
   int dev = 0, sms = 0, optin = 0;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e == cudaSuccess)

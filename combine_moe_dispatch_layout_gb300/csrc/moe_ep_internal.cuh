@@ -496,6 +496,9 @@ struct LinearArgs {
   int c_dtype;                      // moe_dtype
 };
 
+// moe_linear_i8 for groups of a few rows (linear_i8_few.cu), which
+// launch_linear_i8 chooses by the mean rows per group.
+cudaError_t launch_linear_i8_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st);
 cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st);
 
 }  // namespace moe_ep

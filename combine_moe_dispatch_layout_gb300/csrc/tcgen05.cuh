@@ -23,8 +23,8 @@ __device__ __forceinline__ void prefetch_l1(const void* p) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
 
-// ---- mbarriers and words of shared memory by 32-bit address (half the
-// registers of generic pointers) -------------------------------------------------
+// ---- mbarriers by 32-bit shared-memory address (half the registers of
+// generic pointers) -------------------------------------------------
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -52,15 +52,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     if (bar_poll(bar, parity)) return true;
   return false;
 }
-__device__ __forceinline__ int smem_load(uint32_t a) {
-  int v;
-  asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void smem_store(uint32_t a, int v) {
-  asm volatile("st.shared.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-
 // 2-D tensor copy global -> shared, completion counted on `bar`.
 __device__ __forceinline__ void tensor_load_2d(uint32_t sdst, const CUtensorMap* map, int x,
                                                int y, uint32_t bar) {
