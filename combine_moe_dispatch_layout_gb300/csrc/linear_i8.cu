@@ -400,7 +400,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     constexpr int kGroupThreads = 32 * kGroupWarps;
     constexpr int kRows = kGroupThreads / 4;            // rows per pass: a multiple of 8, so
     constexpr int kPasses = (BM + LT) / kRows;          // every pass has one swizzle key
-    constexpr int kBatch = kPasses % 3 == 0 ? 3 : 2;    // passes loaded before widening
+    // passes loaded before widening: as many as the registers hold
+    constexpr int kBatch = CG > 1 ? 2 : kPasses;
     const int grp = (tid - 128) / kGroupThreads, u = (tid - 128) % kGroupThreads;
     const int half = grp % kHalves, turn = grp / kHalves;
     constexpr int kTurns = kConvGroups / kHalves;
@@ -409,6 +410,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     const uint32_t in = ur * BKB + (((half * 4 + uc) ^ (ur & 7)) << 4);
     const uint32_t out0 = ur * (BK * 2) + (((2 * uc) ^ (ur & 7)) << 4);
     const uint32_t out1 = ur * (BK * 2) + (((2 * uc + 1) ^ (ur & 7)) << 4);
+    const uint32_t zero = __float_as_uint(nz) << 1;     // nz is -0
     int s = turn, f = grp;
     uint32_t bphase = 0, fphase = 0;
     int skip = turn;                      // byte stages until this group's next one
@@ -418,12 +420,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       const int rows = BM + tl.cols / CG;               // weight rows, then token rows
       int kb = skip;
       for (; kb < nk; kb += kTurns) {
-        const bool got = bar_wait(bfull(s), bphase) &&
-                         bar_wait(fempty(f), fphase ^ 1u);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, bar_wait(bfull(s), bphase));
+        if (!ok) break;
         const uint32_t src = sbase + St::kOffBytes + s * St::kByteBytes + in;
         const uint32_t dst = sbase + f * St::kF16Bytes;
         auto widen = [&](auto full) {       // full: every token row of the tile is there
@@ -435,10 +433,22 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
             uint4 v[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
-              if (has(i0 + i)) v[i] = lds128(src + (i0 + i) * kRows * BKB);
-            if (i0 + kBatch >= kPasses) {               // this half of the stage is read
+              v[i] = has(i0 + i) ? lds128(src + (i0 + i) * kRows * BKB) : make_uint4(0u, 0u, 0u, 0u);
+            if (i0 + kBatch >= kPasses) {
+              // This half of the stage is read: hand it back to the copies.  The
+              // arrival's address depends on the loaded words (zero is 0, which the
+              // compiler cannot know), so no load can still be pending, or be moved
+              // by the compiler to a point after it, when the copies overwrite them
+              // (seen: wrong products once the next wait stood between).
+              uint32_t words = 0;
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) words |= v[i].x;
               __syncwarp();
-              if (lane == 0) bar_arrive(bempty(s));
+              if (lane == 0) bar_arrive(bempty(s) + (words & zero));
+            }
+            if (i0 == 0) {                              // the fp16 stage is free
+              ok = __all_sync(0xffffffffu, bar_wait(fempty(f), fphase ^ 1u));
+              if (!ok) return;
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
@@ -452,6 +462,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         };
         if (rows == BM + LT) widen(std::true_type());
         else widen(std::false_type());
+        if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -678,7 +689,7 @@ cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const Linear
 // against 13.4 us; 8 rows of 7168 -> 4096: 17.3 against 17.6), and per group on
 // average (256 groups of 7168 -> 4096: mean 2 rows 1.09 against 1.30 ms, mean 3
 // level, mean 4 1.55 against 1.39).
-constexpr int64_t kFewPlain = 4, kFewGrouped = 3;
+constexpr int64_t kFewPlain = 8, kFewGrouped = 3;
 
 }  // namespace
 
