@@ -21,8 +21,8 @@
 //                 each, into a ring of byte stages (tensor copies, 128-byte swizzle)
 //   warp 1        issues tcgen05.mma (K = 16) from fp16 stages into one of two
 //                 TMEM accumulators, alternating per chunk
-//   8 or 16 warps widen byte stages into fp16 stages (64 codes, 128-byte swizzle)
-//   16 or 8 warps drain finished chunks into int32 registers (one channel per
+//   16 warps     widen byte stages into fp16 stages (64 codes, 128-byte swizzle)
+//   8 warps      drain finished chunks into int32 registers (one channel per
 //                 thread), then scale and store: a warp's stores for one token
 //                 are 32 neighbouring channels
 // When a plain product has fewer tiles than the GPU has SMs, a cluster of up to
@@ -73,20 +73,18 @@ constexpr int kHalves = 2;           // fp16 stages per byte stage (128-byte row
 constexpr int BKB = kHalves * BK;
 constexpr int kChunk = 1024 / BKB;   // byte stages per chunk: 1024 products, exact in fp32
 constexpr int kRasterTokens = 8;     // token blocks per raster band (weights reused from L2)
-// Warps that widen (in groups of four on different stages) and warps that drain
-// and store.  A pair's 256-token tiles have long MMAs and 256 accumulator
-// columns per lane: two groups keep up, and 16 warps hold 64 sums per thread.
-// Narrow tiles stream weights: four groups, 8 warps with 32 sums per thread.
-constexpr int kGroupWarps = 4;
-template <int CG>
-struct Roles {
-  static constexpr int kConvWarps = CG > 1 ? 8 : 16;
-  static constexpr int kEpiWarps = 24 - kConvWarps;
-};
-constexpr int kThreads = 128 + 32 * 24;
-// Registers per thread: 72 at launch (896 threads).  With pairs they are handed
-// out again by role: 512 x 96 + 256 x 40 + 128 x 40 = 64512 = 896 x 72.
-constexpr int kEpiRegs = 96, kConvRegs = 40, kCtrlRegs = 40;
+// 28 warps: 4 that copy and multiply (two of them idle), 16 that widen, in groups
+// of four on different stages, and 8 that drain and store.  (With 8 widening and
+// 16 draining warps, 16384 x 7168 x 2048 took 317 us; this way 294.)
+constexpr int kGroupWarps = 4, kConvWarps = 16, kEpiWarps = 8;
+constexpr int kConvGroups = kConvWarps / kGroupWarps;
+constexpr int kThreads = 128 + 32 * (kConvWarps + kEpiWarps);
+// Registers per thread: 72 at launch.  With pairs, whose draining threads hold 128
+// sums, they are handed out again by role: 256 x 152 + 512 x 40 + 128 x 40 = 64512
+// = 896 x 72.
+constexpr int kEpiRegs = 152, kConvRegs = 40, kCtrlRegs = 40;
+static_assert(32 * (kEpiWarps * kEpiRegs + kConvWarps * kConvRegs + 4 * kCtrlRegs) <=
+                  kThreads * 72, "no more registers than the launch has");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAccCols = 256;   // column offset of the second accumulator
 constexpr int kMaxByteStages = 12, kMaxF16Stages = 6;
@@ -171,14 +169,14 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
 }
 
 // One output: its scales, its bias, its rounding.
-template <int OUT>
+template <int OUT, bool BIAS>
 __device__ __forceinline__ void store_out(void* c, int64_t at, int32_t acc, float col, float row,
-                                          float bias, bool has_bias) {
+                                          float bias) {
   if constexpr (OUT == MOE_INT32) {
     static_cast<int32_t*>(c)[at] = acc;
   } else {
     float v = __fmul_rn(__fmul_rn(__int2float_rn(acc), col), row);
-    if (has_bias) v = __fadd_rn(v, bias);
+    if constexpr (BIAS) v = __fadd_rn(v, bias);
     if constexpr (OUT == MOE_FP32) static_cast<float*>(c)[at] = v;
     else static_cast<uint16_t*>(c)[at] = static_cast<uint16_t>(narrow_rn<OUT>(v));
   }
@@ -221,8 +219,6 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
                       int box_rows, int nbyte, float nz, int32_t* dev_status) {
   constexpr int LT = NT / CG;
   using St = Stages<LT>;
-  constexpr int kConvWarps = Roles<CG>::kConvWarps, kEpiWarps = Roles<CG>::kEpiWarps;
-  constexpr int kConvGroups = kConvWarps / kGroupWarps;
   constexpr int NF = St::kF16;
   // every widening group starts on a stage of its own
   static_assert(NF >= kConvGroups && NF <= kMaxF16Stages && kConvGroups % kHalves == 0, "stages");
@@ -239,7 +235,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   auto tfull = [&](int b) { return bars + 8 * (kT0 + b); };                // accumulator final
   auto tempty = [&](int b) { return bars + 8 * (kT0 + 2 + b); };           // ... drained
   const uint32_t tmem_slot = bars + 8 * (kT0 + 4), abort_flag = tmem_slot + 4;
-  static_assert(8 * (kT0 + 5) <= St::kBarBytes, "barriers fit");
+  auto srows = [&](int s) { return abort_flag + 4 + 4 * s; };   // rows in byte stage s
+  static_assert(8 * (kT0 + 5) + 4 * kMaxByteStages <= St::kBarBytes, "barriers fit");
   const uint32_t goff = bars + St::kBarBytes, tpre = goff + 4 * (p.G + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -277,8 +274,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   if constexpr (CG > 1) cluster_sync();      // the peer's barriers are ready too
   tc_fence_after();
 
-  const uint32_t tmem = smem_load(tmem_slot);
-  const int tiles = smem_load(tpre + 4 * p.G);
+  // (each role reads what it needs: registers are short in some)
+  auto tile_count = [&]() { return smem_load(tpre + 4 * p.G); };
   const int nkb = (p.K + BKB - 1) / BKB;     // byte stages (zeros past K)
   const int kb0 = nkb * part / split, kb1 = nkb * (part + 1) / split;   // this CTA's
   const int nk = kb1 - kb0;
@@ -287,6 +284,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 
   if (warp < 4) {
     if constexpr (CG > 1) regs_fewer<kCtrlRegs>();
+    const int tiles = tile_count();
     if (warp == 0) {
       // ---- copies -------------------------------------------------------------------
       const bool issue = elect_one();
@@ -306,6 +304,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           }
           if (issue) {
             const uint32_t dst = sbase + St::kOffBytes + s * St::kByteBytes;
+            smem_store(srows(s), BM + rows);       // weight rows, then token rows
             bar_expect(bfull(s), (BM + boxes * box_rows) * BKB);
             tensor_load_2d(dst, &map_w, kb * BKB, wrow, bfull(s));
             for (int b = 0; b < boxes; ++b)
@@ -326,6 +325,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     } else if (warp == 1 && rank == 0) {
       // ---- products (of the pair, by its first CTA) -----------------------------------
       const bool issue = elect_one();
+      const uint32_t tmem = smem_load(tmem_slot);
       int f = 0;
       uint32_t phase = 0, chunk = 0, ncommit = 0;
       bool ok = true;
@@ -409,72 +409,64 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     const int ur = (uq & ~7) + (((uq >> 1) & 3) ^ ((uq & 1) * 5));
     const uint32_t in = ur * BKB + (((half * 4 + uc) ^ (ur & 7)) << 4);
     const uint32_t out0 = ur * (BK * 2) + (((2 * uc) ^ (ur & 7)) << 4);
-    const uint32_t out1 = ur * (BK * 2) + (((2 * uc + 1) ^ (ur & 7)) << 4);
-    const uint32_t zero = __float_as_uint(nz) << 1;     // nz is -0
     int s = turn, f = grp;
     uint32_t bphase = 0, fphase = 0;
-    int skip = turn;                      // byte stages until this group's next one
     bool ok = true;
-    for (int t = first; ok && t < tiles; t += step) {
-      const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
-      const int rows = BM + tl.cols / CG;               // weight rows, then token rows
-      int kb = skip;
-      for (; kb < nk; kb += kTurns) {
-        ok = __all_sync(0xffffffffu, bar_wait(bfull(s), bphase));
-        if (!ok) break;
-        const uint32_t src = sbase + St::kOffBytes + s * St::kByteBytes + in;
-        const uint32_t dst = sbase + f * St::kF16Bytes;
-        auto widen = [&](auto full) {       // full: every token row of the tile is there
-          auto has = [&](int i) {
-            return decltype(full)::value || (i + 1) * kRows <= BM || i * kRows + ur < rows;
-          };
-#pragma unroll
-          for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
-            uint4 v[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-              v[i] = has(i0 + i) ? lds128(src + (i0 + i) * kRows * BKB) : make_uint4(0u, 0u, 0u, 0u);
-            if (i0 + kBatch >= kPasses) {
-              // This half of the stage is read: hand it back to the copies.  The
-              // arrival's address depends on the loaded words (zero is 0, which the
-              // compiler cannot know), so no load can still be pending, or be moved
-              // by the compiler to a point after it, when the copies overwrite them
-              // (seen: wrong products once the next wait stood between).
-              uint32_t words = 0;
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i) words |= v[i].x;
-              __syncwarp();
-              if (lane == 0) bar_arrive(bempty(s) + (words & zero));
-            }
-            if (i0 == 0) {                              // the fp16 stage is free
-              ok = __all_sync(0xffffffffu, bar_wait(fempty(f), fphase ^ 1u));
-              if (!ok) return;
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-              if (has(i0 + i)) {
-                uint4 o[2];
-                widen16(v[i], o);
-                sts128(dst + (i0 + i) * kRows * BK * 2 + out0, o[0]);
-                sts128(dst + (i0 + i) * kRows * BK * 2 + out1, o[1]);
-              }
-          }
+    const int tiles = tile_count();
+    const int total = first < tiles ? ((tiles - first + step - 1) / step) * nk : 0;
+    for (int i = turn; i < total; i += kTurns) {
+      ok = __all_sync(0xffffffffu, bar_wait(bfull(s), bphase));
+      if (!ok) break;
+      const int rows = smem_load(srows(s));
+      const uint32_t src = sbase + St::kOffBytes + s * St::kByteBytes + in;
+      const uint32_t dst = sbase + f * St::kF16Bytes + out0;   // and dst ^ 16
+      auto widen = [&](auto full) {       // full: every token row of the tile is there
+        auto has = [&](int i) {
+          return decltype(full)::value || (i + 1) * kRows <= BM || i * kRows + ur < rows;
         };
-        if (rows == BM + LT) widen(std::true_type());
-        else widen(std::false_type());
-        if (!ok) break;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG > 1) cluster_arrive(cluster_addr(ffull(f), 0));
-          else bar_arrive(ffull(f));
+#pragma unroll
+        for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            v[i] = has(i0 + i) ? lds128(src + (i0 + i) * kRows * BKB) : make_uint4(0u, 0u, 0u, 0u);
+          if (i0 + kBatch >= kPasses) {
+            // This half of the stage is read: hand it back to the copies.  The
+            // arrival's address depends on the loaded words (meeting a 0 that the compiler
+            // cannot see: nz is -0), so no load can still be pending, or be moved
+            // by the compiler to a point after it, when the copies overwrite them
+            // (seen: wrong products once the next wait stood between).
+            uint32_t words = 0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) words |= v[i].x;
+            __syncwarp();
+            if (lane == 0) bar_arrive(bempty(s) + (words & (__float_as_uint(nz) << 1)));
+          }
+          if (i0 == 0) {                              // the fp16 stage is free
+            ok = __all_sync(0xffffffffu, bar_wait(fempty(f), fphase ^ 1u));
+            if (!ok) return;
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (has(i0 + i)) {
+              uint4 o[2];
+              widen16(v[i], o);
+              sts128(dst + (i0 + i) * kRows * BK * 2, o[0]);
+              sts128((dst ^ 16) + (i0 + i) * kRows * BK * 2, o[1]);
+            }
         }
-        for (s += kTurns; s >= nbyte; s -= nbyte) bphase ^= 1u;
-        for (f += kConvGroups; f >= NF; f -= NF) fphase ^= 1u;
+      };
+      if (rows == BM + LT) widen(std::true_type());
+      else widen(std::false_type());
+      if (!ok) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG > 1) cluster_arrive(cluster_addr(ffull(f), 0));
+        else bar_arrive(ffull(f));
       }
-      skip = kb - nk;
-      ok = ok && !smem_load(abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      for (s += kTurns; s >= nbyte; s -= nbyte) bphase ^= 1u;
+      for (f += kConvGroups; f >= NF; f -= NF) fphase ^= 1u;
     }
     if (!ok) {
       if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
@@ -490,11 +482,11 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     constexpr int kParts = kEpiWarps / 4, kCols = NT / kParts;   // columns per thread
     const int q = warp & 3;                  // TMEM lanes 32 q ..
     const int col0 = ((warp - 4 - kConvWarps) >> 2) * kCols;
-    const uint32_t base = tmem + (uint32_t(q * 32) << 16) + col0;
+    const uint32_t base = smem_load(tmem_slot) + (uint32_t(q * 32) << 16) + col0;
     uint32_t chunk = 0;
     bool ok = true;
-    for (int t = first; ok && t < tiles; t += step) {
-      const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
+    for (int t = first; ok && t < tile_count(); t += step) {
+      Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
       const int live = tl.cols - col0;       // columns of this thread that are computed
       auto wait = [&]() {                    // for the next chunk
         const bool got = bar_wait(tfull(chunk & 1u), (chunk >> 1) & 1u) &&
@@ -512,8 +504,9 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         }
         ++chunk;
       };
-      // scales: into L1 now, into registers after the sums
-      if (OUT != MOE_INT32) {
+      // scales: into L1 now, into registers after the sums (a pair's tiles are long
+      // enough to load them then)
+      if (CG == 1 && OUT != MOE_INT32) {
 #pragma unroll
         for (int i = 0; i < kCols; i += 32)
           if (col0 + i + lane < tl.rows)
@@ -528,22 +521,23 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       for (int c = 1; c < nchunks; ++c) {
         if (!wait()) break;
 #pragma unroll
-        for (int cb = 0; cb < kCols / 8; ++cb)
-          if (cb * 8 < live) {
-            uint32_t v[8];
-            tmem_load8(base + (chunk & 1u) * kAccCols + cb * 8, v);
+        for (int cb = 0; cb < kCols / 4; ++cb)
+          if (cb * 4 < live) {
+            uint32_t v[4];
+            tmem_load4(base + (chunk & 1u) * kAccCols + cb * 4, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              acc[cb * 8 + j] += __float2int_rn(__uint_as_float(v[j]));
+            for (int j = 0; j < 4; ++j)
+              acc[cb * 4 + j] += __float2int_rn(__uint_as_float(v[j]));
           }
         release();
       }
-      // the last one: eight columns at a time through the scales to memory
+      // the last one: four columns at a time through the scales to memory
+      // (the tile is decoded again: the sums leave no registers to hold it)
+      tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
       const int n = tl.n0 + rank * BM + q * 32 + lane;
       const int lim = n < p.N ? tl.rows - col0 : 0;    // tokens of this thread to store
       const int64_t gn = int64_t(tl.g) * p.N + n;
       const float col = OUT != MOE_INT32 && n < p.N ? __ldg(p.col_scale + gn) : 0.0f;
-      const float bias = OUT != MOE_INT32 && p.bias && n < p.N ? __ldg(p.bias + gn) : 0.0f;
       auto row_scale = [&](int j) {         // of the tile's token j (0 past the tile)
         return OUT != MOE_INT32 && j < tl.rows
                    ? __ldg(reinterpret_cast<const float*>(
@@ -557,15 +551,14 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       }
       auto drain = [&](auto&& emit) {
 #pragma unroll
-        for (int cb = 0; cb < kCols / 8; ++cb)
-          if (cb * 8 < live) {
-            uint32_t v[8];
-            int32_t sum[8];
-            tmem_load8(base + (chunk & 1u) * kAccCols + cb * 8, v);
+        for (int cb = 0; cb < kCols / 4; ++cb)
+          if (cb * 4 < live) {
+            uint32_t v[4];
+            tmem_load4(base + (chunk & 1u) * kAccCols + cb * 4, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              sum[j] = acc[cb * 8 + j] + __float2int_rn(__uint_as_float(v[j]));
-            emit(cb * 8, sum);
+            for (int j = 0; j < 4; ++j)
+              acc[cb * 4 + j] += __float2int_rn(__uint_as_float(v[j]));
+            emit(cb * 4, &acc[cb * 4]);
           }
         release();
       };
@@ -574,42 +567,40 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         const uint32_t pitch = p.N * kItem;
         uint8_t* at = static_cast<uint8_t*>(p.c) +
                       (int64_t(tl.row0 + col0) * p.N + n) * kItem;
-        if (tl.rows == NT && tl.n0 + rank * BM + BM <= p.N) {
-          auto full = [&](auto has_bias) {
-            float rs = 0.0f;                // lane l: the scale of token l of 32
-            drain([&](int j0, const int32_t (&sum)[8]) {
-              if (j0 % 32 == 0) rs = row_scale(col0 + j0 + lane);
-#pragma unroll
-              for (int j = 0; j < 8; j += 2, at += 2 * pitch)
-                store_pair<OUT, decltype(has_bias)::value>(
-                    at, pitch, sum[j], sum[j + 1], col,
-                    __shfl_sync(0xffffffffu, rs, (j0 + j) % 32),
-                    __shfl_sync(0xffffffffu, rs, (j0 + j + 1) % 32), bias, nz);
-            });
-          };
-          if (p.bias) full(std::true_type());
-          else full(std::false_type());
-        } else {
-          float rs = 0.0f;
-          drain([&](int j0, const int32_t (&sum)[8]) {
+        auto finish = [&](auto is_full, auto has_bias) {
+          constexpr bool kFull = decltype(is_full)::value, kBias = decltype(has_bias)::value;
+          const float bias = kBias && lim > 0 ? __ldg(p.bias + gn) : 0.0f;
+          float rs = 0.0f;                  // lane l: the scale of token l of 32
+          drain([&](int j0, const int32_t* sum) {
             if (j0 % 32 == 0) rs = row_scale(col0 + j0 + lane);
 #pragma unroll
-            for (int j = 0; j < 8; ++j, at += pitch) {
-              const float row = __shfl_sync(0xffffffffu, rs, (j0 + j) % 32);
-              if (j0 + j < lim)
-                store_out<OUT>(at, 0, sum[j], col, row, bias, p.bias != nullptr);
+            for (int j = 0; j < 4; j += 2, at += 2 * pitch) {
+              const float r0 = __shfl_sync(0xffffffffu, rs, (j0 + j) % 32);
+              const float r1 = __shfl_sync(0xffffffffu, rs, (j0 + j + 1) % 32);
+              if constexpr (kFull) {
+                store_pair<OUT, kBias>(at, pitch, sum[j], sum[j + 1], col, r0, r1, bias, nz);
+              } else {
+                if (j0 + j < lim) store_out<OUT, kBias>(at, 0, sum[j], col, r0, bias);
+                if (j0 + j + 1 < lim)
+                  store_out<OUT, kBias>(at + pitch, 0, sum[j + 1], col, r1, bias);
+              }
             }
           });
-        }
+        };
+        const std::true_type yes;
+        const std::false_type no;
+        const bool is_full = tl.rows == NT && tl.n0 + rank * BM + BM <= p.N;
+        if (p.bias) is_full ? finish(yes, yes) : finish(no, yes);
+        else is_full ? finish(yes, no) : finish(no, no);
       } else if constexpr (CG == 1) {
         // rank d finishes columns [d, d+1) * kCols / split of each thread
         cluster_sync();                     // every CTA is done with its stages
         const int eth = tid - 128 - 32 * kConvWarps;   // epilogue thread
         const int share = kCols / split, shift = 31 - __clz(share);    // powers of two
         const uint32_t mine = sbase + ((part * share) * 256 + eth) * 4;
-        drain([&](int j0, const int32_t (&sum)[8]) {
+        drain([&](int j0, const int32_t* sum) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             const int d = (j0 + j) >> shift, jj = (j0 + j) & (share - 1);
             cluster_store(cluster_addr(mine + jj * 1024, d), static_cast<uint32_t>(sum[j]));
           }
@@ -621,12 +612,13 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           int32_t sum = 0;
           for (int r = 0; r < split; ++r)
             sum += *reinterpret_cast<volatile int32_t*>(smem + ((r * share + jj) * 256 + eth) * 4);
-          store_out<OUT>(p.c, int64_t(tl.row0 + j) * p.N + n, sum, col, row_scale(j), bias,
-                         p.bias != nullptr);
+          const int64_t to = int64_t(tl.row0 + j) * p.N + n;
+          if (p.bias) store_out<OUT, true>(p.c, to, sum, col, row_scale(j), __ldg(p.bias + gn));
+          else store_out<OUT, false>(p.c, to, sum, col, row_scale(j), 0.0f);
         }
       }
     }
-    if (split > 1 && (first >= tiles || !ok)) {   // no tile, or a timeout: the peers still wait
+    if (split > 1 && (first >= tile_count() || !ok)) {   // no tile, or a timeout: the peers still wait
       cluster_sync();
       cluster_sync();
     }
@@ -639,7 +631,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_free<CG>(tmem, kTmemCols);
+    tmem_free<CG>(smem_load(tmem_slot), kTmemCols);
   }
 }
 
