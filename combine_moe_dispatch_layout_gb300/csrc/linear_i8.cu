@@ -67,7 +67,8 @@ cudaError_t encode_bytes_2d(CUtensorMap* map, const void* base, int64_t rows, in
 
 namespace {
 
-constexpr int BM = 128;              // output channels per tile
+constexpr int BM = 128;              // output channels per CTA
+constexpr int CG = 2;                // CTAs per tile (a pair)
 constexpr int BK = 64;               // codes per fp16 stage: one 128-byte row
 constexpr int kHalves = 2;           // fp16 stages per byte stage (128-byte rows both)
 constexpr int BKB = kHalves * BK;
@@ -111,9 +112,8 @@ struct Tile {
   int cols;        // tokens computed: rows rounded up to the MMA's step
 };
 
-// CG CTAs share a tile of CG * BM channels; token counts are multiples of
-// 16 * CG (the MMA's step).
-template <int CG>
+// A pair shares a tile of CG * BM channels; token counts are multiples of 32 (the
+// MMA's step).
 __device__ __forceinline__ Tile decode_tile(int t, uint32_t goff, uint32_t tpre, int G,
                                             int ntn, int block) {
   const int lo = group_of_tile(t, tpre, G);
@@ -168,6 +168,21 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
                "r"(v.w) : "memory");
 }
 
+// Scales and bias of channel n of group g, and of row m (int32 outputs take none).
+template <int OUT>
+__device__ __forceinline__ float col_scale(const LinearArgs& p, int g, int n) {
+  return OUT == MOE_INT32 ? 0.0f : __ldg(p.col_scale + int64_t(g) * p.N + n);
+}
+template <int OUT>
+__device__ __forceinline__ float row_scale(const LinearArgs& p, int64_t m) {
+  return OUT == MOE_INT32
+             ? 0.0f
+             : __ldg(reinterpret_cast<const float*>(p.row_scale + m * p.row_scale_stride));
+}
+__device__ __forceinline__ float bias_of(const LinearArgs& p, int g, int n) {
+  return __ldg(p.bias + int64_t(g) * p.N + n);
+}
+
 // One output: its scales, its bias, its rounding.
 template <int OUT, bool BIAS>
 __device__ __forceinline__ void store_out(void* c, int64_t at, int32_t acc, float col, float row,
@@ -209,10 +224,9 @@ __device__ __forceinline__ void store_pair(uint8_t* at, uint32_t pitch, int32_t 
   }
 }
 
-// NT: tokens per tile at most; CG: CTAs per tile (1, or a pair that shares its
-// operands and runs one MMA of 256 channels).  With CG = 1 a larger cluster
-// splits K.
-template <int NT, int CG, int OUT>
+// NT: tokens per tile at most.  SPLIT: the cluster's pairs split K (one tile per
+// cluster).
+template <int NT, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ CUtensorMap map_a, const LinearArgs p, int block,
@@ -241,12 +255,20 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntn = (p.N + CG * BM - 1) / (CG * BM);
-  const int rank = CG > 1 ? static_cast<int>(cluster_rank()) : 0;    // in the pair
-  const int split = CG > 1 ? 1 : static_cast<int>(cluster_size());
-  const int part = CG > 1 ? 0 : static_cast<int>(cluster_rank());
+  const int crank = static_cast<int>(cluster_rank());
+  const int rank = crank % CG, part = SPLIT ? crank / CG : 0;    // in the pair; of K
+  const int split = SPLIT ? static_cast<int>(cluster_size()) / CG : 1;      // a power of two
+  const int leader = crank - rank;             // the pair's first CTA, in the cluster
 
-  // (the scan borrows the stages, which are not in use yet)
-  build_group_tables<kThreads>(p, block, ntn, smem, goff, tpre, dev_status);
+  if (p.group_rows) {        // the scan borrows the stages, which are not in use yet
+    build_group_tables<kThreads>(p, block, ntn, smem, goff, tpre, dev_status);
+  } else if (tid == 0) {
+    const int rows = static_cast<int>(p.a_rows);
+    smem_store(goff, 0);
+    smem_store(goff + 4, rows);
+    smem_store(tpre, 0);
+    smem_store(tpre + 4, row_blocks(rows, block) * ntn);
+  }
   if (tid == 0) {
     for (int s = 0; s < nbyte; ++s) {
       bar_init(bfull(s), 1);
@@ -267,24 +289,28 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   }
   if (warp == 1) {
     __syncwarp();
-    tmem_alloc<CG>(tmem_slot, kTmemCols);
+    pair_tmem_alloc(tmem_slot, kTmemCols);
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG > 1) cluster_sync();      // the peer's barriers are ready too
+  // The copies start at once; a role waits for the rest of the cluster before it
+  // first reaches into another CTA (its barriers must have been set up).
+  cluster_arrive_all();
   tc_fence_after();
 
   // (each role reads what it needs: registers are short in some)
   auto tile_count = [&]() { return smem_load(tpre + 4 * p.G); };
-  const int nkb = (p.K + BKB - 1) / BKB;     // byte stages (zeros past K)
-  const int kb0 = nkb * part / split, kb1 = nkb * (part + 1) / split;   // this CTA's
-  const int nk = kb1 - kb0;
-  const int nchunks = (nk + kChunk - 1) / kChunk;
-  const int first = blockIdx.x / (CG * split), step = gridDim.x / (CG * split);
+  // byte stages of K (zeros past it) that this CTA's pair takes: [begin, begin + count)
+  auto stage_begin = [&](int i) { return (p.K + BKB - 1) / BKB * i / split; };
+  auto stage_count = [&]() { return stage_begin(part + 1) - stage_begin(part); };
+  auto chunk_count = [&](int nk) { return (nk + kChunk - 1) / kChunk; };
+  auto first_tile = [&]() { return static_cast<int>(blockIdx.x) / (CG * split); };
+  auto tile_step = [&]() { return static_cast<int>(gridDim.x) / (CG * split); };
 
   if (warp < 4) {
-    if constexpr (CG > 1) regs_fewer<kCtrlRegs>();
+    regs_fewer<kCtrlRegs>();
     const int tiles = tile_count();
+    const int nk = stage_count(), first = first_tile(), step = tile_step();
     if (warp == 0) {
       // ---- copies -------------------------------------------------------------------
       const bool issue = elect_one();
@@ -292,12 +318,13 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       uint32_t phase = 0, nload = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += step) {
-        const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
+        const Tile tl = decode_tile(t, goff, tpre, p.G, ntn, block);
         const int rows = tl.cols / CG;                   // this CTA's token rows
         const int boxes = (rows + box_rows - 1) / box_rows;
         const int wrow = tl.g * p.N + tl.n0 + rank * BM;
         const int arow = tl.row0 + rank * rows;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        const int kb0 = stage_begin(part);
+        for (int kb = kb0; kb < kb0 + nk; ++kb) {
           if (!bar_wait(bempty(s), phase ^ 1u)) {
             ok = false;
             break;
@@ -322,16 +349,19 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         for (uint32_t i = nload > uint32_t(nbyte) ? nload - nbyte : 0; i < nload; ++i)
           bar_wait(bfull(i % nbyte), (i / nbyte) & 1u);
       }
+      cluster_wait_all();
     } else if (warp == 1 && rank == 0) {
       // ---- products (of the pair, by its first CTA) -----------------------------------
+      cluster_wait_all();
       const bool issue = elect_one();
       const uint32_t tmem = smem_load(tmem_slot);
       int f = 0;
       uint32_t phase = 0, chunk = 0, ncommit = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += step) {
-        const Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
+        const Tile tl = decode_tile(t, goff, tpre, p.G, ntn, block);
         const uint32_t idesc = f16_mma_desc(CG * BM, tl.cols);
+        const int nchunks = chunk_count(nk);
         for (int c = 0; ok && c < nchunks; ++c, ++chunk) {
           const uint32_t b = chunk & 1u, use = (chunk >> 1) & 1u;
           if (!bar_wait(tempty(b), use ^ 1u) || smem_load(abort_flag)) {
@@ -352,14 +382,14 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
               const uint64_t da = operand_desc(st), db = operand_desc(st + BM * BK * 2);
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk)     // + 32 bytes along K per step
-                mma_f16<CG>(d, da + 2 * kk, db + 2 * kk, idesc, kb != 0 || kk != 0);
-              mma_commit_to<CG>(fempty(f));
+                pair_mma_f16(d, da + 2 * kk, db + 2 * kk, idesc, kb != 0 || kk != 0);
+              pair_commit(fempty(f), uint16_t(3 << leader));
             }
             ++ncommit;
             if (++f == NF) { f = 0; phase ^= 1u; }
           }
           if (!ok) break;
-          if (issue) mma_commit_to<CG>(tfull(b));
+          if (issue) pair_commit(tfull(b), uint16_t(3 << leader));
         }
       }
       if (!ok) {
@@ -374,7 +404,10 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       for (uint32_t i = chunk > 2 ? chunk - 2 : 0; i < chunk; ++i)
         if (!bar_wait(tfull(i & 1u), (i >> 1) & 1u))
           set_status(dev_status, MOE_ERR_TIMEOUT);
-    } else if (CG > 1 && warp == 1) {
+    } else {
+      cluster_wait_all();
+    }
+    if (warp == 1 && rank != 0) {
       // the leader's last commits reach this CTA's barriers before it may go
       const uint32_t ntile = first < tiles ? (tiles - first + step - 1) / step : 0;
       const uint32_t ncommit = ntile * nk * kHalves;
@@ -383,13 +416,13 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           if (bar_poll(fempty(i % NF), (i / NF) & 1u)) break;
     }
     __syncwarp();
-    if (split > 1) {
+    if constexpr (SPLIT) {
       cluster_sync();
       cluster_sync();
     }
   } else if (warp < 4 + kConvWarps) {
     // ---- bytes -> fp16 ------------------------------------------------------------------
-    if constexpr (CG > 1) regs_fewer<kConvRegs>();
+    regs_fewer<kConvRegs>();
     // groups of four warps, each on one 64-code half of every other byte stage:
     // one group's waits and fences overlap the others' widening.  A thread takes
     // 16 codes (quarter uc of the half) of one row in kRows.  Eight neighbouring
@@ -400,8 +433,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     constexpr int kGroupThreads = 32 * kGroupWarps;
     constexpr int kRows = kGroupThreads / 4;            // rows per pass: a multiple of 8, so
     constexpr int kPasses = (BM + LT) / kRows;          // every pass has one swizzle key
-    // passes loaded before widening: as many as the registers hold
-    constexpr int kBatch = CG > 1 ? 2 : kPasses;
+    // passes loaded before widening
+    constexpr int kBatch = 2;
     const int grp = (tid - 128) / kGroupThreads, u = (tid - 128) % kGroupThreads;
     const int half = grp % kHalves, turn = grp / kHalves;
     constexpr int kTurns = kConvGroups / kHalves;
@@ -409,11 +442,12 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     const int ur = (uq & ~7) + (((uq >> 1) & 3) ^ ((uq & 1) * 5));
     const uint32_t in = ur * BKB + (((half * 4 + uc) ^ (ur & 7)) << 4);
     const uint32_t out0 = ur * (BK * 2) + (((2 * uc) ^ (ur & 7)) << 4);
+    cluster_wait_all();
     int s = turn, f = grp;
     uint32_t bphase = 0, fphase = 0;
     bool ok = true;
-    const int tiles = tile_count();
-    const int total = first < tiles ? ((tiles - first + step - 1) / step) * nk : 0;
+    const int tiles = tile_count(), first = first_tile(), step = tile_step();
+    const int total = first < tiles ? ((tiles - first + step - 1) / step) * stage_count() : 0;
     for (int i = turn; i < total; i += kTurns) {
       ok = __all_sync(0xffffffffu, bar_wait(bfull(s), bphase));
       if (!ok) break;
@@ -461,10 +495,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       if (!ok) break;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG > 1) cluster_arrive(cluster_addr(ffull(f), 0));
-        else bar_arrive(ffull(f));
-      }
+      if (lane == 0) cluster_arrive(cluster_addr(ffull(f), leader));
       for (s += kTurns; s >= nbyte; s -= nbyte) bphase ^= 1u;
       for (f += kConvGroups; f >= NF; f -= NF) fphase ^= 1u;
     }
@@ -472,21 +503,22 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
       smem_store(abort_flag, 1);
     }
-    if (split > 1) {
+    if constexpr (SPLIT) {
       cluster_sync();
       cluster_sync();
     }
   } else {
     // ---- chunk sums -> int32, scales, stores ----------------------------------------------
-    if constexpr (CG > 1) regs_more<kEpiRegs>();
+    regs_more<kEpiRegs>();
     constexpr int kParts = kEpiWarps / 4, kCols = NT / kParts;   // columns per thread
     const int q = warp & 3;                  // TMEM lanes 32 q ..
     const int col0 = ((warp - 4 - kConvWarps) >> 2) * kCols;
     const uint32_t base = smem_load(tmem_slot) + (uint32_t(q * 32) << 16) + col0;
+    cluster_wait_all();
     uint32_t chunk = 0;
     bool ok = true;
-    for (int t = first; ok && t < tile_count(); t += step) {
-      Tile tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
+    for (int t = first_tile(); ok && t < tile_count(); t += tile_step()) {
+      Tile tl = decode_tile(t, goff, tpre, p.G, ntn, block);
       const int live = tl.cols - col0;       // columns of this thread that are computed
       auto wait = [&]() {                    // for the next chunk
         const bool got = bar_wait(tfull(chunk & 1u), (chunk >> 1) & 1u) &&
@@ -498,27 +530,14 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG > 1) cluster_arrive(cluster_addr(tempty(chunk & 1u), 0));
-          else bar_arrive(tempty(chunk & 1u));
-        }
+        if (lane == 0) cluster_arrive(cluster_addr(tempty(chunk & 1u), leader));
         ++chunk;
       };
-      // scales: into L1 now, into registers after the sums (a pair's tiles are long
-      // enough to load them then)
-      if (CG == 1 && OUT != MOE_INT32) {
-#pragma unroll
-        for (int i = 0; i < kCols; i += 32)
-          if (col0 + i + lane < tl.rows)
-            prefetch_l1(p.row_scale + int64_t(tl.row0 + col0 + i + lane) * p.row_scale_stride);
-        const int n = tl.n0 + rank * BM + q * 32 + lane;
-        if (n < p.N) prefetch_l1(p.col_scale + int64_t(tl.g) * p.N + n);
-      }
       int32_t acc[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; ++j) acc[j] = 0;
       // every chunk but the last: into the sums
-      for (int c = 1; c < nchunks; ++c) {
+      for (int c = chunk_count(stage_count()) - 1; c > 0; --c) {
         if (!wait()) break;
 #pragma unroll
         for (int cb = 0; cb < kCols / 4; ++cb)
@@ -531,19 +550,9 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           }
         release();
       }
-      // the last one: four columns at a time through the scales to memory
-      // (the tile is decoded again: the sums leave no registers to hold it)
-      tl = decode_tile<CG>(t, goff, tpre, p.G, ntn, block);
-      const int n = tl.n0 + rank * BM + q * 32 + lane;
-      const int lim = n < p.N ? tl.rows - col0 : 0;    // tokens of this thread to store
-      const int64_t gn = int64_t(tl.g) * p.N + n;
-      const float col = OUT != MOE_INT32 && n < p.N ? __ldg(p.col_scale + gn) : 0.0f;
-      auto row_scale = [&](int j) {         // of the tile's token j (0 past the tile)
-        return OUT != MOE_INT32 && j < tl.rows
-                   ? __ldg(reinterpret_cast<const float*>(
-                         p.row_scale + int64_t(tl.row0 + j) * p.row_scale_stride))
-                   : 0.0f;
-      };
+      // the last one: four columns at a time, through the scales to memory or, where
+      // K is split, to the CTA that adds them up (the tile is decoded again: the
+      // sums leave no registers to hold it)
       if (!ok || !wait()) {
         if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
         smem_store(abort_flag, 1);
@@ -562,17 +571,22 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           }
         release();
       };
-      if (CG > 1 || split == 1) {
+      if constexpr (!SPLIT) {
+        tl = decode_tile(t, goff, tpre, p.G, ntn, block);
+        const int n = tl.n0 + rank * BM + q * 32 + lane;
+        const int lim = n < p.N ? tl.rows - col0 : 0;    // tokens of this thread to store
+        const float col = lim > 0 ? col_scale<OUT>(p, tl.g, n) : 0.0f;
         constexpr int kItem = OUT == MOE_BF16 || OUT == MOE_FP16 ? 2 : 4;
         const uint32_t pitch = p.N * kItem;
         uint8_t* at = static_cast<uint8_t*>(p.c) +
                       (int64_t(tl.row0 + col0) * p.N + n) * kItem;
         auto finish = [&](auto is_full, auto has_bias) {
           constexpr bool kFull = decltype(is_full)::value, kBias = decltype(has_bias)::value;
-          const float bias = kBias && lim > 0 ? __ldg(p.bias + gn) : 0.0f;
+          const float bias = kBias && lim > 0 ? bias_of(p, tl.g, n) : 0.0f;
           float rs = 0.0f;                  // lane l: the scale of token l of 32
           drain([&](int j0, const int32_t* sum) {
-            if (j0 % 32 == 0) rs = row_scale(col0 + j0 + lane);
+            if (j0 % 32 == 0 && col0 + j0 + lane < tl.rows)
+              rs = row_scale<OUT>(p, tl.row0 + col0 + j0 + lane);
 #pragma unroll
             for (int j = 0; j < 4; j += 2, at += 2 * pitch) {
               const float r0 = __shfl_sync(0xffffffffu, rs, (j0 + j) % 32);
@@ -592,33 +606,53 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         const bool is_full = tl.rows == NT && tl.n0 + rank * BM + BM <= p.N;
         if (p.bias) is_full ? finish(yes, yes) : finish(no, yes);
         else is_full ? finish(yes, no) : finish(no, no);
-      } else if constexpr (CG == 1) {
-        // rank d finishes columns [d, d+1) * kCols / split of each thread
+      } else {
+        // part d finishes `share` of each thread's live columns, from d * share on
+        const int share = (max(min(live, kCols), 0) + 4 * split - 1) / (4 * split) * 4;
+        const int mine0 = part * share;               // this part's first column
+        float rs[kCols / 64];                         // lane l: token col0 + mine0 + 32 i + l
+#pragma unroll
+        for (int i = 0; i < kCols / 64; ++i) {
+          const int j = col0 + mine0 + 32 * i + lane;
+          rs[i] = 32 * i + lane < share && j < tl.rows ? row_scale<OUT>(p, tl.row0 + j) : 0.0f;
+        }
         cluster_sync();                     // every CTA is done with its stages
         const int eth = tid - 128 - 32 * kConvWarps;   // epilogue thread
-        const int share = kCols / split, shift = 31 - __clz(share);    // powers of two
-        const uint32_t mine = sbase + ((part * share) * 256 + eth) * 4;
         drain([&](int j0, const int32_t* sum) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int d = (j0 + j) >> shift, jj = (j0 + j) & (share - 1);
-            cluster_store(cluster_addr(mine + jj * 1024, d), static_cast<uint32_t>(sum[j]));
-          }
+          const int d = (j0 >= share) + (j0 >= 2 * share) + (j0 >= 3 * share);
+          const uint32_t to = sbase + ((part * share + j0 - d * share) / 4 * 256 + eth) * 16;
+          cluster_store16(cluster_addr(to, d * CG + rank), sum);
         });
         cluster_sync();
-        for (int jj = 0; jj < share; ++jj) {
-          const int j = col0 + part * share + jj;
-          if (j - col0 >= lim) continue;
-          int32_t sum = 0;
-          for (int r = 0; r < split; ++r)
-            sum += *reinterpret_cast<volatile int32_t*>(smem + ((r * share + jj) * 256 + eth) * 4);
-          const int64_t to = int64_t(tl.row0 + j) * p.N + n;
-          if (p.bias) store_out<OUT, true>(p.c, to, sum, col, row_scale(j), __ldg(p.bias + gn));
-          else store_out<OUT, false>(p.c, to, sum, col, row_scale(j), 0.0f);
-        }
+        tl = decode_tile(t, goff, tpre, p.G, ntn, block);
+        const int n = tl.n0 + rank * BM + q * 32 + lane;
+        const float col = n < p.N ? col_scale<OUT>(p, tl.g, n) : 0.0f;
+        const float bias = OUT != MOE_INT32 && p.bias && n < p.N ? bias_of(p, tl.g, n) : 0.0f;
+        const int last = min(share, min(kCols, tl.rows - col0) - mine0);   // tokens to store
+#pragma unroll
+        for (int i = 0; i < kCols / 64; ++i)
+#pragma unroll 2
+          for (int jj = 32 * i; jj < min(last, 32 * i + 32); jj += 4) {
+            int sum[4] = {0, 0, 0, 0};
+            for (int r = 0; r < split; ++r) {
+              const uint4 v = lds128(sbase + ((r * share + jj) / 4 * 256 + eth) * 16);
+              sum[0] += static_cast<int>(v.x);
+              sum[1] += static_cast<int>(v.y);
+              sum[2] += static_cast<int>(v.z);
+              sum[3] += static_cast<int>(v.w);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float row = __shfl_sync(0xffffffffu, rs[i], (jj + k) & 31);
+              if (jj + k >= last || n >= p.N) continue;
+              const int64_t to = int64_t(tl.row0 + col0 + mine0 + jj + k) * p.N + n;
+              if (p.bias) store_out<OUT, true>(p.c, to, sum[k], col, row, bias);
+              else store_out<OUT, false>(p.c, to, sum[k], col, row, 0.0f);
+            }
+          }
       }
     }
-    if (split > 1 && (first >= tile_count() || !ok)) {   // no tile, or a timeout: the peers still wait
+    if (SPLIT && (first_tile() >= tile_count() || !ok)) {   // no tile, or a timeout: the peers wait
       cluster_sync();
       cluster_sync();
     }
@@ -627,61 +661,114 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   tc_fence_before();
   __syncthreads();
   // no CTA of a pair goes while the other may still arrive on its barriers
-  if constexpr (CG > 1) cluster_sync();
+  cluster_sync();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_free<CG>(smem_load(tmem_slot), kTmemCols);
+    pair_tmem_free(smem_load(tmem_slot), kTmemCols);
   }
 }
 
-template <int NT, int CG, int OUT>
-cudaError_t launch_out(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
-                       int block, int box_rows, int clusters, int split, int32_t* dev_status,
-                       int optin, cudaStream_t st) {
+struct Plan {
+  int nt;          // the kernel's token limit per tile: 128 or 256
+  int block;       // tokens per tile at most
+  int box_rows;    // token rows per copy
+  int split;       // pairs that share a tile's K
+  int clusters;
+};
+
+template <int NT, int OUT, bool SPLIT>
+cudaError_t launch_kernel(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
+                          const Plan& plan, int32_t* dev_status, int optin, cudaStream_t st) {
   using S = Stages<NT / CG>;
   int nbyte = kMaxByteStages;    // at least kConvGroups / kHalves = 2
   while (nbyte > 2 && S::bytes(nbyte, p.G) > size_t(optin)) --nbyte;
   const size_t smem = S::bytes(nbyte, p.G);
-  auto kernel = linear_i8_tile_kernel<NT, CG, OUT>;
+  auto kernel = linear_i8_tile_kernel<NT, OUT, SPLIT>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * CG * split));
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters * CG * plan.split));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(CG * split);
+  at[0].val.clusterDim.x = static_cast<unsigned>(CG * plan.split);
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, block, box_rows, nbyte, -0.0f, dev_status);
+  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, plan.block, plan.box_rows, nbyte, -0.0f,
+                            dev_status);
 }
 
-template <int NT, int CG>
+template <int NT, int OUT>
+cudaError_t launch_out(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
+                       const Plan& plan, int32_t* dev_status, int optin, cudaStream_t st) {
+  return plan.split > 1 ? launch_kernel<NT, OUT, true>(mw, ma, p, plan, dev_status, optin, st)
+                        : launch_kernel<NT, OUT, false>(mw, ma, p, plan, dev_status, optin, st);
+}
+
+template <int NT>
 cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
-                      int block, int box_rows, int clusters, int split, int32_t* dev_status,
-                      int optin, cudaStream_t st) {
+                      const Plan& plan, int32_t* dev_status, int optin, cudaStream_t st) {
   switch (p.c_dtype) {
-    case MOE_BF16:
-      return launch_out<NT, CG, MOE_BF16>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
-    case MOE_FP16:
-      return launch_out<NT, CG, MOE_FP16>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
-    case MOE_FP32:
-      return launch_out<NT, CG, MOE_FP32>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
-    default:
-      return launch_out<NT, CG, MOE_INT32>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
+    case MOE_BF16: return launch_out<NT, MOE_BF16>(mw, ma, p, plan, dev_status, optin, st);
+    case MOE_FP16: return launch_out<NT, MOE_FP16>(mw, ma, p, plan, dev_status, optin, st);
+    case MOE_FP32: return launch_out<NT, MOE_FP32>(mw, ma, p, plan, dev_status, optin, st);
+    default: return launch_out<NT, MOE_INT32>(mw, ma, p, plan, dev_status, optin, st);
   }
 }
 
 // Up to this many rows, the kernel that streams weights through integer dot
-// products is the faster one: of a plain product (4 rows of 2048 -> 7168: 8.0
-// against 13.4 us; 8 rows of 7168 -> 4096: 17.3 against 17.6), and per group on
-// average (256 groups of 7168 -> 4096: mean 2 rows 1.09 against 1.30 ms, mean 3
-// level, mean 4 1.55 against 1.39).
+// products is the faster one: of a plain product, and per group on average.
 constexpr int64_t kFewPlain = 8, kFewGrouped = 3;
+constexpr int kMaxSplit = 4;
+
+// Tokens per tile and pairs per K.  A plain product's tiles are known: the
+// cheapest of the block sizes (multiples of 32) and splits by the time of the
+// slowest pair, in clocks: a 64-code step takes 2 clocks a token in the MMA, or
+// about 2 clocks per row (128 channels and half the tokens) to widen, whichever
+// is more; a tile about 1500 besides, an exchange of partial sums 3000 more.
+// Groups (sizes known on the device only): blocks that hold a group somewhat
+// above the mean.
+Plan make_plan(const LinearArgs& p, int sms) {
+  const int64_t ntn = (p.N + CG * BM - 1) / (CG * BM);
+  const int64_t stages = (p.K + BKB - 1) / BKB;
+  const int64_t mean = (p.a_rows + p.G - 1) / p.G;
+  Plan best{};
+  double best_cost = 0.0;
+  const int64_t least = (mean + 255) / 256;
+  for (int64_t blocks = least; blocks <= 2 * least + 3 && blocks * 32 < mean + 32; ++blocks) {
+    const int block = p.G > 1 ? (mean * 5 / 4 <= 128 ? 128 : 256)
+                              : static_cast<int>(((mean + blocks - 1) / blocks + 31) / 32 * 32);
+    // at most this many tiles, for any group sizes
+    const int64_t tiles = p.G == 1
+                              ? (p.a_rows + block - 1) / block * ntn
+                              : (p.a_rows / block + std::min<int64_t>(p.G, p.a_rows)) * ntn;
+    for (int split = 1; split <= kMaxSplit; ++split) {
+      // clusters that run at once: larger ones leave SMs of a GPU cluster unused
+      // (152 SMs hold 76 clusters of 2, 36 of 4, 23 of 6, 15 of 8)
+      const int64_t room = sms * (split == 1 ? 76 : split == 2 ? 36 : split == 3 ? 23 : 15) / 152;
+      if (split > 1 && (tiles > room || stages < 2 * split)) break;
+      const double waves = static_cast<double>((tiles + room - 1) / room);
+      const double step = std::max(2.0 * block, 2.05 * (BM + block / 2));
+      const double cost =
+          waves * (step * kHalves * ((stages + split - 1) / split) + 1500) + (split > 1) * 3000;
+      if (best.nt == 0 || cost < best_cost) {
+        best_cost = cost;
+        best.block = block;
+        best.split = split;
+        best.clusters = static_cast<int>(std::min(tiles, room));
+        best.nt = block <= 128 ? 128 : 256;
+      }
+    }
+    if (p.G > 1) break;
+  }
+  const int64_t tokens = p.G > 1 ? mean : best.block;       // a CTA copies half of them
+  best.box_rows = tokens > 64 ? 64 : tokens > 32 ? 32 : 16;
+  return best;
+}
 
 }  // namespace
 
@@ -693,33 +780,16 @@ cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStrea
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
-  // Pairs of CTAs on 256 x 256 tiles where groups are large enough to fill
-  // them and there are tiles for most SMs; else one CTA on 128 x 64.
-  const bool big = p.a_rows / p.G > 128 &&
-                   (p.a_rows / 256 + 1) * ((p.N + 255) / 256) * 2 >= sms;
-  const int nt = big ? 256 : 64, cg = big ? 2 : 1;
-  const int64_t ntn = (p.N + cg * BM - 1) / (cg * BM);
-  // at most this many tiles, for any group sizes
-  const int64_t most = (p.a_rows / nt + std::min<int64_t>(p.G, p.a_rows)) * ntn;
-  if (most > INT32_MAX) return cudaErrorInvalidValue;
-  int clusters = static_cast<int>(std::min<int64_t>(most, sms / cg));
-  int block = nt, split = 1;
-  if (p.G == 1 && !big) {
-    const int64_t tiles = (p.a_rows + nt - 1) / nt * ntn;
-    const int nkb = (p.K + BKB - 1) / BKB;
-    while (split < 8 && tiles * split * 2 <= sms && nkb >= split * 2 * 2) split *= 2;
-    if (split > 1) clusters = static_cast<int>(tiles);   // one tile per cluster
-  }
+  const Plan plan = make_plan(p, sms);
+  const int64_t ntn = (p.N + CG * BM - 1) / (CG * BM);
+  if ((p.a_rows / 32 + p.G) * ntn > INT32_MAX) return cudaErrorInvalidValue;
   CUtensorMap mw, ma;
-  // token rows per copy: few copies for full tiles, few useless rows for small groups
-  const int64_t mean = (p.a_rows + p.G - 1) / p.G;
-  const int box_rows = big || mean > 32 ? 64 : mean > 16 ? 32 : 16;
   e = encode_bytes_2d(&mw, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, BM);
   if (e == cudaSuccess)
-    e = encode_bytes_2d(&ma, p.a, p.a_rows, p.K, p.a_stride, box_rows);
+    e = encode_bytes_2d(&ma, p.a, p.a_rows, p.K, p.a_stride, plan.box_rows);
   if (e != cudaSuccess) return e;
-  return big ? launch_nt<256, 2>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st)
-             : launch_nt<64, 1>(mw, ma, p, block, box_rows, clusters, split, dev_status, optin, st);
+  return plan.nt == 256 ? launch_nt<256>(mw, ma, p, plan, dev_status, optin, st)
+                        : launch_nt<128>(mw, ma, p, plan, dev_status, optin, st);
 }
 
 }  // namespace moe_ep

@@ -19,10 +19,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ void prefetch_l1(const void* p) {
-  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
-}
-
 // ---- mbarriers by 32-bit shared-memory address (half the registers of
 // generic pointers) -------------------------------------------------
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
@@ -111,9 +107,15 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 // Every thread of every CTA of the cluster; earlier writes (also to another
 // CTA's shared memory) are visible after it.
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive_all() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_all() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive_all();
+  cluster_wait_all();
 }
 // The same shared-memory address in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
@@ -121,8 +123,9 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void cluster_store(uint32_t caddr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
+__device__ __forceinline__ void cluster_store16(uint32_t caddr, const int32_t* v) {
+  asm volatile("st.shared::cluster.v4.s32 [%0], {%1,%2,%3,%4};" ::"r"(caddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
 // One arrival on an mbarrier of any CTA of the cluster (address from
@@ -134,57 +137,32 @@ __device__ __forceinline__ void cluster_arrive(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
-// The products of one instruction (K = 16) of a CTA, or of a pair of CTAs
-// (issued by the leader alone; each CTA holds half of both operands).
-template <int CG>
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        bool accumulate) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
-        : "memory");
+// The products of one instruction (K = 16) of a pair of CTAs, issued by the
+// pair's first CTA alone; each CTA holds half of both operands.
+__device__ __forceinline__ void pair_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+      : "memory");
 }
-// Arrives on `bar` (in both CTAs of a pair, at the same offset) once every
-// product issued so far by this thread is done.
-template <int CG>
-__device__ __forceinline__ void mma_commit_to(uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-        ::"r"(bar) : "memory");
-  else
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
-        ".b64 [%0], %1;" ::"r"(bar), "h"(uint16_t(3)) : "memory");
+// Arrives on `bar` in the CTAs of `mask` (ranks in the cluster), at the same
+// offset, once every product issued so far by this thread is done.
+__device__ __forceinline__ void pair_commit(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+      ".b64 [%0], %1;" ::"r"(bar), "h"(mask) : "memory");
 }
-template <int CG>
-__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
-  if constexpr (CG == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
+// TMEM columns of a pair: one warp of each of its CTAs takes part.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+               "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
-template <int CG>
-__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(cols) : "memory");
-  else
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(cols) : "memory");
+__device__ __forceinline__ void pair_tmem_free(uint32_t tmem, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+               : "memory");
 }
 
 // Registers of this warpgroup (all four warps): more, or fewer.
