@@ -73,6 +73,7 @@ constexpr int BK = 64;               // codes per fp16 stage: one 128-byte row
 constexpr int kHalves = 2;           // fp16 stages per byte stage (128-byte rows both)
 constexpr int BKB = kHalves * BK;
 constexpr int kChunk = 1024 / BKB;   // byte stages per chunk: 1024 products, exact in fp32
+constexpr int kMaxSplit = 4;         // pairs that may share a tile's K
 constexpr int kRasterTokens = 8;     // token blocks per raster band (weights reused from L2)
 // 28 warps: 4 that copy and multiply (two of them idle), 16 that widen, in groups
 // of four on different stages, and 8 that drain and store.  (With 8 widening and
@@ -119,24 +120,28 @@ __device__ __forceinline__ Tile decode_tile(int t, uint32_t goff, uint32_t tpre,
   const int lo = group_of_tile(t, tpre, G);
   const int off = smem_load(goff + 4 * lo);
   const int cnt = smem_load(goff + 4 * lo + 4) - off;
-  const int blocks = row_blocks(cnt, block);    // equal ones, of at most `block` tokens
-  constexpr int kStep = 16 * CG;
-  const int per = ((cnt + blocks - 1) / blocks + kStep - 1) / kStep * kStep;
-  // bands of kRasterTokens token blocks (the last band takes the remainder);
-  // inside a band the token block is fastest, so the CTAs in flight share
-  // weight tiles and a bounded number of token blocks
-  const int nband = max(blocks / kRasterTokens, 1);
-  const int local = t - smem_load(tpre + 4 * lo);
-  const int per_band = kRasterTokens * ntn;
-  const int band = min(local / per_band, nband - 1);
-  const int width = band < nband - 1 ? kRasterTokens : blocks - band * kRasterTokens;
-  const int r = local - band * per_band;
+  const uint32_t local = t - smem_load(tpre + 4 * lo);
+  constexpr uint32_t kStep = 16 * CG;
+  uint32_t per = (cnt + kStep - 1) / kStep * kStep, nblk = local, mblk = 0;   // one block
+  if (cnt > block) {
+    const uint32_t blocks = static_cast<uint32_t>(row_blocks(cnt, block));   // equal ones
+    per = ((cnt + blocks - 1) / blocks + kStep - 1) / kStep * kStep;
+    // bands of kRasterTokens token blocks (the last band takes the remainder);
+    // inside a band the token block is fastest, so the CTAs in flight share
+    // weight tiles and a bounded number of token blocks
+    const uint32_t nband = max(blocks / kRasterTokens, 1u), per_band = kRasterTokens * ntn;
+    const uint32_t band = min(local / per_band, nband - 1);
+    const uint32_t width = band < nband - 1 ? kRasterTokens : blocks - band * kRasterTokens;
+    const uint32_t r = local - band * per_band;
+    nblk = r / width;
+    mblk = band * kRasterTokens + r - nblk * width;
+  }
   Tile tl;
   tl.g = lo;
-  tl.n0 = r / width * (CG * BM);
-  const int first = (band * kRasterTokens + r % width) * per;
+  tl.n0 = static_cast<int>(nblk * (CG * BM));
+  const int first = static_cast<int>(mblk * per);
   tl.row0 = off + first;
-  tl.rows = max(0, min(per, cnt - first));
+  tl.rows = max(0, min(static_cast<int>(per), cnt - first));
   tl.cols = max(kStep, (tl.rows + kStep - 1) / kStep * kStep);
   return tl;
 }
@@ -230,7 +235,8 @@ template <int NT, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ CUtensorMap map_a, const LinearArgs p, int block,
-                      int box_rows, int nbyte, float nz, int32_t* dev_status) {
+                      int box_rows, int nbyte, int stages, int extra, float nz,
+                      int32_t* dev_status) {
   constexpr int LT = NT / CG;
   using St = Stages<LT>;
   constexpr int NF = St::kF16;
@@ -300,17 +306,16 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 
   // (each role reads what it needs: registers are short in some)
   auto tile_count = [&]() { return smem_load(tpre + 4 * p.G); };
-  // byte stages of K (zeros past it) that this CTA's pair takes: [begin, begin + count)
-  auto stage_begin = [&](int i) { return (p.K + BKB - 1) / BKB * i / split; };
-  auto stage_count = [&]() { return stage_begin(part + 1) - stage_begin(part); };
+  // byte stages of K (zeros past it): every part of a split has `stages`, the first
+  // `extra` parts one more
+  auto stage_begin = [&]() { return part * stages + min(part, extra); };
+  auto stage_count = [&]() { return stages + (part < extra ? 1 : 0); };
   auto chunk_count = [&](int nk) { return (nk + kChunk - 1) / kChunk; };
-  auto first_tile = [&]() { return static_cast<int>(blockIdx.x) / (CG * split); };
-  auto tile_step = [&]() { return static_cast<int>(gridDim.x) / (CG * split); };
 
   if (warp < 4) {
     regs_fewer<kCtrlRegs>();
     const int tiles = tile_count();
-    const int nk = stage_count(), first = first_tile(), step = tile_step();
+    const int nk = stage_count(), first = cluster_id(), step = cluster_count();
     if (warp == 0) {
       // ---- copies -------------------------------------------------------------------
       const bool issue = elect_one();
@@ -323,7 +328,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         const int boxes = (rows + box_rows - 1) / box_rows;
         const int wrow = tl.g * p.N + tl.n0 + rank * BM;
         const int arow = tl.row0 + rank * rows;
-        const int kb0 = stage_begin(part);
+        const int kb0 = stage_begin();
         for (int kb = kb0; kb < kb0 + nk; ++kb) {
           if (!bar_wait(bempty(s), phase ^ 1u)) {
             ok = false;
@@ -446,7 +451,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     int s = turn, f = grp;
     uint32_t bphase = 0, fphase = 0;
     bool ok = true;
-    const int tiles = tile_count(), first = first_tile(), step = tile_step();
+    const int tiles = tile_count(), first = cluster_id(), step = cluster_count();
     const int total = first < tiles ? ((tiles - first + step - 1) / step) * stage_count() : 0;
     for (int i = turn; i < total; i += kTurns) {
       ok = __all_sync(0xffffffffu, bar_wait(bfull(s), bphase));
@@ -517,7 +522,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     cluster_wait_all();
     uint32_t chunk = 0;
     bool ok = true;
-    for (int t = first_tile(); ok && t < tile_count(); t += tile_step()) {
+    for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
       Tile tl = decode_tile(t, goff, tpre, p.G, ntn, block);
       const int live = tl.cols - col0;       // columns of this thread that are computed
       auto wait = [&]() {                    // for the next chunk
@@ -609,13 +614,6 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       } else {
         // part d finishes `share` of each thread's live columns, from d * share on
         const int share = (max(min(live, kCols), 0) + 4 * split - 1) / (4 * split) * 4;
-        const int mine0 = part * share;               // this part's first column
-        float rs[kCols / 64];                         // lane l: token col0 + mine0 + 32 i + l
-#pragma unroll
-        for (int i = 0; i < kCols / 64; ++i) {
-          const int j = col0 + mine0 + 32 * i + lane;
-          rs[i] = 32 * i + lane < share && j < tl.rows ? row_scale<OUT>(p, tl.row0 + j) : 0.0f;
-        }
         cluster_sync();                     // every CTA is done with its stages
         const int eth = tid - 128 - 32 * kConvWarps;   // epilogue thread
         drain([&](int j0, const int32_t* sum) {
@@ -623,36 +621,47 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           const uint32_t to = sbase + ((part * share + j0 - d * share) / 4 * 256 + eth) * 16;
           cluster_store16(cluster_addr(to, d * CG + rank), sum);
         });
-        cluster_sync();
         tl = decode_tile(t, goff, tpre, p.G, ntn, block);
+        const int mine0 = part * share;               // this part's first column
+        float rs[kCols / 64];                         // lane l: token col0 + mine0 + 32 i + l
+#pragma unroll
+        for (int i = 0; i < kCols / 64; ++i) {
+          const int j = col0 + mine0 + 32 * i + lane;
+          rs[i] = 32 * i + lane < share && j < tl.rows ? row_scale<OUT>(p, tl.row0 + j) : 0.0f;
+        }
         const int n = tl.n0 + rank * BM + q * 32 + lane;
         const float col = n < p.N ? col_scale<OUT>(p, tl.g, n) : 0.0f;
         const float bias = OUT != MOE_INT32 && p.bias && n < p.N ? bias_of(p, tl.g, n) : 0.0f;
+        cluster_sync();                     // every part's sums are here
         const int last = min(share, min(kCols, tl.rows - col0) - mine0);   // tokens to store
+        constexpr int kItem = OUT == MOE_BF16 || OUT == MOE_FP16 ? 2 : 4;
+        const uint32_t pitch = p.N * kItem;
+        uint8_t* at = static_cast<uint8_t*>(p.c) +
+                      (int64_t(tl.row0 + col0 + mine0) * p.N + n) * kItem;
 #pragma unroll
         for (int i = 0; i < kCols / 64; ++i)
 #pragma unroll 2
           for (int jj = 32 * i; jj < min(last, 32 * i + 32); jj += 4) {
-            int sum[4] = {0, 0, 0, 0};
-            for (int r = 0; r < split; ++r) {
-              const uint4 v = lds128(sbase + ((r * share + jj) / 4 * 256 + eth) * 16);
-              sum[0] += static_cast<int>(v.x);
-              sum[1] += static_cast<int>(v.y);
-              sum[2] += static_cast<int>(v.z);
-              sum[3] += static_cast<int>(v.w);
-            }
+            uint4 v[kMaxSplit];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int r = 0; r < kMaxSplit; ++r)
+              v[r] = r < split ? lds128(sbase + ((r * share + jj) / 4 * 256 + eth) * 16)
+                               : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t sum[4] = {v[0].x + v[1].x + v[2].x + v[3].x,
+                                     v[0].y + v[1].y + v[2].y + v[3].y,
+                                     v[0].z + v[1].z + v[2].z + v[3].z,
+                                     v[0].w + v[1].w + v[2].w + v[3].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k, at += pitch) {
               const float row = __shfl_sync(0xffffffffu, rs[i], (jj + k) & 31);
               if (jj + k >= last || n >= p.N) continue;
-              const int64_t to = int64_t(tl.row0 + col0 + mine0 + jj + k) * p.N + n;
-              if (p.bias) store_out<OUT, true>(p.c, to, sum[k], col, row, bias);
-              else store_out<OUT, false>(p.c, to, sum[k], col, row, 0.0f);
+              if (p.bias) store_out<OUT, true>(at, 0, static_cast<int>(sum[k]), col, row, bias);
+              else store_out<OUT, false>(at, 0, static_cast<int>(sum[k]), col, row, 0.0f);
             }
           }
       }
     }
-    if (SPLIT && (first_tile() >= tile_count() || !ok)) {   // no tile, or a timeout: the peers wait
+    if (SPLIT && (cluster_id() >= tile_count() || !ok)) {   // no tile, or a timeout: the peers wait
       cluster_sync();
       cluster_sync();
     }
@@ -698,8 +707,9 @@ cudaError_t launch_kernel(const CUtensorMap& mw, const CUtensorMap& ma, const Li
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, plan.block, plan.box_rows, nbyte, -0.0f,
-                            dev_status);
+  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, plan.block, plan.box_rows, nbyte,
+                            (p.K + BKB - 1) / BKB / plan.split,
+                            (p.K + BKB - 1) / BKB % plan.split, -0.0f, dev_status);
 }
 
 template <int NT, int OUT>
@@ -723,7 +733,6 @@ cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const Linear
 // Up to this many rows, the kernel that streams weights through integer dot
 // products is the faster one: of a plain product, and per group on average.
 constexpr int64_t kFewPlain = 8, kFewGrouped = 3;
-constexpr int kMaxSplit = 4;
 
 // Tokens per tile and pairs per K.  A plain product's tiles are known: the
 // cheapest of the block sizes (multiples of 32) and splits by the time of the

@@ -105,6 +105,16 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ int cluster_id() {        // which cluster, of how many
+  int r;
+  asm("mov.s32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int cluster_count() {
+  int r;
+  asm("mov.s32 %0, %%nclusterid.x;" : "=r"(r));
+  return r;
+}
 // Every thread of every CTA of the cluster; earlier writes (also to another
 // CTA's shared memory) are visible after it.
 __device__ __forceinline__ void cluster_arrive_all() {
