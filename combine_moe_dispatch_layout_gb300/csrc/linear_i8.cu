@@ -268,30 +268,32 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 
   if (p.group_rows) {        // the scan borrows the stages, which are not in use yet
     build_group_tables<kThreads>(p, block, ntn, smem, goff, tpre, dev_status);
-  } else if (tid == 0) {
+  } else if (tid == 64) {
     const int rows = static_cast<int>(p.a_rows);
     smem_store(goff, 0);
     smem_store(goff + 4, rows);
     smem_store(tpre, 0);
     smem_store(tpre + 4, row_blocks(rows, block) * ntn);
   }
-  if (tid == 0) {
-    for (int s = 0; s < nbyte; ++s) {
-      bar_init(bfull(s), 1);
-      bar_init(bempty(s), kHalves * kGroupWarps);
+  if (warp == 0) {           // barriers: one lane each
+    if (lane < nbyte) {
+      bar_init(bfull(lane), 1);
+      bar_init(bempty(lane), kHalves * kGroupWarps);
     }
-    for (int s = 0; s < NF; ++s) {
-      bar_init(ffull(s), CG * kGroupWarps);
-      bar_init(fempty(s), 1);
+    if (lane < NF) {
+      bar_init(ffull(lane), CG * kGroupWarps);
+      bar_init(fempty(lane), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      bar_init(tfull(b), 1);
-      bar_init(tempty(b), CG * kEpiWarps);
+    if (lane < 2) {
+      bar_init(tfull(lane), 1);
+      bar_init(tempty(lane), CG * kEpiWarps);
     }
-    smem_store(abort_flag, 0);
+    if (lane == 0) {
+      smem_store(abort_flag, 0);
+      tensor_map_prefetch(&map_w);
+      tensor_map_prefetch(&map_a);
+    }
     fence_mbar_init();
-    tensor_map_prefetch(&map_w);
-    tensor_map_prefetch(&map_a);
   }
   if (warp == 1) {
     __syncwarp();
