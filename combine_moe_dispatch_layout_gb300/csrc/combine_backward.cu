@@ -21,12 +21,12 @@
 namespace moe_ep {
 namespace {
 
-constexpr int kBatch = 8;
+constexpr int kBatch = 4;          // rows loaded before they are used
 constexpr int kMaxThreads = 512;
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int DT>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, 2)
 combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict__ y,
                         int64_t y_rows, const int32_t* __restrict__ topk_idx,
                         const float* __restrict__ weights,
@@ -34,10 +34,11 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
                         const int32_t* __restrict__ put_offset,
                         const int64_t* __restrict__ rank_recv_base, int R, int bs, int k,
                         int epr, int H, int64_t T, uint4* __restrict__ d_y,
-                        float* __restrict__ d_weights, int32_t* dev_status) {
+                        float* __restrict__ d_weights, int32_t* dev_status,
+                        bool prefetch_next) {
   __shared__ int64_t s_rows[2][MOE_EP_MAX_TOPK];
   __shared__ float s_w[2][MOE_EP_MAX_TOPK];
-  __shared__ float s_dot[kMaxThreads / 32][MOE_EP_MAX_TOPK];
+  __shared__ float s_dot[2][kMaxThreads / 32][MOE_EP_MAX_TOPK];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ncomp = blockDim.x - 32, nwarps = ncomp >> 5;
   const bool producer = tid >= ncomp;
@@ -53,9 +54,14 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
     const int buf = it & 1;
     if (producer) {
       const int64_t gn = g + gridDim.x;
-      if (gn < T)
+      if (gn < T) {
         resolve_token(gn, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k,
                       epr, y_rows, s_rows[buf ^ 1], s_w[buf ^ 1], dev_status, lane);
+        for (int kk = lane; prefetch_next && kk < k; kk += 32) {
+          const int64_t row = s_rows[buf ^ 1][kk];
+          if (row >= 0) bulk_prefetch_l2(y + row * nch, static_cast<uint32_t>(nch) * 16u);
+        }
+      }
     } else {
       for (int k0 = 0; k0 < k; k0 += kBatch) {
         float dot[kBatch];
@@ -91,20 +97,23 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
 #pragma unroll
           for (int s = 16; s; s >>= 1)
             dot[b] = __fadd_rn(dot[b], __shfl_xor_sync(kAll, dot[b], s));
-          if (lane == 0 && k0 + b < k) s_dot[warp][k0 + b] = dot[b];
+          if (lane == 0 && k0 + b < k) s_dot[buf][warp][k0 + b] = dot[b];
         }
       }
     }
     __syncthreads();   // dots are in; this token's table is free, the next is ready
-    if (!producer && tid < k) {
+    // (the next token's dots go to the other half: no second barrier)
+    if (tid < k) {
       float sum = 0.0f;
-      for (int w = 0; w < nwarps; ++w) sum = __fadd_rn(sum, s_dot[w][tid]);
+      for (int w = 0; w < nwarps; ++w) sum = __fadd_rn(sum, s_dot[buf][w][tid]);
       d_weights[g * k + tid] = sum;
     }
-    // a warp may write the next token's dots once all have read these
-    __syncthreads();
   }
 }
+
+// Rows at least this wide: the next token's rows are brought into L2 while this
+// one's are used.
+constexpr int64_t kPrefetchRowBytes = 12 * 1024;
 
 template <int DT>
 cudaError_t launch_t(const Shape& s, const void* d_out, const void* y, int64_t y_rows,
@@ -112,7 +121,7 @@ cudaError_t launch_t(const Shape& s, const void* d_out, const void* y, int64_t y
                      const int32_t* put_offset, const int64_t* rank_recv_base, void* d_y,
                      float* d_weights, int32_t* dev_status, cudaStream_t st) {
   const int nch = s.H / 8;
-  // at least k compute threads: thread j finishes slot j's dot product
+  // two 16-byte chunks per compute thread; thread j finishes slot j's dot product
   int threads = std::max((nch + 1) / 2, s.k);
   threads = std::min(kMaxThreads - 32, (threads + 31) / 32 * 32) + 32;
   auto kernel = combine_backward_kernel<DT>;
@@ -125,7 +134,7 @@ cudaError_t launch_t(const Shape& s, const void* d_out, const void* y, int64_t y
   kernel<<<static_cast<unsigned>(grid), threads, 0, st>>>(
       static_cast<const uint4*>(d_out), static_cast<const uint4*>(y), y_rows, topk_idx,
       weights, send_idx, put_offset, rank_recv_base, s.R, s.bs, s.k, s.epr, s.H, s.T(),
-      static_cast<uint4*>(d_y), d_weights, dev_status);
+      static_cast<uint4*>(d_y), d_weights, dev_status, int64_t(s.H) * 2 >= kPrefetchRowBytes);
   return cudaGetLastError();
 }
 

@@ -1,22 +1,22 @@
 // route.cu -- routing: logits -> the k expert ids and gate weights of every
 // token (include/moe_ep.h, moe_route).
 //
-// Mathematics.  Every expert e gets a ranking key: without a bias the logit
+// Mathematics.  Every expert e gets a ranked value: without a bias the logit
 // itself (sigmoid and softmax are increasing, so it orders experts as their
-// scores do), with a bias the choice s[e] + b[e].  A float maps to an unsigned
-// key with the same order (sign bit flipped for positive values, all bits for
-// negative ones); key 0 means "not available".  The k best keys are taken one
-// after another; weights are then recomputed for the k chosen logits alone,
-// in full precision, one per lane.  Softmax weights that are renormalised are
-// exp(l - max of the chosen) over their sum: the sum over all experts cancels,
-// so it is not computed.
+// scores do), with a bias the choice s[e] + b[e]; -inf means "not available".
+// The k largest are taken one after another; weights are then recomputed for the
+// k chosen logits alone, in full precision, one per lane.  Softmax weights that
+// are renormalised are exp(l - max of the chosen) over their sum: the sum over
+// all experts cancels, so it is not computed.
 //
 // Warp kernel (E <= 1024): one warp per token, lane L holding VPT neighbouring
 // experts, so the lowest lane and the lowest position inside it are the lowest
-// id and ties need no index compares.  Each lane keeps its two best keys
-// sorted; a round is one warp maximum, one ballot and a pop in the winning
-// lane, which looks through its keys again only when it has won twice (rare:
-// the k winners spread over the lanes).
+// id.  The cost is instructions (one SM does about 7 tokens of 256 experts in
+// the time their logits take to arrive), so the k rounds are kept short: a lane
+// keeps only its two largest values (three instructions per expert), a round is
+// one warp maximum, one ballot and a pop in the winning lane, and positions are
+// looked up once at the end, in the lanes that won.  A lane that wins twice
+// looks through its values again (rare: winners spread over the lanes).
 #include <algorithm>
 
 #include "moe_ep_internal.cuh"
@@ -46,21 +46,30 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return b ^ ((b & 0x80000000u) ? 0xffffffffu : 0x80000000u);
 }
 
-// e^x to about 2 ulp for the ranking of scores: x log2(e) in two parts, the
-// second one (with |part| < 2^-16) to first order.  Clamped where e^x is 0 or
-// inf in fp32 anyway.
-__device__ __forceinline__ float exp_rank(float x) {
-  x = fminf(fmaxf(x, -120.0f), 120.0f);
-  constexpr float kL2e = 1.44269502f, kL2eLo = 1.92596299e-8f, kLn2 = 0.693147181f;
-  const float t = __fmul_rn(x, kL2e);
-  const float r = __fmaf_rn(x, kL2eLo, __fmaf_rn(x, kL2e, -t));
+constexpr float kLog2e = 1.44269502f;      // log2(e), and what that leaves out
+constexpr float kLog2eLo = 1.92596299e-8f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
   float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
+}
+// e^x for x <= 0 to about 2 ulp (0 below -120): x log2(e) in two parts, the
+// second one (with |part| < 2^-16) to first order.  Sums of scores.
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLn2 = 0.693147181f;
+  x = fmaxf(x, -120.0f);
+  const float t = __fmul_rn(x, kLog2e);
+  const float r = __fmaf_rn(x, kLog2eLo, __fmaf_rn(x, kLog2e, -t));
+  const float e = exp2_approx(t);
   return __fmaf_rn(e, __fmul_rn(r, kLn2), e);
 }
+// The sigmoid that ranks: the rounded product in the exponent costs s(1-s)|x|
+// 2^-24 <= 2^-26, less than the rounding of s itself; 0 and 1 at the infinities.
 __device__ __forceinline__ float sigmoid_rank(float x) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, exp_rank(-x))));
+  asm("rcp.approx.ftz.f32 %0, %1;"
+      : "=f"(r) : "f"(__fadd_rn(1.0f, exp2_approx(__fmul_rn(x, -kLog2e)))));
   return r;
 }
 // The score in full precision (the weights).
@@ -74,40 +83,40 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
-// Ids and weights of one token from the chosen experts: slot j = lane or
-// lane + 32 (sel[.] = -1: no expert).  m and inv_sum: the softmax's maximum
-// and 1 / sum (plain softmax only).
-template <int DT>
+// Ids and weights of slots h * 32 + lane of a token from the chosen experts
+// (sel = -1: none).  m and sum: the softmax's maximum and sum (plain softmax
+// only).  H: 1 for k <= 32, else 2.
+template <int DT, int H>
 __device__ __forceinline__ void write_token(const RouteArgs& r,
                                             const typename Elem<DT>::T* row, int64_t t,
-                                            const int (&sel)[2], float m, float sum, int lane,
+                                            const int (&sel)[H], float m, float sum, int lane,
                                             int32_t* idx, float* weights) {
-  float l[2], s[2];
+  float l[H], s[H];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < H; ++h)
     l[h] = sel[h] >= 0 ? fminf(load_logit<DT>(row + sel[h]), kMaxF) : kNegInf;
   if (r.score == MOE_SOFTMAX) {
-    if (r.renormalise) m = warp_max(fmaxf(l[0], l[1]));
+    if (r.renormalise) m = warp_max(H > 1 ? fmaxf(l[0], l[H - 1]) : l[0]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) s[h] = sel[h] >= 0 ? expf(__fsub_rn(l[h], m)) : 0.0f;
+    for (int h = 0; h < H; ++h) s[h] = sel[h] >= 0 ? expf(__fsub_rn(l[h], m)) : 0.0f;
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) s[h] = sel[h] >= 0 ? sigmoid_full(l[h]) : 0.0f;
+    for (int h = 0; h < H; ++h) s[h] = sel[h] >= 0 ? sigmoid_full(l[h]) : 0.0f;
   }
   float d = 1.0f;
   if (r.renormalise) {
-    d = warp_sum(__fadd_rn(s[0], s[1]));
+    d = warp_sum(H > 1 ? __fadd_rn(s[0], s[H - 1]) : s[0]);
     if (d == 0.0f) d = 1.0f;
   } else if (r.score == MOE_SOFTMAX) {
     d = sum;
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < H; ++h) {
     const int j = lane + 32 * h;
     if (j < r.k) {
       idx[t * r.k + j] = sel[h];
@@ -116,160 +125,216 @@ __device__ __forceinline__ void write_token(const RouteArgs& r,
   }
 }
 
-constexpr int kWarps = 4;   // tokens per CTA of the warp kernel
+constexpr int kWarps = 4;   // tokens per CTA of the warp kernel at a time
 
-// vec: row starts and the lanes' chunks are 16-byte aligned.
-template <int DT, int VPT>
+// vec: row starts and the lanes' chunks are 16-byte aligned.  A persistent grid;
+// the bias stays in registers.
+template <int DT, int VPT, bool BIAS>
 __global__ void __launch_bounds__(kWarps * 32)
 route_warp_kernel(const RouteArgs r, bool vec, int lanes_per_group,
                   int32_t* __restrict__ idx, float* __restrict__ weights,
                   int32_t* dev_status) {
   using T = typename Elem<DT>::T;
   constexpr int kPer16 = 16 / sizeof(T);
+  __shared__ int s_sel[kWarps][MOE_EP_MAX_TOPK];
   const int lane = threadIdx.x & 31;
-  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (t >= r.T) return;
-  const T* row = static_cast<const T*>(r.logits) + t * r.stride;
+  int* chosen = s_sel[threadIdx.x >> 5];
   const int e0 = lane * VPT;
-
-  // ---- logits ------------------------------------------------------------------
-  float l[VPT];
-  if (VPT % kPer16 == 0 && vec && e0 + VPT <= r.E) {
-#pragma unroll
-    for (int c = 0; c < VPT / kPer16; ++c) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
-      if constexpr (DT == MOE_FP32) {
-        l[4 * c] = __uint_as_float(v.x);
-        l[4 * c + 1] = __uint_as_float(v.y);
-        l[4 * c + 2] = __uint_as_float(v.z);
-        l[4 * c + 3] = __uint_as_float(v.w);
-      } else {
-        float f[8];
-        unpack8<DT>(v, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) l[8 * c + i] = f[i];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      l[i] = e0 + i < r.E ? load_logit<DT>(row + e0 + i) : kNegInf;
-  }
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    nan |= l[i] != l[i];
-    l[i] = l[i] != l[i] ? kNegInf : fminf(l[i], kMaxF);
-  }
-  if (nan) set_status(dev_status, MOE_ERR_INVALID_ARG);
-
-  // ---- the softmax's maximum and sum, where a weight or a choice needs them --------
   const bool grouped = r.topk_group < r.n_group;
-  float m = 0.0f, sum = 1.0f;
-  if (r.score == MOE_SOFTMAX && (!r.renormalise || r.bias || grouped)) {
-    m = l[0];
-#pragma unroll
-    for (int i = 1; i < VPT; ++i) m = fmaxf(m, l[i]);
-    m = fmaxf(warp_max(m), -kMaxF);
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      sum = __fadd_rn(sum, l[i] > kNegInf ? exp_rank(__fsub_rn(l[i], m)) : 0.0f);
-    sum = warp_sum(sum);
-    if (sum == 0.0f) sum = 1.0f;
-  }
-  const float inv_sum = __fdiv_rn(1.0f, sum);
-  auto score = [&](float x) {
-    return r.score == MOE_SOFTMAX ? __fmul_rn(exp_rank(__fsub_rn(x, m)), inv_sum)
-                                  : sigmoid_rank(x);
-  };
+  const bool want_sum = r.score == MOE_SOFTMAX && (!r.renormalise || BIAS || grouped);
 
-  // ---- ranking keys (l becomes the ranked value), the lane's two best ---------------
-  if (r.bias) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (e0 + i < r.E) {
-        const float c = __fadd_rn(score(l[i]), __ldg(r.bias + e0 + i));
-        l[i] = l[i] > kNegInf && c > kNegInf ? c : kNegInf;
-      }
-  }
-  uint32_t key[VPT];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) key[i] = l[i] > kNegInf ? order_key(l[i]) : 0u;
-  uint32_t k1 = 0, k2 = 0, taken = 0;
-  int i1 = 0, i2 = 0;
-  auto scan = [&]() {
-    k1 = k2 = 0;
-    i1 = i2 = 0;
+  float bias[BIAS ? VPT : 1];
+  bool odd_bias = false;                // an infinite or NaN bias
+  if (BIAS) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const uint32_t v = (taken >> i) & 1u ? 0u : key[i];
-      if (v > k1) {
-        k2 = k1;
-        i2 = i1;
-        k1 = v;
-        i1 = i;
-      } else if (v > k2) {
-        k2 = v;
-        i2 = i;
-      }
+      bias[i] = e0 + i < r.E ? __ldg(r.bias + e0 + i) : 0.0f;
+      odd_bias |= !(fabsf(bias[i]) <= kMaxF);
     }
-  };
-  scan();
+    odd_bias = __any_sync(kAll, odd_bias);
+  }
 
-  // ---- groups: a lane's experts are all of one group, lanes_per_group lanes each --------
-  if (grouped) {
-    auto choice = [&](uint32_t k) {      // the choice behind a key
-      if (k == 0) return kNegInf;
-      const float f = __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
-      return r.bias ? f : score(f);
+  for (int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < r.T;
+       t += int64_t(gridDim.x) * kWarps) {
+    const T* row = static_cast<const T*>(r.logits) + t * r.stride;
+
+    // ---- logits -----------------------------------------------------------------
+    float l[VPT];
+    if (VPT % kPer16 == 0 && vec && e0 + VPT <= r.E) {
+#pragma unroll
+      for (int c = 0; c < VPT / kPer16; ++c) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
+        if constexpr (DT == MOE_FP32) {
+          l[4 * c] = __uint_as_float(v.x);
+          l[4 * c + 1] = __uint_as_float(v.y);
+          l[4 * c + 2] = __uint_as_float(v.z);
+          l[4 * c + 3] = __uint_as_float(v.w);
+        } else {
+          float f[8];
+          unpack8<DT>(v, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) l[8 * c + i] = f[i];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) l[i] = e0 + i < r.E ? load_logit<DT>(row + e0 + i) : 0.0f;
+    }
+    // anything infinite or NaN (0 times it is NaN) takes a second look: NaN is
+    // -inf and reported, +inf the largest finite number
+    float probe = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) probe = __fmaf_rn(l[i], 0.0f, probe);
+    if (__any_sync(kAll, probe != probe)) {
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        nan |= l[i] != l[i];
+        l[i] = l[i] != l[i] ? kNegInf : fminf(l[i], kMaxF);
+      }
+      if (nan) set_status(dev_status, MOE_ERR_INVALID_ARG);
+    }
+    if (VPT * 32 > r.E) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (e0 + i >= r.E) l[i] = kNegInf;
+    }
+
+    // ---- the softmax's maximum and sum, where a weight or a choice needs them -----
+    float m = 0.0f, sum = 1.0f;
+    if (want_sum) {
+      m = l[0];
+#pragma unroll
+      for (int i = 1; i < VPT; ++i) m = fmaxf(m, l[i]);
+      m = fmaxf(warp_max(m), -kMaxF);
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) sum = __fadd_rn(sum, exp_neg(__fsub_rn(l[i], m)));
+      sum = warp_sum(sum);
+      if (sum == 0.0f) sum = 1.0f;
+    }
+    const float inv_sum = want_sum ? __fdiv_rn(1.0f, sum) : 1.0f;
+    auto score = [&](float x) {
+      return r.score == MOE_SOFTMAX ? __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum)
+                                    : sigmoid_rank(x);
     };
-    float a1 = choice(k1), a2 = choice(k2);
-    for (int d = 1; d < lanes_per_group; d <<= 1) {
-      const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
-      a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
-      a1 = fmaxf(a1, b1);
-    }
-    const float gs = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
-    const int mine = lane / lanes_per_group;
-    int better = 0;
-    for (int g = 0; g < r.n_group; ++g) {
-      const float o = __shfl_sync(kAll, gs, g * lanes_per_group);
-      better += o > gs || (o == gs && g < mine);
-    }
-    if (better >= r.topk_group) {
-      k1 = k2 = 0;
-      taken = kAll;
-    }
-  }
 
-  // ---- the k best -----------------------------------------------------------------------
-  int sel[2] = {-1, -1};
-  int held = 2;                       // sorted keys left in this lane
-  for (int j = 0; j < r.k; ++j) {
-    if (VPT > 2 && __any_sync(kAll, held == 0)) {
-      if (held == 0) {
-        scan();
-        held = 2;
+    // ---- ranked values -------------------------------------------------------------
+    if (BIAS) {
+      auto rank = [&](auto&& f) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const float c = __fadd_rn(f(l[i]), bias[i]);
+          l[i] = l[i] > kNegInf ? c : kNegInf;
+        }
+      };
+      if (r.score == MOE_SOFTMAX)
+        rank([&](float x) { return __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum); });
+      else
+        rank([&](float x) { return sigmoid_rank(x); });
+      if (odd_bias) {                    // a NaN choice is no choice
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) l[i] = l[i] > kNegInf ? l[i] : kNegInf;
       }
     }
-    const uint32_t best = __reduce_max_sync(kAll, k1);
-    if (best == 0) break;
-    const int win = __ffs(__ballot_sync(kAll, k1 == best)) - 1;
-    const int e = __shfl_sync(kAll, i1, win) + win * VPT;
-    if (lane == (j & 31)) {
-      if (j < 32) sel[0] = e;
-      else sel[1] = e;
+    // the lane's two largest
+    float k1 = l[0], k2 = kNegInf;
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) {
+      k2 = fmaxf(k2, fminf(k1, l[i]));
+      k1 = fmaxf(k1, l[i]);
     }
-    if (lane == win) {
-      taken |= 1u << i1;
-      k1 = k2;
-      i1 = i2;
-      k2 = 0;
-      --held;
+
+    // ---- groups: a lane's experts are all of one group, lanes_per_group lanes each ----
+    if (grouped) {
+      float a1 = k1, a2 = k2;
+      if (!BIAS) {
+        a1 = a1 > kNegInf ? score(a1) : kNegInf;
+        a2 = a2 > kNegInf ? score(a2) : kNegInf;
+      }
+      for (int d = 1; d < lanes_per_group; d <<= 1) {
+        const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+        a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+        a1 = fmaxf(a1, b1);
+      }
+      float gs = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
+      bool keep = false;
+      const int mine = lane / lanes_per_group;
+      for (int i = 0; i < r.topk_group; ++i) {
+        const float best = warp_max(gs);
+        if (best == kNegInf) break;
+        const int win = __ffs(__ballot_sync(kAll, gs == best)) - 1;
+        if (win / lanes_per_group == mine) {
+          keep = true;
+          gs = kNegInf;
+        }
+      }
+      if (!keep) {
+        k1 = k2 = kNegInf;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) l[i] = kNegInf;
+      }
     }
+
+    // ---- the k largest ---------------------------------------------------------------
+    // slot1, slot2: the slots this lane won with its values v1 >= v2
+    float v1 = k1, v2 = k2;
+    int slot1 = -1, slot2 = -1, n = 0;
+    // writes down the lane's wins, and takes them out of its values
+    auto settle = [&]() {
+      int i1 = 0, i2 = 0;
+#pragma unroll
+      for (int i = VPT - 1; i >= 0; --i)
+        if (l[i] == v1) i1 = i;
+      if (__any_sync(kAll, slot2 >= 0)) {
+#pragma unroll
+        for (int i = VPT - 1; i >= 0; --i)
+          if (l[i] == v2 && i != i1) i2 = i;
+      }
+      if (slot1 >= 0) chosen[slot1] = e0 + i1;
+      if (slot2 >= 0) chosen[slot2] = e0 + i2;
+      return make_int2(i1, i2);
+    };
+    for (int j = 0; j < r.k; ++j) {
+      if (VPT > 2 && __any_sync(kAll, slot2 >= 0 && k1 == kNegInf)) {
+        const int2 at = settle();
+        if (slot2 >= 0 && k1 == kNegInf) {
+          k2 = kNegInf;
+#pragma unroll
+          for (int i = 0; i < VPT; ++i) {
+            if (i == at.x || i == at.y) l[i] = kNegInf;
+            k2 = fmaxf(k2, fminf(k1, l[i]));
+            k1 = fmaxf(k1, l[i]);
+          }
+          // with nothing left, a value that cannot be met again ends the search
+          if (k1 == kNegInf) k2 = kNegInf;
+          v1 = k1;
+          v2 = k2;
+          slot1 = slot2 = -1;
+        }
+      }
+      const float best = warp_max(k1);
+      if (best == kNegInf) break;
+      const int win = __ffs(__ballot_sync(kAll, k1 == best)) - 1;
+      if (lane == win) {
+        if (slot1 < 0) slot1 = j;
+        else slot2 = j;
+        k1 = k2;
+        k2 = kNegInf;
+      }
+      n = j + 1;
+    }
+    settle();
+    __syncwarp();
+    if (r.k <= 32) {
+      const int sel[1] = {lane < n ? chosen[lane] : -1};
+      write_token<DT, 1>(r, row, t, sel, m, sum, lane, idx, weights);
+    } else {
+      const int sel[2] = {lane < n ? chosen[lane] : -1, lane + 32 < n ? chosen[lane + 32] : -1};
+      write_token<DT, 2>(r, row, t, sel, m, sum, lane, idx, weights);
+    }
+    __syncwarp();
   }
-  write_token<DT>(r, row, t, sel, m, sum, lane, idx, weights);
 }
 
 // Any E up to MOE_EP_MAX_EXPERTS and any groups: one CTA per token (persistent
@@ -316,7 +381,7 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
       __syncthreads();
       for (int e = tid; e < r.E; e += kWideThreads) {
         const float l = logit(e);
-        sum = __fadd_rn(sum, l > kNegInf ? exp_rank(__fsub_rn(l, m)) : 0.0f);
+        sum = __fadd_rn(sum, exp_neg(__fsub_rn(l, m)));
       }
       sum = warp_sum(sum);
       if (lane == 0) s_red[warp] = sum;
@@ -327,7 +392,7 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
     const float inv_sum = __fdiv_rn(1.0f, sum);
     for (int e = tid; e < r.E; e += kWideThreads) {
       const float l = logit(e);
-      float c = r.score == MOE_SOFTMAX ? __fmul_rn(exp_rank(__fsub_rn(l, m)), inv_sum)
+      float c = r.score == MOE_SOFTMAX ? __fmul_rn(exp_neg(__fsub_rn(l, m)), inv_sum)
                                        : sigmoid_rank(l);
       if (r.bias) c = __fadd_rn(c, __ldg(r.bias + e));
       const bool on = l > kNegInf && c > kNegInf;
@@ -391,21 +456,35 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
     __syncthreads();
     if (warp == 0) {
       const int sel[2] = {lane < n ? s_sel[lane] : -1, lane + 32 < n ? s_sel[lane + 32] : -1};
-      write_token<DT>(r, row, t, sel, m, sum, lane, idx, weights);
+      write_token<DT, 2>(r, row, t, sel, m, sum, lane, idx, weights);
     }
     __syncthreads();
   }
 }
 
-template <int DT, int VPT>
-cudaError_t launch_warp(const RouteArgs& r, int lanes_per_group, int32_t* idx, float* weights,
+template <int DT, int VPT, bool BIAS>
+cudaError_t launch_bias(const RouteArgs& r, int lanes_per_group, int32_t* idx, float* weights,
                         int32_t* dev_status, cudaStream_t st) {
   const size_t el = DT == MOE_FP32 ? 4 : 2;
   const bool vec = reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 && r.stride * el % 16 == 0;
-  const int64_t grid = (r.T + kWarps - 1) / kWarps;
-  route_warp_kernel<DT, VPT><<<static_cast<unsigned>(grid), kWarps * 32, 0, st>>>(
-      r, vec, lanes_per_group, idx, weights, dev_status);
+  auto kernel = route_warp_kernel<DT, VPT, BIAS>;
+  int dev = 0, sms = 0, per_sm = 0;
+  cudaError_t e = current_device_sms(&dev, &sms);
+  if (e == cudaSuccess)
+    e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), kWarps * 32, 0, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int64_t grid =
+      std::min<int64_t>((r.T + kWarps - 1) / kWarps, int64_t(std::max(1, per_sm)) * sms);
+  kernel<<<static_cast<unsigned>(grid), kWarps * 32, 0, st>>>(r, vec, lanes_per_group, idx,
+                                                              weights, dev_status);
   return cudaGetLastError();
+}
+
+template <int DT, int VPT>
+cudaError_t launch_warp(const RouteArgs& r, int lanes_per_group, int32_t* idx, float* weights,
+                        int32_t* dev_status, cudaStream_t st) {
+  return r.bias ? launch_bias<DT, VPT, true>(r, lanes_per_group, idx, weights, dev_status, st)
+                : launch_bias<DT, VPT, false>(r, lanes_per_group, idx, weights, dev_status, st);
 }
 
 // The warp kernel's experts per lane: the smallest of its sizes that holds E
