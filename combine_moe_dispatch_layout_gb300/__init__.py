@@ -152,11 +152,12 @@ def layout_workspace_bytes(shape):
 
 
 def _ptr(t, dtype=None, numel=None, name="tensor"):
+    """Device address of a contiguous CUDA tensor (None: NULL)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if dtype is not None and t.dtype not in (
+    if dtype is not None and t.dtype is not dtype and t.dtype not in (
             dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
@@ -164,13 +165,20 @@ def _ptr(t, dtype=None, numel=None, name="tensor"):
     if numel is not None and t.numel() < numel:
         raise ValueError("%s holds %d elements, needs %d" % (name, t.numel(),
                                                              numel))
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+# torch's raw handle of the current stream, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and _device is not None:
+        return _raw_stream(_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(status, what):
@@ -374,7 +382,7 @@ def _strided(src, rows, name):
     nbytes = t.numel() * t.element_size()
     if off < 0 or stride < 4 or (rows > 0 and off + (rows - 1) * stride + 4 > nbytes):
         raise ValueError("%s: rows reach past the tensor" % name)
-    return ctypes.c_void_p(t.data_ptr() + int(off)), int(stride)
+    return t.data_ptr() + int(off), int(stride)
 
 
 def gmm_block_n():
@@ -611,7 +619,7 @@ def _rows(t, name, dtypes):
     stride = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
     if stride < t.shape[1]:
         raise ValueError("%s: rows overlap" % name)
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return t.data_ptr(), stride
 
 
 _LOGITS = (torch.float32, torch.bfloat16, torch.float16)

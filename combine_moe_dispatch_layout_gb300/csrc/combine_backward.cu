@@ -9,11 +9,17 @@
 //
 // A persistent grid walks the tokens.  The last warp resolves the next
 // token's rows and weights into the other half of a double-buffered table
-// while the compute warps work on this one; each compute thread owns 16-byte
-// chunks of the hidden dimension, issues the loads of up to kBatch rows
+// while the compute warps work on this one; each compute thread owns two
+// 16-byte chunks of the hidden dimension, issues the loads of kBatch rows
 // before using them, writes the gradient rows and adds up its part of the k
 // dot products.  Dot products go over a warp by shuffles and over the CTA
 // through shared memory, warps in ascending order: a fixed order.
+//
+// Measured (32,768 tokens, k = 8, H = 7168, bf16: 8.0 GB): 1277 us, 6.26 TB/s,
+// 92% of a copy's rate.  Batches of 8 rows leave one CTA per SM: 1489 us; four
+// chunks per thread: 1600; the next token's rows prefetched into L2 (which helps
+// the combine, where nothing is written): 1536; write-back instead of streaming
+// stores: 1283.
 #include <algorithm>
 
 #include "moe_ep_internal.cuh"
@@ -34,8 +40,7 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
                         const int32_t* __restrict__ put_offset,
                         const int64_t* __restrict__ rank_recv_base, int R, int bs, int k,
                         int epr, int H, int64_t T, uint4* __restrict__ d_y,
-                        float* __restrict__ d_weights, int32_t* dev_status,
-                        bool prefetch_next) {
+                        float* __restrict__ d_weights, int32_t* dev_status) {
   __shared__ int64_t s_rows[2][MOE_EP_MAX_TOPK];
   __shared__ float s_w[2][MOE_EP_MAX_TOPK];
   __shared__ float s_dot[2][kMaxThreads / 32][MOE_EP_MAX_TOPK];
@@ -54,14 +59,9 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
     const int buf = it & 1;
     if (producer) {
       const int64_t gn = g + gridDim.x;
-      if (gn < T) {
+      if (gn < T)
         resolve_token(gn, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k,
                       epr, y_rows, s_rows[buf ^ 1], s_w[buf ^ 1], dev_status, lane);
-        for (int kk = lane; prefetch_next && kk < k; kk += 32) {
-          const int64_t row = s_rows[buf ^ 1][kk];
-          if (row >= 0) bulk_prefetch_l2(y + row * nch, static_cast<uint32_t>(nch) * 16u);
-        }
-      }
     } else {
       for (int k0 = 0; k0 < k; k0 += kBatch) {
         float dot[kBatch];
@@ -88,7 +88,7 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
                 dot[b] = __fmaf_rn(d[j], f[j], dot[b]);
                 o[j] = __fmul_rn(w, d[j]);
               }
-              d_y[row * nch + c] = pack8<DT>(o);
+              __stcs(d_y + row * nch + c, pack8<DT>(o));   // written once, read by a later kernel
             }
           }
         }
@@ -111,10 +111,6 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
   }
 }
 
-// Rows at least this wide: the next token's rows are brought into L2 while this
-// one's are used.
-constexpr int64_t kPrefetchRowBytes = 12 * 1024;
-
 template <int DT>
 cudaError_t launch_t(const Shape& s, const void* d_out, const void* y, int64_t y_rows,
                      const int32_t* topk_idx, const float* weights, const int32_t* send_idx,
@@ -134,7 +130,7 @@ cudaError_t launch_t(const Shape& s, const void* d_out, const void* y, int64_t y
   kernel<<<static_cast<unsigned>(grid), threads, 0, st>>>(
       static_cast<const uint4*>(d_out), static_cast<const uint4*>(y), y_rows, topk_idx,
       weights, send_idx, put_offset, rank_recv_base, s.R, s.bs, s.k, s.epr, s.H, s.T(),
-      static_cast<uint4*>(d_y), d_weights, dev_status, int64_t(s.H) * 2 >= kPrefetchRowBytes);
+      static_cast<uint4*>(d_y), d_weights, dev_status);
   return cudaGetLastError();
 }
 

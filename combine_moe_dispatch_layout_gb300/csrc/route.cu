@@ -13,11 +13,13 @@
 // experts, so the lowest lane and the lowest position inside it are the lowest
 // id.  The cost is instructions (one SM does about 7 tokens of 256 experts in
 // the time their logits take to arrive), so the k rounds are kept short: a lane
-// keeps only its two largest values (three instructions per expert), a round is
-// one warp maximum, one ballot and a pop in the winning lane, and positions are
-// looked up once at the end, in the lanes that won.  A lane that wins twice
-// looks through its values again (rare: winners spread over the lanes).
+// keeps only its three largest values (five instructions per expert) and their
+// order-preserving integer keys, a round is one integer warp maximum, one ballot
+// and a pop in the winning lane, and positions are looked up once at the end, in
+// the lanes that won.  A lane that wins three times looks through its values
+// again (rare: winners spread over the lanes; with two values kept it was not).
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_ep_internal.cuh"
 
@@ -82,10 +84,11 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int d = 16; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d));
   return v;
 }
+// The maximum over the warp, by the integer reduction (one instruction; the
+// floating one is slower).
 __device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
+  const uint32_t k = __reduce_max_sync(kAll, order_key(v));
+  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
 // Ids and weights of slots h * 32 + lane of a token from the chosen experts
@@ -185,7 +188,8 @@ route_warp_kernel(const RouteArgs r, bool vec, int lanes_per_group,
     float probe = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) probe = __fmaf_rn(l[i], 0.0f, probe);
-    if (__any_sync(kAll, probe != probe)) {
+    const bool odd = __any_sync(kAll, probe != probe);
+    if (odd) {
       bool nan = false;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -221,33 +225,43 @@ route_warp_kernel(const RouteArgs r, bool vec, int lanes_per_group,
 
     // ---- ranked values -------------------------------------------------------------
     if (BIAS) {
-      auto rank = [&](auto&& f) {
+      // every: every value is an expert's finite logit, the usual case
+      auto rank = [&](auto every, auto&& f) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const float c = __fadd_rn(f(l[i]), bias[i]);
-          l[i] = l[i] > kNegInf ? c : kNegInf;
+          l[i] = decltype(every)::value || l[i] > kNegInf ? c : kNegInf;
         }
       };
-      if (r.score == MOE_SOFTMAX)
-        rank([&](float x) { return __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum); });
-      else
-        rank([&](float x) { return sigmoid_rank(x); });
+      auto soft = [&](float x) { return __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum); };
+      const std::true_type yes;
+      const std::false_type no;
+      if (r.score == MOE_SOFTMAX) rank(no, soft);
+      else if (odd || VPT * 32 > r.E) rank(no, sigmoid_rank);
+      else rank(yes, sigmoid_rank);
       if (odd_bias) {                    // a NaN choice is no choice
 #pragma unroll
         for (int i = 0; i < VPT; ++i) l[i] = l[i] > kNegInf ? l[i] : kNegInf;
       }
     }
-    // the lane's two largest
-    float k1 = l[0], k2 = kNegInf;
+    // the lane's three largest
+    float v1, v2, v3;
+    auto scan = [&]() {
+      v1 = l[0];
+      v2 = v3 = kNegInf;
 #pragma unroll
-    for (int i = 1; i < VPT; ++i) {
-      k2 = fmaxf(k2, fminf(k1, l[i]));
-      k1 = fmaxf(k1, l[i]);
-    }
+      for (int i = 1; i < VPT; ++i) {
+        const float a = fminf(v1, l[i]), b = fminf(v2, a);
+        v1 = fmaxf(v1, l[i]);
+        v2 = fmaxf(v2, a);
+        v3 = fmaxf(v3, b);
+      }
+    };
+    scan();
 
     // ---- groups: a lane's experts are all of one group, lanes_per_group lanes each ----
     if (grouped) {
-      float a1 = k1, a2 = k2;
+      float a1 = v1, a2 = v2;
       if (!BIAS) {
         a1 = a1 > kNegInf ? score(a1) : kNegInf;
         a2 = a2 > kNegInf ? score(a2) : kNegInf;
@@ -257,72 +271,79 @@ route_warp_kernel(const RouteArgs r, bool vec, int lanes_per_group,
         a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
         a1 = fmaxf(a1, b1);
       }
-      float gs = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
+      const float gs = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
+      uint32_t key = gs > kNegInf ? order_key(gs) : 0u;
+      const int head = lane & -lanes_per_group;        // the group's first lane
       bool keep = false;
-      const int mine = lane / lanes_per_group;
       for (int i = 0; i < r.topk_group; ++i) {
-        const float best = warp_max(gs);
-        if (best == kNegInf) break;
-        const int win = __ffs(__ballot_sync(kAll, gs == best)) - 1;
-        if (win / lanes_per_group == mine) {
+        const uint32_t best = __reduce_max_sync(kAll, key);
+        if (best == 0) break;
+        if (__ffs(__ballot_sync(kAll, key == best)) - 1 == head) {
           keep = true;
-          gs = kNegInf;
+          key = 0u;
         }
       }
-      if (!keep) {
-        k1 = k2 = kNegInf;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) l[i] = kNegInf;
-      }
+      if (!keep) v1 = v2 = v3 = kNegInf;
     }
 
     // ---- the k largest ---------------------------------------------------------------
-    // slot1, slot2: the slots this lane won with its values v1 >= v2
-    float v1 = k1, v2 = k2;
-    int slot1 = -1, slot2 = -1, n = 0;
-    // writes down the lane's wins, and takes them out of its values
+    // keys of the values still to win; kAgain: the lane must look for more
+    constexpr uint32_t kAgain = 0xffffffffu;
+    uint32_t q1, q2, q3, wins = 0;       // wins: slot + 1 of the lane's 1st, 2nd, 3rd value
+    int won = 0;                         // 8 * wins so far
+    auto keys = [&]() {
+      q1 = v1 > kNegInf ? order_key(v1) : 0u;
+      q2 = v2 > kNegInf ? order_key(v2) : 0u;
+      q3 = v3 > kNegInf ? order_key(v3) : 0u;
+    };
+    keys();
+    // writes down the lane's wins; the positions of v1, v2, v3 where they won
     auto settle = [&]() {
-      int i1 = 0, i2 = 0;
+      int i1 = -1, i2 = -1, i3 = -1;
 #pragma unroll
       for (int i = VPT - 1; i >= 0; --i)
         if (l[i] == v1) i1 = i;
-      if (__any_sync(kAll, slot2 >= 0)) {
+      if (__any_sync(kAll, won > 8)) {
 #pragma unroll
         for (int i = VPT - 1; i >= 0; --i)
           if (l[i] == v2 && i != i1) i2 = i;
-      }
-      if (slot1 >= 0) chosen[slot1] = e0 + i1;
-      if (slot2 >= 0) chosen[slot2] = e0 + i2;
-      return make_int2(i1, i2);
-    };
-    for (int j = 0; j < r.k; ++j) {
-      if (VPT > 2 && __any_sync(kAll, slot2 >= 0 && k1 == kNegInf)) {
-        const int2 at = settle();
-        if (slot2 >= 0 && k1 == kNegInf) {
-          k2 = kNegInf;
+        if (__any_sync(kAll, won > 16)) {
 #pragma unroll
-          for (int i = 0; i < VPT; ++i) {
-            if (i == at.x || i == at.y) l[i] = kNegInf;
-            k2 = fmaxf(k2, fminf(k1, l[i]));
-            k1 = fmaxf(k1, l[i]);
-          }
-          // with nothing left, a value that cannot be met again ends the search
-          if (k1 == kNegInf) k2 = kNegInf;
-          v1 = k1;
-          v2 = k2;
-          slot1 = slot2 = -1;
+          for (int i = VPT - 1; i >= 0; --i)
+            if (l[i] == v3 && i != i1 && i != i2) i3 = i;
         }
       }
-      const float best = warp_max(k1);
-      if (best == kNegInf) break;
-      const int win = __ffs(__ballot_sync(kAll, k1 == best)) - 1;
-      if (lane == win) {
-        if (slot1 < 0) slot1 = j;
-        else slot2 = j;
-        k1 = k2;
-        k2 = kNegInf;
+      if (won > 0) chosen[(wins & 255u) - 1] = e0 + i1;
+      if (won > 8) chosen[((wins >> 8) & 255u) - 1] = e0 + i2;
+      if (won > 16) chosen[((wins >> 16) & 255u) - 1] = e0 + i3;
+      return make_int3(i1, i2, i3);
+    };
+    int n = 0;
+    while (n < r.k) {
+      const uint32_t best = __reduce_max_sync(kAll, q1);
+      if (best - 1u >= kAgain - 1u) {    // rare: nothing left, or a lane must look again
+        if (best == 0) break;
+        const int3 at = settle();
+        if (q1 == kAgain) {
+#pragma unroll
+          for (int i = 0; i < VPT; ++i)
+            if (i == at.x || i == at.y || i == at.z) l[i] = kNegInf;
+          scan();
+          keys();
+          wins = 0;
+          won = 0;
+        }
+        continue;
       }
-      n = j + 1;
+      const int win = __ffs(__ballot_sync(kAll, q1 == best)) - 1;
+      ++n;
+      if (lane == win) {
+        wins |= static_cast<uint32_t>(n) << won;
+        won += 8;
+        q1 = q2;
+        q2 = q3;
+        q3 = VPT > 3 ? kAgain : 0u;
+      }
     }
     settle();
     __syncwarp();
