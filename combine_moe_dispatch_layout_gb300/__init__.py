@@ -699,7 +699,8 @@ def moe_linear_i8(a, w, K, group_rows, col_scale, row_scale, bias, c, dev_status
                   stream=None):
     """c [rows, N] (bf16, fp16, fp32, or int32 for the accumulators) = int8
     rows a [rows, stride] x int8 weights w [G, N, stride]^T over K codes, times
-    col_scale [G, N] and the row's scale, plus bias [G, N].  a may hold row
+    col_scale [G, N] and the row's scale, plus bias [G, N] (int32 reads none of
+    the three).  a may hold row
     images (uint8) as dispatch writes them; row_scale is (tensor, byte_offset,
     byte_stride); group_rows int32 [G] (None with G = 1: every row)."""
     i8 = (torch.int8, torch.uint8)

@@ -572,20 +572,20 @@ moe_status moe_linear_i8(const void* a, int64_t a_rows, int64_t a_stride, const 
       a_stride % 16 != 0 || w_stride < K || w_stride % 16 != 0 || a_stride >= kMaxStride ||
       w_stride >= kMaxStride || c_dtype < MOE_BF16 || c_dtype > MOE_INT32 || !dev_status)
     return MOE_ERR_INVALID_ARG;
-  const bool scaled = c_dtype != MOE_INT32;
-  if (scaled ? row_scale_stride < 4 || row_scale_stride % 4 != 0 || row_scale_stride >= kMaxStride
-             : bias != nullptr)
+  const bool scaled = c_dtype != MOE_INT32;      // int32 outputs read no scale, no bias
+  if (scaled && (row_scale_stride < 4 || row_scale_stride % 4 != 0 ||
+                 row_scale_stride >= kMaxStride))
     return MOE_ERR_INVALID_ARG;
   if (a_rows == 0) return MOE_OK;
   if (!a || !w || !c || (!group_rows && G != 1) || (scaled && (!col_scale || !row_scale)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(c, 16) || !aligned(group_rows, 4) ||
-      !aligned(bias, 4) || !aligned(dev_status, 4) ||
-      (scaled && (!aligned(col_scale, 4) || !aligned(row_scale, 4))))
+      !aligned(dev_status, 4) ||
+      (scaled && (!aligned(col_scale, 4) || !aligned(row_scale, 4) || !aligned(bias, 4))))
     return MOE_ERR_INVALID_ARG;
   const moe_ep::LinearArgs p{a, a_rows, a_stride, w, w_stride, G, N, K, group_rows, col_scale,
                              static_cast<const unsigned char*>(row_scale), row_scale_stride,
-                             bias, c, c_dtype};
+                             scaled ? bias : nullptr, c, c_dtype};
   return from_cuda(moe_ep::launch_linear_i8(p, dev_status, static_cast<cudaStream_t>(stream)));
 }
 

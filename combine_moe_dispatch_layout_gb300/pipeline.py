@@ -6,16 +6,22 @@ output and scratch buffer the four stages need for one shape, and
 one stream.  The receive buffer is sized for the worst case, T*k rows, which
 is also the exact row count when every expert id is valid, so no host
 synchronisation is needed between the stages.
+
+Around them: ``Routing`` / ``run_route`` (logits -> ids and weights), the
+gradients of a verbatim pipeline (``run_combine_backward``,
+``run_dispatch_backward``, ``run_route_backward``), and ``run_serve_moe``, an
+MoE layer from logits to output on 8-bit weights and activations.
 """
 import torch
 
 from . import (fused_workspace_bytes, make_shape, layout_workspace_bytes,
-               moe_codes_to_bf16, moe_combine, moe_combine_f32, moe_combine_quant,
-               moe_dispatch, moe_dispatch_expand, moe_dispatch_fused,
+               moe_codes_to_bf16, moe_combine, moe_combine_backward, moe_combine_f32,
+               moe_combine_quant, moe_dispatch, moe_dispatch_expand, moe_dispatch_fused,
                moe_dispatch_layout, moe_group_offsets, moe_grouped_gemm_i8,
                moe_grouped_gemm_i8_dequant, moe_grouped_gemm_i8_swiglu,
-               moe_interleave_gate_up, moe_notify_dispatch, moe_quant_rows_bf16,
-               moe_swiglu_quant_grouped_bf16, recv_row_bytes)
+               moe_interleave_gate_up, moe_linear_i8, moe_notify_dispatch,
+               moe_quant_rows_bf16, moe_route, moe_route_backward,
+               moe_swiglu_quant_grouped, moe_swiglu_quant_grouped_bf16, recv_row_bytes)
 
 
 class PipelineBuffers:
@@ -194,3 +200,98 @@ def run_deep_moe(b, wts, x, topk_idx, topk_weights, stream=None):
     run_dispatch_expand(b, x, topk_idx, stream)
     run_deep_moe_experts(b, wts, stream)
     run_deep_combine(b, topk_idx, topk_weights, stream)
+
+
+# ---- routing, and the gradients of a verbatim pipeline --------------------------
+
+class Routing:
+    """How logits become expert ids and gate weights (the arguments of
+    ``moe_route``), with the outputs for T tokens."""
+
+    def __init__(self, T, E, k, score="softmax", bias=None, n_group=1, topk_group=1,
+                 group_top=1, renormalise=True, scale=1.0, device="cuda"):
+        self.E, self.k, self.score, self.bias = E, k, score, bias
+        self.n_group, self.topk_group, self.group_top = n_group, topk_group, group_top
+        self.renormalise, self.scale = renormalise, scale
+        self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty((T, k), dtype=torch.float32, device=device)
+
+
+def run_route(b, routing, logits, stream=None):
+    """logits [T, E] -> routing.topk_idx, routing.topk_weights."""
+    moe_route(logits, routing.bias, routing.score, routing.k, routing.topk_idx,
+              routing.topk_weights, b.dev_status, n_group=routing.n_group,
+              topk_group=routing.topk_group, group_top=routing.group_top,
+              renormalise=routing.renormalise, scale=routing.scale, stream=stream)
+
+
+def run_route_backward(b, routing, logits, d_weights, d_logits, stream=None):
+    """Gradient of the gate weights -> gradient of the logits."""
+    moe_route_backward(logits, routing.topk_idx, d_weights, routing.score, d_logits,
+                       b.dev_status, renormalise=routing.renormalise, scale=routing.scale,
+                       stream=stream)
+
+
+def run_combine_backward(b, d_out, y, topk_idx, topk_weights, d_y, d_weights, stream=None):
+    """Gradient of the combined tokens -> gradients of the experts' rows and of
+    the gate weights."""
+    moe_combine_backward(b.shape, d_out, y, topk_idx, topk_weights, b.send_idx, b.put_offset,
+                         b.rank_recv_base, d_y, d_weights, b.dev_status, stream)
+
+
+def run_dispatch_backward(b, d_recv, topk_idx, ones, d_x, stream=None):
+    """Gradient of a verbatim dispatch: a token's gradient is the sum of its k
+    rows' (the combine with weights of 1; ``ones`` fp32 [T, k])."""
+    moe_combine(b.shape, d_recv, d_recv.shape[0], topk_idx, ones, b.send_idx, b.put_offset,
+                b.rank_recv_base, d_x, b.dev_status, stream)
+
+
+# ---- an MoE layer on 8-bit weights: logits and tokens to output --------------------
+
+class Int8MoeWeights:
+    """Expert weights as they are stored: w1 int8 [E, 2I, H] (gate rows, then up
+    rows), w2 int8 [E, H, I] and fp32 scales per output channel, ws1 [E, 2I] and
+    ws2 [E, H].  Nothing is expanded: one byte per weight."""
+
+    def __init__(self, w1, ws1, w2, ws2):
+        E, N1, H = w1.shape
+        I = N1 // 2
+        if w2.shape != (E, H, I) or H % 16 or I % 16:
+            raise ValueError("w1 must be [E, 2I, H] and w2 [E, H, I], H and I multiples of 16")
+        self.E, self.H, self.I = E, H, I
+        self.w1, self.w2 = w1.contiguous(), w2.contiguous()
+        self.ws1, self.ws2 = ws1.contiguous(), ws2.contiguous()
+
+
+class ServeBuffers(PipelineBuffers):
+    """PipelineBuffers (INT8 dispatch) plus what the layer keeps between its
+    stages: expert row offsets, the gate/up accumulators, the SwiGLU's INT8 row
+    images and the dequantised expert outputs."""
+
+    def __init__(self, R, bs, k, epr, H, I, dtype, device="cuda"):
+        super().__init__(R, bs, k, epr, H, dtype, True, device)
+        P = R * bs * k
+        self.I = I
+        self.group_off = torch.empty((R * epr + 1,), dtype=torch.int64, device=device)
+        self.acc1 = torch.empty((P, 2 * I), dtype=torch.int32, device=device)
+        self.x2 = torch.empty((P, _align32(I) + 32), dtype=torch.uint8, device=device)
+        self.y2 = torch.empty((P, H), dtype=torch.float32, device=device)
+
+
+def run_serve_moe(b, wts, routing, x, logits, stream=None):
+    """Route, dispatch with INT8 quantisation (one launch), gate/up product, SwiGLU
+    with requantisation, down product, weighted sum; the result is ``b.out``.
+    The same arithmetic, bit for bit, as ``run_deep_moe`` on the same ids, from
+    weights of half the bytes."""
+    H, I = b.shape.H, b.I
+    run_route(b, routing, logits, stream)
+    run_dispatch_fused(b, x, routing.topk_idx, stream)
+    moe_group_offsets(b.recv_per_expert, b.group_off, b.dev_status, stream)
+    row1 = (b.recv, _align32(H), b.row_bytes)
+    moe_linear_i8(b.recv, wts.w1, H, b.recv_per_expert, None, None, None, b.acc1,
+                  b.dev_status, stream)
+    moe_swiglu_quant_grouped(b.acc1, wts.ws1, b.group_off, row1, b.x2, b.dev_status, stream)
+    moe_linear_i8(b.x2, wts.w2, I, b.recv_per_expert, wts.ws2,
+                  (b.x2, _align32(I), b.x2.shape[1]), None, b.y2, b.dev_status, stream)
+    moe_combine_f32(b.shape, b.y2, routing.topk_idx, routing.topk_weights, b.send_idx,
+                    b.put_offset, b.rank_recv_base, b.out, b.dev_status, stream)

@@ -572,8 +572,8 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* d_out,
  *   acc[m][n] = sum_{j<K} a[m][j] * w[g][n][j]                 (exact int32)
  *   c[m][n]   = fp32(acc) * col_scale[g][n] * row_scale(m) (+ bias[g][n])
  * each product and the sum rounded to nearest even in fp32, then c rounded to
- * c_dtype; c_dtype MOE_INT32 stores acc itself and reads no scale (what
- * moe_swiglu_quant_grouped takes).  Both operands stay 8-bit in memory, so a
+ * c_dtype; c_dtype MOE_INT32 stores acc itself and reads no scale and no bias
+ * (what moe_swiglu_quant_grouped takes).  Both operands stay 8-bit in memory, so a
  * few rows cost one pass over the weights' bytes; group 0 alone with
  * group_rows NULL is a plain product (a shared expert, a projection).
  *   a           int8 [a_rows], rows a_stride bytes apart: packed codes, or the
@@ -584,7 +584,7 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* d_out,
  *   col_scale   fp32 [G][N] (not read with MOE_INT32)
  *   row_scale   row m's fp32 at byte m * row_scale_stride (not read with
  *               MOE_INT32)
- *   bias        fp32 [G][N] or NULL (NULL with MOE_INT32)
+ *   bias        fp32 [G][N] or NULL (not read with MOE_INT32)
  *   c           [a_rows][N] in c_dtype (MOE_BF16, MOE_FP16, MOE_FP32 or
  *               MOE_INT32); rows past the groups' total are not written
  * a, w and c are 16-byte aligned; a_stride and w_stride are multiples of 16 and
