@@ -22,50 +22,11 @@
 #include <type_traits>
 
 #include "moe_ep_internal.cuh"
+#include "route_math.cuh"
 
 namespace moe_ep {
 namespace {
 
-constexpr unsigned kAll = 0xffffffffu;
-constexpr float kMaxF = 3.402823466e38f;
-constexpr float kNegInf = -__builtin_huge_valf();
-
-template <int DT>
-struct Elem { using T = uint16_t; };
-template <>
-struct Elem<MOE_FP32> { using T = float; };
-
-template <int DT>
-__device__ __forceinline__ float load_logit(const typename Elem<DT>::T* p) {
-  if constexpr (DT == MOE_FP32) return __ldg(p);
-  else return widen<DT>(__ldg(p));
-}
-
-// Order-preserving key of a float; -0 reads as +0.  Keys of numbers above
-// -inf are never 0.
-__device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f));
-  return b ^ ((b & 0x80000000u) ? 0xffffffffu : 0x80000000u);
-}
-
-constexpr float kLog2e = 1.44269502f;      // log2(e), and what that leaves out
-constexpr float kLog2eLo = 1.92596299e-8f;
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-  return e;
-}
-// e^x for x <= 0 to about 2 ulp (0 below -120): x log2(e) in two parts, the
-// second one (with |part| < 2^-16) to first order.  Sums of scores.
-__device__ __forceinline__ float exp_neg(float x) {
-  constexpr float kLn2 = 0.693147181f;
-  x = fmaxf(x, -120.0f);
-  const float t = __fmul_rn(x, kLog2e);
-  const float r = __fmaf_rn(x, kLog2eLo, __fmaf_rn(x, kLog2e, -t));
-  const float e = exp2_approx(t);
-  return __fmaf_rn(e, __fmul_rn(r, kLn2), e);
-}
 // The sigmoid that ranks: the rounded product in the exponent costs s(1-s)|x|
 // 2^-24 <= 2^-26, less than the rounding of s itself; 0 and 1 at the infinities.
 __device__ __forceinline__ float sigmoid_rank(float x) {
@@ -77,18 +38,6 @@ __device__ __forceinline__ float sigmoid_rank(float x) {
 // The score in full precision (the weights).
 __device__ __forceinline__ float sigmoid_full(float x) {
   return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d));
-  return v;
-}
-// The maximum over the warp, by the integer reduction (one instruction; the
-// floating one is slower).
-__device__ __forceinline__ float warp_max(float v) {
-  const uint32_t k = __reduce_max_sync(kAll, order_key(v));
-  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
 // Ids and weights of slots h * 32 + lane of a token from the chosen experts
@@ -128,14 +77,21 @@ __device__ __forceinline__ void write_token(const RouteArgs& r,
   }
 }
 
-constexpr int kWarps = 4;   // tokens per CTA of the warp kernel at a time
+constexpr int kWarps = 4;   // tokens per CTA of the warp kernel
 
-// vec: row starts and the lanes' chunks are 16-byte aligned.  A persistent grid;
-// the bias stays in registers.
+// CTAs that an SM should hold: as many as leave the registers for a lane's logits,
+// its biases and about 32 more.  Occupancy hides the latency of the k rounds, each
+// a chain of reduction, ballot and pop.
+constexpr int warp_ctas(int vpt, bool bias) {
+  const int ctas = 512 / ((bias ? vpt * 9 / 4 : vpt) + 32);
+  return ctas < 12 ? ctas : 12;
+}
+
+// vec, vec_bias: rows, and the bias, start at 16-byte boundaries.
 template <int DT, int VPT, bool BIAS>
-__global__ void __launch_bounds__(kWarps * 32)
-route_warp_kernel(const RouteArgs r, bool vec, int lanes_per_group,
-                  int32_t* __restrict__ idx, float* __restrict__ weights,
+__global__ void __launch_bounds__(kWarps * 32, warp_ctas(VPT, BIAS))
+route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_group,
+                  int32_t* __restrict__ idx, float* __restrict__ weights, float nz,
                   int32_t* dev_status) {
   using T = typename Elem<DT>::T;
   constexpr int kPer16 = 16 / sizeof(T);
@@ -146,215 +102,214 @@ route_warp_kernel(const RouteArgs r, bool vec, int lanes_per_group,
   const bool grouped = r.topk_group < r.n_group;
   const bool want_sum = r.score == MOE_SOFTMAX && (!r.renormalise || BIAS || grouped);
 
+  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= r.T) return;
+  const T* row = static_cast<const T*>(r.logits) + t * r.stride;
+
+  // ---- logits -----------------------------------------------------------------
+  float l[VPT];
+  if (VPT % kPer16 == 0 && vec && e0 + VPT <= r.E) {
+#pragma unroll
+    for (int c = 0; c < VPT / kPer16; ++c) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
+      unpack_logits<DT>(v, l + c * kPer16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) l[i] = e0 + i < r.E ? load_logit<DT>(row + e0 + i) : 0.0f;
+  }
   float bias[BIAS ? VPT : 1];
   bool odd_bias = false;                // an infinite or NaN bias
   if (BIAS) {
+    if (VPT % 4 == 0 && vec_bias && e0 + VPT <= r.E) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      bias[i] = e0 + i < r.E ? __ldg(r.bias + e0 + i) : 0.0f;
-      odd_bias |= !(fabsf(bias[i]) <= kMaxF);
-    }
-    odd_bias = __any_sync(kAll, odd_bias);
-  }
-
-  for (int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < r.T;
-       t += int64_t(gridDim.x) * kWarps) {
-    const T* row = static_cast<const T*>(r.logits) + t * r.stride;
-
-    // ---- logits -----------------------------------------------------------------
-    float l[VPT];
-    if (VPT % kPer16 == 0 && vec && e0 + VPT <= r.E) {
-#pragma unroll
-      for (int c = 0; c < VPT / kPer16; ++c) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
-        if constexpr (DT == MOE_FP32) {
-          l[4 * c] = __uint_as_float(v.x);
-          l[4 * c + 1] = __uint_as_float(v.y);
-          l[4 * c + 2] = __uint_as_float(v.z);
-          l[4 * c + 3] = __uint_as_float(v.w);
-        } else {
-          float f[8];
-          unpack8<DT>(v, f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) l[8 * c + i] = f[i];
-        }
+      for (int c = 0; c < VPT / 4; ++c) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(r.bias + e0) + c);
+        bias[4 * c] = v.x;
+        bias[4 * c + 1] = v.y;
+        bias[4 * c + 2] = v.z;
+        bias[4 * c + 3] = v.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) l[i] = e0 + i < r.E ? load_logit<DT>(row + e0 + i) : 0.0f;
+      for (int i = 0; i < VPT; ++i) bias[i] = e0 + i < r.E ? __ldg(r.bias + e0 + i) : 0.0f;
     }
-    // anything infinite or NaN (0 times it is NaN) takes a second look: NaN is
-    // -inf and reported, +inf the largest finite number
     float probe = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) probe = __fmaf_rn(l[i], 0.0f, probe);
-    const bool odd = __any_sync(kAll, probe != probe);
-    if (odd) {
-      bool nan = false;
+    for (int i = 0; i < VPT; ++i) probe = __fmaf_rn(bias[i], 0.0f, probe);
+    odd_bias = __any_sync(kAll, probe != probe);
+  }
+  // anything infinite or NaN (0 times it is NaN) takes a second look: NaN is
+  // -inf and reported, +inf the largest finite number
+  float probe = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) probe = __fmaf_rn(l[i], 0.0f, probe);
+  const bool odd = __any_sync(kAll, probe != probe);
+  if (odd) {
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      nan |= l[i] != l[i];
+      l[i] = l[i] != l[i] ? kNegInf : fminf(l[i], kMaxF);
+    }
+    if (nan) set_status(dev_status, MOE_ERR_INVALID_ARG);
+  }
+  if (VPT * 32 > r.E) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (e0 + i >= r.E) l[i] = kNegInf;
+  }
+
+  // ---- the softmax's maximum and sum, where a weight or a choice needs them -----
+  float m = 0.0f, sum = 1.0f;
+  if (want_sum) {
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) m = fmaxf(m, l[i]);
+    m = fmaxf(warp_max(m), -kMaxF);
+    float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < VPT; i += 2)
+      part = add2_rn(part, exp_neg2(add2_rn(make_float2(l[i], l[i + 1]), bcast2(-m)), nz));
+    sum = warp_sum(__fadd_rn(part.x, part.y));
+    if (sum == 0.0f) sum = 1.0f;
+  }
+  const float inv_sum = want_sum ? __fdiv_rn(1.0f, sum) : 1.0f;
+  auto score = [&](float x) {
+    return r.score == MOE_SOFTMAX ? __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum)
+                                  : sigmoid_rank(x);
+  };
+
+  // ---- ranked values -------------------------------------------------------------
+  if (BIAS) {
+    // every: every value is an expert's finite logit, the usual case
+    auto rank = [&](auto every, auto&& f) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        nan |= l[i] != l[i];
-        l[i] = l[i] != l[i] ? kNegInf : fminf(l[i], kMaxF);
-      }
-      if (nan) set_status(dev_status, MOE_ERR_INVALID_ARG);
-    }
-    if (VPT * 32 > r.E) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (e0 + i >= r.E) l[i] = kNegInf;
-    }
-
-    // ---- the softmax's maximum and sum, where a weight or a choice needs them -----
-    float m = 0.0f, sum = 1.0f;
-    if (want_sum) {
-      m = l[0];
-#pragma unroll
-      for (int i = 1; i < VPT; ++i) m = fmaxf(m, l[i]);
-      m = fmaxf(warp_max(m), -kMaxF);
-      sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) sum = __fadd_rn(sum, exp_neg(__fsub_rn(l[i], m)));
-      sum = warp_sum(sum);
-      if (sum == 0.0f) sum = 1.0f;
-    }
-    const float inv_sum = want_sum ? __fdiv_rn(1.0f, sum) : 1.0f;
-    auto score = [&](float x) {
-      return r.score == MOE_SOFTMAX ? __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum)
-                                    : sigmoid_rank(x);
-    };
-
-    // ---- ranked values -------------------------------------------------------------
-    if (BIAS) {
-      // every: every value is an expert's finite logit, the usual case
-      auto rank = [&](auto every, auto&& f) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const float c = __fadd_rn(f(l[i]), bias[i]);
-          l[i] = decltype(every)::value || l[i] > kNegInf ? c : kNegInf;
-        }
-      };
-      auto soft = [&](float x) { return __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum); };
-      const std::true_type yes;
-      const std::false_type no;
-      if (r.score == MOE_SOFTMAX) rank(no, soft);
-      else if (odd || VPT * 32 > r.E) rank(no, sigmoid_rank);
-      else rank(yes, sigmoid_rank);
-      if (odd_bias) {                    // a NaN choice is no choice
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) l[i] = l[i] > kNegInf ? l[i] : kNegInf;
-      }
-    }
-    // the lane's three largest
-    float v1, v2, v3;
-    auto scan = [&]() {
-      v1 = l[0];
-      v2 = v3 = kNegInf;
-#pragma unroll
-      for (int i = 1; i < VPT; ++i) {
-        const float a = fminf(v1, l[i]), b = fminf(v2, a);
-        v1 = fmaxf(v1, l[i]);
-        v2 = fmaxf(v2, a);
-        v3 = fmaxf(v3, b);
+        const float c = __fadd_rn(f(l[i]), bias[i]);
+        l[i] = decltype(every)::value || l[i] > kNegInf ? c : kNegInf;
       }
     };
-    scan();
-
-    // ---- groups: a lane's experts are all of one group, lanes_per_group lanes each ----
-    if (grouped) {
-      float a1 = v1, a2 = v2;
-      if (!BIAS) {
-        a1 = a1 > kNegInf ? score(a1) : kNegInf;
-        a2 = a2 > kNegInf ? score(a2) : kNegInf;
-      }
-      for (int d = 1; d < lanes_per_group; d <<= 1) {
-        const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
-        a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
-        a1 = fmaxf(a1, b1);
-      }
-      const float gs = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
-      uint32_t key = gs > kNegInf ? order_key(gs) : 0u;
-      const int head = lane & -lanes_per_group;        // the group's first lane
-      bool keep = false;
-      for (int i = 0; i < r.topk_group; ++i) {
-        const uint32_t best = __reduce_max_sync(kAll, key);
-        if (best == 0) break;
-        if (__ffs(__ballot_sync(kAll, key == best)) - 1 == head) {
-          keep = true;
-          key = 0u;
-        }
-      }
-      if (!keep) v1 = v2 = v3 = kNegInf;
+    auto soft = [&](float x) { return __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum); };
+    const std::true_type yes;
+    const std::false_type no;
+    if (r.score == MOE_SOFTMAX) rank(no, soft);
+    else if (odd || VPT * 32 > r.E) rank(no, sigmoid_rank);
+    else rank(yes, sigmoid_rank);
+    if (odd_bias) {                    // a NaN choice is no choice
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) l[i] = l[i] > kNegInf ? l[i] : kNegInf;
     }
+  }
+  // the lane's three largest
+  float v1, v2, v3;
+  auto scan = [&]() {
+    v1 = l[0];
+    v2 = v3 = kNegInf;
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) {
+      const float a = fminf(v1, l[i]), b = fminf(v2, a);
+      v1 = fmaxf(v1, l[i]);
+      v2 = fmaxf(v2, a);
+      v3 = fmaxf(v3, b);
+    }
+  };
+  scan();
 
-    // ---- the k largest ---------------------------------------------------------------
-    // keys of the values still to win; kAgain: the lane must look for more
-    constexpr uint32_t kAgain = 0xffffffffu;
-    uint32_t q1, q2, q3, wins = 0;       // wins: slot + 1 of the lane's 1st, 2nd, 3rd value
-    int won = 0;                         // 8 * wins so far
-    auto keys = [&]() {
-      q1 = v1 > kNegInf ? order_key(v1) : 0u;
-      q2 = v2 > kNegInf ? order_key(v2) : 0u;
-      q3 = v3 > kNegInf ? order_key(v3) : 0u;
-    };
-    keys();
-    // writes down the lane's wins; the positions of v1, v2, v3 where they won
-    auto settle = [&]() {
-      int i1 = -1, i2 = -1, i3 = -1;
+  // ---- groups: a lane's experts are all of one group, lanes_per_group lanes each ----
+  if (grouped) {
+    float a1 = v1, a2 = v2;
+    if (!BIAS) {
+      a1 = a1 > kNegInf ? score(a1) : kNegInf;
+      a2 = a2 > kNegInf ? score(a2) : kNegInf;
+    }
+    for (int d = 1; d < lanes_per_group; d <<= 1) {
+      const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+      a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+      a1 = fmaxf(a1, b1);
+    }
+    const float gs = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
+    uint32_t key = gs > kNegInf ? order_key(gs) : 0u;
+    const int head = lane & -lanes_per_group;        // the group's first lane
+    bool keep = false;
+    for (int i = 0; i < r.topk_group; ++i) {
+      const uint32_t best = __reduce_max_sync(kAll, key);
+      if (best == 0) break;
+      if (__ffs(__ballot_sync(kAll, key == best)) - 1 == head) {
+        keep = true;
+        key = 0u;
+      }
+    }
+    if (!keep) v1 = v2 = v3 = kNegInf;
+  }
+
+  // ---- the k largest ---------------------------------------------------------------
+  // keys of the values still to win; kAgain: the lane must look for more
+  constexpr uint32_t kAgain = 0xffffffffu;
+  uint32_t q1, q2, q3, wins = 0;       // wins: slot + 1 of the lane's 1st, 2nd, 3rd value
+  int won = 0;                         // 8 * wins so far
+  auto keys = [&]() {
+    q1 = v1 > kNegInf ? order_key(v1) : 0u;
+    q2 = v2 > kNegInf ? order_key(v2) : 0u;
+    q3 = v3 > kNegInf ? order_key(v3) : 0u;
+  };
+  keys();
+  // writes down the lane's wins; the positions of v1, v2, v3 where they won
+  auto settle = [&]() {
+    int i1 = -1, i2 = -1, i3 = -1;
+#pragma unroll
+    for (int i = VPT - 1; i >= 0; --i)
+      if (l[i] == v1) i1 = i;
+    if (__any_sync(kAll, won > 8)) {
 #pragma unroll
       for (int i = VPT - 1; i >= 0; --i)
-        if (l[i] == v1) i1 = i;
-      if (__any_sync(kAll, won > 8)) {
+        if (l[i] == v2 && i != i1) i2 = i;
+      if (__any_sync(kAll, won > 16)) {
 #pragma unroll
         for (int i = VPT - 1; i >= 0; --i)
-          if (l[i] == v2 && i != i1) i2 = i;
-        if (__any_sync(kAll, won > 16)) {
-#pragma unroll
-          for (int i = VPT - 1; i >= 0; --i)
-            if (l[i] == v3 && i != i1 && i != i2) i3 = i;
-        }
-      }
-      if (won > 0) chosen[(wins & 255u) - 1] = e0 + i1;
-      if (won > 8) chosen[((wins >> 8) & 255u) - 1] = e0 + i2;
-      if (won > 16) chosen[((wins >> 16) & 255u) - 1] = e0 + i3;
-      return make_int3(i1, i2, i3);
-    };
-    int n = 0;
-    while (n < r.k) {
-      const uint32_t best = __reduce_max_sync(kAll, q1);
-      if (best - 1u >= kAgain - 1u) {    // rare: nothing left, or a lane must look again
-        if (best == 0) break;
-        const int3 at = settle();
-        if (q1 == kAgain) {
-#pragma unroll
-          for (int i = 0; i < VPT; ++i)
-            if (i == at.x || i == at.y || i == at.z) l[i] = kNegInf;
-          scan();
-          keys();
-          wins = 0;
-          won = 0;
-        }
-        continue;
-      }
-      const int win = __ffs(__ballot_sync(kAll, q1 == best)) - 1;
-      ++n;
-      if (lane == win) {
-        wins |= static_cast<uint32_t>(n) << won;
-        won += 8;
-        q1 = q2;
-        q2 = q3;
-        q3 = VPT > 3 ? kAgain : 0u;
+          if (l[i] == v3 && i != i1 && i != i2) i3 = i;
       }
     }
-    settle();
-    __syncwarp();
-    if (r.k <= 32) {
-      const int sel[1] = {lane < n ? chosen[lane] : -1};
-      write_token<DT, 1>(r, row, t, sel, m, sum, lane, idx, weights);
-    } else {
-      const int sel[2] = {lane < n ? chosen[lane] : -1, lane + 32 < n ? chosen[lane + 32] : -1};
-      write_token<DT, 2>(r, row, t, sel, m, sum, lane, idx, weights);
+    if (won > 0) chosen[(wins & 255u) - 1] = e0 + i1;
+    if (won > 8) chosen[((wins >> 8) & 255u) - 1] = e0 + i2;
+    if (won > 16) chosen[((wins >> 16) & 255u) - 1] = e0 + i3;
+    return make_int3(i1, i2, i3);
+  };
+  int n = 0;
+  while (n < r.k) {
+    const uint32_t best = __reduce_max_sync(kAll, q1);
+    if (best - 1u >= kAgain - 1u) {    // rare: nothing left, or a lane must look again
+      if (best == 0) break;
+      const int3 at = settle();
+      if (q1 == kAgain) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+          if (i == at.x || i == at.y || i == at.z) l[i] = kNegInf;
+        scan();
+        keys();
+        wins = 0;
+        won = 0;
+      }
+      continue;
     }
-    __syncwarp();
+    const int win = __ffs(__ballot_sync(kAll, q1 == best)) - 1;
+    ++n;
+    if (lane == win) {
+      wins |= static_cast<uint32_t>(n) << won;
+      won += 8;
+      q1 = q2;
+      q2 = q3;
+      q3 = VPT > 3 ? kAgain : 0u;
+    }
+  }
+  settle();
+  __syncwarp();
+  if (r.k <= 32) {
+    const int sel[1] = {lane < n ? chosen[lane] : -1};
+    write_token<DT, 1>(r, row, t, sel, m, sum, lane, idx, weights);
+  } else {
+    const int sel[2] = {lane < n ? chosen[lane] : -1, lane + 32 < n ? chosen[lane + 32] : -1};
+    write_token<DT, 2>(r, row, t, sel, m, sum, lane, idx, weights);
   }
 }
 
@@ -488,16 +443,10 @@ cudaError_t launch_bias(const RouteArgs& r, int lanes_per_group, int32_t* idx, f
                         int32_t* dev_status, cudaStream_t st) {
   const size_t el = DT == MOE_FP32 ? 4 : 2;
   const bool vec = reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 && r.stride * el % 16 == 0;
-  auto kernel = route_warp_kernel<DT, VPT, BIAS>;
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaError_t e = current_device_sms(&dev, &sms);
-  if (e == cudaSuccess)
-    e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), kWarps * 32, 0, &per_sm);
-  if (e != cudaSuccess) return e;
-  const int64_t grid =
-      std::min<int64_t>((r.T + kWarps - 1) / kWarps, int64_t(std::max(1, per_sm)) * sms);
-  kernel<<<static_cast<unsigned>(grid), kWarps * 32, 0, st>>>(r, vec, lanes_per_group, idx,
-                                                              weights, dev_status);
+  const bool vec_bias = reinterpret_cast<uintptr_t>(r.bias) % 16 == 0;
+  const unsigned grid = static_cast<unsigned>((r.T + kWarps - 1) / kWarps);
+  route_warp_kernel<DT, VPT, BIAS><<<grid, kWarps * 32, 0, st>>>(
+      r, vec, vec_bias, lanes_per_group, idx, weights, -0.0f, dev_status);
   return cudaGetLastError();
 }
 
@@ -513,7 +462,7 @@ cudaError_t launch_warp(const RouteArgs& r, int lanes_per_group, int32_t* idx, f
 // the butterfly that joins their best choices); 0 where there is none.
 int experts_per_lane(const RouteArgs& r, int* lanes_per_group) {
   *lanes_per_group = 32;
-  for (const int v : {1, 2, 4, 8, 16, 24, 32}) {
+  for (const int v : {2, 4, 8, 16, 24, 32}) {
     if (v * 32 < r.E) continue;
     if (r.topk_group == r.n_group) return v;
     const int per = r.E / r.n_group, lanes = per / v;
@@ -530,7 +479,6 @@ cudaError_t launch_t(const RouteArgs& r, int32_t* idx, float* weights, int32_t* 
                      cudaStream_t st) {
   int lpg = 32;
   switch (experts_per_lane(r, &lpg)) {
-    case 1: return launch_warp<DT, 1>(r, lpg, idx, weights, dev_status, st);
     case 2: return launch_warp<DT, 2>(r, lpg, idx, weights, dev_status, st);
     case 4: return launch_warp<DT, 4>(r, lpg, idx, weights, dev_status, st);
     case 8: return launch_warp<DT, 8>(r, lpg, idx, weights, dev_status, st);

@@ -19,56 +19,23 @@
 #include <type_traits>
 
 #include "moe_ep_internal.cuh"
+#include "route_math.cuh"
 
 namespace moe_ep {
 namespace {
 
-constexpr unsigned kAll = 0xffffffffu;
-constexpr float kMaxF = 3.402823466e38f;
-constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kWarps = 8;   // tokens per CTA at a time
 
+// A logit as moe_route reads it: NaN as -inf, +inf as the largest finite number.
 template <int DT>
-struct Elem { using T = uint16_t; };
-template <>
-struct Elem<MOE_FP32> { using T = float; };
-
-template <int DT>
-__device__ __forceinline__ float load_logit(const typename Elem<DT>::T* p) {
-  float l;
-  if constexpr (DT == MOE_FP32) l = __ldg(p);
-  else l = widen<DT>(__ldg(p));
+__device__ __forceinline__ float clean_logit(const typename Elem<DT>::T* p) {
+  const float l = load_logit<DT>(p);
   return l != l ? kNegInf : fminf(l, kMaxF);
 }
 template <int DT>
 __device__ __forceinline__ typename Elem<DT>::T to_elem(float f) {
   if constexpr (DT == MOE_FP32) return f;
   else return static_cast<uint16_t>(narrow_rn<DT>(f));
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d));
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// e^x of two numbers <= 0 to about 2 ulp (0 below -120): x log2(e) in two parts,
-// the second one to first order.  nz: -0 (see mul2_rn).
-__device__ __forceinline__ float2 exp_neg2(float2 x, float nz) {
-  constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596299e-8f, kLn2 = 0.693147181f;
-  x = make_float2(fmaxf(x.x, -120.0f), fmaxf(x.y, -120.0f));
-  const float2 t = mul2_rn(x, bcast2(kLog2e), nz);
-  const float2 r = fma2_rn(x, bcast2(kLog2eLo),
-                           fma2_rn(x, bcast2(kLog2e), make_float2(-t.x, -t.y)));
-  float2 e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-  return fma2_rn(e, mul2_rn(r, bcast2(kLn2), nz), e);
 }
 
 // CHUNKS: 16-byte pieces of a row per lane, kept in registers (plain softmax, rows
@@ -101,7 +68,7 @@ route_backward_kernel(const RouteArgs r, bool vec, const int32_t* __restrict__ i
         set_status(dev_status, MOE_ERR_EXPERT_ID);
         e[h] = -1;
       }
-      l[h] = e[h] >= 0 ? load_logit<DT>(row + e[h]) : kNegInf;
+      l[h] = e[h] >= 0 ? clean_logit<DT>(row + e[h]) : kNegInf;
       if (e[h] < 0) g[h] = 0.0f;
     }
 
@@ -118,17 +85,7 @@ route_backward_kernel(const RouteArgs r, bool vec, const int32_t* __restrict__ i
         const uint4 q = at < pieces ? __ldg(reinterpret_cast<const uint4*>(row) + at)
                                     : make_uint4(0u, 0u, 0u, 0u);
         float* xc = x + c * kPer16;
-        if constexpr (DT == MOE_FP32) {
-          xc[0] = __uint_as_float(q.x);
-          xc[1] = __uint_as_float(q.y);
-          xc[2] = __uint_as_float(q.z);
-          xc[3] = __uint_as_float(q.w);
-        } else {
-          float f[8];
-          unpack8<DT>(q, f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) xc[i] = f[i];
-        }
+        unpack_logits<DT>(q, xc);
 #pragma unroll
         for (int i = 0; i < kPer16; ++i) probe = __fmaf_rn(xc[i], 0.0f, probe);
       }
@@ -161,11 +118,11 @@ route_backward_kernel(const RouteArgs r, bool vec, const int32_t* __restrict__ i
       inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
     } else if (DENSE) {
       m = kNegInf;
-      for (int i = lane; i < r.E; i += 32) m = fmaxf(m, load_logit<DT>(row + i));
+      for (int i = lane; i < r.E; i += 32) m = fmaxf(m, clean_logit<DT>(row + i));
       m = fmaxf(warp_max(m), -kMaxF);
       float sum = 0.0f;
       for (int i = lane; i < r.E; i += 32)
-        sum = __fadd_rn(sum, expf(__fsub_rn(load_logit<DT>(row + i), m)));
+        sum = __fadd_rn(sum, expf(__fsub_rn(clean_logit<DT>(row + i), m)));
       sum = warp_sum(sum);
       inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
     } else if (r.score == MOE_SOFTMAX) {
@@ -271,7 +228,7 @@ route_backward_kernel(const RouteArgs r, bool vec, const int32_t* __restrict__ i
     } else {
       for (int i = lane; i < r.E; i += 32)
         out[i] = to_elem<DT>(
-            DENSE ? -__fmul_rn(__fmul_rn(expf(__fsub_rn(load_logit<DT>(row + i), m)), inv_sum),
+            DENSE ? -__fmul_rn(__fmul_rn(expf(__fsub_rn(clean_logit<DT>(row + i), m)), inv_sum),
                                back)
                   : 0.0f);
     }
