@@ -77,14 +77,16 @@ __device__ __forceinline__ void write_token(const RouteArgs& r,
   }
 }
 
-constexpr int kWarps = 4;   // tokens per CTA of the warp kernel
+constexpr int kWarps = 2;   // tokens per CTA of the warp kernel
 
 // CTAs that an SM should hold: as many as leave the registers for a lane's logits,
-// its biases and about 32 more.  Occupancy hides the latency of the k rounds, each
-// a chain of reduction, ballot and pop.
+// its biases and about 32 more, an even number (two CTAs are one warp for each of
+// an SM's four schedulers).  Occupancy hides the latency of the k rounds, each a
+// chain of reduction, ballot and pop: 768 experts a token took 59 us at the 20
+// warps the compiler's own choice left, 49 at 32.
 constexpr int warp_ctas(int vpt, bool bias) {
-  const int ctas = 512 / ((bias ? vpt * 9 / 4 : vpt) + 32);
-  return ctas < 12 ? ctas : 12;
+  const int ctas = 1024 / ((bias ? vpt * 9 / 4 : vpt) + 32);
+  return ctas < 24 ? ctas & ~1 : 24;
 }
 
 // vec, vec_bias: rows, and the bias, start at 16-byte boundaries.
@@ -134,17 +136,19 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
 #pragma unroll
       for (int i = 0; i < VPT; ++i) bias[i] = e0 + i < r.E ? __ldg(r.bias + e0 + i) : 0.0f;
     }
-    float probe = 0.0f;
+    float2 all = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) probe = __fmaf_rn(bias[i], 0.0f, probe);
-    odd_bias = __any_sync(kAll, probe != probe);
+    for (int i = 0; i < VPT; i += 2) all = add2_rn(all, make_float2(bias[i], bias[i + 1]));
+    odd_bias = __any_sync(kAll, !(fabsf(__fadd_rn(all.x, all.y)) <= kMaxF));
   }
-  // anything infinite or NaN (0 times it is NaN) takes a second look: NaN is
-  // -inf and reported, +inf the largest finite number
-  float probe = 0.0f;
+  // The sum shows what is special: NaN or +inf in it if there is one among the
+  // logits, -inf if only that (or an overflow, which does no harm).  NaN is -inf
+  // and reported, +inf the largest finite number.
+  float2 all = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) probe = __fmaf_rn(l[i], 0.0f, probe);
-  const bool odd = __any_sync(kAll, probe != probe);
+  for (int i = 0; i < VPT; i += 2) all = add2_rn(all, make_float2(l[i], l[i + 1]));
+  const float probe = __fadd_rn(all.x, all.y);
+  const bool odd = __any_sync(kAll, !(probe <= kMaxF));
   if (odd) {
     bool nan = false;
 #pragma unroll
@@ -160,12 +164,30 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
       if (e0 + i >= r.E) l[i] = kNegInf;
   }
 
+  // the lane's three largest: the largest, second and third of two ordered lists
+  float v1, v2, v3;
+  auto scan = [&]() {
+    v1 = v2 = v3 = kNegInf;
+#pragma unroll
+    for (int i = 0; i < VPT; i += 2) {
+      const float hi = fmaxf(l[i], l[i + 1]), lo = fminf(l[i], l[i + 1]);
+      if (VPT > 2) v3 = fmaxf(fmaxf(v3, fminf(v2, hi)), fminf(v1, lo));
+      v2 = fmaxf(fmaxf(v2, fminf(v1, hi)), lo);
+      v1 = fmaxf(v1, hi);
+    }
+  };
+  if (!BIAS) scan();                     // the logits rank themselves
+
   // ---- the softmax's maximum and sum, where a weight or a choice needs them -----
   float m = 0.0f, sum = 1.0f;
   if (want_sum) {
-    m = l[0];
+    if (!BIAS) {
+      m = v1;
+    } else {
+      m = l[0];
 #pragma unroll
-    for (int i = 1; i < VPT; ++i) m = fmaxf(m, l[i]);
+      for (int i = 1; i < VPT; ++i) m = fmaxf(m, l[i]);
+    }
     m = fmaxf(warp_max(m), -kMaxF);
     float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -180,7 +202,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
                                   : sigmoid_rank(x);
   };
 
-  // ---- ranked values -------------------------------------------------------------
+  // ---- ranked values with a bias --------------------------------------------------
   if (BIAS) {
     // every: every value is an expert's finite logit, the usual case
     auto rank = [&](auto every, auto&& f) {
@@ -194,27 +216,14 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
     const std::true_type yes;
     const std::false_type no;
     if (r.score == MOE_SOFTMAX) rank(no, soft);
-    else if (odd || VPT * 32 > r.E) rank(no, sigmoid_rank);
+    else if (VPT * 32 > r.E || __any_sync(kAll, !(fabsf(probe) <= kMaxF))) rank(no, sigmoid_rank);
     else rank(yes, sigmoid_rank);
-    if (odd_bias) {                    // a NaN choice is no choice
+    if (odd_bias) {                      // a NaN choice is no choice
 #pragma unroll
       for (int i = 0; i < VPT; ++i) l[i] = l[i] > kNegInf ? l[i] : kNegInf;
     }
+    scan();
   }
-  // the lane's three largest
-  float v1, v2, v3;
-  auto scan = [&]() {
-    v1 = l[0];
-    v2 = v3 = kNegInf;
-#pragma unroll
-    for (int i = 1; i < VPT; ++i) {
-      const float a = fminf(v1, l[i]), b = fminf(v2, a);
-      v1 = fmaxf(v1, l[i]);
-      v2 = fmaxf(v2, a);
-      v3 = fmaxf(v3, b);
-    }
-  };
-  scan();
 
   // ---- groups: a lane's experts are all of one group, lanes_per_group lanes each ----
   if (grouped) {

@@ -10,12 +10,12 @@
 // So only plain softmax needs the whole row of logits; every other form reads
 // k of them, and the cost is the write of d_logits (mostly zeros).
 //
-// One warp per token: lane j works out the value of slot j (and j + 32); the
-// row is written in 16-byte pieces (zeros, or -p_e * sum), and after a warp
-// barrier, which orders the warp's own stores, the k chosen elements are
-// stored over it, while the row's lines are still in L2.  Plain softmax keeps
-// the row's exponentials in registers between its two sums and the write.
-#include <algorithm>
+// A lane holds the value of one slot (two for k > 32); a token takes as many
+// lanes as it has slots, rounded up to 8, 16 or 32.  The rows are written in
+// 16-byte pieces (zeros, or -p_e * sum), and after a warp barrier, which orders
+// the warp's own stores, the k chosen elements are stored over them, while the
+// lines are still in L2.  Plain softmax keeps the row's exponentials in registers
+// between its two sums and the write.
 #include <type_traits>
 
 #include "moe_ep_internal.cuh"
@@ -24,7 +24,7 @@
 namespace moe_ep {
 namespace {
 
-constexpr int kWarps = 8;   // tokens per CTA at a time
+constexpr int kWarps = 2;   // per CTA (wide rows: 2 31.0 us, 4 31.5, 8 32.4)
 
 // A logit as moe_route reads it: NaN as -inf, +inf as the largest finite number.
 template <int DT>
@@ -38,256 +38,325 @@ __device__ __forceinline__ typename Elem<DT>::T to_elem(float f) {
   else return static_cast<uint16_t>(narrow_rn<DT>(f));
 }
 
-// CHUNKS: 16-byte pieces of a row per lane, kept in registers (plain softmax, rows
-// of logits 16-byte aligned, E a whole number of pieces); 0: any E and alignment,
-// element by element where plain softmax needs the row.  DENSE: plain softmax.
-// H: slots per lane (1 for k <= 32, else 2).  vec: 16-byte stores.
-template <int DT, bool DENSE, int CHUNKS, int H>
+// Sum and maximum over the W lanes of a token.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int d = W / 2; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+template <int W>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (W == 32) return warp_max(v);
+#pragma unroll
+  for (int d = W / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+
+// What a lane knows of its H slots (j and j + 32 of a token with W lanes).
+template <int H>
+struct Slots {
+  int e[H];            // expert, -1: none
+  float l[H], g[H];    // logit, gradient of the unscaled weight
+};
+
+// at: the token, there: it exists.
+template <int DT, int W, int H>
+__device__ __forceinline__ Slots<H> load_slots(const RouteArgs& r, int64_t at, bool there,
+                                               int j0, const int32_t* __restrict__ idx,
+                                               const float* __restrict__ d_weights,
+                                               int32_t* dev_status) {
+  using T = typename Elem<DT>::T;
+  const T* row = static_cast<const T*>(r.logits) + at * r.stride;
+  Slots<H> s;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const int j = j0 + 32 * h;
+    const bool mine = there && j < r.k;
+    s.e[h] = mine ? __ldg(idx + at * r.k + j) : -1;
+    s.g[h] = mine ? __fmul_rn(__ldg(d_weights + at * r.k + j), r.scale) : 0.0f;
+    if (s.e[h] < -1 || s.e[h] >= r.E) {
+      set_status(dev_status, MOE_ERR_EXPERT_ID);
+      s.e[h] = -1;
+    }
+    s.l[h] = s.e[h] >= 0 ? clean_logit<DT>(row + s.e[h]) : kNegInf;
+    if (s.e[h] < 0) s.g[h] = 0.0f;
+  }
+  return s;
+}
+
+// total: the slots' own gradients; where a token names an expert twice, the sum of
+// its slots, in slot order, at the first of them, which alone keeps first set.
+// Distinct ids, the rule, are recognised by one match.
+template <int W, int H>
+__device__ __forceinline__ void join_repeated(const Slots<H>& s, int k, int lane, int j0,
+                                              float* total, bool* first) {
+#pragma unroll
+  for (int h = 0; h < H; ++h) first[h] = s.e[h] >= 0;
+  if constexpr (H == 1) {              // empty slots differ from one another
+    const int token = lane & -W;
+    const unsigned same =
+        __match_any_sync(kAll, s.e[0] >= 0 ? token * MOE_EP_MAX_EXPERTS + s.e[0] : -1 - lane);
+    if (!__any_sync(kAll, (same & (same - 1)) != 0)) return;
+  }
+  float v[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    v[h] = total[h];
+    total[h] = 0.0f;
+  }
+  for (int j = 0; j < k; ++j) {
+    const int ej = __shfl_sync(kAll, j < 32 ? s.e[0] : s.e[H - 1], j & 31, W);
+    const float vj = __shfl_sync(kAll, j < 32 ? v[0] : v[H - 1], j & 31, W);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (ej == s.e[h]) {
+        total[h] = __fadd_rn(total[h], vj);
+        if (j < j0 + 32 * h) first[h] = false;
+      }
+  }
+}
+
+// Every form but plain softmax.  W lanes per token, 32 / W neighbouring tokens per
+// warp: their rows of d_logits follow one another, and the zeros, which wait for
+// nothing, are on their way before the first load.  vec: 16-byte stores.
+template <int DT, int W, int H>
 __global__ void __launch_bounds__(kWarps * 32)
-route_backward_kernel(const RouteArgs r, bool vec, const int32_t* __restrict__ idx,
-                      const float* __restrict__ d_weights,
-                      typename Elem<DT>::T* __restrict__ d_logits, float nz,
-                      int32_t* dev_status) {
+route_backward_sparse_kernel(const RouteArgs r, bool vec, const int32_t* __restrict__ idx,
+                             const float* __restrict__ d_weights,
+                             typename Elem<DT>::T* __restrict__ d_logits,
+                             int32_t* dev_status) {
+  using T = typename Elem<DT>::T;
+  constexpr int kPer16 = 16 / sizeof(T);
+  constexpr int kTokens = 32 / W;
+  const int lane = threadIdx.x & 31, j0 = lane & (W - 1);
+  const int64_t t0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens;
+  if (t0 >= r.T) return;
+  const int64_t t = t0 + lane / W;
+  const Slots<H> s = load_slots<DT, W, H>(r, t, t < r.T, j0, idx, d_weights, dev_status);
+
+  T* out = d_logits + t0 * r.E;
+  const int fill = static_cast<int>(min(r.T - t0, int64_t(kTokens))) * r.E;
+  const int pieces = vec ? fill / kPer16 : 0;
+  for (int c = lane; c < pieces; c += 32)
+    reinterpret_cast<uint4*>(out)[c] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = pieces * kPer16 + lane; i < fill; i += 32) out[i] = to_elem<DT>(0.0f);
+
+  float p[H], rest[H], v[H];           // score, and 1 - score of a sigmoid
+  if (r.score == MOE_SOFTMAX) {
+    const float m = fmaxf(lanes_max<W>(H > 1 ? fmaxf(s.l[0], s.l[H - 1]) : s.l[0]), -kMaxF);
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      p[h] = s.e[h] >= 0 ? expf(__fsub_rn(s.l[h], m)) : 0.0f;
+      rest[h] = 1.0f;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {      // e^-|l| serves both sides: no cancellation
+      const float ex = expf(-fabsf(s.l[h])), inv = __fdiv_rn(1.0f, __fadd_rn(1.0f, ex));
+      const float small = __fmul_rn(ex, inv);
+      p[h] = s.e[h] < 0 ? 0.0f : s.l[h] >= 0.0f ? inv : small;
+      rest[h] = s.l[h] >= 0.0f ? small : inv;
+    }
+  }
+  if (r.renormalise) {
+    const float d = lanes_sum<W>(H > 1 ? __fadd_rn(p[0], p[H - 1]) : p[0]);
+    const float inv = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+    float part = 0.0f;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      v[h] = __fmul_rn(p[h], inv);
+      part = __fmaf_rn(v[h], s.g[h], part);
+    }
+    const float mean = lanes_sum<W>(part);
+#pragma unroll
+    for (int h = 0; h < H; ++h) v[h] = __fmul_rn(v[h], __fsub_rn(s.g[h], mean));
+  } else {
+#pragma unroll
+    for (int h = 0; h < H; ++h) v[h] = __fmul_rn(p[h], s.g[h]);
+  }
+  bool first[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) v[h] = __fmul_rn(v[h], rest[h]);
+  join_repeated<W, H>(s, r.k, lane, j0, v, first);
+  __syncwarp();                        // the zeros come first
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (first[h]) d_logits[t * r.E + s.e[h]] = to_elem<DT>(v[h]);
+}
+
+// Plain softmax.  CHUNKS: 16-byte pieces of a row per lane, kept in registers (rows
+// of logits 16-byte aligned, E a whole number of pieces); 0: any E and alignment,
+// element by element.  H: slots per lane (1 for k <= 32, else 2).
+template <int DT, int CHUNKS, int H>
+__global__ void __launch_bounds__(kWarps * 32)
+route_backward_dense_kernel(const RouteArgs r, const int32_t* __restrict__ idx,
+                            const float* __restrict__ d_weights,
+                            typename Elem<DT>::T* __restrict__ d_logits, float nz,
+                            int32_t* dev_status) {
   using T = typename Elem<DT>::T;
   constexpr int kPer16 = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
-  for (int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < r.T;
-       t += int64_t(gridDim.x) * kWarps) {
-    const T* row = static_cast<const T*>(r.logits) + t * r.stride;
-    T* out = d_logits + t * r.E;
+  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= r.T) return;
+  const T* row = static_cast<const T*>(r.logits) + t * r.stride;
+  T* out = d_logits + t * r.E;
 
-    // ---- the chosen slots: id, logit, incoming gradient -------------------------
-    int e[H];
-    float l[H], g[H], s[H], v[H];
+  // ---- the row's maximum and sum -----------------------------------------------
+  float m = kNegInf, sum = 0.0f;
+  float x[CHUNKS > 0 ? CHUNKS * kPer16 : 1];   // the lane's logits, then exponentials
+  if constexpr (CHUNKS > 0) {
+    const int pieces = r.E / kPer16;
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int j = lane + 32 * h;
-      e[h] = j < r.k ? __ldg(idx + t * r.k + j) : -1;
-      g[h] = j < r.k ? __fmul_rn(__ldg(d_weights + t * r.k + j), r.scale) : 0.0f;
-      if (e[h] < -1 || e[h] >= r.E) {
-        set_status(dev_status, MOE_ERR_EXPERT_ID);
-        e[h] = -1;
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int at = lane + 32 * c;
+      const uint4 q = at < pieces ? __ldg(reinterpret_cast<const uint4*>(row) + at)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+      unpack_logits<DT>(q, x + c * kPer16);
+    }
+  }
+  const Slots<H> s = load_slots<DT, 32, H>(r, t, true, lane, idx, d_weights, dev_status);
+  if constexpr (CHUNKS > 0) {
+    const int pieces = r.E / kPer16;
+    float probe = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CHUNKS * kPer16; ++i) probe = __fmaf_rn(x[i], 0.0f, probe);
+    if (__any_sync(kAll, probe != probe)) {      // infinities and NaN, as moe_route
+#pragma unroll
+      for (int i = 0; i < CHUNKS * kPer16; ++i)
+        x[i] = x[i] != x[i] ? kNegInf : fminf(x[i], kMaxF);
+    }
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+      if (lane + 32 * c < pieces) {
+#pragma unroll
+        for (int i = 0; i < kPer16; ++i) m = fmaxf(m, x[c * kPer16 + i]);
       }
-      l[h] = e[h] >= 0 ? clean_logit<DT>(row + e[h]) : kNegInf;
-      if (e[h] < 0) g[h] = 0.0f;
-    }
-
-    // ---- scores ------------------------------------------------------------------
-    float m = 0.0f, inv_sum = 1.0f;
-    constexpr int kVals = CHUNKS > 0 ? CHUNKS * kPer16 : 2;
-    float x[kVals];                    // the lane's logits, then their exponentials
-    if (DENSE && CHUNKS > 0) {
-      const int pieces = r.E / kPer16;
-      float probe = 0.0f;
+    m = fmaxf(warp_max(m), -kMaxF);
+    float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int at = lane + 32 * c;
-        const uint4 q = at < pieces ? __ldg(reinterpret_cast<const uint4*>(row) + at)
-                                    : make_uint4(0u, 0u, 0u, 0u);
-        float* xc = x + c * kPer16;
-        unpack_logits<DT>(q, xc);
-#pragma unroll
-        for (int i = 0; i < kPer16; ++i) probe = __fmaf_rn(xc[i], 0.0f, probe);
-      }
-      if (__any_sync(kAll, probe != probe)) {      // infinities and NaN, as moe_route
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) x[i] = x[i] != x[i] ? kNegInf : fminf(x[i], kMaxF);
-      }
-      m = kNegInf;
-#pragma unroll
-      for (int c = 0; c < CHUNKS; ++c)
-        if (lane + 32 * c < pieces) {
-#pragma unroll
-          for (int i = 0; i < kPer16; ++i) m = fmaxf(m, x[c * kPer16 + i]);
-        }
-      m = fmaxf(warp_max(m), -kMaxF);
-      float2 sum2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int c = 0; c < CHUNKS; ++c)
-        if (lane + 32 * c < pieces) {
-#pragma unroll
-          for (int i = 0; i < kPer16; i += 2) {
-            float* p = x + c * kPer16 + i;
-            const float2 ex = exp_neg2(add2_rn(make_float2(p[0], p[1]), bcast2(-m)), nz);
-            p[0] = ex.x;
-            p[1] = ex.y;
-            sum2 = add2_rn(sum2, ex);
-          }
-        }
-      const float sum = warp_sum(__fadd_rn(sum2.x, sum2.y));
-      inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-    } else if (DENSE) {
-      m = kNegInf;
-      for (int i = lane; i < r.E; i += 32) m = fmaxf(m, clean_logit<DT>(row + i));
-      m = fmaxf(warp_max(m), -kMaxF);
-      float sum = 0.0f;
-      for (int i = lane; i < r.E; i += 32)
-        sum = __fadd_rn(sum, expf(__fsub_rn(clean_logit<DT>(row + i), m)));
-      sum = warp_sum(sum);
-      inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-    } else if (r.score == MOE_SOFTMAX) {
-      m = fmaxf(warp_max(H > 1 ? fmaxf(l[0], l[H - 1]) : l[0]), -kMaxF);
-    }
-    float rest[H];                     // 1 - s of a sigmoid (of -l: no cancellation)
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      rest[h] = 1.0f;
-      if (r.score == MOE_SOFTMAX) {
-        s[h] = e[h] >= 0 ? __fmul_rn(expf(__fsub_rn(l[h], m)), inv_sum) : 0.0f;
-      } else {                         // e^-|l| serves both sides
-        const float ex = expf(-fabsf(l[h])), inv = __fdiv_rn(1.0f, __fadd_rn(1.0f, ex));
-        const float small = __fmul_rn(ex, inv);
-        s[h] = e[h] < 0 ? 0.0f : l[h] >= 0.0f ? inv : small;
-        rest[h] = l[h] >= 0.0f ? small : inv;
-      }
-    }
-
-    // ---- the slots' gradients ------------------------------------------------------
-    float back = 0.0f;                 // what every expert loses (plain softmax)
-    if (r.renormalise) {
-      const float d = warp_sum(H > 1 ? __fadd_rn(s[0], s[H - 1]) : s[0]);
-      const float inv = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
-      float part = 0.0f;
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        v[h] = __fmul_rn(s[h], inv);
-        part = __fmaf_rn(v[h], g[h], part);
-      }
-      const float mean = warp_sum(part);
-#pragma unroll
-      for (int h = 0; h < H; ++h) v[h] = __fmul_rn(v[h], __fsub_rn(g[h], mean));
-    } else {
-      float part = 0.0f;
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        v[h] = __fmul_rn(s[h], g[h]);
-        part = __fadd_rn(part, v[h]);
-      }
-      if (DENSE) back = warp_sum(part);
-    }
-    bool first[H];
-    float total[H];
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      if (r.score == MOE_SIGMOID) v[h] = __fmul_rn(v[h], rest[h]);
-      first[h] = e[h] >= 0;
-      total[h] = v[h];
-    }
-    // a repeated id gets the sum of its slots, in slot order, from its first one
-    // (distinct ids, the rule, are recognised by one match; empty slots differ)
-    bool repeated = true;
-    if (H == 1) {
-      const unsigned same = __match_any_sync(kAll, e[0] >= 0 ? e[0] : -1 - lane);
-      repeated = __any_sync(kAll, (same & (same - 1)) != 0);
-    }
-    if (repeated) {
-#pragma unroll
-      for (int h = 0; h < H; ++h) total[h] = 0.0f;
-      for (int j = 0; j < r.k; ++j) {
-        const int ej = __shfl_sync(kAll, j < 32 ? e[0] : e[H - 1], j & 31);
-        const float vj = __shfl_sync(kAll, j < 32 ? v[0] : v[H - 1], j & 31);
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-          if (ej == e[h]) {
-            total[h] = __fadd_rn(total[h], vj);
-            if (j < lane + 32 * h) first[h] = false;
-          }
-      }
-    }
-    if (DENSE) {
-#pragma unroll
-      for (int h = 0; h < H; ++h) total[h] = __fsub_rn(total[h], __fmul_rn(s[h], back));
-    }
-
-    // ---- the row ---------------------------------------------------------------------
-    if (DENSE && CHUNKS > 0) {
-      const float f = -__fmul_rn(inv_sum, back);
-#pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int at = lane + 32 * c;
-        if (at >= r.E / kPer16) continue;
-        float y[kPer16];
+    for (int c = 0; c < CHUNKS; ++c)
+      if (lane + 32 * c < pieces) {
 #pragma unroll
         for (int i = 0; i < kPer16; i += 2) {
-          const float2 q = mul2_rn(make_float2(x[c * kPer16 + i], x[c * kPer16 + i + 1]),
-                                   bcast2(f), nz);
-          y[i] = q.x;
-          y[i + 1] = q.y;
+          float* p = x + c * kPer16 + i;
+          const float2 ex = exp_neg2(add2_rn(make_float2(p[0], p[1]), bcast2(-m)), nz);
+          p[0] = ex.x;
+          p[1] = ex.y;
+          sum2 = add2_rn(sum2, ex);
         }
-        uint4 o;
-        if constexpr (DT == MOE_FP32)
-          o = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
-                         __float_as_uint(y[3]));
-        else
-          o = pack8<DT>(y);
-        reinterpret_cast<uint4*>(out)[at] = o;
       }
-    } else if (!DENSE && vec) {
-      for (int c = lane; c < r.E / kPer16; c += 32)
-        reinterpret_cast<uint4*>(out)[c] = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-      for (int i = lane; i < r.E; i += 32)
-        out[i] = to_elem<DT>(
-            DENSE ? -__fmul_rn(__fmul_rn(expf(__fsub_rn(clean_logit<DT>(row + i), m)), inv_sum),
-                               back)
-                  : 0.0f);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int h = 0; h < H; ++h)
-      if (first[h]) out[e[h]] = to_elem<DT>(total[h]);
+    sum = __fadd_rn(sum2.x, sum2.y);
+  } else {
+    for (int i = lane; i < r.E; i += 32) m = fmaxf(m, clean_logit<DT>(row + i));
+    m = fmaxf(warp_max(m), -kMaxF);
+    for (int i = lane; i < r.E; i += 32)
+      sum = __fadd_rn(sum, expf(__fsub_rn(clean_logit<DT>(row + i), m)));
   }
+  sum = warp_sum(sum);
+  const float inv_sum = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+
+  // ---- the slots' gradients, and what every expert loses ---------------------------
+  float p[H], v[H], part = 0.0f;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    p[h] = s.e[h] >= 0 ? __fmul_rn(expf(__fsub_rn(s.l[h], m)), inv_sum) : 0.0f;
+    v[h] = __fmul_rn(p[h], s.g[h]);
+    part = __fadd_rn(part, v[h]);
+  }
+  const float back = warp_sum(part);
+  bool first[H];
+  join_repeated<32, H>(s, r.k, lane, lane, v, first);
+
+  // ---- the row ---------------------------------------------------------------------
+  const float f = -__fmul_rn(inv_sum, back);
+  if constexpr (CHUNKS > 0) {
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int at = lane + 32 * c;
+      if (at >= r.E / kPer16) continue;
+      float y[kPer16];
+#pragma unroll
+      for (int i = 0; i < kPer16; i += 2) {
+        const float2 q = mul2_rn(make_float2(x[c * kPer16 + i], x[c * kPer16 + i + 1]),
+                                 bcast2(f), nz);
+        y[i] = q.x;
+        y[i + 1] = q.y;
+      }
+      uint4 o;
+      if constexpr (DT == MOE_FP32)
+        o = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                       __float_as_uint(y[3]));
+      else
+        o = pack8<DT>(y);
+      reinterpret_cast<uint4*>(out)[at] = o;
+    }
+  } else {
+    for (int i = lane; i < r.E; i += 32)
+      out[i] = to_elem<DT>(__fmul_rn(expf(__fsub_rn(clean_logit<DT>(row + i), m)), f));
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (first[h])
+      out[s.e[h]] = to_elem<DT>(__fsub_rn(v[h], __fmul_rn(p[h], back)));
 }
 
-template <int DT, bool DENSE, int CHUNKS, int H>
-cudaError_t launch_kernel(const RouteArgs& r, bool vec, const int32_t* idx,
-                          const float* d_weights, void* d_logits, int32_t* dev_status,
-                          cudaStream_t st) {
-  auto kernel = route_backward_kernel<DT, DENSE, CHUNKS, H>;
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaError_t e = current_device_sms(&dev, &sms);
-  if (e == cudaSuccess)
-    e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), kWarps * 32, 0, &per_sm);
-  if (e != cudaSuccess) return e;
-  const int64_t grid =
-      std::min<int64_t>((r.T + kWarps - 1) / kWarps, int64_t(std::max(1, per_sm)) * sms);
-  kernel<<<static_cast<unsigned>(grid), kWarps * 32, 0, st>>>(
-      r, vec, idx, d_weights, static_cast<typename Elem<DT>::T*>(d_logits), -0.0f, dev_status);
+template <int DT, int W, int H>
+cudaError_t launch_sparse(const RouteArgs& r, const int32_t* idx, const float* d_weights,
+                          void* d_logits, int32_t* dev_status, cudaStream_t st) {
+  using T = typename Elem<DT>::T;
+  constexpr int kTokens = kWarps * 32 / W;         // per CTA
+  const bool vec = r.E * sizeof(T) * (32 / W) % 16 == 0;   // each warp's first row is aligned
+  route_backward_sparse_kernel<DT, W, H>
+      <<<static_cast<unsigned>((r.T + kTokens - 1) / kTokens), kWarps * 32, 0, st>>>(
+          r, vec, idx, d_weights, static_cast<T*>(d_logits), dev_status);
   return cudaGetLastError();
 }
 
-template <int DT, bool DENSE, int H>
-cudaError_t launch_t(const RouteArgs& r, const int32_t* idx, const float* d_weights,
+template <int DT, int CHUNKS, int H>
+cudaError_t launch_dense(const RouteArgs& r, const int32_t* idx, const float* d_weights,
+                         void* d_logits, int32_t* dev_status, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>((r.T + kWarps - 1) / kWarps);
+  route_backward_dense_kernel<DT, CHUNKS, H><<<grid, kWarps * 32, 0, st>>>(
+      r, idx, d_weights, static_cast<typename Elem<DT>::T*>(d_logits), -0.0f, dev_status);
+  return cudaGetLastError();
+}
+
+template <int DT, int H>
+cudaError_t launch_h(const RouteArgs& r, const int32_t* idx, const float* d_weights,
                      void* d_logits, int32_t* dev_status, cudaStream_t st) {
+  if (r.score != MOE_SOFTMAX || r.renormalise) {
+    if constexpr (H == 1) {
+      if (r.k <= 8)
+        return launch_sparse<DT, 8, 1>(r, idx, d_weights, d_logits, dev_status, st);
+      if (r.k <= 16)
+        return launch_sparse<DT, 16, 1>(r, idx, d_weights, d_logits, dev_status, st);
+    }
+    return launch_sparse<DT, 32, H>(r, idx, d_weights, d_logits, dev_status, st);
+  }
   constexpr int kPer16 = 16 / sizeof(typename Elem<DT>::T);
-  const bool whole = r.E % kPer16 == 0;            // rows of d_logits are aligned too
-  const bool vec = whole && reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 &&
+  const bool vec = r.E % kPer16 == 0 && reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 &&
                    r.stride % kPer16 == 0;
   auto launch = [&](auto chunks) {
-    return launch_kernel<DT, DENSE, decltype(chunks)::value, H>(
-        r, whole, idx, d_weights, d_logits, dev_status, st);
+    return launch_dense<DT, decltype(chunks)::value, H>(r, idx, d_weights, d_logits,
+                                                        dev_status, st);
   };
   const int pieces = (r.E / kPer16 + 31) / 32;     // per lane
-  if constexpr (DENSE) {
-    if (vec && pieces <= 1) return launch(std::integral_constant<int, 1>());
-    if (vec && pieces <= 2) return launch(std::integral_constant<int, 2>());
-    if (vec && pieces <= 3) return launch(std::integral_constant<int, 3>());
-    if (vec && pieces <= 4) return launch(std::integral_constant<int, 4>());
-    if constexpr (DT == MOE_FP32)
-      if (vec && pieces <= 8) return launch(std::integral_constant<int, 8>());
-  }
+  if (vec && pieces <= 1) return launch(std::integral_constant<int, 1>());
+  if (vec && pieces <= 2) return launch(std::integral_constant<int, 2>());
+  if (vec && pieces <= 3) return launch(std::integral_constant<int, 3>());
+  if (vec && pieces <= 4) return launch(std::integral_constant<int, 4>());
+  if constexpr (DT == MOE_FP32)
+    if (vec && pieces <= 8) return launch(std::integral_constant<int, 8>());
   return launch(std::integral_constant<int, 0>());
 }
 
 template <int DT>
 cudaError_t launch_dt(const RouteArgs& r, const int32_t* idx, const float* d_weights,
                       void* d_logits, int32_t* dev_status, cudaStream_t st) {
-  const bool dense = r.score == MOE_SOFTMAX && !r.renormalise;
-  if (r.k <= 32)
-    return dense ? launch_t<DT, true, 1>(r, idx, d_weights, d_logits, dev_status, st)
-                 : launch_t<DT, false, 1>(r, idx, d_weights, d_logits, dev_status, st);
-  return dense ? launch_t<DT, true, 2>(r, idx, d_weights, d_logits, dev_status, st)
-               : launch_t<DT, false, 2>(r, idx, d_weights, d_logits, dev_status, st);
+  return r.k <= 32 ? launch_h<DT, 1>(r, idx, d_weights, d_logits, dev_status, st)
+                   : launch_h<DT, 2>(r, idx, d_weights, d_logits, dev_status, st);
 }
 
 }  // namespace

@@ -538,7 +538,8 @@ moe_status moe_route(const void* logits, int32_t logits_dtype, int64_t T, int32_
  *               as in the moe_route call (NaN logits: as there, no status)
  *   topk_idx    int32 [T][k] (read)
  *   d_weights   fp32 [T][k] (read)
- *   d_logits    [T][E] in logits_dtype, rows E apart, 16-byte aligned
+ *   d_logits    [T][E] in logits_dtype, rows E apart, 16-byte aligned; apart from
+ *               the inputs
  * One launch. */
 moe_status moe_route_backward(const void* logits, int32_t logits_dtype, int64_t T, int32_t E,
                               int64_t logits_stride, int32_t score, int32_t k,
