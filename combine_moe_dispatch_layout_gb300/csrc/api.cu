@@ -567,11 +567,12 @@ moe_status moe_linear_i8(const void* a, int64_t a_rows, int64_t a_stride, const 
                          const void* row_scale, int64_t row_scale_stride,
                          const float* bias, void* c, int32_t c_dtype,
                          int32_t* dev_status, void* stream) {
-  if (a_rows < 0 || a_rows > INT32_MAX || K < 1 || K > MOE_EP_MAX_HIDDEN || N < 1 ||
+  if (a_rows < 0 || a_rows > INT32_MAX - 1024 || K < 1 || K > MOE_EP_MAX_HIDDEN || N < 1 ||
       N > MOE_EP_MAX_HIDDEN || G < 1 || G > MOE_EP_MAX_EXPERTS || a_stride < K ||
       a_stride % 16 != 0 || w_stride < K || w_stride % 16 != 0 || a_stride >= kMaxStride ||
       w_stride >= kMaxStride || c_dtype < MOE_BF16 || c_dtype > MOE_INT32 || !dev_status)
     return MOE_ERR_INVALID_ARG;
+  if ((a_rows / 32 + G) * ((N + 255) / 256) > INT32_MAX) return MOE_ERR_INVALID_ARG;  // tiles
   const bool scaled = c_dtype != MOE_INT32;      // int32 outputs read no scale, no bias
   if (scaled && (row_scale_stride < 4 || row_scale_stride % 4 != 0 ||
                  row_scale_stride >= kMaxStride))

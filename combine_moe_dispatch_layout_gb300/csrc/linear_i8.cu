@@ -797,8 +797,6 @@ cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStrea
     e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
   const Plan plan = make_plan(p, sms);
-  const int64_t ntn = (p.N + CG * BM - 1) / (CG * BM);
-  if ((p.a_rows / 32 + p.G) * ntn > INT32_MAX) return cudaErrorInvalidValue;
   CUtensorMap mw, ma;
   e = encode_bytes_2d(&mw, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, BM);
   if (e == cudaSuccess)

@@ -553,7 +553,7 @@ moe_status moe_route_backward(const void* logits, int32_t logits_dtype, int64_t 
  *   d_weights[g][k]    = sum_h d_out[g][h] * expert_out[r][h]   (fp32)
  * Rows no pair maps to are left untouched.  A pair with a bad id or a row
  * outside expert_out_rows gets d_weights 0, writes no row and sets the
- * matching status.  The sum's order is fixed by H alone.  (The gradient of a
+ * matching status.  The sum's order is fixed by H and k alone.  (The gradient of a
  * verbatim moe_dispatch needs no entry point of its own: it is moe_combine of
  * the rows' gradients with weights of 1.)
  *   d_out         [T][H] in the token dtype, 16-byte aligned (read)
@@ -590,8 +590,9 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* d_out,
  *               MOE_INT32); rows past the groups' total are not written
  * a, w and c are 16-byte aligned; a_stride and w_stride are multiples of 16 and
  * at least K (bytes past K in a row are never used);
- * 1 <= K, N <= MOE_EP_MAX_HIDDEN, 0 <= a_rows <= 2^31 - 1,
- * 1 <= G <= MOE_EP_MAX_EXPERTS; row_scale_stride >= 4, a multiple of 4.
+ * 1 <= K, N <= MOE_EP_MAX_HIDDEN, 0 <= a_rows < 2^31 - 1024,
+ * 1 <= G <= MOE_EP_MAX_EXPERTS, (a_rows / 32 + G) * ceil(N / 256) < 2^31;
+ * row_scale_stride >= 4, a multiple of 4.
  * Errors found on the device as moe_grouped_gemm_i8.  One launch. */
 moe_status moe_linear_i8(const void* a, int64_t a_rows, int64_t a_stride, const void* w,
                          int64_t w_stride, int32_t G, int32_t N, int32_t K,

@@ -68,6 +68,7 @@ LINEAR = dict(a=OK, rows=4, a_stride=64, w=OK, w_stride=64, G=2, N=24, K=60, siz
 
 @pytest.mark.parametrize("bad", [
     dict(a=None), dict(a=ODD), dict(rows=-1), dict(rows=1 << 31), dict(a_stride=48),
+    dict(rows=(1 << 31) - 512), dict(rows=1 << 30, N=65536),
     dict(a_stride=72), dict(w=None), dict(w=ODD), dict(w_stride=48), dict(w_stride=60),
     dict(a_stride=1 << 32), dict(w_stride=1 << 32), dict(row_stride=1 << 32),
     dict(G=0), dict(G=4097), dict(N=0), dict(N=65537), dict(K=0), dict(K=65537),
