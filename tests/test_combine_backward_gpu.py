@@ -67,6 +67,7 @@ CASES = [W.Workload("one", R=1, epr=1, bs=1, k=1, H=8),
          W.Workload("narrow", R=3, epr=5, bs=77, k=7, H=72, dtype=W.FP16),
          W.Workload("ragged", R=5, epr=3, bs=200, k=4, H=1000),
          W.Workload("deep", R=2, epr=40, bs=50, k=64, H=256, dtype=W.FP16),
+         W.Workload("half", R=2, epr=7, bs=65, k=6, H=504),
          W.Workload("nine", R=4, epr=6, bs=111, k=9, H=520),
          W.Workload("model", R=8, epr=32, bs=64, k=8, H=7168, outlier_p=0.01),
          W.Workload("wide", R=1, epr=4, bs=9, k=3, H=65536)]
