@@ -737,9 +737,19 @@ cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const Linear
   }
 }
 
-// Up to this many rows, the kernel that streams weights through integer dot
-// products is the faster one: of a plain product, and per group on average.
-constexpr int64_t kFewPlain = 8, kFewGrouped = 3;
+// Whether the kernel that streams weights through integer dot products is the
+// faster one.  A few rows of a plain product: 8 rows of 4096 x 7168 take 11.0 us
+// there and 16.4 on the tensor cores, 9 rows 16.8 and 16.6.  A few per group on
+// average: with 3, 256 groups of 4096 x 7168 take 1313 and 1281 us, 64 309 and
+// 354, 32 of 7168 x 2048 89 and 102; with 4 1583 and 1334, 349 and 358, 105 and
+// 102.  Small products, where the tile kernel's start-up (barriers, TMEM, clusters)
+// is most of its time: 64 x 512 x 2048 takes 6.0 and 9.0 us, 512 x 256 x 1024 (at
+// both limits) 9.0 and 9.3, 64 x 7168 x 256 (past the second) 16.9 and 7.4.
+bool use_few(const LinearArgs& p) {
+  const int64_t outputs = p.a_rows * p.N;
+  return p.a_rows <= (p.G == 1 ? 8 : 3 * p.G) ||
+         (outputs <= (1 << 17) && outputs * p.K <= (1 << 27));
+}
 
 // Tokens per tile and pairs per K.  A plain product's tiles are known: the
 // cheapest of the block sizes (multiples of 32) and splits by the time of the
@@ -789,8 +799,7 @@ Plan make_plan(const LinearArgs& p, int sms) {
 }  // namespace
 
 cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
-  if (p.a_rows <= (p.G == 1 ? kFewPlain : kFewGrouped * p.G))
-    return launch_linear_i8_few(p, dev_status, st);
+  if (use_few(p)) return launch_linear_i8_few(p, dev_status, st);
   int dev = 0, sms = 0, optin = 0;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e == cudaSuccess)

@@ -16,6 +16,12 @@
 // K.  A persistent grid walks (group, channels, token block); the token blocks
 // of a group are fastest, so a second block finds the weights in L2.  (Blocks of
 // 8 tokens were slower: 32 sums a lane leave no registers for loads in flight.)
+//
+// Measured: one token by 4096 x 7168 7.4 us (29 MB: 4.3 us at a copy's rate; the
+// rest is the launch, the first load's way and the sums), 164 of 256 experts'
+// 4096 x 7168 for 256 tokens 681 us, 7.1 TB/s: bound by memory.  Seven CTAs of 128
+// threads to an SM spread 1024 quads of channels more evenly over 152 SMs than
+// three of 256 did (8.4 and 725 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -25,7 +31,7 @@
 namespace moe_ep {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kChannels = 4;         // weight rows per warp
 constexpr int kTokens = 4;           // tokens per block at most
 constexpr int kPiece = 512;          // bytes of K per warp step
@@ -87,10 +93,10 @@ __device__ __forceinline__ void channels_by_tokens(const uint8_t* w, int64_t w_s
   for (int i = 0; i < CH * TB; ++i) acc[i] = 0;
   const int step = parts * kPiece;
   int j = part * kPiece + lane * 16;
-  // one or two tokens: the next step's weights are on their way while this
-  // one's are used (with more, the sums take those registers and the longer
-  // arithmetic of the other warps covers the loads)
-  constexpr bool kAhead = TB < 4;
+  // one token: the next step's weights are on their way while this one's are used
+  // (with more, the sums take those registers and the longer arithmetic of the
+  // other warps covers the loads)
+  constexpr bool kAhead = TB < 2;
   uint4 next[CH];
   if (kAhead) {
 #pragma unroll
@@ -122,7 +128,7 @@ __device__ __forceinline__ void channels_by_tokens(const uint8_t* w, int64_t w_s
 }
 
 // parts: warps that split K (a divisor of kWarps).
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 7)
 linear_i8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
   extern __shared__ int s_tables[];
   __shared__ int64_t s_scan[kThreads * 12 / 8];

@@ -94,7 +94,12 @@ SHAPES = [  # sizes, N, K
     ((1100,), 520, 2064), ((2000,), 264, 72),
     ((3, 0, 5), 72, 96), ((0, 0, 4), 40, 200), ((1,) * 40, 100, 160),
     ((100, 1, 0, 31, 260), 200, 1030), ((0, 700, 45), 264, 1104),
-    ((5, 0, 17, 130, 64, 1, 0, 300), 384, 2048), ((0, 0), 64, 64)]
+    ((5, 0, 17, 130, 64, 1, 0, 300), 384, 2048), ((0, 0), 64, 64),
+    # past the limits of small products
+    ((9,), 14600, 40), ((12,), 11000, 300), ((16,), 8208, 1024), ((17,), 8200, 1025),
+    ((33,), 4100, 520), ((64,), 2056, 128), ((65,), 2040, 96), ((128,), 1100, 256),
+    ((129,), 1027, 130), ((255,), 1000, 640), ((300,), 600, 1), ((20, 1, 0, 44), 96, 32800),
+    ((40,) * 8, 1001, 33), ((100, 1, 0, 31, 260), 1000, 1030), ((4,) * 40, 1001, 161)]
 
 
 @pytest.mark.parametrize("sizes,N,K", SHAPES, ids=lambda v: str(v).replace(" ", "")[:40])
@@ -113,7 +118,8 @@ def test_types_and_sizes(ep, sizes, N, K):
 
 
 @pytest.mark.parametrize("sizes,N,K", [((2,), 200, 300), ((40,), 136, 1000),
-                                       ((130, 3), 300, 2050), ((600,), 520, 1500)],
+                                       ((130, 3), 300, 2050), ((130, 3), 1100, 2050),
+                                       ((600,), 520, 1500)],
                          ids=lambda v: str(v).replace(" ", ""))
 def test_strides_images_and_rows_past_the_groups(ep, sizes, N, K):
     """Row images, padded strides of both operands, garbage past K, and a
@@ -128,7 +134,7 @@ def test_strides_images_and_rows_past_the_groups(ep, sizes, N, K):
             assert (rest == 0xA5).all()
 
 
-@pytest.mark.parametrize("rows", [1, 12, 40, 150, 700])
+@pytest.mark.parametrize("rows", [1, 12, 40, 150, 411, 700])
 def test_one_group_without_counts(ep, rows):
     c = _case((rows,), 320, 1300, seed=rows)
     for out in ("bf16", "int32"):
@@ -137,7 +143,7 @@ def test_one_group_without_counts(ep, rows):
         _same(got, _want(c, out, bias=out == "bf16"))
 
 
-@pytest.mark.parametrize("rows,K", [(1, 65536), (9, 65536), (40, 20000), (200, 65536)])
+@pytest.mark.parametrize("rows,K", [(1, 65536), (9, 65536), (40, 20000), (90, 65536), (200, 65536)])
 @pytest.mark.parametrize("code", [-128, 127])
 def test_extreme_codes_stay_exact(ep, rows, K, code):
     """Every product 2^14 (or 127^2): sums far beyond 2^24 in one row."""
@@ -162,8 +168,8 @@ def test_many_groups(ep, G, rows):
 
 
 def test_device_errors(ep):
-    for sizes in ((3, 2), (200, 300)):
-        c = _case(sizes, 72, 96, seed=5)
+    for sizes, N in (((3, 2), 72), ((200, 300), 72), ((200, 300), 520)):
+        c = _case(sizes, N, 96, seed=5)
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
         c["dev"]["sizes"][0] += 1                            # more rows than a holds
         got, code = _run(ep, c, "fp32", st=st)
