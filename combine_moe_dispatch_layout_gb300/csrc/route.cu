@@ -89,10 +89,10 @@ constexpr int warp_ctas(int vpt, bool bias) {
   return ctas < 24 ? ctas & ~1 : 24;
 }
 
-// vec, vec_bias: rows, and the bias, start at 16-byte boundaries.
+// vec, vec_bias: rows, and the bias, start at 16-byte boundaries, and so do groups.
 template <int DT, int VPT, bool BIAS>
 __global__ void __launch_bounds__(kWarps * 32, warp_ctas(VPT, BIAS))
-route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_group,
+route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, int per,
                   int32_t* __restrict__ idx, float* __restrict__ weights, float nz,
                   int32_t* dev_status) {
   using T = typename Elem<DT>::T;
@@ -100,8 +100,12 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
   __shared__ int s_sel[kWarps][MOE_EP_MAX_TOPK];
   const int lane = threadIdx.x & 31;
   int* chosen = s_sel[threadIdx.x >> 5];
-  const int e0 = lane * VPT;
   const bool grouped = r.topk_group < r.n_group;
+  // the lane's experts: e0 .. e0 + mine - 1, all of one group of `per` (ungrouped: E)
+  const int lanes_per_group = 1 << group_shift;
+  const int skip = (lane & (lanes_per_group - 1)) * VPT;
+  const int e0 = (lane >> group_shift) * per + skip;
+  const int mine = e0 < r.E ? min(per - skip, VPT) : 0;
   const bool want_sum = r.score == MOE_SOFTMAX && (!r.renormalise || BIAS || grouped);
 
   const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -110,7 +114,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
 
   // ---- logits -----------------------------------------------------------------
   float l[VPT];
-  if (VPT % kPer16 == 0 && vec && e0 + VPT <= r.E) {
+  if (VPT % kPer16 == 0 && vec && mine == VPT) {
 #pragma unroll
     for (int c = 0; c < VPT / kPer16; ++c) {
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
@@ -118,12 +122,12 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) l[i] = e0 + i < r.E ? load_logit<DT>(row + e0 + i) : 0.0f;
+    for (int i = 0; i < VPT; ++i) l[i] = i < mine ? load_logit<DT>(row + e0 + i) : 0.0f;
   }
   float bias[BIAS ? VPT : 1];
   bool odd_bias = false;                // an infinite or NaN bias
   if (BIAS) {
-    if (VPT % 4 == 0 && vec_bias && e0 + VPT <= r.E) {
+    if (VPT % 4 == 0 && vec_bias && mine == VPT) {
 #pragma unroll
       for (int c = 0; c < VPT / 4; ++c) {
         const float4 v = __ldg(reinterpret_cast<const float4*>(r.bias + e0) + c);
@@ -134,7 +138,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) bias[i] = e0 + i < r.E ? __ldg(r.bias + e0 + i) : 0.0f;
+      for (int i = 0; i < VPT; ++i) bias[i] = i < mine ? __ldg(r.bias + e0 + i) : 0.0f;
     }
     float2 all = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -161,7 +165,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
   if (VPT * 32 > r.E) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (e0 + i >= r.E) l[i] = kNegInf;
+      if (i >= mine) l[i] = kNegInf;
   }
 
   // the lane's three largest: the largest, second and third of two ordered lists
@@ -225,7 +229,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int lanes_per_grou
     scan();
   }
 
-  // ---- groups: a lane's experts are all of one group, lanes_per_group lanes each ----
+  // ---- groups: a power of two of lanes each ----------------------------------------
   if (grouped) {
     float a1 = v1, a2 = v2;
     if (!BIAS) {
@@ -448,52 +452,53 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
 }
 
 template <int DT, int VPT, bool BIAS>
-cudaError_t launch_bias(const RouteArgs& r, int lanes_per_group, int32_t* idx, float* weights,
+cudaError_t launch_bias(const RouteArgs& r, int group_shift, int32_t* idx, float* weights,
                         int32_t* dev_status, cudaStream_t st) {
   const size_t el = DT == MOE_FP32 ? 4 : 2;
-  const bool vec = reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 && r.stride * el % 16 == 0;
-  const bool vec_bias = reinterpret_cast<uintptr_t>(r.bias) % 16 == 0;
+  const bool grouped = r.topk_group < r.n_group;
+  const int per = grouped ? r.E / r.n_group : r.E;
+  const bool vec = reinterpret_cast<uintptr_t>(r.logits) % 16 == 0 && r.stride * el % 16 == 0 &&
+                   (!grouped || per * el % 16 == 0);
+  const bool vec_bias =
+      reinterpret_cast<uintptr_t>(r.bias) % 16 == 0 && (!grouped || per % 4 == 0);
   const unsigned grid = static_cast<unsigned>((r.T + kWarps - 1) / kWarps);
   route_warp_kernel<DT, VPT, BIAS><<<grid, kWarps * 32, 0, st>>>(
-      r, vec, vec_bias, lanes_per_group, idx, weights, -0.0f, dev_status);
+      r, vec, vec_bias, group_shift, per, idx, weights, -0.0f, dev_status);
   return cudaGetLastError();
 }
 
 template <int DT, int VPT>
-cudaError_t launch_warp(const RouteArgs& r, int lanes_per_group, int32_t* idx, float* weights,
+cudaError_t launch_warp(const RouteArgs& r, int group_shift, int32_t* idx, float* weights,
                         int32_t* dev_status, cudaStream_t st) {
-  return r.bias ? launch_bias<DT, VPT, true>(r, lanes_per_group, idx, weights, dev_status, st)
-                : launch_bias<DT, VPT, false>(r, lanes_per_group, idx, weights, dev_status, st);
+  return r.bias ? launch_bias<DT, VPT, true>(r, group_shift, idx, weights, dev_status, st)
+                : launch_bias<DT, VPT, false>(r, group_shift, idx, weights, dev_status, st);
 }
 
-// The warp kernel's experts per lane: the smallest of its sizes that holds E
-// and, with groups in play, cuts no group (a power of two of lanes each, for
-// the butterfly that joins their best choices); 0 where there is none.
-int experts_per_lane(const RouteArgs& r, int* lanes_per_group) {
-  *lanes_per_group = 32;
-  for (const int v : {2, 4, 8, 16, 24, 32}) {
-    if (v * 32 < r.E) continue;
-    if (r.topk_group == r.n_group) return v;
-    const int per = r.E / r.n_group, lanes = per / v;
-    if (per % v == 0 && (lanes & (lanes - 1)) == 0) {
-      *lanes_per_group = lanes;
-      return v;
-    }
-  }
+// The warp kernel's experts per lane: the smallest of its sizes that holds E or,
+// with groups in play, a group in its power of two of lanes (for the butterfly
+// that joins their best choices); 0 where there is none.
+int experts_per_lane(const RouteArgs& r, int* group_shift) {
+  const bool grouped = r.topk_group < r.n_group;
+  const int groups = grouped ? r.n_group : 1, per = r.E / groups;
+  *group_shift = 5;
+  while (*group_shift >= 0 && (groups << *group_shift) > 32) --*group_shift;
+  if (*group_shift < 0) return 0;
+  for (const int v : {2, 4, 8, 16, 24, 32})
+    if ((v << *group_shift) >= per) return v;
   return 0;
 }
 
 template <int DT>
 cudaError_t launch_t(const RouteArgs& r, int32_t* idx, float* weights, int32_t* dev_status,
                      cudaStream_t st) {
-  int lpg = 32;
-  switch (experts_per_lane(r, &lpg)) {
-    case 2: return launch_warp<DT, 2>(r, lpg, idx, weights, dev_status, st);
-    case 4: return launch_warp<DT, 4>(r, lpg, idx, weights, dev_status, st);
-    case 8: return launch_warp<DT, 8>(r, lpg, idx, weights, dev_status, st);
-    case 16: return launch_warp<DT, 16>(r, lpg, idx, weights, dev_status, st);
-    case 24: return launch_warp<DT, 24>(r, lpg, idx, weights, dev_status, st);
-    case 32: return launch_warp<DT, 32>(r, lpg, idx, weights, dev_status, st);
+  int shift = 5;
+  switch (experts_per_lane(r, &shift)) {
+    case 2: return launch_warp<DT, 2>(r, shift, idx, weights, dev_status, st);
+    case 4: return launch_warp<DT, 4>(r, shift, idx, weights, dev_status, st);
+    case 8: return launch_warp<DT, 8>(r, shift, idx, weights, dev_status, st);
+    case 16: return launch_warp<DT, 16>(r, shift, idx, weights, dev_status, st);
+    case 24: return launch_warp<DT, 24>(r, shift, idx, weights, dev_status, st);
+    case 32: return launch_warp<DT, 32>(r, shift, idx, weights, dev_status, st);
     default: break;
   }
   const size_t smem = (2 * size_t(r.E) + r.n_group) * 4;

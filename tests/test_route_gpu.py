@@ -121,6 +121,14 @@ CASES = [  # T, E, k, dtype, score, bias, groups (n, keep, top), renorm, scale, 
     (9, 4096, 64, "fp32", "softmax", True, (64, 7, 2), False, 1.0, 5),
     (3, 4096, 8, "fp16", "sigmoid", True, (2048, 3, 2), True, 1.0, 0),
     (50, 40, 40, "fp32", "sigmoid", False, (1, 1, 1), True, 1.0, 0),     # every expert
+    # groups that fill no whole number of lanes
+    (60, 488, 4, "fp32", "softmax", True, (8, 2, 1), True, 1.0, 0),
+    (60, 480, 7, "bf16", "sigmoid", True, (12, 5, 2), False, 2.5, 0),
+    (33, 96, 8, "fp32", "sigmoid", False, (32, 9, 2), True, 1.0, 0),
+    (33, 66, 3, "fp16", "softmax", True, (33, 4, 1), True, 1.0, 0),
+    (41, 255, 9, "fp32", "softmax", False, (5, 2, 2), False, 1.0, 2),
+    (41, 1000, 50, "bf16", "sigmoid", True, (2, 1, 1), True, 1.0, 0),
+    (21, 31, 6, "fp32", "sigmoid", True, (31, 30, 1), True, 1.0, 0),
 ]
 
 
