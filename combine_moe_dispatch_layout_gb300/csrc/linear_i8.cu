@@ -14,23 +14,41 @@
 // fp16 number 1024 + (b + 128); subtracting 1152 leaves b: five instructions
 // for four codes.
 //
-// Tile: 128 output channels (the MMA's M, TMEM lanes) x up to NT tokens (the
-// MMA's N), so few tokens make narrow, cheap instructions while every weight
-// is still read once.  Warps of a CTA (one CTA per SM, persistent):
-//   warp 0        copies 128 weight rows and up to NT token rows, 128 bytes of
-//                 each, into a ring of byte stages (tensor copies, 128-byte swizzle)
-//   warp 1        issues tcgen05.mma (K = 16) from fp16 stages into one of two
-//                 TMEM accumulators, alternating per chunk
-//   16 warps     widen byte stages into fp16 stages (64 codes, 128-byte swizzle)
-//   8 warps      drain finished chunks into int32 registers (one channel per
+// Tile: a pair of CTAs (on two SMs of a cluster) takes 256 output channels (the
+// MMA's M, 128 TMEM lanes on each SM) x up to 256 tokens (the MMA's N), so each
+// SM widens 128 weight rows and half the tokens, and few tokens make narrow, cheap
+// instructions while every weight is still read once.  Warps of a CTA (one CTA
+// per SM, persistent):
+//   warp 0        copies 128 weight rows and its half of the token rows, 128 bytes
+//                 of each, into a ring of byte stages (tensor copies, 128-byte swizzle)
+//   warp 1        of the pair's first CTA: issues tcgen05.mma (K = 16) from fp16
+//                 stages of both SMs into one of two TMEM accumulators,
+//                 alternating per chunk
+//   16 warps      widen byte stages into fp16 stages (64 codes, 128-byte swizzle)
+//   8 warps       drain finished chunks into int32 registers (one channel per
 //                 thread), then scale and store: a warp's stores for one token
 //                 are 32 neighbouring channels
-// When a plain product has fewer tiles than the GPU has SMs, a cluster of up to
-// 8 CTAs splits K; the partial sums (integers, so any order gives the same
-// result) meet in shared memory across the cluster, each CTA finishing its
-// share of the tile's tokens.
+// When there are fewer tiles than pairs of SMs, a cluster of 2 to 4 pairs splits
+// K; the partial sums (integers, so any order gives the same result) meet in
+// shared memory across the cluster, each CTA finishing its share of the tile's
+// tokens.
 // Every wait is bounded: a timeout sets MOE_ERR_TIMEOUT, the CTA stops issuing
 // work and drains what is in flight.
+//
+// What bounds it.  A 64-code step of a full tile is 512 clocks of MMA on an SM, and
+// 384 of its load and store unit (16 KB of bytes read, 32 KB of fp16 written, 128
+// bytes a clock) beside the copies' and the MMA's own traffic; so large tiles run
+// at the tensor cores' rate and tiles of fewer tokens at that of shared memory
+// (128 weight rows are widened for however few tokens).  The store of a tile adds
+// shuffles and stores to the same unit, which shows where K is short.  Measured:
+// 8192 x 4096 x 7168 251 us, 1916 TFLOP/s (a library bf16 product: 1874); 4096 x
+// 4096 x 7168 143 us, 1680 (304 tiles of 224 tokens on 76 pairs); 32,768 x 7168 x
+// 2048 583 us, 1650, in 32 even groups 616, in 32 uneven ones (half of them under
+// 512 rows, so of two narrower tiles) 662.  Without the store's arithmetic and
+// stores the last three would take 528, 568 and 635.  Tried and slower: two
+// channels per store after an exchange between lanes (598 instead of 583), row
+// scales through shared memory instead of shuffles (584), both paths of the store
+// in one loop (650).
 #include <cuda.h>
 
 #include <algorithm>

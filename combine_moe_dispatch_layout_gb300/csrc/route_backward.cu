@@ -16,6 +16,12 @@
 // the warp's own stores, the k chosen elements are stored over them, while the
 // lines are still in L2.  Plain softmax keeps the row's exponentials in registers
 // between its two sums and the write.
+//
+// Measured: 32,768 x 256 fp32, renormalised sigmoid, k = 8: 7.5 us (4.5 TB/s of
+// writes; 12.5 with a warp per token, zeros after the sums: the chain id -> logit ->
+// sums was paid four times as often).  49,152 x 768 bf16, plain softmax: 30.7 us, 4.9
+// TB/s both ways; the exponentials' instructions (75% of the issue slots) are what
+// keeps it from a copy's 23 us.
 #include <type_traits>
 
 #include "moe_ep_internal.cuh"
