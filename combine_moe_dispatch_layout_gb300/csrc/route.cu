@@ -20,9 +20,9 @@
 // spread over the lanes; with two values kept it was not).
 //
 // Measured: 32,768 tokens x 256 fp32 logits, sigmoid with bias, 4 of 8 groups, k = 8:
-// 21.7 us, of which 10.3 are the read and the scan, 1.9 the sigmoid and the bias,
-// 5.6 the seven further rounds, 3.9 the groups; 49,152 x 768 bf16, plain softmax:
-// 43 us.  Memory would allow 5.3 and 11.6: the schedulers issue in 75% of their
+// 21.3 us, of which 9.5 are the read, the scan and the write, 2.3 the sigmoid and the
+// bias, 5.6 the seven further rounds, 3.9 the groups; 49,152 x 768 bf16, plain
+// softmax: 43 us.  Memory would allow 5.3 and 11.6: the schedulers issue in 75% of their
 // cycles and wait for the chain of a round in most others.  32 tokens: 3.3 us, a
 // launch.  Tried and not faster: 8 or 16 lanes per token (half the instructions, but
 // maxima run at half rate and the registers leave few warps: 28-34 us where this
@@ -49,20 +49,20 @@ __device__ __forceinline__ float sigmoid_full(float x) {
   return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
 }
 
-// Ids and weights of slots h * 32 + lane of a token from the chosen experts
-// (sel = -1: none).  m and sum: the softmax's maximum and sum (plain softmax
-// only).  H: 1 for k <= 32, else 2.
-template <int DT, int H>
-__device__ __forceinline__ void write_token(const RouteArgs& r,
-                                            const typename Elem<DT>::T* row, int64_t t,
-                                            const int (&sel)[H], float m, float sum, int lane,
+// Ids and weights of token t (there: it exists) by W lanes: slots j0 (of this lane)
+// and, with H = 2 (k > 32), j0 + 32, from the chosen experts (sel = -1: none).
+// m and sum: the softmax's maximum and sum (plain softmax only).
+template <int DT, int H, int W>
+__device__ __forceinline__ void write_token(const RouteArgs& r, int64_t t, bool there,
+                                            const int (&sel)[H], float m, float sum, int j0,
                                             int32_t* idx, float* weights) {
+  const auto* row = static_cast<const typename Elem<DT>::T*>(r.logits) + t * r.stride;
   float l[H], s[H];
 #pragma unroll
   for (int h = 0; h < H; ++h)
     l[h] = sel[h] >= 0 ? fminf(load_logit<DT>(row + sel[h]), kMaxF) : kNegInf;
   if (r.score == MOE_SOFTMAX) {
-    if (r.renormalise) m = warp_max(H > 1 ? fmaxf(l[0], l[H - 1]) : l[0]);
+    if (r.renormalise) m = lanes_max<W>(H > 1 ? fmaxf(l[0], l[H - 1]) : l[0]);
 #pragma unroll
     for (int h = 0; h < H; ++h) s[h] = sel[h] >= 0 ? expf(__fsub_rn(l[h], m)) : 0.0f;
   } else {
@@ -71,31 +71,34 @@ __device__ __forceinline__ void write_token(const RouteArgs& r,
   }
   float d = 1.0f;
   if (r.renormalise) {
-    d = warp_sum(H > 1 ? __fadd_rn(s[0], s[H - 1]) : s[0]);
+    d = lanes_sum<W>(H > 1 ? __fadd_rn(s[0], s[H - 1]) : s[0]);
     if (d == 0.0f) d = 1.0f;
   } else if (r.score == MOE_SOFTMAX) {
     d = sum;
   }
 #pragma unroll
   for (int h = 0; h < H; ++h) {
-    const int j = lane + 32 * h;
-    if (j < r.k) {
+    const int j = j0 + 32 * h;
+    if (there && j < r.k) {
       idx[t * r.k + j] = sel[h];
       weights[t * r.k + j] = sel[h] >= 0 ? __fmul_rn(__fdiv_rn(s[h], d), r.scale) : 0.0f;
     }
   }
 }
 
-constexpr int kWarps = 2;   // tokens per CTA of the warp kernel
+// Tokens per CTA of the warp kernel: as many as write their weights together at
+// k <= 8 (8 a CTA: 43 -> 47 us at 768 experts, one writing for itself: 21.9 instead of
+// 21.3 at 256).
+constexpr int kWarps = 4;
 
 // CTAs that an SM should hold: as many as leave the registers for a lane's logits,
-// its biases and about 32 more, an even number (two CTAs are one warp for each of
-// an SM's four schedulers).  Occupancy hides the latency of the k rounds, each a
+// its biases and about 32 more (a CTA is a warp for each of an SM's four schedulers).
+// Occupancy hides the latency of the k rounds, each a
 // chain of reduction, ballot and pop: 768 experts a token took 59 us at the 20
 // warps the compiler's own choice left, 49 at 32.
 constexpr int warp_ctas(int vpt, bool bias) {
-  const int ctas = 1024 / ((bias ? vpt * 9 / 4 : vpt) + 32);
-  return ctas < 24 ? ctas & ~1 : 24;
+  const int ctas = 512 / ((bias ? vpt * 9 / 4 : vpt) + 32);
+  return ctas < 12 ? ctas : 12;
 }
 
 // vec, vec_bias: rows, and the bias, start at 16-byte boundaries, and so do groups.
@@ -106,9 +109,10 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
                   int32_t* dev_status) {
   using T = typename Elem<DT>::T;
   constexpr int kPer16 = 16 / sizeof(T);
-  __shared__ int s_sel[kWarps][MOE_EP_MAX_TOPK];
-  const int lane = threadIdx.x & 31;
-  int* chosen = s_sel[threadIdx.x >> 5];
+  __shared__ int s_sel[kWarps][MOE_EP_MAX_TOPK], s_n[kWarps];
+  __shared__ float s_m[kWarps], s_sum[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int* chosen = s_sel[warp];
   const bool grouped = r.topk_group < r.n_group;
   // the lane's experts: e0 .. e0 + mine - 1, all of one group of `per` (ungrouped: E)
   const int lanes_per_group = 1 << group_shift;
@@ -117,7 +121,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
   const int mine = e0 < r.E ? min(per - skip, VPT) : 0;
   const bool want_sum = r.score == MOE_SOFTMAX && (!r.renormalise || BIAS || grouped);
 
-  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = int64_t(blockIdx.x) * kWarps + warp;
   if (t >= r.T) return;
   const T* row = static_cast<const T*>(r.logits) + t * r.stride;
 
@@ -325,14 +329,31 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
     }
   }
   settle();
-  __syncwarp();
-  if (r.k <= 32) {
-    const int sel[1] = {lane < n ? chosen[lane] : -1};
-    write_token<DT, 1>(r, row, t, sel, m, sum, lane, idx, weights);
-  } else {
-    const int sel[2] = {lane < n ? chosen[lane] : -1, lane + 32 < n ? chosen[lane + 32] : -1};
-    write_token<DT, 2>(r, row, t, sel, m, sum, lane, idx, weights);
+
+  // ---- ids and weights: 8, 16 or 32 lanes per token, one warp for several tokens --------
+  if (lane == 0) {
+    s_n[warp] = n;
+    s_m[warp] = m;
+    s_sum[warp] = sum;
   }
+  __syncthreads();
+  auto write = [&](auto h, auto w) {
+    constexpr int H = decltype(h)::value, W = decltype(w)::value;
+    if (warp % (32 / W) != 0) return;
+    const int from = warp + lane / W, j0 = lane % W;   // the token's warp
+    const int64_t t = int64_t(blockIdx.x) * kWarps + from;
+    const bool there = t < r.T;
+    const int n = there ? s_n[from] : 0;
+    int sel[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) sel[i] = j0 + 32 * i < n ? s_sel[from][j0 + 32 * i] : -1;
+    write_token<DT, H, W>(r, t, there, sel, s_m[from], s_sum[from], j0, idx, weights);
+  };
+  const std::integral_constant<int, 1> one;
+  if (r.k <= 8) write(one, std::integral_constant<int, 8>());
+  else if (r.k <= 16) write(one, std::integral_constant<int, 16>());
+  else if (r.k <= 32) write(one, std::integral_constant<int, 32>());
+  else write(std::integral_constant<int, 2>(), std::integral_constant<int, 32>());
 }
 
 // Any E up to MOE_EP_MAX_EXPERTS and any groups: one CTA per token (persistent
@@ -454,7 +475,7 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
     __syncthreads();
     if (warp == 0) {
       const int sel[2] = {lane < n ? s_sel[lane] : -1, lane + 32 < n ? s_sel[lane + 32] : -1};
-      write_token<DT, 2>(r, row, t, sel, m, sum, lane, idx, weights);
+      write_token<DT, 2, 32>(r, t, true, sel, m, sum, lane, idx, weights);
     }
     __syncthreads();
   }

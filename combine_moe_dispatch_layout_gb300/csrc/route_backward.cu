@@ -44,21 +44,6 @@ __device__ __forceinline__ typename Elem<DT>::T to_elem(float f) {
   else return static_cast<uint16_t>(narrow_rn<DT>(f));
 }
 
-// Sum and maximum over the W lanes of a token.
-template <int W>
-__device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int d = W / 2; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d));
-  return v;
-}
-template <int W>
-__device__ __forceinline__ float lanes_max(float v) {
-  if constexpr (W == 32) return warp_max(v);
-#pragma unroll
-  for (int d = W / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-  return v;
-}
-
 // What a lane knows of its H slots (j and j + 32 of a token with W lanes).
 template <int H>
 struct Slots {

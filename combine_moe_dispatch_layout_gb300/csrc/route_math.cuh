@@ -59,6 +59,21 @@ __device__ __forceinline__ float warp_max(float v) {
   return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
+// Sum and maximum over the W lanes of a token.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int d = W / 2; d; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+template <int W>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (W == 32) return warp_max(v);
+#pragma unroll
+  for (int d = W / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
