@@ -22,7 +22,7 @@
 // Measured: 32,768 tokens x 256 fp32 logits, sigmoid with bias, 4 of 8 groups, k = 8:
 // 21.3 us, of which 9.5 are the read, the scan and the write, 2.3 the sigmoid and the
 // bias, 5.6 the seven further rounds, 3.9 the groups; 49,152 x 768 bf16, plain
-// softmax: 43 us.  Memory would allow 5.3 and 11.6: the schedulers issue in 75% of their
+// softmax: 43 us.  Memory would allow 5.3 and 11.6: the schedulers issue in 74% of their
 // cycles and wait for the chain of a round in most others.  32 tokens: 3.3 us, a
 // launch.  Tried and not faster: 8 or 16 lanes per token (half the instructions, but
 // maxima run at half rate and the registers leave few warps: 28-34 us where this
