@@ -608,21 +608,29 @@ def moe_quant_rows_bf16(h, group_off, codes, inv_scale, stream=None):
 
 
 def _rows(t, name, dtypes):
-    """(pointer, row stride in elements) of a CUDA matrix whose rows are
-    contiguous but may lie apart (a column slice of a wider matrix)."""
+    """(pointer, row stride in elements, rows, columns) of a CUDA matrix whose
+    rows are contiguous but may lie apart (a column slice of a wider matrix)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype not in dtypes:
         raise TypeError("%s must have dtype %s, got %s" % (name, tuple(dtypes), t.dtype))
-    if t.dim() != 2 or (t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("%s must be a matrix with contiguous rows" % name)
-    stride = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
-    if stride < t.shape[1]:
+    rows, cols = shape
+    stride, unit = t.stride()
+    if unit != 1 and cols > 1 and rows > 0:
+        raise ValueError("%s must be a matrix with contiguous rows" % name)
+    if rows < 2:
+        stride = max(cols, stride)
+    elif stride < cols:
         raise ValueError("%s: rows overlap" % name)
-    return t.data_ptr(), stride
+    return t.data_ptr(), stride, rows, cols
 
 
 _LOGITS = (torch.float32, torch.bfloat16, torch.float16)
+_CODES = (torch.int8, torch.uint8)
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _score(score):
@@ -639,16 +647,16 @@ def moe_route(logits, bias, score, k, topk_idx, topk_weights, dev_status, n_grou
     choice, not the weights; of n_group groups the topk_group with the best
     sums of their group_top best choices stay; renormalise divides the weights
     by their sum; scale multiplies them."""
-    p, stride = _rows(logits, "logits", _LOGITS)
-    T, E = logits.shape
+    p, stride, T, E = _rows(logits, "logits", _LOGITS)
     if T == 0:
         return MOE_OK
+    n = T * k
     st = _lib.moe_route(
-        p, _ANY_DTYPE[logits.dtype], T, E, stride, _ptr(bias, torch.float32, E, "bias"),
+        p, _ANY_DTYPE[logits.dtype], T, E, stride, _ptr(bias, _F32, E, "bias"),
         _score(score), int(n_group), int(topk_group), int(group_top), int(k),
-        int(bool(renormalise)), float(scale), _ptr(topk_idx, torch.int32, T * k, "topk_idx"),
-        _ptr(topk_weights, torch.float32, T * k, "topk_weights"),
-        _ptr(dev_status, torch.int32, 1, "dev_status"), _stream(stream))
+        1 if renormalise else 0, float(scale), _ptr(topk_idx, _I32, n, "topk_idx"),
+        _ptr(topk_weights, _F32, n, "topk_weights"),
+        _ptr(dev_status, _I32, 1, "dev_status"), _stream(stream))
     return _check(st, "moe_route")
 
 
@@ -656,19 +664,18 @@ def moe_route_backward(logits, topk_idx, d_weights, score, d_logits, dev_status,
                        renormalise=True, scale=1.0, stream=None):
     """Gradient of moe_route's weights: d_logits [T, E] (the logits' dtype)
     from topk_idx [T, k] and d_weights fp32 [T, k]."""
-    p, stride = _rows(logits, "logits", _LOGITS)
-    T, E = logits.shape
+    p, stride, T, E = _rows(logits, "logits", _LOGITS)
     if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
         raise ValueError("topk_idx must be [T, k]")
     k = topk_idx.shape[1]
     if T == 0:
         return MOE_OK
+    n = T * k
     st = _lib.moe_route_backward(
-        p, _ANY_DTYPE[logits.dtype], T, E, stride, _score(score), k, int(bool(renormalise)),
-        float(scale), _ptr(topk_idx, torch.int32, T * k, "topk_idx"),
-        _ptr(d_weights, torch.float32, T * k, "d_weights"),
+        p, _ANY_DTYPE[logits.dtype], T, E, stride, _score(score), k, 1 if renormalise else 0,
+        float(scale), _ptr(topk_idx, _I32, n, "topk_idx"), _ptr(d_weights, _F32, n, "d_weights"),
         _ptr(d_logits, logits.dtype, T * E, "d_logits"),
-        _ptr(dev_status, torch.int32, 1, "dev_status"), _stream(stream))
+        _ptr(dev_status, _I32, 1, "dev_status"), _stream(stream))
     return _check(st, "moe_route_backward")
 
 
@@ -703,24 +710,25 @@ def moe_linear_i8(a, w, K, group_rows, col_scale, row_scale, bias, c, dev_status
     the three).  a may hold row
     images (uint8) as dispatch writes them; row_scale is (tensor, byte_offset,
     byte_stride); group_rows int32 [G] (None with G = 1: every row)."""
-    i8 = (torch.int8, torch.uint8)
-    ap, a_stride = _rows(a, "a", i8)
-    if w.dim() != 3 or w.shape[2] < K or a.shape[1] < K:
+    ap, a_stride, rows, cols = _rows(a, "a", _CODES)
+    if w.dim() != 3:
+        raise ValueError("w must be [G, N, >= K]")
+    G, N, w_stride = w.shape
+    if w_stride < K or cols < K:
         raise ValueError("a must be [rows, >= K] and w [G, N, >= K]")
-    rows, (G, N, w_stride) = a.shape[0], w.shape
     if rows == 0:
         return MOE_OK
-    if c.shape != (rows, N) or c.dtype not in _ANY_DTYPE:
+    out = _ANY_DTYPE.get(c.dtype)
+    if out is None or c.shape != (rows, N):
         raise ValueError("c must be [rows, N] in bf16, fp16, fp32 or int32")
     if group_rows is not None and group_rows.numel() != G:
         raise ValueError("group_rows must have G entries")
     rp, rstride = (None, 4) if row_scale is None else _strided(row_scale, rows, "row_scale")
     st = _lib.moe_linear_i8(
-        ap, rows, a_stride, _ptr(w, i8, None, "w"), w_stride, G, N, int(K),
-        _ptr(group_rows, torch.int32, G, "group_rows"),
-        _ptr(col_scale, torch.float32, G * N, "col_scale"), rp, rstride,
-        _ptr(bias, torch.float32, G * N, "bias"), _ptr(c, None, None, "c"),
-        _ANY_DTYPE[c.dtype], _ptr(dev_status, torch.int32, 1, "dev_status"), _stream(stream))
+        ap, rows, a_stride, _ptr(w, _CODES, None, "w"), w_stride, G, N, int(K),
+        _ptr(group_rows, _I32, G, "group_rows"), _ptr(col_scale, _F32, G * N, "col_scale"),
+        rp, rstride, _ptr(bias, _F32, G * N, "bias"), _ptr(c, None, None, "c"), out,
+        _ptr(dev_status, _I32, 1, "dev_status"), _stream(stream))
     return _check(st, "moe_linear_i8")
 
 
