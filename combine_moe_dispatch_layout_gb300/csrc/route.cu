@@ -20,8 +20,8 @@
 // spread over the lanes; with two values kept it was not).
 //
 // Measured: 32,768 tokens x 256 fp32 logits, sigmoid with bias, 4 of 8 groups, k = 8:
-// 21.3 us, of which 9.5 are the read, the scan and the write, 2.3 the sigmoid and the
-// bias, 5.6 the seven further rounds, 3.9 the groups; 49,152 x 768 bf16, plain
+// 21.0 us, of which 9.4 are the read, the scan and the write, 2.3 the sigmoid and the
+// bias, 5.5 the seven further rounds, 3.8 the groups; 49,152 x 768 bf16, plain
 // softmax: 43 us.  Memory would allow 5.3 and 11.6: the schedulers issue in 74% of their
 // cycles and wait for the chain of a round in most others.  32 tokens: 3.3 us, a
 // launch.  Tried and not faster: 8 or 16 lanes per token (half the instructions, but
@@ -42,6 +42,15 @@ __device__ __forceinline__ float sigmoid_rank(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;"
       : "=f"(r) : "f"(__fadd_rn(1.0f, exp2_approx(__fmul_rn(x, -kLog2e)))));
+  return r;
+}
+// The same of two numbers.  nz: -0 (see mul2_rn).
+__device__ __forceinline__ float2 sigmoid_rank2(float2 x, float nz) {
+  const float2 t = mul2_rn(x, bcast2(-kLog2e), nz);
+  const float2 d = add2_rn(make_float2(exp2_approx(t.x), exp2_approx(t.y)), bcast2(1.0f));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
   return r;
 }
 // The score in full precision (the weights).
@@ -224,17 +233,21 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
     // every: every value is an expert's finite logit, the usual case
     auto rank = [&](auto every, auto&& f) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const float c = __fadd_rn(f(l[i]), bias[i]);
-        l[i] = decltype(every)::value || l[i] > kNegInf ? c : kNegInf;
+      for (int i = 0; i < VPT; i += 2) {
+        const float2 c = add2_rn(f(make_float2(l[i], l[i + 1])), make_float2(bias[i], bias[i + 1]));
+        l[i] = decltype(every)::value || l[i] > kNegInf ? c.x : kNegInf;
+        l[i + 1] = decltype(every)::value || l[i + 1] > kNegInf ? c.y : kNegInf;
       }
     };
-    auto soft = [&](float x) { return __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum); };
+    auto soft = [&](float2 x) {
+      return mul2_rn(exp_neg2(add2_rn(x, bcast2(-m)), nz), bcast2(inv_sum), nz);
+    };
+    auto sigmoid = [&](float2 x) { return sigmoid_rank2(x, nz); };
     const std::true_type yes;
     const std::false_type no;
     if (r.score == MOE_SOFTMAX) rank(no, soft);
-    else if (VPT * 32 > r.E || __any_sync(kAll, !(fabsf(probe) <= kMaxF))) rank(no, sigmoid_rank);
-    else rank(yes, sigmoid_rank);
+    else if (VPT * 32 > r.E || __any_sync(kAll, !(fabsf(probe) <= kMaxF))) rank(no, sigmoid);
+    else rank(yes, sigmoid);
     if (odd_bias) {                      // a NaN choice is no choice
 #pragma unroll
       for (int i = 0; i < VPT; ++i) l[i] = l[i] > kNegInf ? l[i] : kNegInf;
