@@ -255,7 +255,8 @@ def _grad_bound(l, ids, dw, score, renorm, scale):
 @pytest.mark.parametrize("T,E,k,dtype,pad", [
     (1, 1, 1, "fp32", 0), (7, 2, 2, "bf16", 0), (65, 60, 4, "bf16", 4), (130, 256, 8, "fp32", 0),
     (33, 257, 8, "fp32", 3), (40, 768, 8, "bf16", 0), (9, 1025, 40, "fp16", 0),
-    (5, 4096, 64, "fp32", 8)])
+    (5, 4096, 64, "fp32", 8), (37, 33, 8, "bf16", 0), (50, 100, 12, "fp16", 0),
+    (35, 33, 13, "fp32", 0), (37, 90, 20, "bf16", 6), (6, 5, 5, "fp16", 0)])
 def test_route_backward(ep, score, renorm, T, E, k, dtype, pad):
     l, dev = _logits(T, E, dtype, seed=T + E, pad=pad, masked=0.1)
     ids, _ = P.route(l, None, score, k)
@@ -306,6 +307,27 @@ def test_route_backward_bad_and_repeated_ids(ep):
     clean = np.where((ids < 0) | (ids >= 40), -1, ids)
     ref = P.route_backward(l, clean, dw, "sigmoid", False, 1.0)
     _assert_grad(got, ref, _grad_bound(l, clean, dw, "sigmoid", False, 1.0), "fp32")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("k", [5, 8, 12, 16, 20, 40])
+def test_route_backward_repeated_ids(ep, score, renorm, k):
+    """Tokens that name experts several times and others not at all, among
+    tokens that do not."""
+    T, E = 23, 48
+    l, dev = _logits(T, E, "fp32", seed=k)
+    rng = np.random.default_rng(k)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[2] = ids[2, 0]
+    ids[5, k - 1] = ids[5, 1]
+    ids[6, ::2] = -1
+    ids[22, 1:4] = ids[22, 0]
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    got, st = _backward(ep, dev, ids, dw, score, renorm, 1.5)
+    assert st == 0
+    ref = P.route_backward(l, ids, dw, score, renorm, 1.5)
+    _assert_grad(got, ref, _grad_bound(l, ids, dw, score, renorm, 1.5), "fp32")
 
 
 NEG = float("-inf")
