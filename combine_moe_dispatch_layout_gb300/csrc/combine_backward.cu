@@ -52,6 +52,8 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
   const bool producer = tid >= ncomp;
   const int nch = H / 8;
 
+  wait_for_stream();
+  let_next_start();
   int64_t g = blockIdx.x;
   if (producer)
     resolve_token(g, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k, epr,
@@ -137,6 +139,8 @@ combine_backward_warp_kernel(const uint4* __restrict__ d_out, const uint4* __res
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nch = H / 8;
   const int64_t g = int64_t(blockIdx.x) * kTokenWarps + warp;
+  wait_for_stream();
+  let_next_start();
   if (g >= T) return;
   uint4 q[CH];
 #pragma unroll
@@ -189,12 +193,10 @@ cudaError_t launch_t(const Shape& s, const void* d_out, const void* y, int64_t y
                      float* d_weights, int32_t* dev_status, cudaStream_t st) {
   const int nch = s.H / 8;
   auto by_warps = [&](auto kernel) {
-    const unsigned grid = static_cast<unsigned>((s.T() + kTokenWarps - 1) / kTokenWarps);
-    kernel<<<grid, kTokenWarps * 32, 0, st>>>(
-        static_cast<const uint4*>(d_out), static_cast<const uint4*>(y), y_rows, topk_idx,
-        weights, send_idx, put_offset, rank_recv_base, s.R, s.bs, s.k, s.epr, s.H, s.T(),
-        static_cast<uint4*>(d_y), d_weights, dev_status);
-    return cudaGetLastError();
+    return launch_early(kernel, (s.T() + kTokenWarps - 1) / kTokenWarps, kTokenWarps * 32, 0, st,
+                        static_cast<const uint4*>(d_out), static_cast<const uint4*>(y), y_rows,
+                        topk_idx, weights, send_idx, put_offset, rank_recv_base, s.R, s.bs, s.k,
+                        s.epr, s.H, s.T(), static_cast<uint4*>(d_y), d_weights, dev_status);
   };
   // (H alone decides, so a sum's order depends on nothing else)
   if (nch <= 32) return by_warps(combine_backward_warp_kernel<DT, 1>);
@@ -210,11 +212,10 @@ cudaError_t launch_t(const Shape& s, const void* d_out, const void* y, int64_t y
     e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), threads, 0, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t grid = std::min<int64_t>(s.T(), int64_t(std::max(1, per_sm)) * sms);
-  kernel<<<static_cast<unsigned>(grid), threads, 0, st>>>(
-      static_cast<const uint4*>(d_out), static_cast<const uint4*>(y), y_rows, topk_idx,
-      weights, send_idx, put_offset, rank_recv_base, s.R, s.bs, s.k, s.epr, s.H, s.T(),
-      static_cast<uint4*>(d_y), d_weights, dev_status);
-  return cudaGetLastError();
+  return launch_early(kernel, grid, threads, 0, st, static_cast<const uint4*>(d_out),
+                      static_cast<const uint4*>(y), y_rows, topk_idx, weights, send_idx,
+                      put_offset, rank_recv_base, s.R, s.bs, s.k, s.epr, s.H, s.T(),
+                      static_cast<uint4*>(d_y), d_weights, dev_status);
 }
 
 }  // namespace

@@ -289,6 +289,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   const int split = SPLIT ? static_cast<int>(cluster_size()) / CG : 1;      // a power of two
   const int leader = crank - rank;             // the pair's first CTA, in the cluster
 
+  wait_for_stream();
+  let_next_start();
   if (p.group_rows) {        // the scan borrows the stages, which are not in use yet
     build_group_tables<kThreads>(p, block, ntn, smem, goff, tpre, dev_status);
   } else if (tid == 64) {
@@ -726,12 +728,14 @@ cudaError_t launch_kernel(const CUtensorMap& mw, const CUtensorMap& ma, const Li
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = static_cast<unsigned>(CG * plan.split);
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;      // see launch_early
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, plan.block, plan.box_rows, nbyte,
                             (p.K + BKB - 1) / BKB / plan.split,
                             (p.K + BKB - 1) / BKB % plan.split, -0.0f, dev_status);

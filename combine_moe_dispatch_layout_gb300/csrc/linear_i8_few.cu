@@ -133,6 +133,8 @@ linear_i8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
   extern __shared__ int s_tables[];
   __shared__ int64_t s_scan[kThreads * 12 / 8];
   __shared__ int s_sums[kWarps][kChannels * kTokens];
+  wait_for_stream();
+  let_next_start();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = warp % parts, slot = warp / parts;
   const int chans = kWarps / parts * kChannels;          // channels per CTA
@@ -216,9 +218,7 @@ cudaError_t launch_linear_i8_few(const LinearArgs& p, int32_t* dev_status, cudaS
     parts *= 2;
   if (ctas(parts) > INT32_MAX) return cudaErrorInvalidValue;
   const int64_t grid = std::min(ctas(parts), room);
-  linear_i8_few_kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(p, parts,
-                                                                            dev_status);
-  return cudaGetLastError();
+  return launch_early(linear_i8_few_kernel, grid, kThreads, smem, st, p, parts, dev_status);
 }
 
 }  // namespace moe_ep

@@ -131,6 +131,8 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
   const bool want_sum = r.score == MOE_SOFTMAX && (!r.renormalise || BIAS || grouped);
 
   const int64_t t = int64_t(blockIdx.x) * kWarps + warp;
+  wait_for_stream();
+  let_next_start();
   if (t >= r.T) return;
   const T* row = static_cast<const T*>(r.logits) + t * r.stride;
 
@@ -390,6 +392,8 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
   const bool grouped = r.topk_group < r.n_group;
   const int per = r.E / r.n_group;
 
+  wait_for_stream();
+  let_next_start();
   for (int64_t t = blockIdx.x; t < r.T; t += gridDim.x) {
     const T* row = static_cast<const T*>(r.logits) + t * r.stride;
     auto logit = [&](int e) {
@@ -504,10 +508,8 @@ cudaError_t launch_bias(const RouteArgs& r, int group_shift, int32_t* idx, float
                    (!grouped || per * el % 16 == 0);
   const bool vec_bias =
       reinterpret_cast<uintptr_t>(r.bias) % 16 == 0 && (!grouped || per % 4 == 0);
-  const unsigned grid = static_cast<unsigned>((r.T + kWarps - 1) / kWarps);
-  route_warp_kernel<DT, VPT, BIAS><<<grid, kWarps * 32, 0, st>>>(
-      r, vec, vec_bias, group_shift, per, idx, weights, -0.0f, dev_status);
-  return cudaGetLastError();
+  return launch_early(route_warp_kernel<DT, VPT, BIAS>, (r.T + kWarps - 1) / kWarps, kWarps * 32,
+                      0, st, r, vec, vec_bias, group_shift, per, idx, weights, -0.0f, dev_status);
 }
 
 template <int DT, int VPT>
@@ -551,9 +553,8 @@ cudaError_t launch_t(const RouteArgs& r, int32_t* idx, float* weights, int32_t* 
   if (e == cudaSuccess) e = kernel_blocks_per_sm(fn, kWideThreads, smem, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t grid = std::min<int64_t>(r.T, int64_t(std::max(1, per_sm)) * sms);
-  route_wide_kernel<DT><<<static_cast<unsigned>(grid), kWideThreads, smem, st>>>(
-      r, idx, weights, dev_status);
-  return cudaGetLastError();
+  return launch_early(route_wide_kernel<DT>, grid, kWideThreads, smem, st, r, idx, weights,
+                      dev_status);
 }
 
 }  // namespace

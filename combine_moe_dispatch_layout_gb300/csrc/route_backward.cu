@@ -122,6 +122,8 @@ route_backward_sparse_kernel(const RouteArgs r, bool vec, const int32_t* __restr
   constexpr int kTokens = 32 / W;
   const int lane = threadIdx.x & 31, j0 = lane & (W - 1);
   const int64_t t0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens;
+  wait_for_stream();
+  let_next_start();
   if (t0 >= r.T) return;
   const int64_t t = t0 + lane / W;
   const Slots<H> s = load_slots<DT, W, H>(r, t, t < r.T, j0, idx, d_weights, dev_status);
@@ -189,6 +191,8 @@ route_backward_dense_kernel(const RouteArgs r, const int32_t* __restrict__ idx,
   constexpr int kPer16 = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  wait_for_stream();
+  let_next_start();
   if (t >= r.T) return;
   const T* row = static_cast<const T*>(r.logits) + t * r.stride;
   T* out = d_logits + t * r.E;
@@ -299,19 +303,17 @@ cudaError_t launch_sparse(const RouteArgs& r, const int32_t* idx, const float* d
   using T = typename Elem<DT>::T;
   constexpr int kTokens = kWarps * 32 / W;         // per CTA
   const bool vec = r.E * sizeof(T) * (32 / W) % 16 == 0;   // each warp's first row is aligned
-  route_backward_sparse_kernel<DT, W, H>
-      <<<static_cast<unsigned>((r.T + kTokens - 1) / kTokens), kWarps * 32, 0, st>>>(
-          r, vec, idx, d_weights, static_cast<T*>(d_logits), dev_status);
-  return cudaGetLastError();
+  return launch_early(route_backward_sparse_kernel<DT, W, H>, (r.T + kTokens - 1) / kTokens,
+                      kWarps * 32, 0, st, r, vec, idx, d_weights, static_cast<T*>(d_logits),
+                      dev_status);
 }
 
 template <int DT, int CHUNKS, int H>
 cudaError_t launch_dense(const RouteArgs& r, const int32_t* idx, const float* d_weights,
                          void* d_logits, int32_t* dev_status, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((r.T + kWarps - 1) / kWarps);
-  route_backward_dense_kernel<DT, CHUNKS, H><<<grid, kWarps * 32, 0, st>>>(
-      r, idx, d_weights, static_cast<typename Elem<DT>::T*>(d_logits), -0.0f, dev_status);
-  return cudaGetLastError();
+  return launch_early(route_backward_dense_kernel<DT, CHUNKS, H>, (r.T + kWarps - 1) / kWarps,
+                      kWarps * 32, 0, st, r, idx, d_weights,
+                      static_cast<typename Elem<DT>::T*>(d_logits), -0.0f, dev_status);
 }
 
 template <int DT, int H>
