@@ -17,7 +17,7 @@
 // lines are still in L2.  Plain softmax keeps the row's exponentials in registers
 // between its two sums and the write.
 //
-// Measured: 32,768 x 256 fp32, renormalised sigmoid, k = 8: 7.5 us (4.5 TB/s of
+// Measured: 32,768 x 256 fp32, renormalised sigmoid, k = 8: 7.9 us (4.3 TB/s of
 // writes; 12.5 with a warp per token, zeros after the sums: the chain id -> logit ->
 // sums was paid four times as often).  49,152 x 768 bf16, plain softmax: 30.7 us, 4.9
 // TB/s both ways; the exponentials' instructions (75% of the issue slots) are what
@@ -126,7 +126,6 @@ route_backward_sparse_kernel(const RouteArgs r, bool vec, const int32_t* __restr
   let_next_start();
   if (t0 >= r.T) return;
   const int64_t t = t0 + lane / W;
-  const Slots<H> s = load_slots<DT, W, H>(r, t, t < r.T, j0, idx, d_weights, dev_status);
 
   T* out = d_logits + t0 * r.E;
   const int fill = static_cast<int>(min(r.T - t0, int64_t(kTokens))) * r.E;
@@ -135,6 +134,7 @@ route_backward_sparse_kernel(const RouteArgs r, bool vec, const int32_t* __restr
     reinterpret_cast<uint4*>(out)[c] = make_uint4(0u, 0u, 0u, 0u);
   for (int i = pieces * kPer16 + lane; i < fill; i += 32) out[i] = to_elem<DT>(0.0f);
 
+  const Slots<H> s = load_slots<DT, W, H>(r, t, t < r.T, j0, idx, d_weights, dev_status);
   float p[H], rest[H], v[H];           // score, and 1 - score of a sigmoid
   if (r.score == MOE_SOFTMAX) {
     const float m = fmaxf(lanes_max<W>(H > 1 ? fmaxf(s.l[0], s.l[H - 1]) : s.l[0]), -kMaxF);

@@ -68,10 +68,13 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 template <int W>
 __device__ __forceinline__ float lanes_max(float v) {
-  if constexpr (W == 32) return warp_max(v);
+  if constexpr (W == 32) {
+    return warp_max(v);
+  } else {
 #pragma unroll
-  for (int d = W / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-  return v;
+    for (int d = W / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+    return v;
+  }
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
