@@ -110,6 +110,11 @@ constexpr int kThreads = 128 + 32 * (kConvWarps + kEpiWarps);
 constexpr int kEpiRegs = 152, kConvRegs = 40, kCtrlRegs = 40;
 static_assert(32 * (kEpiWarps * kEpiRegs + kConvWarps * kConvRegs + 4 * kCtrlRegs) <=
                   kThreads * 72, "no more registers than the launch has");
+// Tiles of up to 128 tokens hold 64 sums per draining thread and leave 8 registers
+// more to a widening one (with 40 it spilled).
+constexpr int kEpiRegs128 = 136, kConvRegs128 = 48;
+static_assert(32 * (kEpiWarps * kEpiRegs128 + kConvWarps * kConvRegs128 + 4 * kCtrlRegs) <=
+                  kThreads * 72, "no more registers than the launch has");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAccCols = 256;   // column offset of the second accumulator
 constexpr int kMaxByteStages = 12, kMaxF16Stages = 6;
@@ -279,7 +284,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   auto tempty = [&](int b) { return bars + 8 * (kT0 + 2 + b); };           // ... drained
   const uint32_t tmem_slot = bars + 8 * (kT0 + 4), abort_flag = tmem_slot + 4;
   auto srows = [&](int s) { return abort_flag + 4 + 4 * s; };   // rows in byte stage s
-  static_assert(8 * (kT0 + 5) + 4 * kMaxByteStages <= St::kBarBytes, "barriers fit");
+  const uint32_t issued = srows(kMaxByteStages);   // the pair's commits: of stages, of chunks
+  static_assert(8 * (kT0 + 5) + 4 * kMaxByteStages + 8 <= St::kBarBytes, "barriers fit");
   const uint32_t goff = bars + St::kBarBytes, tpre = goff + 4 * (p.G + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -338,6 +344,21 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   auto stage_begin = [&]() { return part * stages + min(part, extra); };
   auto stage_count = [&]() { return stages + (part < extra ? 1 : 0); };
   auto chunk_count = [&](int nk) { return (nk + kChunk - 1) / kChunk; };
+  // Waits for the last commit on each of this CTA's barriers, once all of them are
+  // issued: ncommit of fp16 stages, nchunk of accumulators.  A barrier's n-th commit
+  // is issued only after this CTA's threads have seen its n-1-th, so at most one is
+  // outstanding and the parity tells (it would not while commits are still to be
+  // issued: a phase two uses back looks the same).  Also after a timeout.
+  auto await_commits = [&](uint32_t ncommit, uint32_t nchunk) {
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t i = ncommit > uint32_t(NF) ? ncommit - NF : 0; i < ncommit; ++i)
+      ok &= bar_wait(fempty(i % NF), (i / NF) & 1u);
+#pragma unroll 1
+    for (uint32_t i = nchunk > 2 ? nchunk - 2 : 0; i < nchunk; ++i)
+      ok &= bar_wait(tfull(i & 1u), (i >> 1) & 1u);
+    if (!ok) set_status(dev_status, MOE_ERR_TIMEOUT);
+  };
 
   if (warp < 4) {
     regs_fewer<kCtrlRegs>();
@@ -428,24 +449,18 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
         smem_store(abort_flag, 1);
       }
-      // every commit has arrived (the last one of each barrier) before the CTA
-      // may go, also after a timeout
-      for (uint32_t i = ncommit > uint32_t(NF) ? ncommit - NF : 0; i < ncommit; ++i)
-        if (!bar_wait(fempty(i % NF), (i / NF) & 1u))
-          set_status(dev_status, MOE_ERR_TIMEOUT);
-      for (uint32_t i = chunk > 2 ? chunk - 2 : 0; i < chunk; ++i)
-        if (!bar_wait(tfull(i & 1u), (i >> 1) & 1u))
-          set_status(dev_status, MOE_ERR_TIMEOUT);
+      await_commits(ncommit, chunk);
+      // the pair's other CTA, whose barriers the commits arrive on too, learns how
+      // many there were; it waits for them after the closing barrier
+      if (issue) {
+        const uint32_t to = cluster_addr(issued, leader + 1);
+        cluster_store(to, ncommit);
+        cluster_store(to + 4, chunk);
+        smem_store(issued, 0);            // none left for this one
+        smem_store(issued + 4, 0);
+      }
     } else {
       cluster_wait_all();
-    }
-    if (warp == 1 && rank != 0) {
-      // the leader's last commits reach this CTA's barriers before it may go
-      const uint32_t ntile = first < tiles ? (tiles - first + step - 1) / step : 0;
-      const uint32_t ncommit = ntile * nk * kHalves;
-      for (uint32_t i = ncommit > uint32_t(NF) ? ncommit - NF : 0; i < ncommit; ++i)
-        for (uint32_t k = 0; k < kGemmSpin && !smem_load(abort_flag); ++k)
-          if (bar_poll(fempty(i % NF), (i / NF) & 1u)) break;
     }
     __syncwarp();
     if constexpr (SPLIT) {
@@ -454,7 +469,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     }
   } else if (warp < 4 + kConvWarps) {
     // ---- bytes -> fp16 ------------------------------------------------------------------
-    regs_fewer<kConvRegs>();
+    regs_fewer<NT == 128 ? kConvRegs128 : kConvRegs>();
     // groups of four warps, each on one 64-code half of every other byte stage:
     // one group's waits and fences overlap the others' widening.  A thread takes
     // 16 codes (quarter uc of the half) of one row in kRows.  Eight neighbouring
@@ -541,7 +556,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     }
   } else {
     // ---- chunk sums -> int32, scales, stores ----------------------------------------------
-    regs_more<kEpiRegs>();
+    regs_more<NT == 128 ? kEpiRegs128 : kEpiRegs>();
     constexpr int kParts = kEpiWarps / 4, kCols = NT / kParts;   // columns per thread
     const int q = warp & 3;                  // TMEM lanes 32 q ..
     const int col0 = ((warp - 4 - kConvWarps) >> 2) * kCols;
@@ -696,9 +711,11 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 
   tc_fence_before();
   __syncthreads();
-  // no CTA of a pair goes while the other may still arrive on its barriers
+  // no CTA of a pair goes while the other's threads may still arrive on its barriers ...
   cluster_sync();
   if (warp == 1) {
+    // ... nor while a commit may (the first CTA's role has waited for its own)
+    await_commits(smem_load(issued), smem_load(issued + 4));
     __syncwarp();
     tc_fence_after();
     pair_tmem_free(smem_load(tmem_slot), kTmemCols);

@@ -133,6 +133,9 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
+__device__ __forceinline__ void cluster_store(uint32_t caddr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_store16(uint32_t caddr, const int32_t* v) {
   asm volatile("st.shared::cluster.v4.s32 [%0], {%1,%2,%3,%4};" ::"r"(caddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
