@@ -396,12 +396,14 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         }
         ok = ok && !smem_load(abort_flag);
       }
-      if (!ok) {      // after a timeout, no copy may land once the CTA has gone
+      if (!ok) {
         if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
         smem_store(abort_flag, 1);
-        for (uint32_t i = nload > uint32_t(nbyte) ? nload - nbyte : 0; i < nload; ++i)
-          bar_wait(bfull(i % nbyte), (i / nbyte) & 1u);
       }
+      // no copy may land once the CTA has gone (the widening warps wait for all of
+      // them, unless one of them has given up)
+      for (uint32_t i = nload > uint32_t(nbyte) ? nload - nbyte : 0; i < nload; ++i)
+        bar_wait(bfull(i % nbyte), (i / nbyte) & 1u);
       cluster_wait_all();
     } else if (warp == 1 && rank == 0) {
       // ---- products (of the pair, by its first CTA) -----------------------------------

@@ -16,7 +16,7 @@ As the kernel does it:
   other role joins at its end;
 - a wait that runs out sets the CTA's abort flag, and the role goes to its end.
 
-Checks: when a CTA goes, no commit may still arrive in it, the
+Checks: when a CTA goes, nothing may still arrive in it (a copy, a commit), the
 pair's products are done, every wait of the closing part ends, and all barriers
 balance (every CTA does go); without timeouts every chunk is read by every warp."""
 import os
@@ -61,6 +61,7 @@ class Cta:
         self.tfull = [Bar(1) for _ in range(2)]
         self.tempty = [Bar(2 * warps) for _ in range(2)]
         self.abort = False
+        self.coming = 0                 # copies in flight
         self.issued = None              # what the first CTA tells of its commits
         self.at_block = 0
         self.read = set()
@@ -71,12 +72,12 @@ class Cluster:
     """`pairs` pairs share one tile's K (split), or one pair walks `tiles` tiles."""
 
     def __init__(self, seed, pairs, tiles, nk, chunk, nbyte, warps, limit, early_wait=False,
-                 idle=False):
+                 own_drain=False, idle=False):
         self.rng = random.Random(seed)
         self.split = pairs > 1
         self.tiles = 0 if idle else (1 if self.split else tiles)
         self.nk, self.chunk, self.nbyte, self.warps = nk, chunk, nbyte, warps
-        self.limit, self.early_wait = limit, early_wait
+        self.limit, self.early_wait, self.own_drain = limit, early_wait, own_drain
         self.ctas = [[Cta(p, r, nbyte, warps) for r in range(2)] for p in range(pairs)]
         self.flat = [c for pair in self.ctas for c in pair]
         self.mma_issued = [0] * pairs
@@ -121,6 +122,7 @@ class Cluster:
                     self.give_up(c)
                     break
                 self.fills.append((c, s))
+                c.coming += 1
                 n += 1
                 s += 1
                 if s == self.nbyte:
@@ -130,7 +132,7 @@ class Cluster:
             if not ok:
                 c.abort = True
                 break
-        for i in range(max(0, n - self.nbyte), n if not ok else 0):
+        for i in range(max(0, n - self.nbyte), 0 if self.own_drain and ok else n):
             got = yield from self.wait(c.bfull[i % self.nbyte], (i // self.nbyte) & 1, DRAIN)
             assert got, "a closing wait ran out"
         yield from self.finish(c)
@@ -252,6 +254,8 @@ class Cluster:
             c.left += 1
             if c.rank == 1 and not self.early_wait:
                 yield from self.await_commits(c, *c.issued)
+            if c.coming:
+                self.faults.append("a copy is still in flight")
             if any(to is c for _, _, to, _ in self.commits):
                 self.faults.append("a commit may arrive in a CTA that has gone")
             if self.mma_done[c.pair] != self.mma_issued[c.pair]:
@@ -271,6 +275,7 @@ class Cluster:
         kind = self.rng.choice(some)
         if kind == "copy":
             c, s = self.fills.pop(self.rng.randrange(len(self.fills)))
+            c.coming -= 1
             c.bfull[s].arrive()
         elif kind == "mma":
             p = self.rng.choice([p for p in range(len(self.ctas))
@@ -343,6 +348,20 @@ def test_a_wait_that_starts_before_the_commits_guards_nothing():
         c = Cluster(seed, 1, 1, 6, 2, 3, 1, DRAIN, early_wait=True).run(0.02)
         left += "a commit may arrive in a CTA that has gone" in c.faults
     assert left > 0
+
+
+def test_copies_are_waited_for_also_when_another_role_gave_up():
+    """A copying warp that waits only after a timeout of its own leaves copies
+    behind that a widening warp no longer waits for."""
+    left = 0
+    for seed in range(60):
+        c = Cluster(seed, 1, 1, 3, 2, 5, 1, 3, own_drain=True).run(0.02)
+        left += "a copy is still in flight" in c.faults
+    assert left > 0
+    kernel = _code().split("linear_i8_tile_kernel", 1)[1]
+    role = kernel[kernel.index("tensor_load_2d"):kernel.index("cluster_wait_all();")]
+    own = role[role.index("if (!ok) {"):]
+    assert own.index("}") < own.index("bar_wait(bfull(i % nbyte)")
 
 
 def _code():
