@@ -36,14 +36,11 @@ constexpr unsigned kAll = 0xffffffffu;
 
 template <int DT>
 __global__ void __launch_bounds__(kMaxThreads, 2)
-combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict__ y,
-                        int64_t y_rows, const int32_t* __restrict__ topk_idx,
-                        const float* __restrict__ weights,
-                        const int32_t* __restrict__ send_idx,
-                        const int32_t* __restrict__ put_offset,
-                        const int64_t* __restrict__ rank_recv_base, int R, int bs, int k,
-                        int epr, int H, int64_t T, uint4* __restrict__ d_y,
-                        float* __restrict__ d_weights, int32_t* dev_status) {
+combine_backward_kernel(const uint4* d_out, const uint4* y, int64_t y_rows,
+                        const int32_t* topk_idx, const float* weights, const int32_t* send_idx,
+                        const int32_t* put_offset, const int64_t* rank_recv_base, int R, int bs,
+                        int k, int epr, int H, int64_t T, uint4* d_y, float* d_weights,
+                        int32_t* dev_status) {
   __shared__ int64_t s_rows[2][MOE_EP_MAX_TOPK];
   __shared__ float s_w[2][MOE_EP_MAX_TOPK];
   __shared__ float s_dot[2][kMaxThreads / 32][MOE_EP_MAX_TOPK];
@@ -56,8 +53,8 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
   let_next_start();
   int64_t g = blockIdx.x;
   if (producer)
-    resolve_token(g, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k, epr,
-                  y_rows, s_rows[0], s_w[0], dev_status, lane);
+    resolve_token<true>(g, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k, epr,
+                        y_rows, s_rows[0], s_w[0], dev_status, lane);
   __syncthreads();
 
   for (int it = 0; g < T; ++it, g += gridDim.x) {
@@ -65,8 +62,8 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
     if (producer) {
       const int64_t gn = g + gridDim.x;
       if (gn < T)
-        resolve_token(gn, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k,
-                      epr, y_rows, s_rows[buf ^ 1], s_w[buf ^ 1], dev_status, lane);
+        resolve_token<true>(gn, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k,
+                            epr, y_rows, s_rows[buf ^ 1], s_w[buf ^ 1], dev_status, lane);
     } else {
       for (int k0 = 0; k0 < k; k0 += kBatch) {
         float dot[kBatch];
@@ -77,10 +74,10 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
 #pragma unroll
           for (int b = 0; b < kBatch; ++b) {
             const int64_t row = k0 + b < k ? s_rows[buf][k0 + b] : -1;
-            v[b] = row >= 0 ? ld_stream_16(y + row * nch + c) : make_uint4(0u, 0u, 0u, 0u);
+            v[b] = row >= 0 ? ld_once_16(y + row * nch + c) : make_uint4(0u, 0u, 0u, 0u);
           }
           float d[8];
-          unpack8<DT>(__ldg(d_out + g * nch + c), d);
+          unpack8<DT>(d_out[g * nch + c], d);
 #pragma unroll
           for (int b = 0; b < kBatch; ++b) {
             const int64_t row = k0 + b < k ? s_rows[buf][k0 + b] : -1;
@@ -125,14 +122,11 @@ combine_backward_kernel(const uint4* __restrict__ d_out, const uint4* __restrict
 // with 2 rows at a time took 22 us, CH = 1 with 16 45.
 template <int DT, int CH>
 __global__ void __launch_bounds__(kTokenWarps * 32)
-combine_backward_warp_kernel(const uint4* __restrict__ d_out, const uint4* __restrict__ y,
-                             int64_t y_rows, const int32_t* __restrict__ topk_idx,
-                             const float* __restrict__ weights,
-                             const int32_t* __restrict__ send_idx,
-                             const int32_t* __restrict__ put_offset,
-                             const int64_t* __restrict__ rank_recv_base, int R, int bs, int k,
-                             int epr, int H, int64_t T, uint4* __restrict__ d_y,
-                             float* __restrict__ d_weights, int32_t* dev_status) {
+combine_backward_warp_kernel(const uint4* d_out, const uint4* y, int64_t y_rows,
+                             const int32_t* topk_idx, const float* weights, const int32_t* send_idx,
+                             const int32_t* put_offset, const int64_t* rank_recv_base, int R, int bs,
+                             int k, int epr, int H, int64_t T, uint4* d_y, float* d_weights,
+                             int32_t* dev_status) {
   constexpr int kRows = CH == 1 ? 8 : 4;
   __shared__ int64_t s_rows[kTokenWarps][MOE_EP_MAX_TOPK];
   __shared__ float s_w[kTokenWarps][MOE_EP_MAX_TOPK];
@@ -145,10 +139,9 @@ combine_backward_warp_kernel(const uint4* __restrict__ d_out, const uint4* __res
   uint4 q[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c)
-    q[c] = lane + 32 * c < nch ? __ldg(d_out + g * nch + lane + 32 * c)
-                               : make_uint4(0u, 0u, 0u, 0u);
-  resolve_token(g, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k, epr,
-                y_rows, s_rows[warp], s_w[warp], dev_status, lane);
+    q[c] = lane + 32 * c < nch ? d_out[g * nch + lane + 32 * c] : make_uint4(0u, 0u, 0u, 0u);
+  resolve_token<true>(g, topk_idx, weights, send_idx, put_offset, rank_recv_base, R, bs, k, epr,
+                      y_rows, s_rows[warp], s_w[warp], dev_status, lane);
   __syncwarp();
   for (int k0 = 0; k0 < k; k0 += kRows) {
     uint4 v[kRows][CH];
@@ -157,7 +150,7 @@ combine_backward_warp_kernel(const uint4* __restrict__ d_out, const uint4* __res
       const int64_t row = k0 + b < k ? s_rows[warp][k0 + b] : -1;
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        v[b][c] = row >= 0 && lane + 32 * c < nch ? ld_stream_16(y + row * nch + lane + 32 * c)
+        v[b][c] = row >= 0 && lane + 32 * c < nch ? ld_once_16(y + row * nch + lane + 32 * c)
                                                   : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll

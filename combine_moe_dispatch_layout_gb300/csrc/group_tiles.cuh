@@ -10,7 +10,7 @@ namespace moe_ep {
 // there is one group of every row.
 __device__ __forceinline__ int group_count(const LinearArgs& p, int g, int32_t* dev_status) {
   if (!p.group_rows) return static_cast<int>(p.a_rows);
-  const int c = __ldg(p.group_rows + g);
+  const int c = p.group_rows[g];
   if (c < 0 && dev_status) set_status(dev_status, MOE_ERR_INVALID_ARG);
   return c < 0 ? 0 : c;
 }

@@ -204,16 +204,16 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
 // Scales and bias of channel n of group g, and of row m (int32 outputs take none).
 template <int OUT>
 __device__ __forceinline__ float col_scale(const LinearArgs& p, int g, int n) {
-  return OUT == MOE_INT32 ? 0.0f : __ldg(p.col_scale + int64_t(g) * p.N + n);
+  return OUT == MOE_INT32 ? 0.0f : p.col_scale[int64_t(g) * p.N + n];
 }
 template <int OUT>
 __device__ __forceinline__ float row_scale(const LinearArgs& p, int64_t m) {
   return OUT == MOE_INT32
              ? 0.0f
-             : __ldg(reinterpret_cast<const float*>(p.row_scale + m * p.row_scale_stride));
+             : *reinterpret_cast<const float*>(p.row_scale + m * p.row_scale_stride);
 }
 __device__ __forceinline__ float bias_of(const LinearArgs& p, int g, int n) {
-  return __ldg(p.bias + int64_t(g) * p.N + n);
+  return p.bias[int64_t(g) * p.N + n];
 }
 
 // One output: its scales, its bias, its rounding.

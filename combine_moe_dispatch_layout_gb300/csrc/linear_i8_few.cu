@@ -86,7 +86,7 @@ __device__ __forceinline__ void channels_by_tokens(const uint8_t* w, int64_t w_s
                                                    int last, const uint8_t* a,
                                                    int64_t a_stride, int tokens, int K,
                                                    int part, int parts, int lane, int* sums) {
-  auto weights = [&](int r, int j) { return ld_stream_16(w + min(r, last) * w_stride + j); };
+  auto weights = [&](int r, int j) { return ld_once_16(w + min(r, last) * w_stride + j); };
   constexpr int CH = kChannels;
   int acc[CH * TB];
 #pragma unroll
@@ -114,7 +114,7 @@ __device__ __forceinline__ void channels_by_tokens(const uint8_t* w, int64_t w_s
     for (int t = 0; t < TB; ++t) {
       // (a weight row's bytes past K meet zeros here)
       const uint8_t* at = a + (t < tokens ? t : tokens - 1) * a_stride + j;
-      uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+      uint4 x = *reinterpret_cast<const uint4*>(at);
       if (j + 16 > K) x = keep_bytes(x, K - j);
 #pragma unroll
       for (int r = 0; r < CH; ++r) acc[r * TB + t] = dot16(cur[r], x, acc[r * TB + t]);
@@ -182,9 +182,9 @@ linear_i8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
         continue;
       }
       const float row =
-          __ldg(reinterpret_cast<const float*>(p.row_scale + m * p.row_scale_stride));
-      float v = __fmul_rn(__fmul_rn(__int2float_rn(acc), __ldg(p.col_scale + gn)), row);
-      if (p.bias) v = __fadd_rn(v, __ldg(p.bias + gn));
+          *reinterpret_cast<const float*>(p.row_scale + m * p.row_scale_stride);
+      float v = __fmul_rn(__fmul_rn(__int2float_rn(acc), p.col_scale[gn]), row);
+      if (p.bias) v = __fadd_rn(v, p.bias[gn]);
       if (p.c_dtype == MOE_FP32)
         static_cast<float*>(p.c)[at] = v;
       else

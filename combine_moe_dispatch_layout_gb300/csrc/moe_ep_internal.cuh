@@ -308,27 +308,34 @@ __device__ __forceinline__ float2 swiglu2_rn(float2 gate, float2 up, float nz) {
   return mul2_rn(sg, up, nz);
 }
 
+// An argument's element: EARLY in a kernel that launch_early starts (see there).
+template <bool EARLY, class T>
+__device__ __forceinline__ T ld_arg(const T* p) {
+  if constexpr (EARLY) return *p;
+  else return __ldg(p);
+}
+
 // Combine: resolve the receive rows and gate weights of token g into the
 // shared tables rows[k], w[k] (one warp; lane kk handles pair kk).  A bad
 // expert id or a row outside [0, y_rows) gives row -1 and a status code.
+template <bool EARLY = false>
 __device__ __forceinline__ void resolve_token(
-    int64_t g, const int32_t* __restrict__ topk_idx,
-    const float* __restrict__ weights, const int32_t* __restrict__ send_idx,
-    const int32_t* __restrict__ put_offset,
-    const int64_t* __restrict__ rank_recv_base, int R, int bs, int k, int epr,
+    int64_t g, const int32_t* topk_idx, const float* weights, const int32_t* send_idx,
+    const int32_t* put_offset, const int64_t* rank_recv_base, int R, int bs, int k, int epr,
     int64_t y_rows, int64_t* rows, float* w, int32_t* dev_status, int lane) {
   const int E = R * epr;
   const int s = static_cast<int>(g / bs);
   for (int kk = lane; kk < k; kk += 32) {
     const int64_t pair = g * k + kk;
-    const int e = __ldg(topk_idx + pair);
-    const int32_t sidx = __ldg(send_idx + pair);
-    const float wt = __ldg(weights + pair);
+    const int e = ld_arg<EARLY>(topk_idx + pair);
+    const int32_t sidx = ld_arg<EARLY>(send_idx + pair);
+    const float wt = ld_arg<EARLY>(weights + pair);
     int64_t row = -1;
     if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) {
       set_status(dev_status, MOE_ERR_EXPERT_ID);
     } else {
-      row = __ldg(rank_recv_base + e / epr) + __ldg(put_offset + int64_t(e) * R + s) + sidx;
+      row = ld_arg<EARLY>(rank_recv_base + e / epr) +
+            ld_arg<EARLY>(put_offset + int64_t(e) * R + s) + sidx;
       if (row < 0 || row >= y_rows) {
         set_status(dev_status, MOE_ERR_CAPACITY);
         row = -1;
@@ -344,6 +351,10 @@ __device__ __forceinline__ void resolve_token(
 // still runs (if that one allows it, or at its end, without the pause between two
 // launches); it calls wait_for_stream() before it first touches memory that is not
 // its own, and from there on everything earlier in the stream is done and visible.
+// Its loads are ordinary ones: the read-only path (__ldg, or what the compiler makes of
+// a const __restrict__ pointer) asks that nobody write the data for the kernel's whole
+// life, which begins while the previous kernel still writes, and such a load may be
+// moved across the wait.
 // (Call after call on one stream: one token by 4096 x 7168 9.5 -> 7.5 us, 197 x 1001 x
 // 1992 12.3 -> 10.6, routing 32,768 tokens 24.6 -> 21.8.)
 __device__ __forceinline__ void wait_for_stream() {
@@ -352,6 +363,14 @@ __device__ __forceinline__ void wait_for_stream() {
 // The stream's next kernel, if launched early, may take up SMs that this one leaves free.
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// ld_stream_16 by an ordinary load.
+__device__ __forceinline__ uint4 ld_once_16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), int64_t grid, int block, size_t smem,

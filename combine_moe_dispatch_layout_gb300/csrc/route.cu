@@ -141,7 +141,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
   if (VPT % kPer16 == 0 && vec && mine == VPT) {
 #pragma unroll
     for (int c = 0; c < VPT / kPer16; ++c) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
+      const uint4 v = reinterpret_cast<const uint4*>(row + e0)[c];
       unpack_logits<DT>(v, l + c * kPer16);
     }
   } else {
@@ -154,7 +154,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
     if (VPT % 4 == 0 && vec_bias && mine == VPT) {
 #pragma unroll
       for (int c = 0; c < VPT / 4; ++c) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(r.bias + e0) + c);
+        const float4 v = reinterpret_cast<const float4*>(r.bias + e0)[c];
         bias[4 * c] = v.x;
         bias[4 * c + 1] = v.y;
         bias[4 * c + 2] = v.z;
@@ -162,7 +162,7 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) bias[i] = i < mine ? __ldg(r.bias + e0 + i) : 0.0f;
+      for (int i = 0; i < VPT; ++i) bias[i] = i < mine ? r.bias[e0 + i] : 0.0f;
     }
     float2 all = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -430,7 +430,7 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
       const float l = logit(e);
       float c = r.score == MOE_SOFTMAX ? __fmul_rn(exp_neg(__fsub_rn(l, m)), inv_sum)
                                        : sigmoid_rank(l);
-      if (r.bias) c = __fadd_rn(c, __ldg(r.bias + e));
+      if (r.bias) c = __fadd_rn(c, r.bias[e]);
       const bool on = l > kNegInf && c > kNegInf;
       key[e] = on ? order_key(r.bias ? c : l) : 0u;
       choice[e] = on ? c : kNegInf;

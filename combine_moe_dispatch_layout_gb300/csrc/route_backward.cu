@@ -54,9 +54,8 @@ struct Slots {
 // at: the token, there: it exists.
 template <int DT, int W, int H>
 __device__ __forceinline__ Slots<H> load_slots(const RouteArgs& r, int64_t at, bool there,
-                                               int j0, const int32_t* __restrict__ idx,
-                                               const float* __restrict__ d_weights,
-                                               int32_t* dev_status) {
+                                               int j0, const int32_t* idx,
+                                               const float* d_weights, int32_t* dev_status) {
   using T = typename Elem<DT>::T;
   const T* row = static_cast<const T*>(r.logits) + at * r.stride;
   Slots<H> s;
@@ -64,8 +63,8 @@ __device__ __forceinline__ Slots<H> load_slots(const RouteArgs& r, int64_t at, b
   for (int h = 0; h < H; ++h) {
     const int j = j0 + 32 * h;
     const bool mine = there && j < r.k;
-    s.e[h] = mine ? __ldg(idx + at * r.k + j) : -1;
-    s.g[h] = mine ? __fmul_rn(__ldg(d_weights + at * r.k + j), r.scale) : 0.0f;
+    s.e[h] = mine ? idx[at * r.k + j] : -1;
+    s.g[h] = mine ? __fmul_rn(d_weights[at * r.k + j], r.scale) : 0.0f;
     if (s.e[h] < -1 || s.e[h] >= r.E) {
       set_status(dev_status, MOE_ERR_EXPERT_ID);
       s.e[h] = -1;
@@ -113,9 +112,8 @@ __device__ __forceinline__ void join_repeated(const Slots<H>& s, int k, int lane
 // nothing, are on their way before the first load.  vec: 16-byte stores.
 template <int DT, int W, int H>
 __global__ void __launch_bounds__(kWarps * 32)
-route_backward_sparse_kernel(const RouteArgs r, bool vec, const int32_t* __restrict__ idx,
-                             const float* __restrict__ d_weights,
-                             typename Elem<DT>::T* __restrict__ d_logits,
+route_backward_sparse_kernel(const RouteArgs r, bool vec, const int32_t* idx,
+                             const float* d_weights, typename Elem<DT>::T* d_logits,
                              int32_t* dev_status) {
   using T = typename Elem<DT>::T;
   constexpr int kPer16 = 16 / sizeof(T);
@@ -183,9 +181,8 @@ route_backward_sparse_kernel(const RouteArgs r, bool vec, const int32_t* __restr
 // element by element.  H: slots per lane (1 for k <= 32, else 2).
 template <int DT, int CHUNKS, int H>
 __global__ void __launch_bounds__(kWarps * 32)
-route_backward_dense_kernel(const RouteArgs r, const int32_t* __restrict__ idx,
-                            const float* __restrict__ d_weights,
-                            typename Elem<DT>::T* __restrict__ d_logits, float nz,
+route_backward_dense_kernel(const RouteArgs r, const int32_t* idx,
+                            const float* d_weights, typename Elem<DT>::T* d_logits, float nz,
                             int32_t* dev_status) {
   using T = typename Elem<DT>::T;
   constexpr int kPer16 = 16 / sizeof(T);
@@ -205,8 +202,7 @@ route_backward_dense_kernel(const RouteArgs r, const int32_t* __restrict__ idx,
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       const int at = lane + 32 * c;
-      const uint4 q = at < pieces ? __ldg(reinterpret_cast<const uint4*>(row) + at)
-                                  : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 q = at < pieces ? reinterpret_cast<const uint4*>(row)[at] : make_uint4(0u, 0u, 0u, 0u);
       unpack_logits<DT>(q, x + c * kPer16);
     }
   }

@@ -21,8 +21,8 @@ struct Elem<MOE_FP32> { using T = float; };
 // A logit as fp32.
 template <int DT>
 __device__ __forceinline__ float load_logit(const typename Elem<DT>::T* p) {
-  if constexpr (DT == MOE_FP32) return __ldg(p);
-  else return widen<DT>(__ldg(p));
+  if constexpr (DT == MOE_FP32) return *p;
+  else return widen<DT>(*p);
 }
 // The 16 / sizeof(T) logits of a 16-byte piece.
 template <int DT>
