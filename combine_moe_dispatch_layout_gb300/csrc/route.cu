@@ -7,7 +7,8 @@
 // The k largest are taken one after another; weights are then recomputed for the
 // k chosen logits alone, in full precision, one per lane.  Softmax weights that
 // are renormalised are exp(l - max of the chosen) over their sum: the sum over
-// all experts cancels, so it is not computed.
+// all experts cancels, so it is not computed.  Sigmoid weights that are renormalised
+// take their common factor out first (sigmoid_scaled): small scores have quotients too.
 //
 // Warp kernel (E <= 1024): one warp per token, a lane holding VPT neighbouring
 // experts, so the lowest lane and the lowest position inside it are the lowest
@@ -53,10 +54,6 @@ __device__ __forceinline__ float2 sigmoid_rank2(float2 x, float nz) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
   return r;
 }
-// The score in full precision (the weights).
-__device__ __forceinline__ float sigmoid_full(float x) {
-  return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
-}
 
 // Ids and weights of token t (there: it exists) by W lanes: slots j0 (of this lane)
 // and, with H = 2 (k > 32), j0 + 32, from the chosen experts (sel = -1: none).
@@ -70,13 +67,17 @@ __device__ __forceinline__ void write_token(const RouteArgs& r, int64_t t, bool 
 #pragma unroll
   for (int h = 0; h < H; ++h)
     l[h] = sel[h] >= 0 ? fminf(load_logit<DT>(row + sel[h]), kMaxF) : kNegInf;
+  if (r.renormalise) m = lanes_max<W>(H > 1 ? fmaxf(l[0], l[H - 1]) : l[0]);
   if (r.score == MOE_SOFTMAX) {
-    if (r.renormalise) m = lanes_max<W>(H > 1 ? fmaxf(l[0], l[H - 1]) : l[0]);
 #pragma unroll
     for (int h = 0; h < H; ++h) s[h] = sel[h] >= 0 ? expf(__fsub_rn(l[h], m)) : 0.0f;
   } else {
+    m = r.renormalise ? fminf(m, 0.0f) : 0.0f;
 #pragma unroll
-    for (int h = 0; h < H; ++h) s[h] = sel[h] >= 0 ? sigmoid_full(l[h]) : 0.0f;
+    for (int h = 0; h < H; ++h) {
+      float rest;
+      s[h] = sel[h] >= 0 ? sigmoid_scaled(l[h], m, &rest) : 0.0f;
+    }
   }
   float d = 1.0f;
   if (r.renormalise) {

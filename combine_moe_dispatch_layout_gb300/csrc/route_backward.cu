@@ -133,21 +133,23 @@ route_backward_sparse_kernel(const RouteArgs r, bool vec, const int32_t* idx,
   for (int i = pieces * kPer16 + lane; i < fill; i += 32) out[i] = to_elem<DT>(0.0f);
 
   const Slots<H> s = load_slots<DT, W, H>(r, t, t < r.T, j0, idx, d_weights, dev_status);
-  float p[H], rest[H], v[H];           // score, and 1 - score of a sigmoid
+  // score (scaled by a common factor where it is renormalised), and 1 - score of a sigmoid
+  float p[H], rest[H], v[H];
+  float m = 0.0f;
+  if (r.renormalise)
+    m = fmaxf(lanes_max<W>(H > 1 ? fmaxf(s.l[0], s.l[H - 1]) : s.l[0]), -kMaxF);
   if (r.score == MOE_SOFTMAX) {
-    const float m = fmaxf(lanes_max<W>(H > 1 ? fmaxf(s.l[0], s.l[H - 1]) : s.l[0]), -kMaxF);
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       p[h] = s.e[h] >= 0 ? expf(__fsub_rn(s.l[h], m)) : 0.0f;
       rest[h] = 1.0f;
     }
   } else {
+    m = fminf(m, 0.0f);
 #pragma unroll
-    for (int h = 0; h < H; ++h) {      // e^-|l| serves both sides: no cancellation
-      const float ex = expf(-fabsf(s.l[h])), inv = __fdiv_rn(1.0f, __fadd_rn(1.0f, ex));
-      const float small = __fmul_rn(ex, inv);
-      p[h] = s.e[h] < 0 ? 0.0f : s.l[h] >= 0.0f ? inv : small;
-      rest[h] = s.l[h] >= 0.0f ? small : inv;
+    for (int h = 0; h < H; ++h) {
+      const float sig = sigmoid_scaled(s.l[h], m, &rest[h]);
+      p[h] = s.e[h] >= 0 ? sig : 0.0f;
     }
   }
   if (r.renormalise) {

@@ -101,4 +101,16 @@ __device__ __forceinline__ float2 exp_neg2(float2 x, float nz) {
   return fma2_rn(e, mul2_rn(r, bcast2(kLn2), nz), e);
 }
 
+// Sigmoid of x times e^-m = e^(min(x, 0) - m) / (1 + e^-|x|), m the smaller of 0 and
+// the largest chosen logit of the token.  No exponential exceeds 1, so nothing
+// overflows, and the largest of a token's scaled scores is at least 1/2, however far
+// below 0 its logits are (the scores alone are subnormal from -87 on and 0 from -104).
+// m = 0: the sigmoid itself.  rest: 1 - sigmoid(x), without cancellation.
+__device__ __forceinline__ float sigmoid_scaled(float x, float m, float* rest) {
+  const float ex = expf(-fabsf(x)), d = __fadd_rn(1.0f, ex);
+  const float top = x >= 0.0f ? 1.0f : m < 0.0f ? expf(__fsub_rn(x, m)) : ex;
+  *rest = __fdiv_rn(x >= 0.0f ? ex : 1.0f, d);
+  return __fdiv_rn(top, d);
+}
+
 }  // namespace moe_ep

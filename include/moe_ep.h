@@ -505,7 +505,9 @@ moe_status moe_deq_combine(const moe_shape* shape, const int32_t* expert_acc,
  * weight 0 (moe_dispatch_layout does not count such a pair, gives it send
  * index -1 and reports MOE_ERR_EXPERT_ID).  A NaN logit is read as -inf and
  * sets MOE_ERR_INVALID_ARG in *dev_status; +inf is read as the largest
- * finite number.  Renormalised weights of scores that sum to 0 are 0.
+ * finite number.  Renormalised weights are the quotients of the definition however
+ * small the scores are (chosen logits of -100, or of the type's lowest value, share a
+ * token as any others): only a token without an available expert has a sum of 0.
  *   logits        [T] rows of E values, logits_stride elements apart, in
  *                 logits_dtype (MOE_BF16, MOE_FP16 or MOE_FP32), aligned to
  *                 their element
