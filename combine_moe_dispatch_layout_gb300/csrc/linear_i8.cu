@@ -103,6 +103,8 @@ constexpr int kRasterTokens = 8;     // token blocks per raster band (weights re
 // 16 draining warps, 16384 x 7168 x 2048 took 317 us; this way 294.)
 constexpr int kGroupWarps = 4, kConvWarps = 16, kEpiWarps = 8;
 constexpr int kConvGroups = kConvWarps / kGroupWarps;
+constexpr int kTurns = kConvGroups / kHalves;      // groups take byte stages in turns
+static_assert(kTurns == 2, "turns");
 constexpr int kThreads = 128 + 32 * (kConvWarps + kEpiWarps);
 // Registers per thread: 72 at launch.  With pairs, whose draining threads hold 128
 // sums, they are handed out again by role: 256 x 152 + 512 x 40 + 128 x 40 = 64512
@@ -118,6 +120,7 @@ static_assert(32 * (kEpiWarps * kEpiRegs128 + kConvWarps * kConvRegs128 + 4 * kC
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAccCols = 256;   // column offset of the second accumulator
 constexpr int kMaxByteStages = 12, kMaxF16Stages = 6;
+static_assert(kTurns * kMaxByteStages <= 32, "a lane sets up each barrier");
 
 // LT: token rows that one CTA holds (a pair of CTAs shares the tile's tokens).
 template <int LT>
@@ -275,9 +278,15 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
   const uint32_t bars = sbase + St::kOffBytes + nbyte * St::kByteBytes;
-  auto bfull = [&](int s) { return bars + 8 * s; };                        // byte stage filled
-  auto bempty = [&](int s) { return bars + 8 * (kMaxByteStages + s); };    // ... widened
-  constexpr int kF0 = 2 * kMaxByteStages, kT0 = kF0 + 2 * kMaxF16Stages;
+  // Byte stage filled: one barrier per stage and turn (load i: barrier i modulo 2 nbyte,
+  // stage i modulo nbyte).  Were there one per stage, both turns of widening groups
+  // would wait on it where nbyte is odd, each skipping the other's phases; when loads
+  // land out of order, a group would take the parity of a phase two back for its own
+  // and read what the stage held before (seen with 3 stages and rows just copied: one
+  // call in 200).
+  auto bfull = [&](int i) { return bars + 8 * i; };
+  auto bempty = [&](int s) { return bars + 8 * (kTurns * kMaxByteStages + s); };   // ... widened
+  constexpr int kF0 = (kTurns + 1) * kMaxByteStages, kT0 = kF0 + 2 * kMaxF16Stages;
   auto ffull = [&](int f) { return bars + 8 * (kF0 + f); };                // fp16 stage written
   auto fempty = [&](int f) { return bars + 8 * (kF0 + kMaxF16Stages + f); };  // ... multiplied
   auto tfull = [&](int b) { return bars + 8 * (kT0 + b); };                // accumulator final
@@ -307,10 +316,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     smem_store(tpre + 4, row_blocks(rows, block) * ntn);
   }
   if (warp == 0) {           // barriers: one lane each
-    if (lane < nbyte) {
-      bar_init(bfull(lane), 1);
-      bar_init(bempty(lane), kHalves * kGroupWarps);
-    }
+    if (lane < kTurns * nbyte) bar_init(bfull(lane), 1);
+    if (lane < nbyte) bar_init(bempty(lane), kHalves * kGroupWarps);
     if (lane < NF) {
       bar_init(ffull(lane), CG * kGroupWarps);
       bar_init(fempty(lane), 1);
@@ -367,7 +374,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     if (warp == 0) {
       // ---- copies -------------------------------------------------------------------
       const bool issue = elect_one();
-      int s = 0;
+      int s = 0, full = 0;
       uint32_t phase = 0, nload = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += step) {
@@ -385,14 +392,15 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           if (issue) {
             const uint32_t dst = sbase + St::kOffBytes + s * St::kByteBytes;
             smem_store(srows(s), BM + rows);       // weight rows, then token rows
-            bar_expect(bfull(s), (BM + boxes * box_rows) * BKB);
-            tensor_load_2d(dst, &map_w, kb * BKB, wrow, bfull(s));
+            bar_expect(bfull(full), (BM + boxes * box_rows) * BKB);
+            tensor_load_2d(dst, &map_w, kb * BKB, wrow, bfull(full));
             for (int b = 0; b < boxes; ++b)
               tensor_load_2d(dst + (BM + b * box_rows) * BKB, &map_a, kb * BKB,
-                             arow + b * box_rows, bfull(s));
+                             arow + b * box_rows, bfull(full));
           }
           ++nload;
           if (++s == nbyte) { s = 0; phase ^= 1u; }
+          if (++full == kTurns * nbyte) full = 0;
         }
         ok = ok && !smem_load(abort_flag);
       }
@@ -403,7 +411,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       // no copy may land once the CTA has gone (the widening warps wait for all of
       // them, unless one of them has given up)
       for (uint32_t i = nload > uint32_t(nbyte) ? nload - nbyte : 0; i < nload; ++i)
-        bar_wait(bfull(i % nbyte), (i / nbyte) & 1u);
+        bar_wait(bfull(i % (kTurns * nbyte)), (i / (kTurns * nbyte)) & 1u);
       cluster_wait_all();
     } else if (warp == 1 && rank == 0) {
       // ---- products (of the pair, by its first CTA) -----------------------------------
@@ -486,20 +494,20 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     constexpr int kBatch = 2;
     const int grp = (tid - 128) / kGroupThreads, u = (tid - 128) % kGroupThreads;
     const int half = grp % kHalves, turn = grp / kHalves;
-    constexpr int kTurns = kConvGroups / kHalves;
     const int uq = u >> 2, uc = u & 3;
     const int ur = (uq & ~7) + (((uq >> 1) & 3) ^ ((uq & 1) * 5));
     const uint32_t in = ur * BKB + (((half * 4 + uc) ^ (ur & 7)) << 4);
     const uint32_t out0 = ur * (BK * 2) + (((2 * uc) ^ (ur & 7)) << 4);
     cluster_wait_all();
-    int s = turn, f = grp;
+    int load = turn, f = grp;            // load: modulo 2 nbyte
     uint32_t bphase = 0, fphase = 0;
     bool ok = true;
     const int tiles = tile_count(), first = cluster_id(), step = cluster_count();
     const int total = first < tiles ? ((tiles - first + step - 1) / step) * stage_count() : 0;
     for (int i = turn; i < total; i += kTurns) {
-      ok = __all_sync(0xffffffffu, bar_wait(bfull(s), bphase));
+      ok = __all_sync(0xffffffffu, bar_wait(bfull(load), bphase));
       if (!ok) break;
+      const int s = load < nbyte ? load : load - nbyte;
       const int rows = smem_load(srows(s));
       const uint32_t src = sbase + St::kOffBytes + s * St::kByteBytes + in;
       const uint32_t dst = sbase + f * St::kF16Bytes + out0;   // and dst ^ 16
@@ -517,8 +525,9 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
             // This half of the stage is read: hand it back to the copies.  The
             // arrival's address depends on the loaded words (meeting a 0 that the compiler
             // cannot see: nz is -0), so no load can still be pending, or be moved
-            // by the compiler to a point after it, when the copies overwrite them
-            // (seen: wrong products once the next wait stood between).
+            // by the compiler to a point after it, when the copies overwrite them.  (Wrong
+            // products were seen without this, but before every turn had barriers of its
+            // own, which may have been their cause too.)
             uint32_t words = 0;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) words |= v[i].x;
@@ -545,7 +554,10 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) cluster_arrive(cluster_addr(ffull(f), leader));
-      for (s += kTurns; s >= nbyte; s -= nbyte) bphase ^= 1u;
+      if ((load += kTurns) >= kTurns * nbyte) {
+        load -= kTurns * nbyte;
+        bphase ^= 1u;
+      }
       for (f += kConvGroups; f >= NF; f -= NF) fphase ^= 1u;
     }
     if (!ok) {
