@@ -10,6 +10,9 @@
 // plus dynamic) is a per-context function attribute, which a device reset
 // clears, so it is set on every launch that needs it (a cheap call) rather
 // than remembered; the kernel's static size it depends on is looked up once.
+// Every launch sets the same value, all that a block can have: were it the launch's
+// own size, a smaller launch of the same kernel from another host thread could take
+// the limit below a larger one between that one's setting and its launch.
 #include <mutex>
 #include <vector>
 
@@ -36,25 +39,31 @@ std::mutex g_mu;
 std::vector<OccEntry> g_occ;
 std::vector<StaticEntry> g_static;
 int g_sms[kMaxDevs] = {};
+int g_optin[kMaxDevs] = {};
+
+// A device attribute, looked up once per device.
+cudaError_t device_fact(cudaDeviceAttr attr, int dev, int (&known)[kMaxDevs], int* value) {
+  const bool keep = dev >= 0 && dev < kMaxDevs;
+  if (keep) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (known[dev] > 0) {
+      *value = known[dev];
+      return cudaSuccess;
+    }
+  }
+  const cudaError_t e = cudaDeviceGetAttribute(value, attr, dev);
+  if (e == cudaSuccess && keep && *value > 0) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    known[dev] = *value;
+  }
+  return e;
+}
 
 }  // namespace
 
 cudaError_t current_device_sms(int* dev, int* sms) {
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return e;
-  if (*dev >= 0 && *dev < kMaxDevs) {
-    std::lock_guard<std::mutex> lock(g_mu);
-    if (g_sms[*dev] > 0) {
-      *sms = g_sms[*dev];
-      return cudaSuccess;
-    }
-  }
-  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
-  if (e == cudaSuccess && *dev >= 0 && *dev < kMaxDevs && *sms > 0) {
-    std::lock_guard<std::mutex> lock(g_mu);
-    g_sms[*dev] = *sms;
-  }
-  return e;
+  const cudaError_t e = cudaGetDevice(dev);
+  return e != cudaSuccess ? e : device_fact(cudaDevAttrMultiProcessorCount, *dev, g_sms, sms);
 }
 
 // Static shared memory of a kernel (a property of the compiled function,
@@ -84,8 +93,14 @@ cudaError_t ensure_dynamic_smem(const void* fn, size_t smem) {
   if (e != cudaSuccess) return e;
   // the default per-block limit (48 KB) covers static plus dynamic memory
   if (smem + stat <= 48 * 1024) return cudaSuccess;
+  int dev = 0, optin = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = device_fact(cudaDevAttrMaxSharedMemoryPerBlockOptin, dev, g_optin, &optin);
+  if (e != cudaSuccess) return e;
+  if (smem + stat > static_cast<size_t>(optin)) return cudaErrorInvalidValue;
   return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(smem));
+                              optin - static_cast<int>(stat));
 }
 
 cudaError_t kernel_blocks_per_sm(const void* fn, int threads, size_t smem, int* per_sm) {

@@ -400,7 +400,7 @@ struct Shape {
 // Launch facts (launch_cache.cu): the current device and its SM count, and
 // the CTAs of kernel `fn` resident per SM at a block size and dynamic shared
 // memory (occupancy cached per kernel, device and size; the >48 KB dynamic
-// shared memory attribute is set first when needed).
+// shared memory attribute is set first when needed, to all a block can have).
 cudaError_t current_device_sms(int* dev, int* sms);
 cudaError_t ensure_dynamic_smem(const void* fn, size_t smem);
 cudaError_t kernel_blocks_per_sm(const void* fn, int threads, size_t smem, int* per_sm);
