@@ -37,7 +37,7 @@
 namespace moe_ep {
 namespace {
 
-// The sigmoid that ranks: the rounded product in the exponent costs s(1-s)|x|
+// The sigmoid that ranks with a bias: the rounded product in the exponent costs s(1-s)|x|
 // 2^-24 <= 2^-26, less than the rounding of s itself; 0 and 1 at the infinities.
 __device__ __forceinline__ float sigmoid_rank(float x) {
   float r;
@@ -53,6 +53,28 @@ __device__ __forceinline__ float2 sigmoid_rank2(float2 x, float nz) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
   return r;
+}
+
+// Rank of a group without a bias, from its two highest logits x1 >= x2 (-inf: none); m:
+// the row's maximum (softmax).  The sum of the scores (a softmax's without the common
+// divisor) by the full-precision exponential, or, below 2^-100, where the scores leave
+// fp32, its logarithm: a negative number, so below every sum, and as increasing.
+__device__ __forceinline__ float group_rank(const RouteArgs& r, float x1, float x2, float m) {
+  if (!(x1 > kNegInf)) return kNegInf;
+  const bool two = r.group_top == 2 && x2 > kNegInf;
+  float g, rest;
+  if (r.score == MOE_SOFTMAX) {
+    x1 = __fsub_rn(x1, m);
+    x2 = __fsub_rn(x2, m);
+    g = expf(x1);
+    if (two) g = __fadd_rn(g, expf(x2));
+  } else {
+    g = sigmoid_scaled(x1, 0.0f, &rest);
+    if (two) g = __fadd_rn(g, sigmoid_scaled(x2, 0.0f, &rest));
+  }
+  if (g >= 0x1p-100f) return g;
+  // (a difference of infinities, from logits 3e38 apart, is a NaN, which fmaxf drops)
+  return fmaxf(two ? __fadd_rn(x1, log1pf(expf(__fsub_rn(x2, x1)))) : x1, -kMaxF);
 }
 
 // Ids and weights of token t (there: it exists) by W lanes: slots j0 (of this lane)
@@ -225,14 +247,10 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
     sum = warp_sum(__fadd_rn(part.x, part.y));
     if (sum == 0.0f) sum = 1.0f;
   }
-  const float inv_sum = want_sum ? __fdiv_rn(1.0f, sum) : 1.0f;
-  auto score = [&](float x) {
-    return r.score == MOE_SOFTMAX ? __fmul_rn(exp_neg(__fsub_rn(x, m)), inv_sum)
-                                  : sigmoid_rank(x);
-  };
 
   // ---- ranked values with a bias --------------------------------------------------
   if (BIAS) {
+    const float inv_sum = want_sum ? __fdiv_rn(1.0f, sum) : 1.0f;
     // every: every value is an expert's finite logit, the usual case
     auto rank = [&](auto every, auto&& f) {
 #pragma unroll
@@ -261,16 +279,14 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
   // ---- groups: a power of two of lanes each ----------------------------------------
   if (grouped) {
     float a1 = v1, a2 = v2;
-    if (!BIAS) {
-      a1 = a1 > kNegInf ? score(a1) : kNegInf;
-      a2 = a2 > kNegInf ? score(a2) : kNegInf;
-    }
     for (int d = 1; d < lanes_per_group; d <<= 1) {
       const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
       a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
       a1 = fmaxf(a1, b1);
     }
-    const float gs = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
+    const float gs = !BIAS                               ? group_rank(r, a1, a2, m)
+                     : r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2)
+                                                        : a1;
     uint32_t key = gs > kNegInf ? order_key(gs) : 0u;
     const int head = lane & -lanes_per_group;        // the group's first lane
     bool keep = false;
@@ -384,7 +400,7 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
   using T = typename Elem<DT>::T;
   extern __shared__ uint32_t s_dyn[];
   uint32_t* key = s_dyn;                                       // [E]
-  float* choice = reinterpret_cast<float*>(s_dyn + r.E);       // [E]
+  float* choice = reinterpret_cast<float*>(s_dyn + r.E);       // [E], logits without a bias
   float* gscore = choice + r.E;                                // [n_group]
   __shared__ float s_red[kWideThreads / 32];
   __shared__ uint64_t s_best[2][kWideThreads / 32];
@@ -429,11 +445,14 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
     const float inv_sum = __fdiv_rn(1.0f, sum);
     for (int e = tid; e < r.E; e += kWideThreads) {
       const float l = logit(e);
-      float c = r.score == MOE_SOFTMAX ? __fmul_rn(exp_neg(__fsub_rn(l, m)), inv_sum)
-                                       : sigmoid_rank(l);
-      if (r.bias) c = __fadd_rn(c, r.bias[e]);
+      float c = l;
+      if (r.bias) {
+        c = r.score == MOE_SOFTMAX ? __fmul_rn(exp_neg(__fsub_rn(l, m)), inv_sum)
+                                   : sigmoid_rank(l);
+        c = __fadd_rn(c, r.bias[e]);
+      }
       const bool on = l > kNegInf && c > kNegInf;
-      key[e] = on ? order_key(r.bias ? c : l) : 0u;
+      key[e] = on ? order_key(c) : 0u;
       choice[e] = on ? c : kNegInf;
     }
     __syncthreads();
@@ -445,7 +464,9 @@ route_wide_kernel(const RouteArgs r, int32_t* __restrict__ idx, float* __restric
           a2 = fmaxf(fminf(a1, c), a2);
           a1 = fmaxf(a1, c);
         }
-        gscore[g] = r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2) : a1;
+        gscore[g] = !r.bias                            ? group_rank(r, a1, a2, m)
+                    : r.group_top == 2 && a2 > kNegInf ? __fadd_rn(a1, a2)
+                                                       : a1;
       }
       __syncthreads();
       for (int g = tid; g < r.n_group; g += kWideThreads) {

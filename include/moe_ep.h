@@ -516,9 +516,14 @@ moe_status moe_deq_combine(const moe_shape* shape, const int32_t* expert_acc,
  *   topk_weights  fp32 [T][k]
  * 0 <= T, T*k < 2^31, 1 <= E <= MOE_EP_MAX_EXPERTS, logits_stride >= E,
  * 1 <= k <= min(E, MOE_EP_MAX_TOPK), 1 <= topk_group <= n_group, E % n_group
- * == 0, group_top 1 or 2, scale finite.  Choices are fp32 within a few ulp of
- * the definition; weights are computed from the chosen logits alone where the
- * definition allows it.  One launch. */
+ * == 0, group_top 1 or 2, scale finite.  Accuracy: without a bias the experts'
+ * order is exact, and a group's score is an fp32 sum of scores within 3 ulp (a
+ * softmax's also within |l - max| 2^-24, relative); sums below 2^-100 are compared by
+ * their logarithms.  With a bias the score inside a choice is within 2^-22 of the
+ * definition (sigmoid), or within 2^-18 of itself plus 2^-126 (softmax, where the sum
+ * over E experts has its part), and the choice is its fp32 sum with the bias.
+ * Weights are computed from the chosen logits alone where the definition allows
+ * it.  One launch. */
 moe_status moe_route(const void* logits, int32_t logits_dtype, int64_t T, int32_t E,
                      int64_t logits_stride, const float* bias, int32_t score,
                      int32_t n_group, int32_t topk_group, int32_t group_top, int32_t k,
