@@ -59,14 +59,20 @@ __device__ __forceinline__ void warp_totals(int (&v)[V], int lane) {
   }
 }
 
-// Zeroes the bytes of a 16-byte piece past the first n (n > 0).
-__device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The first n (0 < n < 16) bytes of a 16-byte piece, zeros behind them.  Reads those n
+// alone: a row of a may end there, and the buffer with it.
+__device__ __forceinline__ uint4 first_bytes(const uint8_t* p, int n) {
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int left = n - 4 * i;
-    if (left <= 0) w[i] = 0u;
-    else if (left < 4) w[i] &= (1u << (8 * left)) - 1u;
+    w[i] = 0u;
+    if (4 * i + 4 <= n) {
+      w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 3; ++b)
+        if (4 * i + b < n) w[i] |= uint32_t(p[4 * i + b]) << (8 * b);
+    }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -114,8 +120,7 @@ __device__ __forceinline__ void channels_by_tokens(const uint8_t* w, int64_t w_s
     for (int t = 0; t < TB; ++t) {
       // (a weight row's bytes past K meet zeros here)
       const uint8_t* at = a + (t < tokens ? t : tokens - 1) * a_stride + j;
-      uint4 x = *reinterpret_cast<const uint4*>(at);
-      if (j + 16 > K) x = keep_bytes(x, K - j);
+      const uint4 x = j + 16 <= K ? *reinterpret_cast<const uint4*>(at) : first_bytes(at, K - j);
 #pragma unroll
       for (int r = 0; r < CH; ++r) acc[r * TB + t] = dot16(cur[r], x, acc[r * TB + t]);
     }

@@ -596,7 +596,8 @@ moe_status moe_combine_backward(const moe_shape* shape, const void* d_out,
  *   c           [a_rows][N] in c_dtype (MOE_BF16, MOE_FP16, MOE_FP32 or
  *               MOE_INT32); rows past the groups' total are not written
  * a, w and c are 16-byte aligned; a_stride and w_stride are multiples of 16 and
- * at least K (bytes past K in a row are never used);
+ * at least K (bytes past K in a row are never used; a row of w is read up to the
+ * next multiple of 16, a row of a only up to K);
  * 1 <= K, N <= MOE_EP_MAX_HIDDEN, 0 <= a_rows < 2^31 - 1024,
  * 1 <= G <= MOE_EP_MAX_EXPERTS, (a_rows / 32 + G) * ceil(N / 256) < 2^31;
  * row_scale_stride >= 4, a multiple of 4.
