@@ -61,6 +61,16 @@
 
 namespace moe_ep {
 
+// linear_i8_polls.cu compiles this file a second time, for tests of the waits that run
+// out: with role_wait of its own, and without the two functions that others call.
+#ifndef MOE_LINEAR_I8_POLLS
+namespace {
+// A role's wait for its next work; false after kGemmSpin polls.
+__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity) {
+  return bar_wait(bar, parity);
+}
+}  // namespace
+
 cudaError_t encode_bytes_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                             int64_t stride, uint32_t box_rows) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -99,6 +109,7 @@ cudaError_t encode_bytes_2d(CUtensorMap* map, const void* base, int64_t rows, in
   }
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+#endif
 
 namespace {
 
@@ -397,7 +408,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         const int arow = tl.row0 + rank * rows;
         const int kb0 = stage_begin();
         for (int kb = kb0; kb < kb0 + nk; ++kb) {
-          if (!bar_wait(bempty(s), phase ^ 1u)) {
+          if (!role_wait(bempty(s), phase ^ 1u)) {
             ok = false;
             break;
           }
@@ -421,8 +432,8 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         smem_store(abort_flag, 1);
       }
       // no copy may land once the CTA has gone (the widening warps wait for all of
-      // them, unless one of them has given up)
-      for (uint32_t i = nload > uint32_t(nbyte) ? nload - nbyte : 0; i < nload; ++i)
+      // them, unless one of them has given up); the issuing lane's count is the true one
+      for (uint32_t i = nload > uint32_t(nbyte) ? nload - nbyte : 0; issue && i < nload; ++i)
         bar_wait(bfull(i % (kTurns * nbyte)), (i / (kTurns * nbyte)) & 1u);
       cluster_wait_all();
     } else if (warp == 1 && rank == 0) {
@@ -439,7 +450,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         const int nchunks = chunk_count(nk);
         for (int c = 0; ok && c < nchunks; ++c, ++chunk) {
           const uint32_t b = chunk & 1u, use = (chunk >> 1) & 1u;
-          if (!bar_wait(tempty(b), use ^ 1u) || smem_load(abort_flag)) {
+          if (!role_wait(tempty(b), use ^ 1u) || smem_load(abort_flag)) {
             ok = false;
             break;
           }
@@ -447,7 +458,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           const uint32_t d = tmem + b * kAccCols;
           const int n = min(kChunk, nk - c * kChunk) * kHalves;
           for (int kb = 0; kb < n; ++kb) {
-            if (!bar_wait(ffull(f), phase)) {
+            if (!role_wait(ffull(f), phase)) {
               ok = false;
               break;
             }
@@ -471,10 +482,10 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
         if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
         smem_store(abort_flag, 1);
       }
-      await_commits(ncommit, chunk);
       // the pair's other CTA, whose barriers the commits arrive on too, learns how
       // many there were; it waits for them after the closing barrier
       if (issue) {
+        await_commits(ncommit, chunk);
         const uint32_t to = cluster_addr(issued, leader + 1);
         cluster_store(to, ncommit);
         cluster_store(to + 4, chunk);
@@ -517,7 +528,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
     const int tiles = tile_count(), first = cluster_id(), step = cluster_count();
     const int total = first < tiles ? ((tiles - first + step - 1) / step) * stage_count() : 0;
     for (int i = turn; i < total; i += kTurns) {
-      ok = __all_sync(0xffffffffu, bar_wait(bfull(load), bphase));
+      ok = __all_sync(0xffffffffu, role_wait(bfull(load), bphase));
       if (!ok) break;
       const int s = load < nbyte ? load : load - nbyte;
       const int rows = smem_load(srows(s));
@@ -547,7 +558,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
             if (lane == 0) bar_arrive(bempty(s) + (words & (__float_as_uint(nz) << 1)));
           }
           if (i0 == 0) {                              // the fp16 stage is free
-            ok = __all_sync(0xffffffffu, bar_wait(fempty(f), fphase ^ 1u));
+            ok = __all_sync(0xffffffffu, role_wait(fempty(f), fphase ^ 1u));
             if (!ok) return;
           }
 #pragma unroll
@@ -594,7 +605,7 @@ linear_i8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       Tile tl = decode_tile(t, goff, tpre, p.G, ntn, block);
       const int live = tl.cols - col0;       // columns of this thread that are computed
       auto wait = [&]() {                    // for the next chunk
-        const bool got = bar_wait(tfull(chunk & 1u), (chunk >> 1) & 1u) &&
+        const bool got = role_wait(tfull(chunk & 1u), (chunk >> 1) & 1u) &&
                          !smem_load(abort_flag);
         ok = __all_sync(0xffffffffu, got);
         tc_fence_after();
@@ -863,6 +874,7 @@ Plan make_plan(const LinearArgs& p, int sms) {
 
 }  // namespace
 
+#ifndef MOE_LINEAR_I8_POLLS
 cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
   if (use_few(p)) return launch_linear_i8_few(p, dev_status, st);
   int dev = 0, sms = 0, optin = 0;
@@ -879,5 +891,6 @@ cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStrea
   return plan.nt == 256 ? launch_nt<256>(mw, ma, p, plan, dev_status, optin, st)
                         : launch_nt<128>(mw, ma, p, plan, dev_status, optin, st);
 }
+#endif
 
 }  // namespace moe_ep

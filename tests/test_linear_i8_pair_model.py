@@ -400,7 +400,7 @@ def test_a_turn_that_skips_the_other_turns_phases_reads_old_bytes():
     for nbyte in (2, 3, 4, 5, 7):
         assert faults(nbyte, False) == 0
     kernel = _code().split("linear_i8_tile_kernel", 1)[1]
-    assert "bar_wait(bfull(load), bphase)" in kernel
+    assert "role_wait(bfull(load), bphase)" in kernel
     assert re.search(r"\(load \+= kTurns\) >= kTurns \* nbyte", kernel)
     assert "bar_init(bfull(lane), 1)" in kernel and "lane < kTurns * nbyte" in kernel
 
