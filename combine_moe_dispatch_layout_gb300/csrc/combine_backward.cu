@@ -119,7 +119,8 @@ combine_backward_kernel(const uint4* d_out, const uint4* y, int64_t y_rows,
 // 35 instead of 56, 4096 x 8 x 1024 20 instead of 24.  At H = 2048 the two meet (343 and
 // 348 us at 32,768 tokens) and few tokens are slower (9.0 and 5.4 us at 128): it
 // stays with the kernel above, which puts a whole CTA's threads on a token.  CH = 4
-// with 2 rows at a time took 22 us, CH = 1 with 16 45.
+// with 2 rows at a time took 22 us, CH = 1 with 16 45.  Rows of less than 256 elements
+// leave lanes without a chunk: 131,072 x 6 x 64 takes 101 us, x 128 112, 65,536 x 6 x 256 72.
 template <int DT, int CH>
 __global__ void __launch_bounds__(kTokenWarps * 32)
 combine_backward_warp_kernel(const uint4* d_out, const uint4* y, int64_t y_rows,

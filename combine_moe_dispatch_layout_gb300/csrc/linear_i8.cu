@@ -40,15 +40,15 @@
 // bytes a clock) beside the copies' and the MMA's own traffic; so large tiles run
 // at the tensor cores' rate and tiles of fewer tokens at that of shared memory
 // (128 weight rows are widened for however few tokens).  The store of a tile adds
-// shuffles and stores to the same unit, which shows where K is short.  Measured:
-// 8192 x 4096 x 7168 251 us, 1916 TFLOP/s (a library bf16 product: 1874); 4096 x
-// 4096 x 7168 143 us, 1680 (304 tiles of 224 tokens on 76 pairs); 32,768 x 7168 x
-// 2048 583 us, 1650, in 32 even groups 616, in 32 uneven ones (half of them under
-// 512 rows, so of two narrower tiles) 662.  Without the store's arithmetic and
-// stores the last three would take 528, 568 and 635.  Tried and slower: two
-// channels per store after an exchange between lanes (598 instead of 583), row
-// scales through shared memory instead of shuffles (584), both paths of the store
-// in one loop (650).
+// shuffles and stores to the same unit, which shows where K is short.  Measured (in
+// a graph, SM clock at its maximum; boxes differ by 3%): 8192 x 4096 x 7168 253 to 260
+// us, a library bf16 product's rate; 4096 x 4096 x 7168 145 to 148, 1640 TFLOP/s (304
+// tiles of 224 tokens, four for each of 76 pairs: 4% of the columns are empty);
+// 32,768 x 7168 x 2048 590, 1630; in 32 uneven groups (half of them under 512 rows, so
+// of two narrower tiles) 671.  Without the store's arithmetic and stores the last two
+// took 9% and 4% less.  Tried and slower for the whole product: two channels per store
+// after an exchange between lanes (3%), row scales through shared memory instead of
+// shuffles (the same), both paths of the store in one loop (11%).
 #include <cuda.h>
 
 #include <algorithm>
@@ -820,7 +820,10 @@ cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const Linear
 // 354, 32 of 7168 x 2048 89 and 102; with 4 1583 and 1334, 349 and 358, 105 and
 // 102.  Small products, where the tile kernel's start-up (barriers, TMEM, clusters)
 // is most of its time: 64 x 512 x 2048 takes 6.0 and 9.0 us, 512 x 256 x 1024 (at
-// both limits) 9.0 and 9.3, 64 x 7168 x 256 (past the second) 16.9 and 7.4.
+// both limits) 9.0 and 9.3, 64 x 7168 x 256 (past the second) 16.9 and 7.4.  The rule
+// does not see K below 1024 or how rows fall to the groups: 8 x 65,536 x 64 takes 18 us
+// and would take 13 on the tensor cores, 512 rows over 256 groups of 2048 x 128 72 and
+// 65, and 3 G rows that all fall to one group pass over its weights once per four rows.
 bool use_few(const LinearArgs& p) {
   const int64_t outputs = p.a_rows * p.N;
   return p.a_rows <= (p.G == 1 ? 8 : 3 * p.G) ||

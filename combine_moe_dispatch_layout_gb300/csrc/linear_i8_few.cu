@@ -17,11 +17,13 @@
 // of a group are fastest, so a second block finds the weights in L2.  (Blocks of
 // 8 tokens were slower: 32 sums a lane leave no registers for loads in flight.)
 //
-// Measured: one token by 4096 x 7168 7.4 us (29 MB: 4.3 us at a copy's rate; the
-// rest is the launch, the first load's way and the sums), 164 of 256 experts'
-// 4096 x 7168 for 256 tokens 681 us, 7.1 TB/s: bound by memory.  Seven CTAs of 128
-// threads to an SM spread 1024 quads of channels more evenly over 152 SMs than
-// three of 256 did (8.4 and 725 us).
+// Measured: one token by 4096 x 7168 4.7 us in a graph, weights partly in L2, and 7.4 to
+// 8.0 call by call (29 MB: 4.3 us at a copy's rate; the rest is the launch, the first
+// load's way and the sums), 164 of 256 experts' 4096 x 7168 for 256 tokens 667 to 720
+// us, 6.7 to 7.2 TB/s: bound by memory.  Seven CTAs of 128 threads to an SM spread 1024
+// quads of channels more evenly over 152 SMs than three of 256 did (8.4 and 725 us).
+// Short K leaves lanes without a piece: 80 rows in 138 groups of 4096 x 64 take 35 us,
+// of 4096 x 256 38.
 #include <algorithm>
 #include <type_traits>
 

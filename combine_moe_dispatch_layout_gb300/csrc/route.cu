@@ -20,12 +20,12 @@
 // lane that wins three times looks through its values again (rare: winners
 // spread over the lanes; with two values kept it was not).
 //
-// Measured: 32,768 tokens x 256 fp32 logits, sigmoid with bias, 4 of 8 groups, k = 8:
-// 21.0 us, of which 9.4 are the read, the scan and the write, 2.3 the sigmoid and the
-// bias, 5.5 the seven further rounds, 3.8 the groups; 49,152 x 768 bf16, plain
-// softmax: 43 us.  Memory would allow 5.3 and 11.6: the schedulers issue in 74% of their
-// cycles and wait for the chain of a round in most others.  32 tokens: 3.3 us, a
-// launch.  Tried and not faster: 8 or 16 lanes per token (half the instructions, but
+// Measured (in a graph, inputs as warm as they stay): 32,768 tokens x 256 fp32 logits,
+// sigmoid with bias, 4 of 8 groups, k = 8: 21.2 us, of which 9.4 are the read, the scan
+// and the write, 2.3 the sigmoid and the bias, 5.5 the seven further rounds, 3.8 the
+// groups; 49,152 x 768 bf16, plain softmax: 42 us.  Memory would allow 5.3 and 11.6: the
+// schedulers issue in 74% of their cycles and wait for the chain of a round in most
+// others.  32 tokens: 3.4 us, a launch.  Tried and not faster: 8 or 16 lanes per token (half the instructions, but
 // maxima run at half rate and the registers leave few warps: 28-34 us where this
 // took 28.7, and 6.8 instead of 3.4 at 1024 tokens); a persistent grid (24 and 49).
 #include <algorithm>
@@ -390,7 +390,10 @@ route_warp_kernel(const RouteArgs r, bool vec, bool vec_bias, int group_shift, i
 
 // Any E up to MOE_EP_MAX_EXPERTS and any groups: one CTA per token (persistent
 // grid), ranking keys and choices in shared memory, a block-wide maximum of
-// (key, lowest id) per chosen expert.
+// (key, lowest id) per chosen expert.  4096 tokens x 2048 fp32, sigmoid: 42 us (5.0 of
+// reads), in 64 groups of which 8 stay 106; x 4096 bf16, softmax 95; 32,768 x 320 in 40
+// groups 209 (6.5): every token pays the CTA's barriers, two per chosen expert, and a
+// thread scores a whole group by itself.
 constexpr int kWideThreads = 128;
 
 template <int DT>

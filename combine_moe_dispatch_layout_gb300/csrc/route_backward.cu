@@ -17,11 +17,12 @@
 // lines are still in L2.  Plain softmax keeps the row's exponentials in registers
 // between its two sums and the write.
 //
-// Measured: 32,768 x 256 fp32, renormalised sigmoid, k = 8: 7.9 us (4.3 TB/s of
-// writes; 12.5 with a warp per token, zeros after the sums: the chain id -> logit ->
-// sums was paid four times as often).  49,152 x 768 bf16, plain softmax: 30.7 us, 4.9
-// TB/s both ways; the exponentials' instructions (75% of the issue slots) are what
-// keeps it from a copy's 23 us.
+// Measured (in a graph): 32,768 x 256 fp32, renormalised sigmoid, k = 8: 8.1 us (4.2
+// TB/s of writes; 12.5 with a warp per token, zeros after the sums: the chain id ->
+// logit -> sums was paid four times as often).  49,152 x 768 bf16, plain softmax: 30 us,
+// 5.0 TB/s both ways; the exponentials' instructions (75% of the issue slots) are what
+// keeps it from a copy's 23 us.  Rows of any other length or alignment are read three
+// times, element by element: 49,152 x 767 77 us, 32,768 x 250 fp32 27 (x 256: 17).
 #include <type_traits>
 
 #include "moe_ep_internal.cuh"

@@ -33,10 +33,10 @@
  *    enqueued on `stream` (a cudaStream_t; NULL = the legacy default
  *    stream) and returns immediately.
  *  - Global state: two things only.  The launchers remember each device's
- *    SM count and, per kernel, block size and shared-memory size, the
- *    occupancy they queried on first use (read-only device facts, behind a
- *    mutex; they change no result), and the address of the driver's
- *    tensor-map encoder.  moe_dispatch_layout_static owns one
+ *    SM count and shared-memory limit and, per kernel, block size and
+ *    shared-memory size, the occupancy they queried on first use (read-only
+ *    device facts, behind a mutex; they change no result), and the address of
+ *    the driver's tensor-map encoder.  moe_dispatch_layout_static owns one
  *    device array (see there).  Nothing else outlives a call.
  *  - Host-checkable problems (NULL or misaligned pointers, sizes out of
  *    range) are reported synchronously by the return value and nothing is
