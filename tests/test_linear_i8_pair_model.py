@@ -86,6 +86,8 @@ class Cluster:
         self.flat = [c for pair in self.ctas for c in pair]
         self.mma_issued = [0] * pairs
         self.mma_done = [0] * pairs
+        self.queue = [[] for _ in range(pairs)]              # (accumulator, chunk) of products
+        self.acc = [[(None, 0), (None, 0)] for _ in range(pairs)]   # chunk, products in it
         self.fills = []                 # (cta, stage)
         self.commits = []               # [pair, products it follows, cta, barrier]
         # barriers that the byte stages take turns with: 2 nbyte, or nbyte
@@ -158,7 +160,7 @@ class Cluster:
     def products(self, c):
         f = phase = chunk = ncommit = step = 0
         ok = True
-        for _ in range(self.tiles):
+        for t in range(self.tiles):
             for k in range(self.nchunks()):
                 b, use = chunk & 1, (chunk >> 1) & 1
                 ok = yield from self.wait(c.tempty[b], use ^ 1)
@@ -174,6 +176,7 @@ class Cluster:
                             self.faults.append("a product of the wrong codes")
                     step += 1
                     self.mma_issued[c.pair] += 1
+                    self.queue[c.pair].append((b, (t, k)))
                     self.commit(c, "fempty", f)
                     ncommit += 1
                     f += 1
@@ -243,6 +246,10 @@ class Cluster:
                     break
                 if self.split and k == self.nchunks() - 1:
                     yield from self.cluster_sync()
+                want = min(self.chunk, self.nk - k * self.chunk) * HALVES
+                yield
+                if self.acc[c.pair][chunk & 1] != ((t, k), want):
+                    self.faults.append("sums of the wrong chunk")
                 c.read.add((w, t, k))
                 self.ctas[c.pair][0].tempty[chunk & 1].arrive()
                 chunk += 1
@@ -297,6 +304,9 @@ class Cluster:
         elif kind == "mma":
             p = self.rng.choice([p for p in range(len(self.ctas))
                                  if self.mma_done[p] < self.mma_issued[p]])
+            b, chunk = self.queue[p][self.mma_done[p]]
+            at, n = self.acc[p][b]
+            self.acc[p][b] = (chunk, n + 1 if at == chunk else 1)
             self.mma_done[p] += 1
         else:
             x = self.rng.choice(ready)
