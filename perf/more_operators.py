@@ -161,7 +161,8 @@ def _prepare_norm(case, seed):
     # rows of a residual stream: some channels much larger than the others
     loud = torch.rand(H, generator=g, device="cuda") < 0.01
     size = torch.where(loud, 20.0, 1.0)
-    st = {"case": case, "gamma": 1.0 + 0.2 * torch.randn(H, generator=g, device="cuda")}
+    st = {"case": case, "gamma": 1.0 + 0.2 * torch.randn(H, generator=g, device="cuda"),
+          "status": torch.zeros(1, dtype=torch.int32, device="cuda")}
     x = _randn((T, H), dtype, g)
     x.mul_(size.to(dtype))
     if case["op"] == "norm_backward":
@@ -188,7 +189,7 @@ def _prepare_swiglu(case, seed):
     g = _gen(seed, 5)
     rows, I = case["rows"], case["I"]
     h = _randn((rows, 2 * I), _DT[case["dtype"]], g, 1.5)
-    return {"case": case, "h": h,
+    return {"case": case, "h": h, "status": torch.zeros(1, dtype=torch.int32, device="cuda"),
             "codes": torch.empty((rows, _image_bytes(I)), dtype=torch.uint8, device="cuda")}
 
 
@@ -317,7 +318,7 @@ def _own(st):
     case = st["case"]
     if case["op"] == "norm":
         ep.moe_rms_norm(st["x"], st["residual"], st["gamma"], _EPS, st["sum"], st["out"],
-                        st["codes"], st["rstd"])
+                        st["codes"], st["rstd"], st["status"])
         outputs = [t for t in (st["sum"], st["out"]) if t is not None]
         if case["codes"]:
             outputs += _codes(st["codes"], case["H"])
@@ -327,10 +328,10 @@ def _own(st):
             size = ep.rms_norm_backward_workspace_bytes(case["T"], case["H"])
             st["workspace"] = torch.empty(size, dtype=torch.uint8, device="cuda")
         ep.moe_rms_norm_backward(st["d_out"], st["x"], st["gamma"], st["rstd"], st["d_sum"],
-                                 st["d_x"], st["d_gamma"], st["workspace"])
+                                 st["d_x"], st["d_gamma"], st["workspace"], st["status"])
         return [st["d_x"], st["d_gamma"]]
     if case["op"] == "swiglu":
-        ep.moe_swiglu_f8(st["h"], None, st["codes"])
+        ep.moe_swiglu_f8(st["h"], None, st["codes"], st["status"])
         return list(_codes(st["codes"], case["I"]))
     a = st["a"]
     ep.moe_linear_f8(a, st["w"], case["K"], st["group_rows"] if case["G"] > 1 else None,
