@@ -31,6 +31,8 @@ MOE_FP32 = 2
 MOE_INT32 = 3
 MOE_SIGMOID = 0
 MOE_SOFTMAX = 1
+MOE_CODE_I8 = 0
+MOE_CODE_F8 = 1
 
 _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16}
 _ANY_DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16,
@@ -109,6 +111,17 @@ def _load():
     L.moe_combine_backward.argtypes = [sp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_linear_i8.argtypes = [vp, i64, i64, vp, i64, i32, i32, i32, vp, vp, vp, i64, vp,
                                 vp, i32, vp, vp]
+    L.moe_f8_row_bytes.argtypes = [i32]
+    L.moe_f8_row_bytes.restype = i64
+    L.moe_rms_norm.argtypes = [vp, i32, i64, i32, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp,
+                               i32, vp, vp, vp]
+    L.moe_rms_norm_backward_workspace_bytes.argtypes = [i64, i32]
+    L.moe_rms_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.moe_rms_norm_backward.argtypes = [vp, i32, i64, i32, i64, vp, i64, vp, vp, vp, i64, vp,
+                                        i64, vp, vp, vp, vp]
+    L.moe_swiglu_f8.argtypes = [vp, i32, i64, i32, i64, vp, i32, vp, vp, vp]
+    L.moe_linear_f8.argtypes = [vp, i64, i64, vp, i64, i32, i32, i32, vp, vp, vp, i64, vp, vp,
+                                i32, vp, vp]
     for name in ("moe_dispatch_layout", "moe_notify_dispatch", "moe_dispatch",
                  "moe_combine", "moe_combine_quant", "moe_token_layout",
                  "moe_dispatch_fused", "moe_swiglu_quant", "moe_group_offsets",
@@ -119,7 +132,8 @@ def _load():
                  "moe_grouped_gemm_i8_swiglu", "moe_interleave_gate_up",
                  "moe_quant_rows_bf16", "moe_dispatch_layout_static",
                  "moe_route", "moe_route_backward", "moe_combine_backward",
-                 "moe_linear_i8"):
+                 "moe_linear_i8", "moe_rms_norm", "moe_rms_norm_backward",
+                 "moe_swiglu_f8", "moe_linear_f8"):
         getattr(L, name).restype = ctypes.c_int
     return L
 
@@ -373,14 +387,14 @@ def moe_swiglu_quant(acc, weight_scale, token_scale, out, dev_status,
 
 # ---- fused deep MoE ---------------------------------------------------------
 
-def _strided(src, rows, name):
-    """(tensor, byte_offset, byte_stride) -> pointer to the fp32 at
-    offset + r * stride for r < rows, checked against the tensor's bytes."""
+def _strided(src, rows, name, each=4):
+    """(tensor, byte_offset, byte_stride) -> pointer to the fp32 (``each`` bytes of
+    them) at offset + r * stride for r < rows, checked against the tensor's bytes."""
     t, off, stride = src
     if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
         raise TypeError("%s must be a contiguous CUDA tensor" % name)
     nbytes = t.numel() * t.element_size()
-    if off < 0 or stride < 4 or (rows > 0 and off + (rows - 1) * stride + 4 > nbytes):
+    if off < 0 or stride < 4 or (rows > 0 and off + (rows - 1) * stride + each > nbytes):
         raise ValueError("%s: rows reach past the tensor" % name)
     return t.data_ptr() + int(off), int(stride)
 
@@ -732,9 +746,137 @@ def moe_linear_i8(a, w, K, group_rows, col_scale, row_scale, bias, c, dev_status
     return _check(st, "moe_linear_i8")
 
 
+# ---- the norm in front of the layer, and the layer in 8-bit floating point -----------
+
+_F8_CODES = (torch.float8_e4m3fn, torch.uint8)
+_CODE = {"i8": MOE_CODE_I8, "f8": MOE_CODE_F8}
+
+
+def f8_row_bytes(H):
+    """Bytes of an e4m3 row image of H codes: the codes, their scales from byte
+    align32(H) on, each part padded to a multiple of 32."""
+    return int(_lib.moe_f8_row_bytes(int(H)))
+
+
+def _token_rows(t, name, dtype, T, H):
+    """(pointer, row stride) of [T, H] rows of the token dtype (None: NULL)."""
+    if t is None:
+        return None, 0
+    p, stride, rows, cols = _rows(t, name, (dtype,))
+    if rows != T or cols != H:
+        raise ValueError("%s must be [%d, %d]" % (name, T, H))
+    return p, stride
+
+
+def _images(t, rows, row_bytes, name):
+    """Pointer of packed row images (None: NULL)."""
+    if t is None:
+        return None
+    p = _ptr(t, (torch.uint8, torch.int8, torch.float8_e4m3fn), None, name)
+    if t.numel() < rows * row_bytes:
+        raise ValueError("%s is smaller than %d rows of %d bytes" % (name, rows, row_bytes))
+    return p
+
+
+def moe_rms_norm(x, residual, gamma, eps, sum_out, out, codes, rstd, dev_status, code="f8",
+                 stream=None):
+    """Root-mean-square norm of rows x [T, H] (bf16 or fp16; rows may lie apart).
+    With a residual [T, H] the sum x + residual, rounded, goes to sum_out and is
+    what is normed.  gamma fp32 [H].  Any of: out [T, H], the norm in the rows'
+    dtype; codes, the norm in 8 bits as row images (code 'f8': e4m3 with a scale
+    per 128 values, f8_row_bytes(H) a row; 'i8': INT8 as dispatch quantises rows);
+    rstd fp32 [T], for the gradient.  sum_out and out may be x or residual."""
+    p, stride, T, H = _rows(x, "x", (torch.bfloat16, torch.float16))
+    if code not in _CODE:
+        raise ValueError("code must be 'f8' or 'i8', got %r" % (code,))
+    rp, rstride = _token_rows(residual, "residual", x.dtype, T, H)
+    sp, sstride = _token_rows(sum_out, "sum_out", x.dtype, T, H)
+    op, ostride = _token_rows(out, "out", x.dtype, T, H)
+    row = f8_row_bytes(H) if code == "f8" else (H + 31) // 32 * 32 + 32
+    st = _lib.moe_rms_norm(
+        p, _DTYPE[x.dtype], T, H, stride, rp, rstride, _ptr(gamma, _F32, H, "gamma"), float(eps),
+        sp, sstride, op, ostride, _images(codes, T, row, "codes"), _CODE[code],
+        _ptr(rstd, _F32, T, "rstd"), _ptr(dev_status, _I32, 1, "dev_status"), _stream(stream))
+    return _check(st, "moe_rms_norm")
+
+
+def rms_norm_backward_workspace_bytes(T, H):
+    return int(_lib.moe_rms_norm_backward_workspace_bytes(int(T), int(H)))
+
+
+def moe_rms_norm_backward(d_out, x, gamma, rstd, d_sum, d_x, d_gamma, workspace, dev_status,
+                          stream=None):
+    """Gradient of moe_rms_norm: d_x [T, H] (of the rows and of the residual alike)
+    and d_gamma fp32 [H], from d_out [T, H], the normed rows x (sum_out, where there
+    was a residual) and rstd; d_sum [T, H] or None is the gradient that reaches the
+    rows past the norm.  d_x may be d_out, x or d_sum."""
+    p, stride, T, H = _rows(d_out, "d_out", (torch.bfloat16, torch.float16))
+    xp, xstride = _token_rows(x, "x", d_out.dtype, T, H)
+    sp, sstride = _token_rows(d_sum, "d_sum", d_out.dtype, T, H)
+    dp, dstride = _token_rows(d_x, "d_x", d_out.dtype, T, H)
+    need = rms_norm_backward_workspace_bytes(T, H)
+    wp = _ptr(workspace, None, None, "workspace")
+    if workspace is not None and workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace is smaller than %d bytes" % need)
+    st = _lib.moe_rms_norm_backward(
+        p, _DTYPE[d_out.dtype], T, H, stride, xp, xstride, _ptr(gamma, _F32, H, "gamma"),
+        _ptr(rstd, _F32, T, "rstd"), sp, sstride, dp, dstride,
+        _ptr(d_gamma, _F32, H, "d_gamma"), wp, _ptr(dev_status, _I32, 1, "dev_status"),
+        _stream(stream))
+    return _check(st, "moe_rms_norm_backward")
+
+
+def moe_swiglu_f8(h, group_off, codes, dev_status, stream=None):
+    """Rows h [M, 2I] (gate, then up; bf16, fp16 or fp32; rows may lie apart) ->
+    e4m3 row images of silu(gate) * up.  group_off int64 [G+1] or None: rows at or
+    past its last entry are not written."""
+    p, stride, M, cols = _rows(h, "h", _LOGITS)
+    if cols % 2:
+        raise ValueError("h must be [M, 2I]")
+    I = cols // 2
+    G = 0 if group_off is None else group_off.numel() - 1
+    st = _lib.moe_swiglu_f8(
+        p, _ANY_DTYPE[h.dtype], M, I, stride, _ptr(group_off, torch.int64, None, "group_off"), G,
+        _images(codes, M, f8_row_bytes(I), "codes"), _ptr(dev_status, _I32, 1, "dev_status"),
+        _stream(stream))
+    return _check(st, "moe_swiglu_f8")
+
+
+def moe_linear_f8(a, w, K, group_rows, w_scale, a_scale, bias, c, dev_status, stream=None):
+    """c [rows, N] (bf16, fp16 or fp32) = e4m3 rows a [rows, stride] x e4m3 weights
+    w [G, N, stride]^T over K codes, with a scale per 128 codes of a row and per
+    128 x 128 block of a weight matrix (w_scale fp32 [G, ceil(N/128), ceil(K/128)]),
+    plus bias [G, N].  a may hold row images (uint8); a_scale is (tensor,
+    byte_offset, byte_stride) of each row's scales: (a, align32(K), row bytes) for
+    images.  group_rows int32 [G] (None with G = 1: every row)."""
+    ap, a_stride, rows, cols = _rows(a, "a", _F8_CODES)
+    if w.dim() != 3:
+        raise ValueError("w must be [G, N, >= K]")
+    G, N, w_stride = w.shape
+    if w_stride < K or cols < K:
+        raise ValueError("a must be [rows, >= K] and w [G, N, >= K]")
+    if rows == 0:
+        return MOE_OK
+    out = _ANY_DTYPE.get(c.dtype)
+    if out is None or out == MOE_INT32 or c.shape != (rows, N):
+        raise ValueError("c must be [rows, N] in bf16, fp16 or fp32")
+    if group_rows is not None and group_rows.numel() != G:
+        raise ValueError("group_rows must have G entries")
+    nb, kb = (N + 127) // 128, (K + 127) // 128
+    sp, sstride = _strided(a_scale, rows, "a_scale", 4 * kb)
+    st = _lib.moe_linear_f8(
+        ap, rows, a_stride, _ptr(w, _F8_CODES, None, "w"), w_stride, G, N, int(K),
+        _ptr(group_rows, _I32, G, "group_rows"), _ptr(w_scale, _F32, G * nb * kb, "w_scale"),
+        sp, sstride, _ptr(bias, _F32, G * N, "bias"), _ptr(c, None, None, "c"), out,
+        _ptr(dev_status, _I32, 1, "dev_status"), _stream(stream))
+    return _check(st, "moe_linear_f8")
+
+
 # the size queries and the status names under the C entry points' own names
 moe_status_string = status_string
 moe_recv_row_bytes = recv_row_bytes
 moe_layout_workspace_bytes = layout_workspace_bytes
 moe_fused_workspace_bytes = fused_workspace_bytes
 moe_gmm_block_n = gmm_block_n
+moe_f8_row_bytes = f8_row_bytes
+moe_rms_norm_backward_workspace_bytes = rms_norm_backward_workspace_bytes

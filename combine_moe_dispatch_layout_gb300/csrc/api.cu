@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "moe_ep_internal.cuh"
+#include "row_codes.cuh"
 
 namespace {
 
@@ -43,6 +44,18 @@ bool valid_routing(int32_t dtype, int64_t T, int32_t E, int64_t stride, int32_t 
   if (stride < E || stride >= kMaxStride) return false;
   if (score != MOE_SIGMOID && score != MOE_SOFTMAX) return false;
   return scale - scale == 0.0f;
+}
+
+// Sizes of moe_rms_norm and its gradient.
+bool valid_norm(int32_t dtype, int64_t T, int32_t H) {
+  return (dtype == MOE_BF16 || dtype == MOE_FP16) && T >= 0 && T < (int64_t(1) << 31) && H >= 8 &&
+         H <= MOE_EP_MAX_HIDDEN && H % 8 == 0;
+}
+
+// T rows of H elements at p, `unit` elements to 16 bytes.
+bool valid_rows(const void* p, int64_t T, int64_t H, int64_t stride, int unit) {
+  return aligned(p, 16) &&
+         (T <= 1 || (stride >= H && stride < kMaxStride && stride % unit == 0));
 }
 
 moe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -588,6 +601,100 @@ moe_status moe_linear_i8(const void* a, int64_t a_rows, int64_t a_stride, const 
                              static_cast<const unsigned char*>(row_scale), row_scale_stride,
                              scaled ? bias : nullptr, c, c_dtype};
   return from_cuda(moe_ep::launch_linear_i8(p, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_f8_row_bytes(int32_t H) {
+  return H < 1 || H > MOE_EP_MAX_HIDDEN ? -1 : moe_ep::f8_row_bytes(H);
+}
+
+moe_status moe_rms_norm(const void* x, int32_t dtype, int64_t T, int32_t H, int64_t x_stride,
+                        const void* residual, int64_t residual_stride, const float* gamma,
+                        float eps, void* sum, int64_t sum_stride, void* out,
+                        int64_t out_stride, void* codes, int32_t code_type, float* rstd,
+                        int32_t* dev_status, void* stream) {
+  if (!valid_norm(dtype, T, H) || !dev_status || !aligned(dev_status, 4) || !(eps > 0.0f) || eps - eps != 0.0f ||
+      (code_type != MOE_CODE_I8 && code_type != MOE_CODE_F8))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !gamma || (!out && !codes) || (residual == nullptr) != (sum == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!valid_rows(x, T, H, x_stride, 8) || !aligned(gamma, 16) || !aligned(codes, 16) ||
+      !aligned(rstd, 4) || (out && !valid_rows(out, T, H, out_stride, 8)) ||
+      (residual && (!valid_rows(residual, T, H, residual_stride, 8) ||
+                    !valid_rows(sum, T, H, sum_stride, 8))))
+    return MOE_ERR_INVALID_ARG;
+  const moe_ep::NormArgs p{x, residual, sum, out, codes, gamma, rstd, T, x_stride,
+                           residual_stride, sum_stride, out_stride, H, dtype, code_type, eps};
+  return from_cuda(moe_ep::launch_rms_norm(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_rms_norm_backward_workspace_bytes(int64_t T, int32_t H) {
+  return valid_norm(MOE_BF16, T, H) ? moe_ep::rms_norm_backward_workspace_bytes(T, H) : 0;
+}
+
+moe_status moe_rms_norm_backward(const void* d_out, int32_t dtype, int64_t T, int32_t H,
+                                 int64_t d_out_stride, const void* x, int64_t x_stride,
+                                 const float* gamma, const float* rstd, const void* d_sum,
+                                 int64_t d_sum_stride, void* d_x, int64_t d_x_stride,
+                                 float* d_gamma, void* workspace, int32_t* dev_status,
+                                 void* stream) {
+  if (!valid_norm(dtype, T, H) || !d_gamma || !aligned(d_gamma, 4) || !dev_status ||
+      !aligned(dev_status, 4))
+    return MOE_ERR_INVALID_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) return from_cuda(cudaMemsetAsync(d_gamma, 0, sizeof(float) * size_t(H), st));
+  if (!d_out || !x || !gamma || !rstd || !d_x || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!valid_rows(d_out, T, H, d_out_stride, 8) || !valid_rows(x, T, H, x_stride, 8) ||
+      !valid_rows(d_x, T, H, d_x_stride, 8) ||
+      (d_sum && !valid_rows(d_sum, T, H, d_sum_stride, 8)) || !aligned(gamma, 16) ||
+      !aligned(rstd, 4) || !aligned(workspace, 16))
+    return MOE_ERR_INVALID_ARG;
+  const moe_ep::NormBackwardArgs p{d_out, x, d_sum, gamma, rstd, d_x,
+                                   static_cast<float*>(workspace), T, d_out_stride, x_stride,
+                                   d_sum_stride, d_x_stride, H, dtype};
+  return from_cuda(moe_ep::launch_rms_norm_backward(p, d_gamma, st));
+}
+
+moe_status moe_swiglu_f8(const void* h, int32_t dtype, int64_t M, int32_t I, int64_t h_stride,
+                         const int64_t* group_off, int32_t G, void* codes,
+                         int32_t* dev_status, void* stream) {
+  if (!dev_status || !aligned(dev_status, 4) || (dtype != MOE_BF16 && dtype != MOE_FP16 && dtype != MOE_FP32) || M < 0 ||
+      M >= (int64_t(1) << 31) || I < 8 || I > MOE_EP_MAX_HIDDEN / 2 || I % 8 != 0 ||
+      (group_off && (G < 1 || G > MOE_EP_MAX_EXPERTS)))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!h || !codes || !valid_rows(h, M, 2 * int64_t(I), h_stride, dtype == MOE_FP32 ? 4 : 8) ||
+      !aligned(codes, 16) || !aligned(group_off, 8))
+    return MOE_ERR_INVALID_ARG;
+  const moe_ep::SwigluF8Args p{h, group_off, codes, dev_status, M, h_stride, I, G, dtype};
+  return from_cuda(moe_ep::launch_swiglu_f8(p, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_linear_f8(const void* a, int64_t a_rows, int64_t a_stride, const void* w,
+                         int64_t w_stride, int32_t G, int32_t N, int32_t K,
+                         const int32_t* group_rows, const float* w_scale,
+                         const void* a_scale, int64_t a_scale_stride, const float* bias,
+                         void* c, int32_t c_dtype, int32_t* dev_status, void* stream) {
+  if (a_rows < 0 || a_rows > INT32_MAX - 1024 || K < 1 || K > MOE_EP_MAX_HIDDEN || N < 1 ||
+      N > MOE_EP_MAX_HIDDEN || G < 1 || G > MOE_EP_MAX_EXPERTS || a_stride < K ||
+      a_stride % 16 != 0 || w_stride < K || w_stride % 16 != 0 || a_stride >= kMaxStride ||
+      w_stride >= kMaxStride || c_dtype < MOE_BF16 || c_dtype > MOE_FP32 || !dev_status)
+    return MOE_ERR_INVALID_ARG;
+  if ((a_rows / 32 + G) * ((N + 255) / 256) > INT32_MAX) return MOE_ERR_INVALID_ARG;  // tiles
+  if (a_scale_stride % 4 != 0 || a_scale_stride >= kMaxStride ||
+      a_scale_stride < (a_rows <= 1 ? 0 : 4 * int64_t(moe_ep::code_blocks(K))))
+    return MOE_ERR_INVALID_ARG;
+  if (a_rows == 0) return MOE_OK;
+  if (!a || !w || !c || (!group_rows && G != 1) || !w_scale || !a_scale)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(c, 16) || !aligned(group_rows, 4) ||
+      !aligned(dev_status, 4) || !aligned(w_scale, 4) || !aligned(a_scale, 4) ||
+      !aligned(bias, 4))
+    return MOE_ERR_INVALID_ARG;
+  const moe_ep::LinearArgs p{a, a_rows, a_stride, w, w_stride, G, N, K, group_rows, w_scale,
+                             static_cast<const unsigned char*>(a_scale), a_scale_stride, bias, c,
+                             c_dtype};
+  return from_cuda(moe_ep::launch_linear_f8(p, dev_status, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,500 @@
+// linear_f8.cu -- matrix product of e4m3 rows and weights with a scale per 128 codes of a
+// row and per 128 x 128 block of a weight matrix, rows grouped by expert
+// (include/moe_ep.h, moe_linear_f8).
+//
+// Mathematics.  c[m][n] = sum over blocks b of 128 codes of
+//   (a_scale[m][b] * w_scale[n / 128][b]) * sum_{j in b} a[m][j] w[n][j]   (+ bias[n]).
+// The inner sums are the tensor cores' (fp32); their scales differ from block to block, so
+// every block's sums leave TMEM and meet their scale in one fused multiply-add in fp32
+// registers.
+//
+// Tile: a pair of CTAs (two SMs of a cluster) takes 256 tokens (the MMA's M, 128 TMEM
+// lanes on each SM) x up to 256 channels (its N); each SM holds its 128 token rows and half
+// of the weight rows.  Tokens are on the lanes so that a draining thread has one token:
+// its scale is one register, and the multiply-adds take two columns per instruction.
+// Warps of a CTA (one CTA per SM, persistent):
+//   warp 0   copies its 128 token rows and half of the weight rows, 128 bytes of each,
+//            into a ring of stages (tensor copies, 128-byte swizzle)
+//   warp 1   of the pair's first CTA: issues tcgen05.mma (K = 32), four per 128-code
+//            block, into one of two TMEM accumulators in turn; of its second CTA: tells
+//            the first which of its stages have landed
+//   8 warps  drain a block's sums, scale and add them, and store the tile
+// Every wait is bounded: a timeout sets MOE_ERR_TIMEOUT, the CTA stops issuing work and
+// drains what is in flight.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "group_tiles.cuh"
+#include "moe_ep_internal.cuh"
+#include "row_codes.cuh"
+#include "tcgen05.cuh"
+
+namespace moe_ep {
+namespace {
+
+constexpr int CG = 2;                // CTAs per tile (a pair)
+constexpr int TM = 128;              // tokens per CTA
+constexpr int BK = kCodeBlock;       // codes per stage: one 128-byte row
+constexpr int kRasterTokens = 8;     // token blocks per raster band (weights reused from L2)
+constexpr int kEpiWarps = 8, kCtrlWarps = 4;
+constexpr int kThreads = 32 * (kCtrlWarps + kEpiWarps);
+// Registers per thread: 168 at launch, handed out again by role.
+constexpr int kEpiRegs = 208, kCtrlRegs = 88;
+static_assert(32 * (kEpiWarps * kEpiRegs + kCtrlWarps * kCtrlRegs) <= kThreads * 168,
+              "no more registers than the launch has");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kAccCols = 256;   // column offset of the second accumulator
+constexpr int kAhead = 4;            // blocks that a thread's scales are loaded ahead
+constexpr int kMaxStages = 10;
+
+// NT: channels per tile.
+template <int NT>
+struct Stages {
+  static constexpr uint32_t kBytes = (TM + NT / CG) * BK;
+  static constexpr uint32_t kBarBytes = 512;
+  static size_t bytes(int stages, int G) {
+    return 1024 + size_t(stages) * kBytes + kBarBytes + size_t(G + 1) * 8;
+  }
+};
+
+struct Tile {
+  int g;           // group
+  int n0;          // first output channel
+  int row0;        // first token row
+  int rows;        // tokens of the group from there on, at most CG * TM
+};
+
+template <int NT>
+__device__ __forceinline__ Tile decode_tile(int t, uint32_t goff, uint32_t tpre, int G, int ntn) {
+  const int lo = group_of_tile(t, tpre, G);
+  const int off = smem_load(goff + 4 * lo);
+  const int cnt = smem_load(goff + 4 * lo + 4) - off;
+  const int local = t - smem_load(tpre + 4 * lo);
+  const int blocks = row_blocks(cnt, CG * TM);
+  // bands of kRasterTokens token blocks (the last band takes the remainder); inside a
+  // band the token block is fastest, so the CTAs in flight share weight tiles and a
+  // bounded number of token blocks
+  const int nband = max(blocks / kRasterTokens, 1), per_band = kRasterTokens * ntn;
+  const int band = min(local / per_band, nband - 1);
+  const int width = band < nband - 1 ? kRasterTokens : blocks - band * kRasterTokens;
+  const int r = local - band * per_band;
+  const int nblk = r / width, mblk = band * kRasterTokens + r - nblk * width;
+  Tile tl;
+  tl.g = lo;
+  tl.n0 = nblk * NT;
+  tl.row0 = off + mblk * (CG * TM);
+  tl.rows = min(CG * TM, cnt - mblk * (CG * TM));
+  return tl;
+}
+
+template <int OUT>
+__device__ __forceinline__ void store_one(void* c, int64_t at, float v) {
+  if constexpr (OUT == MOE_FP32) static_cast<float*>(c)[at] = v;
+  else static_cast<uint16_t*>(c)[at] = static_cast<uint16_t>(narrow_rn<OUT>(v));
+}
+
+template <int OUT>
+__device__ __forceinline__ uint32_t narrow_pair(float lo, float hi) {
+  uint32_t h;
+  if constexpr (OUT == MOE_BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  return h;
+}
+
+template <int NT, int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ CUtensorMap map_a, const LinearArgs p, int stages,
+                      int32_t* dev_status) {
+  using St = Stages<NT>;
+  constexpr int kCols = NT / 2;              // columns per draining thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t bars = sbase + stages * St::kBytes;
+  auto full = [&](int s) { return bars + 8 * s; };                      // this CTA's copies landed
+  auto peer = [&](int s) { return bars + 8 * (kMaxStages + s); };       // ... the other CTA's
+  auto empty = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };  // multiplied
+  constexpr int kT0 = 3 * kMaxStages;
+  auto tfull = [&](int b) { return bars + 8 * (kT0 + b); };             // accumulator final
+  auto tempty = [&](int b) { return bars + 8 * (kT0 + 2 + b); };        // ... drained
+  const uint32_t tmem_slot = bars + 8 * (kT0 + 4), abort_flag = tmem_slot + 4;
+  const uint32_t issued = abort_flag + 4;    // the pair's commits: of stages, of accumulators
+  static_assert(8 * (kT0 + 4) + 16 <= St::kBarBytes, "barriers fit");
+  const uint32_t goff = bars + St::kBarBytes, tpre = goff + 4 * (p.G + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ntn = (p.N + NT - 1) / NT;
+  const int rank = static_cast<int>(cluster_rank());
+  const int nk = code_blocks(p.K);
+
+  wait_for_stream();
+  let_next_start();
+  if (p.group_rows) {        // the scan borrows the stages, which are not in use yet
+    build_group_tables<kThreads>(p, CG * TM, ntn, smem, goff, tpre, dev_status);
+  } else if (tid == 64) {
+    const int rows = static_cast<int>(p.a_rows);
+    smem_store(goff, 0);
+    smem_store(goff + 4, rows);
+    smem_store(tpre, 0);
+    smem_store(tpre + 4, row_blocks(rows, CG * TM) * ntn);
+  }
+  if (warp == 0) {           // barriers: one lane each
+    if (lane < stages) {
+      bar_init(full(lane), 1);
+      bar_init(peer(lane), 1);
+      bar_init(empty(lane), 1);
+    }
+    if (lane < 2) {
+      bar_init(tfull(lane), 1);
+      bar_init(tempty(lane), CG * kEpiWarps);
+    }
+    if (lane == 0) {
+      smem_store(abort_flag, 0);
+      smem_store(issued, 0);
+      smem_store(issued + 4, 0);
+      tensor_map_prefetch(&map_w);
+      tensor_map_prefetch(&map_a);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    pair_tmem_alloc(tmem_slot, kTmemCols);
+  }
+  tc_fence_before();
+  __syncthreads();
+  // The copies start at once; a role waits for the other CTA before it first reaches
+  // into it (its barriers must have been set up).
+  cluster_arrive_all();
+  tc_fence_after();
+
+  const int tiles = smem_load(tpre + 4 * p.G), first = cluster_id(), step = cluster_count();
+  // Waits for the last commit on each of this CTA's barriers, once all of them are
+  // issued: ncommit of stages, nacc of accumulators.  A barrier's n-th commit is issued
+  // only after this CTA's threads have seen its n-1-th, so at most one is outstanding and
+  // the parity tells.  Also after a timeout.
+  auto await_commits = [&](uint32_t ncommit, uint32_t nacc) {
+    bool ok = true;
+    const uint32_t ns = stages;
+#pragma unroll 1
+    for (uint32_t i = ncommit > ns ? ncommit - ns : 0; i < ncommit; ++i)
+      ok &= bar_wait(empty(i % ns), (i / ns) & 1u);
+#pragma unroll 1
+    for (uint32_t i = nacc > 2 ? nacc - 2 : 0; i < nacc; ++i)
+      ok &= bar_wait(tfull(i & 1u), (i >> 1) & 1u);
+    if (!ok) set_status(dev_status, MOE_ERR_TIMEOUT);
+  };
+
+  if (warp < kCtrlWarps) {
+    regs_fewer<kCtrlRegs>();
+    if (warp == 0) {
+      // ---- copies -------------------------------------------------------------------
+      const bool issue = elect_one();
+      int s = 0;
+      uint32_t phase = 0, nload = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += step) {
+        const Tile tl = decode_tile<NT>(t, goff, tpre, p.G, ntn);
+        const int wrow = tl.g * p.N + tl.n0 + rank * (NT / CG);
+        const int arow = tl.row0 + rank * TM;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!bar_wait(empty(s), phase ^ 1u)) {
+            ok = false;
+            break;
+          }
+          if (issue) {
+            const uint32_t dst = sbase + s * St::kBytes;
+            bar_expect(full(s), St::kBytes);
+            tensor_load_2d(dst, &map_a, kb * BK, arow, full(s));
+            tensor_load_2d(dst + TM * BK, &map_w, kb * BK, wrow, full(s));
+          }
+          ++nload;
+          if (++s == stages) { s = 0; phase ^= 1u; }
+        }
+        ok = ok && !smem_load(abort_flag);
+      }
+      if (!ok) {
+        if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
+        smem_store(abort_flag, 1);
+      }
+      // no copy may land once the CTA has gone (only after a timeout are there any that
+      // nobody waited for)
+      const uint32_t ns = stages;
+      for (uint32_t i = nload > ns ? nload - ns : 0; issue && i < nload; ++i)
+        bar_wait(full(i % ns), (i / ns) & 1u);
+      cluster_wait_all();
+    } else if (warp == 1 && rank == 1) {
+      // ---- which stages of this CTA have landed ---------------------------------------
+      cluster_wait_all();
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += step) {
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!bar_wait(full(s), phase) || smem_load(abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) cluster_arrive(cluster_addr(peer(s), 0));
+          if (++s == stages) { s = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
+        smem_store(abort_flag, 1);
+      }
+    } else if (warp == 1) {
+      // ---- products of the pair ---------------------------------------------------------
+      cluster_wait_all();
+      const bool issue = elect_one();
+      const uint32_t tmem = smem_load(tmem_slot);
+      constexpr int kM = CG * TM;
+      const uint32_t idesc = f16_mma_desc(kM, NT);
+      int s = 0;
+      uint32_t phase = 0, nacc = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += step) {
+        for (int kb = 0; kb < nk; ++kb) {
+          const uint32_t b = nacc & 1u, use = (nacc >> 1) & 1u;
+          if (!bar_wait(tempty(b), use ^ 1u) || !bar_wait(full(s), phase) ||
+              !bar_wait(peer(s), phase) || smem_load(abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (issue) {
+            const uint32_t st = sbase + s * St::kBytes;
+            const uint64_t da = operand_desc(st), db = operand_desc(st + TM * BK);
+            const uint32_t d = tmem + b * kAccCols;
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)     // + 32 bytes along K per step
+              pair_mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk != 0);
+            pair_commit(empty(s), uint16_t(3));
+            pair_commit(tfull(b), uint16_t(3));
+          }
+          ++nacc;
+          if (++s == stages) { s = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
+        smem_store(abort_flag, 1);
+      }
+      // the pair's other CTA, whose barriers the commits arrive on too, learns how many
+      // there were (of stages as of accumulators); it waits for them after the closing
+      // barrier
+      if (issue) {
+        await_commits(nacc, nacc);
+        const uint32_t to = cluster_addr(issued, 1);
+        cluster_store(to, nacc);
+        cluster_store(to + 4, nacc);
+      }
+    } else {
+      cluster_wait_all();
+    }
+    __syncwarp();
+  } else {
+    // ---- blocks' sums -> scaled sums -> stores --------------------------------------------
+    regs_more<kEpiRegs>();
+    const int q = warp & 3;                  // TMEM lanes 32 q ..
+    const int col0 = ((warp - kCtrlWarps) >> 2) * kCols;
+    const uint32_t base = smem_load(tmem_slot) + (uint32_t(q * 32) << 16) + col0;
+    const int nblocks = code_blocks(p.N);
+    cluster_wait_all();
+    uint32_t nacc = 0;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += step) {
+      const Tile tl = decode_tile<NT>(t, goff, tpre, p.G, ntn);
+      const int mine = rank * TM + q * 32 + lane;          // this thread's token of the tile
+      const int64_t row = tl.row0 + mine;
+      const int n0 = tl.n0 + col0;
+      const bool work = rank * TM + q * 32 < tl.rows && n0 < p.N;     // of the warp
+      const unsigned char* as =
+          p.row_scale + min(row, p.a_rows - 1) * p.row_scale_stride;
+      const float* ws = p.col_scale +
+                        (int64_t(tl.g) * nblocks + min(n0 / kCodeBlock, nblocks - 1)) * nk;
+      auto scale = [&](int kb) {
+        kb = min(kb, nk - 1);
+        return __fmul_rn(*reinterpret_cast<const float*>(as + 4 * kb), ws[kb]);
+      };
+      float sc[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) sc[i] = work ? scale(i) : 0.0f;
+      float2 acc[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+      for (int kb = 0; kb < nk; ++kb, ++nacc) {
+        const uint32_t b = nacc & 1u;
+        const bool got = bar_wait(tfull(b), (nacc >> 1) & 1u) && !smem_load(abort_flag);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
+        tc_fence_after();
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cluster_arrive(cluster_addr(tempty(b), 0));
+        };
+        if (!work) {
+          release();
+          continue;
+        }
+        const float2 s2 = bcast2(sc[0]);
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) sc[i] = sc[i + 1];
+        sc[kAhead - 1] = scale(kb + kAhead);
+        constexpr int kParts = kCols / 16;
+        float v[2][16];
+        tmem_start16(base + b * kAccCols, v[0]);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          tmem_wait16(v[i & 1]);
+          if (i + 1 < kParts) tmem_start16(base + b * kAccCols + 16 * (i + 1), v[(i + 1) & 1]);
+          else release();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            acc[8 * i + j] = fma2_rn(make_float2(v[i & 1][2 * j], v[i & 1][2 * j + 1]), s2,
+                                      acc[8 * i + j]);
+        }
+      }
+      if (!ok) {
+        if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
+        smem_store(abort_flag, 1);
+        break;
+      }
+      if (!work) continue;
+      if (p.bias) {
+        const float* bias = p.bias + int64_t(tl.g) * p.N;
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j) {
+          const int n = n0 + 2 * j;
+          acc[j] = add2_rn(acc[j], make_float2(bias[min(n, p.N - 1)], bias[min(n + 1, p.N - 1)]));
+        }
+      }
+      if (mine < tl.rows) {
+        const int64_t at = row * p.N + n0;
+        constexpr int kItem = OUT == MOE_FP32 ? 4 : 2, kVec = 16 / kItem;     // per 16 bytes
+        if (p.N % kVec == 0) {
+#pragma unroll
+          for (int j = 0; j < kCols; j += kVec) {
+            uint4 o;
+            if constexpr (OUT == MOE_FP32) {
+              o = make_uint4(__float_as_uint(acc[j / 2].x), __float_as_uint(acc[j / 2].y),
+                             __float_as_uint(acc[j / 2 + 1].x),
+                             __float_as_uint(acc[j / 2 + 1].y));
+            } else {
+              o = make_uint4(narrow_pair<OUT>(acc[j / 2].x, acc[j / 2].y),
+                             narrow_pair<OUT>(acc[j / 2 + 1].x, acc[j / 2 + 1].y),
+                             narrow_pair<OUT>(acc[j / 2 + 2].x, acc[j / 2 + 2].y),
+                             narrow_pair<OUT>(acc[j / 2 + 3].x, acc[j / 2 + 3].y));
+            }
+            if (n0 + j < p.N)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.c) + (at + j) * kItem) = o;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (n0 + j < p.N) store_one<OUT>(p.c, at + j, j & 1 ? acc[j / 2].y : acc[j / 2].x);
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // no CTA of a pair goes while the other's threads may still arrive on its barriers ...
+  cluster_sync();
+  if (warp == 1) {
+    // ... nor while a commit may (the first CTA's role has waited for its own)
+    await_commits(smem_load(issued), smem_load(issued + 4));
+    __syncwarp();
+    tc_fence_after();
+    pair_tmem_free(smem_load(tmem_slot), kTmemCols);
+  }
+}
+
+struct Plan {
+  int nt;          // channels per tile
+  int clusters;
+};
+
+template <int NT, int OUT>
+cudaError_t launch_kernel(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
+                          const Plan& plan, int32_t* dev_status, int optin, cudaStream_t st) {
+  using S = Stages<NT>;
+  int stages = kMaxStages;
+  while (stages > 2 && S::bytes(stages, p.G) > size_t(optin)) --stages;
+  const size_t smem = S::bytes(stages, p.G);
+  auto kernel = linear_f8_tile_kernel<NT, OUT>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;      // see launch_early
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, stages, dev_status);
+}
+
+template <int NT>
+cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
+                      const Plan& plan, int32_t* dev_status, int optin, cudaStream_t st) {
+  switch (p.c_dtype) {
+    case MOE_BF16: return launch_kernel<NT, MOE_BF16>(mw, ma, p, plan, dev_status, optin, st);
+    case MOE_FP16: return launch_kernel<NT, MOE_FP16>(mw, ma, p, plan, dev_status, optin, st);
+    default: return launch_kernel<NT, MOE_FP32>(mw, ma, p, plan, dev_status, optin, st);
+  }
+}
+
+// Whether the kernel that streams weights to the warps' own products is the faster one.
+bool use_few(const LinearArgs& p) { return p.a_rows <= 32 * int64_t(p.G); }
+
+// The widest tile that gives every pair of SMs something to do.
+Plan make_plan(const LinearArgs& p, int sms) {
+  const int64_t pairs = std::max(1, sms / CG);
+  // at most this many, for any group sizes
+  const int64_t blocks = p.G == 1 ? (p.a_rows + CG * TM - 1) / (CG * TM)
+                                  : p.a_rows / (CG * TM) + std::min<int64_t>(p.G, p.a_rows);
+  Plan plan{};
+  for (int nt : {256, 128, 64}) {
+    const int64_t tiles = blocks * ((p.N + nt - 1) / nt);
+    plan.nt = nt;
+    plan.clusters = static_cast<int>(std::min(tiles, pairs));
+    if (tiles >= pairs) break;
+  }
+  return plan;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_f8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
+  if (use_few(p)) return launch_linear_f8_few(p, dev_status, st);
+  int dev = 0, sms = 0, optin = 0;
+  cudaError_t e = current_device_sms(&dev, &sms);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e != cudaSuccess) return e;
+  const Plan plan = make_plan(p, sms);
+  CUtensorMap mw, ma;
+  e = encode_bytes_2d(&mw, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, plan.nt / CG);
+  if (e == cudaSuccess) e = encode_bytes_2d(&ma, p.a, p.a_rows, p.K, p.a_stride, TM);
+  if (e != cudaSuccess) return e;
+  return plan.nt == 256   ? launch_nt<256>(mw, ma, p, plan, dev_status, optin, st)
+         : plan.nt == 128 ? launch_nt<128>(mw, ma, p, plan, dev_status, optin, st)
+                          : launch_nt<64>(mw, ma, p, plan, dev_status, optin, st);
+}
+
+}  // namespace moe_ep

@@ -373,10 +373,10 @@ __device__ __forceinline__ uint4 ld_once_16(const void* p) {
   return v;
 }
 template <class... P, class... A>
-cudaError_t launch_early(void (*kernel)(P...), int64_t grid, int block, size_t smem,
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, size_t smem,
                          cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -386,6 +386,11 @@ cudaError_t launch_early(void (*kernel)(P...), int64_t grid, int block, size_t s
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), int64_t grid, int block, size_t smem,
+                         cudaStream_t st, A... args) {
+  return launch_early(kernel, dim3(static_cast<unsigned>(grid)), block, smem, st, args...);
 }
 
 // ---- launchers (one per translation unit) ----------------------------------
@@ -549,5 +554,50 @@ struct LinearArgs {
 // launch_linear_i8 chooses by the mean rows per group.
 cudaError_t launch_linear_i8_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st);
 cudaError_t launch_linear_i8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st);
+
+// moe_linear_f8: a LinearArgs whose col_scale is [G][ceil(N/128)][ceil(K/128)] and whose
+// row_scale holds a row's ceil(K/128) scales from byte m * row_scale_stride on.
+cudaError_t launch_linear_f8_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st);
+cudaError_t launch_linear_f8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st);
+
+// Strides in elements.
+struct NormArgs {
+  const void* x;
+  const void* residual;             // or nullptr
+  void* sum;                        // where there is a residual
+  void* out;                        // or nullptr
+  void* codes;                      // row images or nullptr
+  const float* gamma;
+  float* rstd;                      // or nullptr
+  int64_t T, x_stride, residual_stride, sum_stride, out_stride;
+  int H, dtype, code_type;
+  float eps;
+};
+cudaError_t launch_rms_norm(const NormArgs& p, cudaStream_t st);
+
+struct NormBackwardArgs {
+  const void* d_out;
+  const void* x;
+  const void* d_sum;                // or nullptr
+  const float* gamma;
+  const float* rstd;
+  void* d_x;
+  float* parts;                     // the workspace
+  int64_t T, d_out_stride, x_stride, d_sum_stride, d_x_stride;
+  int H, dtype;
+};
+size_t rms_norm_backward_workspace_bytes(int64_t T, int H);
+cudaError_t launch_rms_norm_backward(const NormBackwardArgs& p, float* d_gamma,
+                                     cudaStream_t st);
+
+struct SwigluF8Args {
+  const void* h;
+  const int64_t* group_off;         // [G + 1] or nullptr
+  void* codes;
+  int32_t* dev_status;
+  int64_t M, h_stride;
+  int I, G, dtype;
+};
+cudaError_t launch_swiglu_f8(const SwigluF8Args& p, cudaStream_t st);
 
 }  // namespace moe_ep

@@ -20,7 +20,9 @@
  * epilogue moe_swiglu_quant*, moe_combine_f32 / moe_deq_combine); and what
  * stands around them: routing (moe_route), the gradients of routing and
  * combine (moe_route_backward, moe_combine_backward), and the INT8 product
- * that reads 8-bit operands (moe_linear_i8).
+ * that reads 8-bit operands (moe_linear_i8); the norm in front of the layer and
+ * its gradient (moe_rms_norm, moe_rms_norm_backward), and the layer's products
+ * in 8-bit floating point (moe_linear_f8, moe_swiglu_f8).
  *
  * Notation: R ranks, epr experts per rank, E = R*epr experts, bs tokens per
  * rank, T = R*bs tokens, k experts per token, P = T*k (token, k) pairs,
@@ -73,6 +75,9 @@ typedef enum {
 /* Element types.  A shape's dtype (tokens, expert outputs) is MOE_BF16 or
  * MOE_FP16; the wider types are for the arguments that name them. */
 typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_INT32 = 3 } moe_dtype;
+
+/* 8-bit codes of a row image. */
+typedef enum { MOE_CODE_I8 = 0, MOE_CODE_F8 = 1 } moe_code;
 
 /* Score function of moe_route. */
 typedef enum { MOE_SIGMOID = 0, MOE_SOFTMAX = 1 } moe_score;
@@ -608,6 +613,116 @@ moe_status moe_linear_i8(const void* a, int64_t a_rows, int64_t a_stride, const 
                          const void* row_scale, int64_t row_scale_stride,
                          const float* bias, void* c, int32_t c_dtype,
                          int32_t* dev_status, void* stream);
+
+/* ---- the norm in front of the layer, and the layer in 8-bit floating point (no
+ * counterpart in the page) -------------------------------------------------------
+ *
+ * An e4m3 row image holds H codes (the OCP e4m3 type without infinities, largest
+ * number 448), zeros up to the next multiple of 32 bytes, a fp32 scale for each 128
+ * codes (the last block may be shorter), zeros up to the next multiple of 32:
+ * align32(H) + align32(4 ceil(H / 128)) bytes.  Code j stands for
+ * code * scale[j / 128].  A block of values y gets
+ *   scale = max(max|y|, 1e-12f) / 448,  code = e4m3 nearest even of y / scale
+ * (the scale within 2 ulp, the quotient within 2 ulp before its rounding); a block with
+ * a NaN has a NaN scale and NaN codes, one with an infinity an infinite scale.  An
+ * image is a row of f8_row_bytes / 2 16-bit elements for moe_dispatch (quant 0),
+ * which copies it verbatim. */
+
+/* Bytes of an e4m3 row image of H codes; -1 unless 1 <= H <= MOE_EP_MAX_HIDDEN. */
+int64_t moe_f8_row_bytes(int32_t H);
+
+/* Root-mean-square norm of token rows, with the residual's addition before it and
+ * 8-bit codes after it.  For every row
+ *   s    = x + residual, rounded to nearest even in the token type (x itself without a
+ *          residual); what the residual stream carries on
+ *   rstd = 1 / sqrt(mean(s^2) + eps)                 (fp32, the sum too)
+ *   y    = (s * rstd) * gamma                        (fp32)
+ * and each of these that is asked for:
+ *   sum    s, in the token type (exactly with a residual: both NULL or neither)
+ *   out    y rounded to the token type
+ *   codes  y in 8 bits, rounded once from the fp32 values: MOE_CODE_F8 e4m3 row images
+ *          (moe_f8_row_bytes(H) apart), MOE_CODE_I8 the row images that moe_dispatch
+ *          makes of 16-bit rows (align32(H) + 32 bytes apart: scale = 127 / (max|y| +
+ *          1e-12f), codes half to even of y * scale, 1 / scale behind them)
+ *   rstd   fp32, what moe_rms_norm_backward takes
+ * x, residual, sum and out are [T] rows of H elements of dtype (MOE_BF16 or MOE_FP16),
+ * *_stride elements apart; 16-byte aligned, strides multiples of 8 and at least H (not
+ * looked at with T <= 1).  sum and out may be x or residual themselves (the same rows);
+ * no other two overlap.
+ *   gamma  fp32 [H], 16-byte aligned
+ *   codes  16-byte aligned
+ * 0 <= T < 2^31, 8 <= H <= MOE_EP_MAX_HIDDEN with H % 8 == 0, eps > 0 and finite; out or
+ * codes or both.  (A sum of squares past fp32's range, |s| beyond 1e17, makes rstd 0.)
+ * Nothing in the data is an error: dev_status is required as everywhere and not written.
+ * One launch. */
+moe_status moe_rms_norm(const void* x, int32_t dtype, int64_t T, int32_t H, int64_t x_stride,
+                        const void* residual, int64_t residual_stride, const float* gamma,
+                        float eps, void* sum, int64_t sum_stride, void* out,
+                        int64_t out_stride, void* codes, int32_t code_type, float* rstd,
+                        int32_t* dev_status, void* stream);
+
+/* Bytes of device workspace moe_rms_norm_backward needs for T rows of H (0 for sizes out
+ * of range).  Its contents need no preparation and mean nothing between calls; calls that
+ * overlap on the GPU need one each. */
+size_t moe_rms_norm_backward_workspace_bytes(int64_t T, int32_t H);
+
+/* Gradient of moe_rms_norm.  With x the normed rows (s there), xh = x * rstd and
+ * a = gamma * d_out:
+ *   d_x     = rstd * (a - xh * mean(a * xh)) + d_sum     (fp32, then rounded)
+ *   d_gamma = sum over rows of d_out * xh                (fp32, a fixed order)
+ * d_x is the gradient of x and, where there was one, of the residual alike; d_sum, the
+ * gradient that reaches s past the norm, may be NULL.
+ *   d_out, x, d_sum, d_x   [T] rows of H, as in moe_rms_norm; d_x may be d_out, x or
+ *                          d_sum itself
+ *   rstd                   fp32 [T] (read)
+ *   d_gamma                fp32 [H] (written; zeros with T == 0)
+ *   workspace              16-byte aligned
+ * Limits and dev_status as moe_rms_norm.  Two launches (three with H > 16384). */
+moe_status moe_rms_norm_backward(const void* d_out, int32_t dtype, int64_t T, int32_t H,
+                                 int64_t d_out_stride, const void* x, int64_t x_stride,
+                                 const float* gamma, const float* rstd, const void* d_sum,
+                                 int64_t d_sum_stride, void* d_x, int64_t d_x_stride,
+                                 float* d_gamma, void* workspace, int32_t* dev_status,
+                                 void* stream);
+
+/* The step between an e4m3 layer's two products: rows [gate | up] of 2I values ->
+ * e4m3 row images of h = gate / (1 + exp(-gate)) * up (fp32, within 2^-16 of itself).
+ *   h          [M] rows of 2I elements of dtype (MOE_BF16, MOE_FP16 or MOE_FP32),
+ *              h_stride elements apart (at least 2I; not looked at with M <= 1),
+ *              16-byte aligned, the stride too
+ *   group_off  int64 [G+1] (moe_group_offsets) or NULL: rows at or past group_off[G]
+ *              are not written; an offset past M sets MOE_ERR_CAPACITY
+ *   codes      moe_f8_row_bytes(I) apart, 16-byte aligned, apart from h
+ * 0 <= M < 2^31, 8 <= I <= MOE_EP_MAX_HIDDEN / 2, I % 8 == 0.  One launch. */
+moe_status moe_swiglu_f8(const void* h, int32_t dtype, int64_t M, int32_t I, int64_t h_stride,
+                         const int64_t* group_off, int32_t G, void* codes,
+                         int32_t* dev_status, void* stream);
+
+/* Matrix product of e4m3 rows and weights with a scale per 128 codes of a row and per
+ * 128 x 128 block of a weight matrix, the rows grouped by expert: for row m of group g
+ *   c[m][n] = sum_b (a_scale(m)[b] * w_scale[g][n / 128][b])
+ *                   * sum_{128 b <= j < min(K, 128 b + 128)} a[m][j] * w[g][n][j]
+ *             (+ bias[g][n])
+ * with the inner sums on the tensor cores (fp32), the scales' product rounded to fp32
+ * once and every further step one fp32 operation; then c rounded to c_dtype.  The order
+ * of the sums depends on the sizes alone.  Codes of NaN and scales of any value take part
+ * as such.
+ *   a        [a_rows], rows a_stride bytes apart: e4m3 row images, or codes alone
+ *   w        [G][N], rows w_stride bytes apart (w[g] N rows after w[g-1])
+ *   w_scale  fp32 [G][ceil(N/128)][ceil(K/128)]
+ *   a_scale  row m's ceil(K/128) fp32 scales from byte m * a_scale_stride on (in row
+ *            images: a + align32(K), a_scale_stride = a_stride)
+ *   bias     fp32 [G][N] or NULL
+ *   c        [a_rows][N] in c_dtype (MOE_BF16, MOE_FP16 or MOE_FP32); rows past the
+ *            groups' total are not written
+ * group_rows, alignments, limits and what is read of rows past K: as moe_linear_i8, with
+ * a_scale_stride >= 4 ceil(K/128) (not looked at with a_rows <= 1).  Errors found on the
+ * device as there.  One launch. */
+moe_status moe_linear_f8(const void* a, int64_t a_rows, int64_t a_stride, const void* w,
+                         int64_t w_stride, int32_t G, int32_t N, int32_t K,
+                         const int32_t* group_rows, const float* w_scale,
+                         const void* a_scale, int64_t a_scale_stride, const float* bias,
+                         void* c, int32_t c_dtype, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }
