@@ -40,13 +40,19 @@ constexpr int kRasterTokens = 8;     // token blocks per raster band (weights re
 constexpr int kEpiWarps = 8, kCtrlWarps = 4;
 constexpr int kThreads = 32 * (kCtrlWarps + kEpiWarps);
 // Registers per thread: 168 at launch, handed out again by role.
-constexpr int kEpiRegs = 208, kCtrlRegs = 88;
+constexpr int kEpiRegs = 216, kCtrlRegs = 72;
 static_assert(32 * (kEpiWarps * kEpiRegs + kCtrlWarps * kCtrlRegs) <= kThreads * 168,
               "no more registers than the launch has");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAccCols = 256;   // column offset of the second accumulator
-constexpr int kAhead = 4;            // blocks that a thread's scales are loaded ahead
+constexpr int kTurn = 4;             // blocks per turn of a draining thread, see there
 constexpr int kMaxStages = 10;
+constexpr uint32_t kBoxBytes = 32 * 128;             // a warp's 32 rows of 128 output bytes
+constexpr uint32_t kOutBytes = kEpiWarps * 2 * kBoxBytes;
+
+struct Maps {
+  CUtensorMap w, a, c;       // weights, token rows, the result
+};
 
 // NT: channels per tile.
 template <int NT>
@@ -54,7 +60,7 @@ struct Stages {
   static constexpr uint32_t kBytes = (TM + NT / CG) * BK;
   static constexpr uint32_t kBarBytes = 512;
   static size_t bytes(int stages, int G) {
-    return 1024 + size_t(stages) * kBytes + kBarBytes + size_t(G + 1) * 8;
+    return 1024 + size_t(stages) * kBytes + kOutBytes + kBarBytes + size_t(G + 1) * 8;
   }
 };
 
@@ -106,16 +112,15 @@ __device__ __forceinline__ uint32_t narrow_pair(float lo, float hi) {
 
 template <int NT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
-linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
-                      const __grid_constant__ CUtensorMap map_a, const LinearArgs p, int stages,
-                      int32_t* dev_status) {
+linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, bool wide_scales,
+                      int stages, int32_t* dev_status) {
   using St = Stages<NT>;
-  constexpr int kCols = NT / 2;              // columns per draining thread
+  constexpr int kCols = NT / (kEpiWarps / 4);          // columns per draining thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
-  const uint32_t bars = sbase + stages * St::kBytes;
+  const uint32_t outs = sbase + stages * St::kBytes, bars = outs + kOutBytes;
   auto full = [&](int s) { return bars + 8 * s; };                      // this CTA's copies landed
   auto peer = [&](int s) { return bars + 8 * (kMaxStages + s); };       // ... the other CTA's
   auto empty = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };  // multiplied
@@ -129,8 +134,8 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntn = (p.N + NT - 1) / NT;
-  const int rank = static_cast<int>(cluster_rank());
-  const int nk = code_blocks(p.K);
+  auto crank = []() { return static_cast<int>(cluster_rank()); };
+  auto blocks_of_k = [&]() { return code_blocks(p.K); };
 
   wait_for_stream();
   let_next_start();
@@ -157,8 +162,9 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       smem_store(abort_flag, 0);
       smem_store(issued, 0);
       smem_store(issued + 4, 0);
-      tensor_map_prefetch(&map_w);
-      tensor_map_prefetch(&map_a);
+      tensor_map_prefetch(&maps.w);
+      tensor_map_prefetch(&maps.a);
+      tensor_map_prefetch(&maps.c);
     }
     fence_mbar_init();
   }
@@ -173,7 +179,8 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   cluster_arrive_all();
   tc_fence_after();
 
-  const int tiles = smem_load(tpre + 4 * p.G), first = cluster_id(), step = cluster_count();
+  // (each role reads what it needs: registers are short in some)
+  auto tile_count = [&]() { return smem_load(tpre + 4 * p.G); };
   // Waits for the last commit on each of this CTA's barriers, once all of them are
   // issued: ncommit of stages, nacc of accumulators.  A barrier's n-th commit is issued
   // only after this CTA's threads have seen its n-1-th, so at most one is outstanding and
@@ -192,13 +199,14 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 
   if (warp < kCtrlWarps) {
     regs_fewer<kCtrlRegs>();
+    const int rank = crank(), nk = blocks_of_k();
     if (warp == 0) {
       // ---- copies -------------------------------------------------------------------
       const bool issue = elect_one();
       int s = 0;
       uint32_t phase = 0, nload = 0;
       bool ok = true;
-      for (int t = first; ok && t < tiles; t += step) {
+      for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         const Tile tl = decode_tile<NT>(t, goff, tpre, p.G, ntn);
         const int wrow = tl.g * p.N + tl.n0 + rank * (NT / CG);
         const int arow = tl.row0 + rank * TM;
@@ -210,8 +218,8 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
           if (issue) {
             const uint32_t dst = sbase + s * St::kBytes;
             bar_expect(full(s), St::kBytes);
-            tensor_load_2d(dst, &map_a, kb * BK, arow, full(s));
-            tensor_load_2d(dst + TM * BK, &map_w, kb * BK, wrow, full(s));
+            tensor_load_2d(dst, &maps.a, kb * BK, arow, full(s));
+            tensor_load_2d(dst + TM * BK, &maps.w, kb * BK, wrow, full(s));
           }
           ++nload;
           if (++s == stages) { s = 0; phase ^= 1u; }
@@ -234,7 +242,7 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       int s = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; ok && t < tiles; t += step) {
+      for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
           if (!bar_wait(full(s), phase) || smem_load(abort_flag)) {
             ok = false;
@@ -258,11 +266,11 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
       int s = 0;
       uint32_t phase = 0, nacc = 0;
       bool ok = true;
-      for (int t = first; ok && t < tiles; t += step) {
+      for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
-          const uint32_t b = nacc & 1u, use = (nacc >> 1) & 1u;
-          if (!bar_wait(tempty(b), use ^ 1u) || !bar_wait(full(s), phase) ||
-              !bar_wait(peer(s), phase) || smem_load(abort_flag)) {
+          const uint32_t b = nacc & 1u;
+          if (!bar_wait(full(s), phase) || !bar_wait(peer(s), phase) ||
+              !bar_wait(tempty(b), ((nacc >> 1) & 1u) ^ 1u)) {
             ok = false;
             break;
           }
@@ -274,20 +282,20 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 #pragma unroll
             for (int kk = 0; kk < BK / 32; ++kk)     // + 32 bytes along K per step
               pair_mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk != 0);
-            pair_commit(empty(s), uint16_t(3));
             pair_commit(tfull(b), uint16_t(3));
+            pair_commit(empty(s), uint16_t(3));
           }
           ++nacc;
           if (++s == stages) { s = 0; phase ^= 1u; }
         }
+        ok = ok && !smem_load(abort_flag);
       }
       if (!ok) {
         if (issue) set_status(dev_status, MOE_ERR_TIMEOUT);
         smem_store(abort_flag, 1);
       }
       // the pair's other CTA, whose barriers the commits arrive on too, learns how many
-      // there were (of stages as of accumulators); it waits for them after the closing
-      // barrier
+      // there were; it waits for them after the closing barrier
       if (issue) {
         await_commits(nacc, nacc);
         const uint32_t to = cluster_addr(issued, 1);
@@ -301,108 +309,161 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
   } else {
     // ---- blocks' sums -> scaled sums -> stores --------------------------------------------
     regs_more<kEpiRegs>();
+    const int rank = crank(), nk = blocks_of_k();
     const int q = warp & 3;                  // TMEM lanes 32 q ..
     const int col0 = ((warp - kCtrlWarps) >> 2) * kCols;
     const uint32_t base = smem_load(tmem_slot) + (uint32_t(q * 32) << 16) + col0;
+    const uint32_t drained = cluster_addr(tempty(0), 0);
+    const uint32_t box = outs + (warp - kCtrlWarps) * 2 * kBoxBytes;
     const int nblocks = code_blocks(p.N);
     cluster_wait_all();
     uint32_t nacc = 0;
     bool ok = true;
-    for (int t = first; ok && t < tiles; t += step) {
+    for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
       const Tile tl = decode_tile<NT>(t, goff, tpre, p.G, ntn);
-      const int mine = rank * TM + q * 32 + lane;          // this thread's token of the tile
-      const int64_t row = tl.row0 + mine;
+      const int first_row = tl.row0 + rank * TM + q * 32;   // of the warp; a lane's token is
+      const int rows = tl.rows - rank * TM - q * 32;        // first_row + lane, rows there are
       const int n0 = tl.n0 + col0;
-      const bool work = rank * TM + q * 32 < tl.rows && n0 < p.N;     // of the warp
+      const bool work = rows > 0 && n0 < p.N;
+      // kTurn blocks a turn, their scales loaded a turn ahead: the token's 16 bytes at once
+      // (every load of a warp touches 32 lines, and takes as many of the L1 cycles that the
+      // products need to read shared memory: 8192 x 4096 x 7168 took 182 us by loads of 4
+      // bytes, 174 by these, 197 with tensor copies of 128 x 16 bytes, which hold up the
+      // operands' copies, and 187 with a warp that loads for the others)
       const unsigned char* as =
-          p.row_scale + min(row, p.a_rows - 1) * p.row_scale_stride;
+          p.row_scale + min(int64_t(first_row) + lane, p.a_rows - 1) * p.row_scale_stride;
       const float* ws = p.col_scale +
                         (int64_t(tl.g) * nblocks + min(n0 / kCodeBlock, nblocks - 1)) * nk;
-      auto scale = [&](int kb) {
-        kb = min(kb, nk - 1);
-        return __fmul_rn(*reinterpret_cast<const float*>(as + 4 * kb), ws[kb]);
-      };
-      float sc[kAhead];
+      float ra[kTurn], rw[kTurn];
+      auto load_scales = [&](int kb) {
+        const float* from = reinterpret_cast<const float*>(as) + kb;
+        if (work && wide_scales && kb + kTurn <= nk) {
+          const float4 v = *reinterpret_cast<const float4*>(from);
+          ra[0] = v.x; ra[1] = v.y; ra[2] = v.z; ra[3] = v.w;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) sc[i] = work ? scale(i) : 0.0f;
+          for (int i = 0; i < kTurn; ++i) rw[i] = ws[kb + i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTurn; ++i) {
+            const bool in = work && kb + i < nk;
+            ra[i] = in ? from[i] : 0.0f;
+            rw[i] = in ? ws[kb + i] : 0.0f;
+          }
+        }
+      };
+      load_scales(0);
       float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-      for (int kb = 0; kb < nk; ++kb, ++nacc) {
-        const uint32_t b = nacc & 1u;
-        const bool got = bar_wait(tfull(b), (nacc >> 1) & 1u) && !smem_load(abort_flag);
-        ok = __all_sync(0xffffffffu, got);
-        if (!ok) break;
-        tc_fence_after();
-        auto release = [&]() {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) cluster_arrive(cluster_addr(tempty(b), 0));
-        };
-        if (!work) {
-          release();
-          continue;
-        }
-        const float2 s2 = bcast2(sc[0]);
+      for (int kb = 0; ok && kb < nk; kb += kTurn) {
+        float sc[kTurn];
 #pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) sc[i] = sc[i + 1];
-        sc[kAhead - 1] = scale(kb + kAhead);
-        constexpr int kParts = kCols / 16;
-        float v[2][16];
-        tmem_start16(base + b * kAccCols, v[0]);
+        for (int i = 0; i < kTurn; ++i) sc[i] = __fmul_rn(ra[i], rw[i]);
+        load_scales(kb + kTurn);
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-          tmem_wait16(v[i & 1]);
-          if (i + 1 < kParts) tmem_start16(base + b * kAccCols + 16 * (i + 1), v[(i + 1) & 1]);
-          else release();
+        for (int turn = 0; turn < kTurn; ++turn) {
+          if (kb + turn >= nk) break;
+          const uint32_t b = nacc & 1u;
+          ok = warp_bar_wait(tfull(b), (nacc >> 1) & 1u);
+          if (!ok) break;
+          ++nacc;
+          tc_fence_after();
+          auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            cluster_arrive_if(lane == 0, drained + 8 * b);
+          };
+          if (!work) {
+            release();
+            continue;
+          }
+          const float2 s2 = bcast2(sc[turn]);
+          const uint32_t from = base + b * kAccCols;
+          constexpr int kParts = kCols / 8;
+          float v[2][8];
+          tmem_start8(from, v[0]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[8 * i + j] = fma2_rn(make_float2(v[i & 1][2 * j], v[i & 1][2 * j + 1]), s2,
-                                      acc[8 * i + j]);
+          for (int i = 0; i < kParts; ++i) {
+            tmem_wait8(v[i & 1]);
+            if (i + 1 < kParts) tmem_start8(from + 8 * (i + 1), v[(i + 1) & 1]);
+            else release();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[4 * i + j] = fma2_rn(make_float2(v[i & 1][2 * j], v[i & 1][2 * j + 1]), s2,
+                                       acc[4 * i + j]);
+          }
         }
       }
+      ok = ok && !smem_load(abort_flag);
       if (!ok) {
         if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
         smem_store(abort_flag, 1);
         break;
       }
       if (!work) continue;
-      if (p.bias) {
-        const float* bias = p.bias + int64_t(tl.g) * p.N;
-#pragma unroll
-        for (int j = 0; j < kCols / 2; ++j) {
-          const int n = n0 + 2 * j;
-          acc[j] = add2_rn(acc[j], make_float2(bias[min(n, p.N - 1)], bias[min(n + 1, p.N - 1)]));
+      const float* bias = p.bias ? p.bias + int64_t(tl.g) * p.N + n0 : nullptr;
+      auto value = [&](int j) {                // column j, which is one of the product's
+        const float v = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+        return bias ? __fadd_rn(v, bias[j]) : v;
+      };
+      constexpr int kItem = OUT == MOE_FP32 ? 4 : 2, kVec = 16 / kItem;     // per 16 bytes
+      auto piece = [&](int j) {                // columns j .. j + kVec - 1, narrowed
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (n0 + j < p.N) {
+          if constexpr (OUT == MOE_FP32)
+            o = make_uint4(__float_as_uint(value(j)), __float_as_uint(value(j + 1)),
+                           __float_as_uint(value(j + 2)), __float_as_uint(value(j + 3)));
+          else
+            o = make_uint4(narrow_pair<OUT>(value(j), value(j + 1)),
+                           narrow_pair<OUT>(value(j + 2), value(j + 3)),
+                           narrow_pair<OUT>(value(j + 4), value(j + 5)),
+                           narrow_pair<OUT>(value(j + 6), value(j + 7)));
         }
-      }
-      if (mine < tl.rows) {
-        const int64_t at = row * p.N + n0;
-        constexpr int kItem = OUT == MOE_FP32 ? 4 : 2, kVec = 16 / kItem;     // per 16 bytes
+        return o;
+      };
+      constexpr int kBoxCols = 128 / kItem, kBoxes = kCols / kBoxCols;
+      if (kBoxes > 0 && p.N % kVec == 0 && rows >= 32) {
+        // 32 whole rows: 128 bytes of each at a time through shared memory (16-byte pieces
+        // swizzled as the copy reads them) and out by one tensor copy
+#pragma unroll
+        for (int j = 0; j < kBoxes * kBoxCols; j += kBoxCols) {
+          const uint32_t at = box + (j / kBoxCols % 2) * kBoxBytes;
+          if (lane == 0) bulk_wait_read<kBoxes == 1 ? 0 : 1>();    // this buffer's last copy
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 o = piece(j + i * kVec);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                             at + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                         "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w) : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (n0 + j < p.N)
+              tensor_store_2d(&maps.c, (n0 + j) * kItem, first_row, at);
+            bulk_commit();
+          }
+        }
+      } else if (lane < rows) {
+        const int64_t at = (int64_t(first_row) + lane) * p.N + n0;
         if (p.N % kVec == 0) {
 #pragma unroll
           for (int j = 0; j < kCols; j += kVec) {
-            uint4 o;
-            if constexpr (OUT == MOE_FP32) {
-              o = make_uint4(__float_as_uint(acc[j / 2].x), __float_as_uint(acc[j / 2].y),
-                             __float_as_uint(acc[j / 2 + 1].x),
-                             __float_as_uint(acc[j / 2 + 1].y));
-            } else {
-              o = make_uint4(narrow_pair<OUT>(acc[j / 2].x, acc[j / 2].y),
-                             narrow_pair<OUT>(acc[j / 2 + 1].x, acc[j / 2 + 1].y),
-                             narrow_pair<OUT>(acc[j / 2 + 2].x, acc[j / 2 + 2].y),
-                             narrow_pair<OUT>(acc[j / 2 + 3].x, acc[j / 2 + 3].y));
-            }
+            const uint4 o = piece(j);
             if (n0 + j < p.N)
               *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.c) + (at + j) * kItem) = o;
           }
         } else {
 #pragma unroll
           for (int j = 0; j < kCols; ++j)
-            if (n0 + j < p.N) store_one<OUT>(p.c, at + j, j & 1 ? acc[j / 2].y : acc[j / 2].x);
+            if (n0 + j < p.N) store_one<OUT>(p.c, at + j, value(j));
         }
       }
       __syncwarp();
     }
+    if (lane == 0) bulk_wait_all<0>();
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -421,11 +482,12 @@ linear_f8_tile_kernel(const __grid_constant__ CUtensorMap map_w,
 struct Plan {
   int nt;          // channels per tile
   int clusters;
+  bool wide_scales;          // every row's scales start on 16 bytes
 };
 
 template <int NT, int OUT>
-cudaError_t launch_kernel(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
-                          const Plan& plan, int32_t* dev_status, int optin, cudaStream_t st) {
+cudaError_t launch_kernel(const Maps& maps, const LinearArgs& p, const Plan& plan,
+                          int32_t* dev_status, int optin, cudaStream_t st) {
   using S = Stages<NT>;
   int stages = kMaxStages;
   while (stages > 2 && S::bytes(stages, p.G) > size_t(optin)) --stages;
@@ -446,16 +508,16 @@ cudaError_t launch_kernel(const CUtensorMap& mw, const CUtensorMap& ma, const Li
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p, stages, dev_status);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p, plan.wide_scales, stages, dev_status);
 }
 
 template <int NT>
-cudaError_t launch_nt(const CUtensorMap& mw, const CUtensorMap& ma, const LinearArgs& p,
-                      const Plan& plan, int32_t* dev_status, int optin, cudaStream_t st) {
+cudaError_t launch_nt(const Maps& maps, const LinearArgs& p, const Plan& plan,
+                      int32_t* dev_status, int optin, cudaStream_t st) {
   switch (p.c_dtype) {
-    case MOE_BF16: return launch_kernel<NT, MOE_BF16>(mw, ma, p, plan, dev_status, optin, st);
-    case MOE_FP16: return launch_kernel<NT, MOE_FP16>(mw, ma, p, plan, dev_status, optin, st);
-    default: return launch_kernel<NT, MOE_FP32>(mw, ma, p, plan, dev_status, optin, st);
+    case MOE_BF16: return launch_kernel<NT, MOE_BF16>(maps, p, plan, dev_status, optin, st);
+    case MOE_FP16: return launch_kernel<NT, MOE_FP16>(maps, p, plan, dev_status, optin, st);
+    default: return launch_kernel<NT, MOE_FP32>(maps, p, plan, dev_status, optin, st);
   }
 }
 
@@ -487,14 +549,21 @@ cudaError_t launch_linear_f8(const LinearArgs& p, int32_t* dev_status, cudaStrea
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
-  const Plan plan = make_plan(p, sms);
-  CUtensorMap mw, ma;
-  e = encode_bytes_2d(&mw, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, plan.nt / CG);
-  if (e == cudaSuccess) e = encode_bytes_2d(&ma, p.a, p.a_rows, p.K, p.a_stride, TM);
+  Plan plan = make_plan(p, sms);
+  Maps maps;
+  e = encode_bytes_2d(&maps.w, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, plan.nt / CG);
+  if (e == cudaSuccess) e = encode_bytes_2d(&maps.a, p.a, p.a_rows, p.K, p.a_stride, TM);
+  // (rows of c that do not start on 16 bytes are stored without the map)
+  const int64_t pitch = int64_t(p.N) * (p.c_dtype == MOE_FP32 ? 4 : 2);
+  maps.c = maps.a;
+  if (e == cudaSuccess && pitch % 16 == 0)
+    e = encode_bytes_2d(&maps.c, p.c, p.a_rows, pitch, pitch, 32);
+  plan.wide_scales = reinterpret_cast<uintptr_t>(p.row_scale) % 16 == 0 &&
+                     (p.a_rows == 1 || p.row_scale_stride % 16 == 0);
   if (e != cudaSuccess) return e;
-  return plan.nt == 256   ? launch_nt<256>(mw, ma, p, plan, dev_status, optin, st)
-         : plan.nt == 128 ? launch_nt<128>(mw, ma, p, plan, dev_status, optin, st)
-                          : launch_nt<64>(mw, ma, p, plan, dev_status, optin, st);
+  return plan.nt == 256   ? launch_nt<256>(maps, p, plan, dev_status, optin, st)
+         : plan.nt == 128 ? launch_nt<128>(maps, p, plan, dev_status, optin, st)
+                          : launch_nt<64>(maps, p, plan, dev_status, optin, st);
 }
 
 }  // namespace moe_ep

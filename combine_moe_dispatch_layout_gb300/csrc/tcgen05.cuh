@@ -48,6 +48,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     if (bar_poll(bar, parity)) return true;
   return false;
 }
+// The same for a whole converged warp, which stays so (a lane's own loop made the compiler
+// guard every wait against divergence, and spill what it keeps for that).
+__device__ __forceinline__ bool warp_bar_wait(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kGemmSpin; ++i)
+    if (__any_sync(0xffffffffu, bar_poll(bar, parity))) return true;
+  return false;
+}
 // 2-D tensor copy global -> shared, completion counted on `bar`.
 __device__ __forceinline__ void tensor_load_2d(uint32_t sdst, const CUtensorMap* map, int x,
                                                int y, uint32_t bar) {
@@ -56,6 +63,14 @@ __device__ __forceinline__ void tensor_load_2d(uint32_t sdst, const CUtensorMap*
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(sdst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+// 2-D tensor copy shared -> global (tracked by bulk groups); what lies outside the map is
+// left out.
+__device__ __forceinline__ void tensor_store_2d(const CUtensorMap* map, int x, int y,
+                                                uint32_t ssrc) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(ssrc) : "memory");
 }
 
 __device__ __forceinline__ void tensor_map_prefetch(const CUtensorMap* map) {
@@ -94,26 +109,21 @@ __device__ __forceinline__ void tmem_load4(uint32_t taddr, uint32_t (&v)[4]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// 16 consecutive TMEM columns of this warp's 32 lanes: the load starts here, and v may be
-// read after tmem_wait16(v) alone (which names the registers, so that no use of them can
+// 8 consecutive TMEM columns of this warp's 32 lanes: the load starts here, and v may be
+// read after tmem_wait8(v) alone (which names the registers, so that no use of them can
 // be moved before it).
-__device__ __forceinline__ void tmem_start16(uint32_t taddr, float (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
-        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
-        "=f"(v[14]), "=f"(v[15])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_start8(uint32_t taddr, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
-        "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
-        "+f"(v[14]), "+f"(v[15])
-      :
-      : "memory");
+__device__ __forceinline__ void tmem_wait8(float (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7])
+               :
+               : "memory");
 }
 
 // ---- clusters -------------------------------------------------------------------
@@ -170,6 +180,14 @@ __device__ __forceinline__ void cluster_store16(uint32_t caddr, const int32_t* v
 // every arrival wait over 1000 cycles for the CTA's stores in flight.
 __device__ __forceinline__ void cluster_arrive(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+
+// The same from the lanes where `lane` holds, without a branch.
+__device__ __forceinline__ void cluster_arrive_if(bool lane, uint32_t caddr) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(caddr), "r"(uint32_t(lane))
+      : "memory");
 }
 
 // The products of one instruction (K = 16) of a pair of CTAs, issued by the
