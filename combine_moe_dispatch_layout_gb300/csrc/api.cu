@@ -650,8 +650,8 @@ moe_status moe_rms_norm_backward(const void* d_out, int32_t dtype, int64_t T, in
       !aligned(rstd, 4) || !aligned(workspace, 16))
     return MOE_ERR_INVALID_ARG;
   const moe_ep::NormBackwardArgs p{d_out, x, d_sum, gamma, rstd, d_x,
-                                   static_cast<float*>(workspace), T, d_out_stride, x_stride,
-                                   d_sum_stride, d_x_stride, H, dtype};
+                                   static_cast<float*>(workspace), dev_status, T, d_out_stride,
+                                   x_stride, d_sum_stride, d_x_stride, H, dtype};
   return from_cuda(moe_ep::launch_rms_norm_backward(p, d_gamma, st));
 }
 

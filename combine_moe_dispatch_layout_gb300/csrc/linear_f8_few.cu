@@ -6,8 +6,16 @@
 // 8 tokens (fp32 sums), four of them a 128-code block, whose sums then get the block's
 // scales, one fused multiply-add each.  The sum over K does not care which code stands
 // where as long as both operands agree, so a lane takes 16 consecutive bytes of its rows
-// as four words of the instructions' fragments and nothing is shuffled: weights go from
-// memory to registers, 64 consecutive bytes of 8 rows per load.
+// as four words of the instructions' fragments and nothing is shuffled.
+//
+// What bounds it is the weights' way from memory, and that wants long runs and many bytes
+// on their way: loads of 64 or 128 bytes a row reached 6.1 TB/s, of 256 or 512 7.1, with
+// 130 KB of an SM in flight 6.5 and with 190 7.05.  So a step of a warp is 256 codes of 16
+// rows, copied asynchronously into a ring of kDepth steps of its own in shared memory (no
+// barrier but the warp's own stands between copy and use), four CTAs to an SM.  The ring
+// runs on over tile ends.  Tokens and scales come through L1, a step ahead, in registers.
+// (With the weights a block ahead in registers too, 32 groups of 8 rows of 4096 x 7168
+// took 282 us at 3.3 TB/s.)
 //
 // A warp takes 16 channels and up to 8 TB tokens; `parts` warps of a CTA split K where
 // there are too few channels to fill the GPU (their sums are added in order).  A
@@ -22,8 +30,12 @@
 namespace moe_ep {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kChannels = 16;        // weight rows per warp
+constexpr int kStep = 256;           // codes of K per step: two blocks
+constexpr int kDepth = 3;            // steps in a warp's ring
+constexpr uint32_t kStepBytes = kChannels * kStep;
+constexpr size_t kRingBytes = size_t(kWarps) * kDepth * kStepBytes;
 
 __device__ __forceinline__ void mma_f8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                        uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -34,43 +46,45 @@ __device__ __forceinline__ void mma_f8(float (&c)[4], uint32_t a0, uint32_t a1, 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The first n bytes of a 16-byte piece, zeros behind them, reading those n alone where
-// EXACT (a row of a may end there, and the buffer with it), else the whole piece if n > 0.
-template <bool EXACT>
-__device__ __forceinline__ uint4 first_bytes(const uint8_t* p, int n) {
-  if (n >= 16) return EXACT ? *reinterpret_cast<const uint4*>(p) : ld_once_16(p);
+// The first `bytes` (0 to 16) of a 16-byte piece to shared memory, zeros behind them;
+// reads those bytes alone.
+__device__ __forceinline__ void copy_piece(uint32_t to, const uint8_t* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ uint4 read_piece(uint32_t from) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+  return v;
+}
+
+// The first n bytes of a 16-byte piece of a token row, zeros behind them; reads those n
+// alone: the row may end there, and the buffer with it.
+__device__ __forceinline__ uint4 token_piece(const uint8_t* p, int n) {
+  if (n >= 16) return *reinterpret_cast<const uint4*>(p);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if (n > 0) {
-    if constexpr (EXACT) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) w[i / 4] |= uint32_t(p[i]) << (8 * (i % 4));
-    } else {
-      const uint4 v = ld_once_16(p);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int keep = n - 4 * i;
-        w[i] = keep >= 4 ? u[i] : keep <= 0 ? 0u : u[i] & ((1u << (8 * keep)) - 1u);
-      }
-    }
-  }
+  for (int i = 0; i < 16; ++i)
+    if (i < n) w[i / 4] |= uint32_t(p[i]) << (8 * (i % 4));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+struct Tile {
+  int g, n0, row0, tokens;
+};
+
 template <int TB>
-struct Block {                       // a 128-code block as a lane holds it
-  uint4 w[2][2];                     // weight rows gid and gid + 8, pieces tig and tig + 4
-  uint4 x[TB][2];                    // tokens gid of each eight
-  float row[TB][2];                  // scales of tokens 2 tig and 2 tig + 1 of each eight
-  float col;
+struct Tokens {                      // a step as a lane holds it
+  uint4 x[TB][4];                    // tokens gid of each eight: pieces tig, tig + 4, ...
+  float s[TB][2][2];                 // scales of tokens 2 tig and 2 tig + 1, of both blocks
 };
 
 // TB: tokens per block / 8.
 template <int TB>
 __global__ void __launch_bounds__(kThreads)
 linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
-  extern __shared__ int s_tables[];
+  extern __shared__ __align__(16) uint8_t s_ring[];          // the rings, then the group tables
   __shared__ int64_t s_scan[kThreads * 12 / 8];
   __shared__ float s_sums[kWarps][8 * TB][kChannels];
   wait_for_stream();
@@ -79,8 +93,9 @@ linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
   const int part = warp % parts, slot = warp / parts;
   const int chans = kWarps / parts * kChannels;          // channels per CTA
   const int ntn = (p.N + chans - 1) / chans;
-  const int kblocks = code_blocks(p.K), nblocks = code_blocks(p.N), whole = p.K / kCodeBlock;
-  const uint32_t goff = smem_addr(s_tables), tpre = goff + 4 * (p.G + 1);
+  const int kblocks = code_blocks(p.K), nblocks = code_blocks(p.N);
+  const int steps = (p.K + kStep - 1) / kStep;
+  const uint32_t goff = smem_addr(s_ring) + kRingBytes, tpre = goff + 4 * (p.G + 1);
   const bool grouped = p.group_rows != nullptr;
   int tiles = row_blocks(static_cast<int>(p.a_rows), 8 * TB) * ntn;
   if (grouped) {
@@ -88,7 +103,7 @@ linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
     __syncthreads();
     tiles = smem_load(tpre + 4 * p.G);
   }
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+  auto decode = [&](int t) {
     int g = 0, local = t, off = 0, end = static_cast<int>(p.a_rows);
     if (grouped) {
       g = group_of_tile(t, tpre, p.G);
@@ -97,74 +112,112 @@ linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
       end = smem_load(goff + 4 * g + 4);
     }
     const int blocks = row_blocks(end - off, 8 * TB);
-    const int row0 = off + local % blocks * (8 * TB), n0 = local / blocks * chans;
-    const int tokens = min(8 * TB, end - row0);
-    // rows past the last channel or token repeat that one; their sums go nowhere
-    const int n = n0 + slot * kChannels, last = p.N - 1;
-    const uint8_t* wbase = static_cast<const uint8_t*>(p.w) + int64_t(g) * p.N * p.w_stride;
-    const uint8_t* w0 = wbase + min(n + gid, last) * p.w_stride;
-    const uint8_t* w1 = wbase + min(n + gid + 8, last) * p.w_stride;
-    const float* col = p.col_scale +
-                       (int64_t(g) * nblocks + min(n, last) / kCodeBlock) * kblocks;
-    const uint8_t* a = static_cast<const uint8_t*>(p.a) + int64_t(row0) * p.a_stride;
-    const uint8_t* rs = p.row_scale + int64_t(row0) * p.row_scale_stride;
+    Tile tl;
+    tl.g = g;
+    tl.n0 = local / blocks * chans;
+    tl.row0 = off + local % blocks * (8 * TB);
+    tl.tokens = min(8 * TB, end - tl.row0);
+    return tl;
+  };
 
-    auto load = [&](Block<TB>& b, int kb) {
-      const int at = kb * kCodeBlock + 16 * tig;
-      if (kb < whole) {
+  // ---- copies of weights, kDepth - 1 steps ahead of the products --------------------------
+  // Copy j takes rows 2 j and 2 j + 1, a half warp 256 bytes of each.  16-byte piece q of row
+  // r lies at q ^ 4 (r & 1), so that the reads of two rows' pieces meet no bank twice.
+  const uint32_t ring = smem_addr(s_ring) + warp * kDepth * kStepBytes;
+  const int crow = lane >> 4, cpiece = lane & 15;
+  const uint32_t cto = ring + crow * kStep + ((cpiece ^ (crow << 2)) << 4);
+  int load_tile = blockIdx.x, load_step = part, load_slot = 0;
+  const uint8_t* w = nullptr;          // of the tile's first row, this lane's piece
+  int last = 0;                        // rows past the last channel repeat that one
+  auto aim = [&]() {
+    if (load_tile >= tiles) return;
+    const Tile tl = decode(load_tile);
+    const int n = min(tl.n0 + slot * kChannels, p.N - 1);
+    w = static_cast<const uint8_t*>(p.w) + (int64_t(tl.g) * p.N + n) * p.w_stride;
+    last = p.N - 1 - n;
+  };
+  auto copy_step = [&]() {
+    if (load_tile < tiles) {
+      const int at = load_step * kStep + 16 * cpiece;
+      const int bytes = max(0, min(16, p.K - at));
+      const uint8_t* from = w + (bytes ? at : 0);
+      const uint32_t to = cto + load_slot * kStepBytes;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          b.w[0][h] = ld_once_16(w0 + at + 64 * h);
-          b.w[1][h] = ld_once_16(w1 + at + 64 * h);
-        }
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          b.w[0][h] = first_bytes<false>(w0 + at + 64 * h, p.K - at - 64 * h);
-          b.w[1][h] = first_bytes<false>(w1 + at + 64 * h, p.K - at - 64 * h);
-        }
+      for (int j = 0; j < kChannels / 2; ++j)
+        copy_piece(to + 2 * j * kStep, from + min(2 * j + crow, last) * p.w_stride, bytes);
+      load_step += parts;
+      if (load_step >= steps) {        // (every warp has a step in every tile)
+        load_step = part;
+        load_tile += gridDim.x;
+        aim();
       }
-      b.col = col[kb];
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++load_slot == kDepth) load_slot = 0;
+  };
+  aim();
+  for (int i = 0; i < kDepth - 1; ++i) copy_step();
+
+  int use_slot = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const Tile tl = decode(t);
+    const int n = min(tl.n0 + slot * kChannels, p.N - 1);
+    const float* col = p.col_scale + (int64_t(tl.g) * nblocks + n / kCodeBlock) * kblocks;
+    const unsigned char* rs = p.row_scale + int64_t(tl.row0) * p.row_scale_stride;
+    const uint8_t* a = static_cast<const uint8_t*>(p.a) + int64_t(tl.row0) * p.a_stride + 16 * tig;
+    auto load_tokens = [&](int step, Tokens<TB>& v) {     // tokens past the last repeat it
+      float c[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) c[b] = 2 * step + b < kblocks ? col[2 * step + b] : 0.0f;
 #pragma unroll
       for (int i = 0; i < TB; ++i) {
-        const uint8_t* x = a + min(8 * i + gid, tokens - 1) * p.a_stride + at;
+        const uint8_t* x = a + min(8 * i + gid, tl.tokens - 1) * p.a_stride + step * kStep;
+        const int left = p.K - step * kStep - 16 * tig;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          b.x[i][h] = kb < whole ? *reinterpret_cast<const uint4*>(x + 64 * h)
-                                 : first_bytes<true>(x + 64 * h, p.K - at - 64 * h);
+        for (int q = 0; q < 4; ++q) v.x[i][q] = token_piece(x + 64 * q, left - 64 * q);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          b.row[i][j] = *reinterpret_cast<const float*>(
-              rs + min(8 * i + 2 * tig + j, tokens - 1) * p.row_scale_stride + 4 * kb);
+        for (int j = 0; j < 2; ++j) {
+          const float* r = reinterpret_cast<const float*>(
+              rs + min(8 * i + 2 * tig + j, tl.tokens - 1) * p.row_scale_stride) + 2 * step;
+          v.s[i][0][j] = __fmul_rn(r[0], c[0]);
+          v.s[i][1][j] = 2 * step + 1 < kblocks ? __fmul_rn(r[1], c[1]) : 0.0f;
+        }
       }
     };
     float acc[TB][4] = {};
-    auto use = [&](const Block<TB>& b) {
+    Tokens<TB> cur, next;
+    load_tokens(part, cur);
+    for (int step = part; step < steps; step += parts) {
+      if (step + parts < steps) load_tokens(step + parts, next);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+      __syncwarp();
+      const uint32_t from =
+          ring + use_slot * kStepBytes + gid * kStep + ((tig ^ ((gid & 1) << 2)) << 4);
 #pragma unroll
-      for (int i = 0; i < TB; ++i) {
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int b = 0; b < 2; ++b) {
+        uint4 u[2][2];                 // rows gid and gid + 8, pieces tig and tig + 4
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mma_f8(c, b.w[0][h].x, b.w[1][h].x, b.w[0][h].y, b.w[1][h].y, b.x[i][h].x,
-                 b.x[i][h].y);
-          mma_f8(c, b.w[0][h].z, b.w[1][h].z, b.w[0][h].w, b.w[1][h].w, b.x[i][h].z,
-                 b.x[i][h].w);
+        for (int r = 0; r < 2; ++r) {
+          u[r][0] = read_piece(from + r * 8 * kStep + b * 128);
+          u[r][1] = read_piece((from ^ 64) + r * 8 * kStep + b * 128);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __fmaf_rn(c[j], __fmul_rn(b.row[i][j & 1], b.col), acc[i][j]);
+        for (int i = 0; i < TB; ++i) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = cur.x[i][2 * b + h];
+            mma_f8(c, u[0][h].x, u[1][h].x, u[0][h].y, u[1][h].y, v.x, v.y);
+            mma_f8(c, u[0][h].z, u[1][h].z, u[0][h].w, u[1][h].w, v.z, v.w);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(c[j], cur.s[i][b][j & 1], acc[i][j]);
+        }
       }
-    };
-    // the next block is on its way while this one is used
-    Block<TB> cur, next;
-    int kb = part;
-    if (kb < kblocks) load(cur, kb);
-    while (kb < kblocks) {
-      const int then = kb + parts;
-      if (then < kblocks) load(next, then);
-      use(cur);
+      if (++use_slot == kDepth) use_slot = 0;
+      __syncwarp();
+      copy_step();               // into the slot of the step before this one
       cur = next;
-      kb = then;
     }
 #pragma unroll
     for (int i = 0; i < TB; ++i)
@@ -172,14 +225,14 @@ linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
       for (int j = 0; j < 4; ++j)
         s_sums[warp][8 * i + 2 * tig + (j & 1)][gid + 8 * (j >> 1)] = acc[i][j];
     __syncthreads();
-    for (int o = tid; o < tokens * chans; o += kThreads) {
-      const int tk = o / chans, ch = o - tk * chans, nn = n0 + ch;
+    for (int o = tid; o < tl.tokens * chans; o += kThreads) {
+      const int tk = o / chans, ch = o - tk * chans, nn = tl.n0 + ch;
       if (nn >= p.N) continue;
       float v = 0.0f;
       for (int i = 0; i < parts; ++i)
         v = __fadd_rn(v, s_sums[ch / kChannels * parts + i][tk][ch % kChannels]);
-      if (p.bias) v = __fadd_rn(v, p.bias[int64_t(g) * p.N + nn]);
-      const int64_t at = int64_t(row0 + tk) * p.N + nn;
+      if (p.bias) v = __fadd_rn(v, p.bias[int64_t(tl.g) * p.N + nn]);
+      const int64_t at = int64_t(tl.row0 + tk) * p.N + nn;
       if (p.c_dtype == MOE_FP32)
         static_cast<float*>(p.c)[at] = v;
       else
@@ -188,11 +241,12 @@ linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
     }
     __syncthreads();
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int TB>
 cudaError_t launch_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
-  const size_t smem = size_t(p.G + 1) * 8;
+  const size_t smem = kRingBytes + size_t(p.G + 1) * 8;
   auto kernel = linear_f8_few_kernel<TB>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   int dev = 0, sms = 0, per_sm = 0;
@@ -204,7 +258,7 @@ cudaError_t launch_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st
                              ? (p.a_rows + 8 * TB - 1) / (8 * TB)
                              : p.a_rows / (8 * TB) + std::min<int64_t>(p.G, p.a_rows);
   const int64_t room = int64_t(std::max(1, per_sm)) * sms;
-  const int pieces = code_blocks(p.K);
+  const int pieces = (p.K + kStep - 1) / kStep;
   int parts = 1;
   auto ctas = [&](int parts) {
     const int chans = kWarps / parts * kChannels;
@@ -220,8 +274,7 @@ cudaError_t launch_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st
 
 cudaError_t launch_linear_f8_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
   const int64_t mean = (p.a_rows + p.G - 1) / p.G;
-  return mean <= 8 ? launch_few<1>(p, dev_status, st) : mean <= 16
-             ? launch_few<2>(p, dev_status, st) : launch_few<4>(p, dev_status, st);
+  return mean <= 8 ? launch_few<1>(p, dev_status, st) : launch_few<2>(p, dev_status, st);
 }
 
 }  // namespace moe_ep

@@ -583,6 +583,7 @@ struct NormBackwardArgs {
   const float* rstd;
   void* d_x;
   float* parts;                     // the workspace
+  int32_t* dev_status;
   int64_t T, d_out_stride, x_stride, d_sum_stride, d_x_stride;
   int H, dtype;
 };

@@ -168,56 +168,89 @@ rms_norm_kernel(const NormArgs p) {
 // ---- gradient --------------------------------------------------------------------
 
 // CTAs walk over rows and keep d_gamma's sums of their columns in registers; their
-// partial sums go to the workspace, and a second kernel adds them in order.
+// partial sums go to the workspace, and a second kernel adds them in order.  Rows (of d_out,
+// of x and of d_sum) come by bulk copies into a ring of `depth` rows a team of TPR threads,
+// so that the next rows are on their way while one is reduced and written; both passes over
+// a row read it from there.  (By loads into registers a CTA waited for every row: 32,768 x
+// 7168 440 us.)
+constexpr int kMaxDepth = 4;
+__host__ __device__ constexpr int backward_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+
 template <int DT, int TPR, int NV>
-__global__ void __launch_bounds__(block_threads(TPR))
-rms_norm_backward_kernel(const NormBackwardArgs p) {
-  constexpr int kBlock = block_threads(TPR), kRows = kBlock / TPR;
+__global__ void __launch_bounds__(backward_threads(TPR))
+rms_norm_backward_kernel(const NormBackwardArgs p, int depth) {
+  constexpr int kRows = backward_threads(TPR) / TPR;
+  constexpr bool kKeepGamma = NV < 4;            // in registers
+  extern __shared__ __align__(16) uint8_t s_ring[];
+  __shared__ __align__(8) uint64_t s_full[kRows][kMaxDepth];
   __shared__ float s_part[2][TPR > 32 ? TPR / 32 : 1];
-  __shared__ float s_cols[kRows > 1 ? kRows * TPR * NV * 8 : 1];
   wait_for_stream();
   let_next_start();
   const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   const int chunks = p.H / 8;
-  float acc[NV][8];
+  const uint32_t row_bytes = 2 * p.H, parts = p.d_sum ? 3 : 2;
+  uint8_t* ring = s_ring + size_t(slot) * depth * parts * row_bytes;
+  uint64_t* full = s_full[slot];
+  if (t == 0) {
+    for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  auto team_sync = [&]() {
+    if constexpr (TPR == 32) __syncwarp();
+    else __syncthreads();
+  };
+  const int64_t first = int64_t(blockIdx.x) * kRows + slot, stride = int64_t(gridDim.x) * kRows;
+  auto fetch = [&](int64_t row, int at) {          // one thread
+    if (row >= p.T) return;
+    uint8_t* to = ring + size_t(at) * parts * row_bytes;
+    mbar_arrive_expect_tx(&full[at], parts * row_bytes);
+    bulk_load(to, static_cast<const uint16_t*>(p.d_out) + row * p.d_out_stride, row_bytes,
+              &full[at]);
+    bulk_load(to + row_bytes, static_cast<const uint16_t*>(p.x) + row * p.x_stride, row_bytes,
+              &full[at]);
+    if (p.d_sum)
+      bulk_load(to + 2 * row_bytes, static_cast<const uint16_t*>(p.d_sum) + row * p.d_sum_stride,
+                row_bytes, &full[at]);
+  };
+  float acc[NV][8], kept[kKeepGamma ? NV : 1][8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int c = i * TPR + t;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-  int turn = 0;
-  for (int64_t row = int64_t(blockIdx.x) * kRows + slot; row < p.T;
-       row += int64_t(gridDim.x) * kRows, turn ^= 1) {
-    const uint16_t* dy = static_cast<const uint16_t*>(p.d_out) + row * p.d_out_stride;
-    const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.x_stride;
-    const float rstd = p.rstd[row];
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    // with few chunks d_sum is on its way during the reduction too; with four a thread's
-    // registers hold no more
-    constexpr bool kSumEarly = NV < 4;
-    uint4 dv[NV], xv[NV], sv[kSumEarly ? NV : 1];
-    auto sum_chunk = [&](int c) {
-      return p.d_sum && c < chunks ? ld_once_16(static_cast<const uint16_t*>(p.d_sum) +
-                                                row * p.d_sum_stride + 8 * c)
-                                   : zero;
-    };
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = i * TPR + t;
-      dv[i] = c < chunks ? ld_once_16(dy + 8 * c) : zero;
-      xv[i] = c < chunks ? ld_once_16(x + 8 * c) : zero;
+    for (int j = 0; j < 8; ++j) {
+      acc[i][j] = 0.0f;
+      if constexpr (kKeepGamma) kept[i][j] = 0.0f;
     }
-    if constexpr (kSumEarly) {
+    if constexpr (kKeepGamma)
+      if (c < chunks) load8(p.gamma + 8 * c, kept[i]);
+  }
+  auto gamma_of = [&](int i, float (&g)[8]) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sv[i] = sum_chunk(i * TPR + t);
-    }
+    for (int j = 0; j < 8; ++j) g[j] = kKeepGamma ? kept[kKeepGamma ? i : 0][j] : 0.0f;
+    if constexpr (!kKeepGamma) load8(p.gamma + 8 * (i * TPR + t), g);
+  };
+  team_sync();
+  if (t == 0)
+    for (int i = 0; i < depth; ++i) fetch(first + i * stride, i);
+  int at = 0, turn = 0;
+  uint32_t phase = 0;
+  bool ok = true;                     // a wait that ran out: no further one
+  float rstd_next = first < p.T ? p.rstd[first] : 0.0f;
+  for (int64_t row = first; row < p.T; row += stride, turn ^= 1) {
+    const float rstd = rstd_next;
+    if (row + stride < p.T) rstd_next = p.rstd[row + stride];
+    if (ok) ok = mbar_wait_bounded(&full[at], phase, kGemmSpin);
+    const uint4* dv = reinterpret_cast<const uint4*>(ring + size_t(at) * parts * row_bytes);
+    const uint4 *xv = dv + chunks, *sv = xv + chunks;
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * TPR + t;
-      float d[8], xh[8], g[8] = {};
-      unpack8<DT>(dv[i], d);
-      unpack8<DT>(xv[i], xh);
-      if (c < chunks) load8(p.gamma + 8 * c, g);
+      if (c >= chunks) break;
+      float d[8], xh[8], g[8];
+      unpack8<DT>(dv[c], d);
+      unpack8<DT>(xv[c], xh);
+      gamma_of(i, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         xh[j] = __fmul_rn(xh[j], rstd);
@@ -226,22 +259,41 @@ rms_norm_backward_kernel(const NormBackwardArgs p) {
       }
     }
     const float mean = __fdiv_rn(row_reduce<TPR>(dot, s_part[turn], t, Add()), float(p.H));
+    // every thread is done with the row before this one: its place is free
+    if (TPR == 32) __syncwarp();
+    if (t == 0 && row != first) {
+      const int prev = at == 0 ? depth - 1 : at - 1;
+      fetch(row + (depth - 1) * stride, prev);
+    }
     uint16_t* dx = static_cast<uint16_t*>(p.d_x) + row * p.d_x_stride;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * TPR + t;
-      float d[8], xh[8], s[8], g[8] = {};
-      unpack8<DT>(dv[i], d);
-      unpack8<DT>(xv[i], xh);
-      unpack8<DT>(kSumEarly ? sv[kSumEarly ? i : 0] : sum_chunk(c), s);
-      if (c < chunks) load8(p.gamma + 8 * c, g);
+      if (c >= chunks) break;
+      float d[8], xh[8], s[8] = {}, g[8];
+      unpack8<DT>(dv[c], d);
+      unpack8<DT>(xv[c], xh);
+      if (p.d_sum) unpack8<DT>(sv[c], s);
+      gamma_of(i, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        xh[j] = __fmul_rn(xh[j], rstd);
         const float a = __fmul_rn(d[j], g[j]);
-        const float o = __fmaf_rn(-__fmul_rn(xh[j], rstd), mean, a);
-        d[j] = __fmaf_rn(o, rstd, s[j]);
+        d[j] = __fmaf_rn(__fmaf_rn(-xh[j], mean, a), rstd, s[j]);
       }
-      if (c < chunks) *reinterpret_cast<uint4*>(dx + 8 * c) = pack8<DT>(d);
+      *reinterpret_cast<uint4*>(dx + 8 * c) = pack8<DT>(d);
+    }
+    if (++at == depth) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+  if (!ok) {
+    // no copy may land once the CTA has gone
+    set_status(p.dev_status, MOE_ERR_TIMEOUT);
+    for (int i = 0; i < depth; ++i) {
+      mbar_wait_bounded(&full[i], 0, kGemmSpin);
+      mbar_wait_bounded(&full[i], 1, kGemmSpin);
     }
   }
   float* part = p.parts + int64_t(blockIdx.x) * p.H;
@@ -255,6 +307,8 @@ rms_norm_backward_kernel(const NormBackwardArgs p) {
     for (int i = 0; i < NV; ++i) put(i * TPR + t, acc[i]);
   } else {                       // the CTA's warps first, in order
     constexpr int kCols = TPR * NV * 8;
+    float* s_cols = reinterpret_cast<float*>(s_ring);        // the rings are done with
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -485,16 +539,37 @@ cudaError_t launch_norm(const NormArgs& p, cudaStream_t st) {
   });
 }
 
+// CTAs that an SM's shared memory and registers are shared by: two, so that one's
+// reductions overlap the other's; rows of which two do not fit twice have an SM alone.
+// (32,768 x 7168 with one CTA an SM and twice its ring 326 us, with two 288.)
+template <int TPR, int NV>
+constexpr int kCtasPerSm = TPR * NV <= 1024 ? 2 : 1;
+template <int TPR, int NV>
+constexpr int kRingRoom = 196 * 1024 / kCtasPerSm<TPR, NV>;
+
 constexpr int kMaxParts = 304;          // two CTAs for each of 152 SMs
 
 int backward_parts(int64_t T, int H) {
-  if (H > kMaxWidth) return static_cast<int>(std::min<int64_t>(kGammaParts, std::max<int64_t>(1, T)));
-  int rows = 1;
-  by_width(H, [&](auto tpr, auto) {
-    rows = block_threads(decltype(tpr)::value) / decltype(tpr)::value;
+  if (H > kMaxWidth)
+    return static_cast<int>(std::min<int64_t>(kGammaParts, std::max<int64_t>(1, T)));
+  int rows = 1, most = kMaxParts;
+  by_width(H, [&](auto tpr, auto nv) {
+    rows = backward_threads(decltype(tpr)::value) / decltype(tpr)::value;
+    most = kMaxParts / 2 * kCtasPerSm<decltype(tpr)::value, decltype(nv)::value>;
     return cudaSuccess;
   });
-  return static_cast<int>(std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (T + rows - 1) / rows)));
+  return static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, (T + rows - 1) / rows)));
+}
+
+// The ring's rows: as many as fit.
+template <int TPR, int NV>
+int ring_depth(const NormBackwardArgs& p, size_t* smem) {
+  constexpr int kTeams = backward_threads(TPR) / TPR;
+  const size_t row = size_t(kTeams) * 2 * p.H * (p.d_sum ? 3 : 2);
+  int depth = kMaxDepth;
+  while (depth > 2 && row * depth > size_t(kRingRoom<TPR, NV>)) --depth;
+  *smem = std::max(row * depth, kTeams > 1 ? sizeof(float) * kTeams * TPR * NV * 8 : size_t(0));
+  return depth;
 }
 
 template <int DT>
@@ -508,8 +583,12 @@ cudaError_t launch_backward(const NormBackwardArgs& p, int parts, cudaStream_t s
   }
   return by_width(p.H, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    return launch_early(rms_norm_backward_kernel<DT, TPR, NV>, parts, block_threads(TPR), 0, st,
-                        p);
+    size_t smem = 0;
+    const int depth = ring_depth<TPR, NV>(p, &smem);
+    auto kernel = rms_norm_backward_kernel<DT, TPR, NV>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    return launch_early(kernel, parts, backward_threads(TPR), smem, st, p, depth);
   });
 }
 
