@@ -23,10 +23,17 @@ __host__ __device__ constexpr int64_t f8_row_bytes(int H) {
 // The largest magnitude of 8 values as bits (ordered as unsigned numbers; a NaN is
 // above every number, so it reaches the scale and the whole block).
 __device__ __forceinline__ uint32_t abs_max_bits(const float (&y)[8]) {
-  uint32_t m = 0;
+  float m = fabsf(y[0]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(y[j]) & 0x7fffffffu);
-  return m;
+  for (int j = 1; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(y[j])));
+  return __float_as_uint(m) & 0x7fffffffu;
+}
+
+// 1 / x within 1 ulp for normal x (a number that comes out subnormal is 0).
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Over the 16 lanes of a half warp, which hold a block's 128 values.
@@ -42,7 +49,7 @@ struct F8Scale {
 };
 __device__ __forceinline__ F8Scale f8_scale(uint32_t max_bits) {
   const float top = __uint_as_float(max(max_bits, __float_as_uint(kTinyMax)));
-  return {__fmul_rn(top, 1.0f / kF8Max), __fdiv_rn(kF8Max, top)};
+  return {__fmul_rn(top, 1.0f / kF8Max), __fmul_rn(kF8Max, reciprocal(top))};
 }
 
 // 8 values -> 8 e4m3 codes, nearest even (a product that rounding took past 448 is

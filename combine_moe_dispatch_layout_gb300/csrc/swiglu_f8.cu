@@ -2,17 +2,17 @@
 // rows -> e4m3 row images of silu(gate) * up (include/moe_ep.h, moe_swiglu_f8).
 //
 // h = gate / (1 + exp(-gate)) * up in fp32, a scale per 128 values, one rounding to
-// e4m3.  Bound by memory: a half warp takes kBlocks neighbouring blocks of a row, lane l
-// the 8 values from 8 l of each, so all its loads are under way at once and its scales
-// leave in one store.
+// e4m3.  A half warp takes kBlocks neighbouring blocks of a row, lane l the 8 values from
+// 8 l of each, so all its loads are under way at once and its scales leave in one store.
+// Bound by memory, with the arithmetic close behind: at 31 instructions a value (IEEE
+// division and exponential, maxima of integers) the issue slots were 84% busy and 262,144 x
+// 2048 took 492 us.
 #include "row_codes.cuh"
 
 namespace moe_ep {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = 4;              // 128-value blocks per half warp
-
 template <int DT>
 struct Raw8 {                           // 8 values as they lie in memory
   uint4 v[DT == MOE_FP32 ? 2 : 1];
@@ -36,14 +36,17 @@ struct Raw8 {                           // 8 values as they lie in memory
   }
 };
 
-// x / (1 + exp(-x)) by e = exp(-|x|) <= 1, which overflows nowhere and leaves a divisor
-// of 1 to 2: within 2^-20 of itself, and up to |x| 2^-23 more from the exponential.
-__device__ __forceinline__ float silu(float x) {
-  const float e = __expf(-fabsf(x));
-  return __fdividef(__fmul_rn(x, x < 0.0f ? e : 1.0f), __fadd_rn(1.0f, e));
+// 1 / (1 + exp(-x)): the exponential as 2^(-x log2 e), within 2^-21 and |x| 2^-23 of itself
+// (the argument's rounding); from x = -87 on down the divisor leaves fp32 and the result is 0.
+__device__ __forceinline__ float sigmoid(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(x, -1.44269504f)));
+  return reciprocal(__fadd_rn(1.0f, e));
 }
 
-template <int DT>
+// kBlocks: 128-value blocks per half warp; with fewer than 4 a row is one half warp's.
+// (Rows of 128 values by half warps of 4 blocks: three in four loads less under way.)
+template <int DT, int kBlocks>
 __global__ void __launch_bounds__(kThreads)
 swiglu_f8_kernel(const SwigluF8Args p) {
   wait_for_stream();
@@ -51,7 +54,7 @@ swiglu_f8_kernel(const SwigluF8Args p) {
   const int lane = threadIdx.x % 16;
   const int nb = code_blocks(p.I), spans = (nb + kBlocks - 1) / kBlocks;   // per row
   const int64_t unit = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / 16;
-  const int64_t row = unit / spans;
+  const int64_t row = unit <= UINT32_MAX ? uint32_t(unit) / uint32_t(spans) : unit / spans;
   const int b0 = static_cast<int>(unit - row * spans) * kBlocks;
   int64_t rows = p.M;
   if (p.group_off) {
@@ -84,31 +87,47 @@ swiglu_f8_kernel(const SwigluF8Args p) {
     g[i].get(a);
     u[i].get(b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a[j] = __fmul_rn(silu(a[j]), b[j]);
+    for (int j = 0; j < 8; ++j) a[j] = __fmul_rn(__fmul_rn(a[j], sigmoid(a[j])), b[j]);
     const F8Scale sc = f8_scale(block_max_bits(c < p.I ? abs_max_bits(a) : 0u));
     scales[i] = b0 + i < nb ? sc.scale : 0.0f;
     if (live && c < padded)
       *reinterpret_cast<uint2*>(codes + c) = c < p.I ? f8_codes(a, sc.inv) : make_uint2(0u, 0u);
   }
-  if (live && lane == 0)
-    *reinterpret_cast<float4*>(codes + padded + 4 * b0) =
-        make_float4(scales[0], scales[1], scales[2], scales[3]);
-  // the zeros up to the next multiple of 8 scales
-  if (live && lane == 0 && b0 + kBlocks >= nb && (b0 + kBlocks) % 8 != 0)
-    *reinterpret_cast<float4*>(codes + padded + 4 * (b0 + kBlocks)) =
-        make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if constexpr (kBlocks < 4) {            // all of the row's scales, and zeros up to 8
+    float mine = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) mine = lane == i ? scales[i] : mine;
+    if (live && lane < 8) reinterpret_cast<float*>(codes + padded)[lane] = mine;
+  } else {
+    float4* to = reinterpret_cast<float4*>(codes + padded + 4 * b0);
+    if (live && lane == 0) to[0] = make_float4(scales[0], scales[1], scales[2], scales[3]);
+    // the zeros up to the next multiple of 8 scales
+    if (live && lane == 0 && b0 + kBlocks >= nb && (b0 + kBlocks) % 8 != 0)
+      to[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+}
+
+template <int DT, int kBlocks>
+cudaError_t launch(const SwigluF8Args& p, cudaStream_t st) {
+  const int64_t spans = (code_blocks(p.I) + kBlocks - 1) / kBlocks;
+  const int64_t grid = (p.M * spans * 16 + kThreads - 1) / kThreads;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_early(swiglu_f8_kernel<DT, kBlocks>, grid, kThreads, 0, st, p);
+}
+
+template <int DT>
+cudaError_t launch_type(const SwigluF8Args& p, cudaStream_t st) {
+  const int nb = code_blocks(p.I);
+  return nb == 1 ? launch<DT, 1>(p, st) : nb == 2 ? launch<DT, 2>(p, st) : launch<DT, 4>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_swiglu_f8(const SwigluF8Args& p, cudaStream_t st) {
-  const int64_t spans = (code_blocks(p.I) + kBlocks - 1) / kBlocks;
-  const int64_t grid = (p.M * spans * 16 + kThreads - 1) / kThreads;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
   switch (p.dtype) {
-    case MOE_BF16: return launch_early(swiglu_f8_kernel<MOE_BF16>, grid, kThreads, 0, st, p);
-    case MOE_FP16: return launch_early(swiglu_f8_kernel<MOE_FP16>, grid, kThreads, 0, st, p);
-    default: return launch_early(swiglu_f8_kernel<MOE_FP32>, grid, kThreads, 0, st, p);
+    case MOE_BF16: return launch_type<MOE_BF16>(p, st);
+    case MOE_FP16: return launch_type<MOE_FP16>(p, st);
+    default: return launch_type<MOE_FP32>(p, st);
   }
 }
 

@@ -623,7 +623,7 @@ moe_status moe_linear_i8(const void* a, int64_t a_rows, int64_t a_stride, const 
  * align32(H) + align32(4 ceil(H / 128)) bytes.  Code j stands for
  * code * scale[j / 128].  A block of values y gets
  *   scale = max(max|y|, 1e-12f) / 448,  code = e4m3 nearest even of y / scale
- * (the scale within 2 ulp, the quotient within 2 ulp before its rounding); a block with
+ * (the scale within 2 ulp, the quotient within 4 ulp before its rounding); a block with
  * a NaN has a NaN scale and NaN codes, one with an infinity an infinite scale.  An
  * image is a row of f8_row_bytes / 2 16-bit elements for moe_dispatch (quant 0),
  * which copies it verbatim. */
@@ -687,7 +687,8 @@ moe_status moe_rms_norm_backward(const void* d_out, int32_t dtype, int64_t T, in
                                  void* stream);
 
 /* The step between an e4m3 layer's two products: rows [gate | up] of 2I values ->
- * e4m3 row images of h = gate / (1 + exp(-gate)) * up (fp32, within 2^-16 of itself).
+ * e4m3 row images of h = gate / (1 + exp(-gate)) * up (fp32, within 2^-16 of itself; from
+ * gate = -87 on down h is 0).
  *   h          [M] rows of 2I elements of dtype (MOE_BF16, MOE_FP16 or MOE_FP32),
  *              h_stride elements apart (at least 2I; not looked at with M <= 1),
  *              16-byte aligned, the stride too
