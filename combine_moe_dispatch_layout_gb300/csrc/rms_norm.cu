@@ -21,7 +21,7 @@ namespace {
 constexpr int kNoCodes = -1;
 constexpr unsigned kAll = 0xffffffffu;
 
-__host__ __device__ constexpr int block_threads(int tpr) { return tpr < 128 ? 128 : tpr; }
+__host__ __device__ constexpr int block_threads(int tpr) { return tpr < 64 ? 128 : tpr; }
 
 // Over the TPR threads of a row, in an order fixed by TPR alone; every thread gets
 // the result.  part: this row's TPR / 32 words of shared memory, not in use by an
@@ -112,7 +112,12 @@ rms_norm_kernel(const NormArgs p) {
     unpack8<DT>(v[i], y);
     if (c < chunks) load8(p.gamma + 8 * c, g);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(__fmul_rn(y[j], rstd), g[j]);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 z = mul_pair(mul_pair(make_float2(y[j], y[j + 1]), make_float2(rstd, rstd)),
+                                make_float2(g[j], g[j + 1]));
+      y[j] = z.x;
+      y[j + 1] = z.y;
+    }
   };
   uint16_t* out = p.out ? static_cast<uint16_t*>(p.out) + row * p.out_stride : nullptr;
   const int padded = static_cast<int>(align_up(p.H, 32)) / 8;     // chunks with the zeros
@@ -520,6 +525,20 @@ cudaError_t by_width(int H, F&& f) {
 }
 constexpr int kMaxWidth = 512 * 4 * 8;      // wider rows: the kernels that read a row again
 
+// The norm's own: many rows want 64 bytes of loads a thread under way (65,536 rows of 2048:
+// 81 us with 4 chunks a thread, 125 with one), few rows many threads each.
+template <class F>
+cudaError_t by_width_and_rows(int H, int64_t T, F&& f) {
+  const int chunks = H / 8;
+  using std::integral_constant;
+  if (T > 256 && chunks > 128) {
+    if (chunks <= 256) return f(integral_constant<int, 64>(), integral_constant<int, 4>());
+    if (chunks <= 512) return f(integral_constant<int, 128>(), integral_constant<int, 4>());
+    if (chunks <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+  }
+  return by_width(H, f);
+}
+
 template <int DT>
 cudaError_t launch_norm(const NormArgs& p, cudaStream_t st) {
   if (p.H > kMaxWidth)
@@ -527,7 +546,7 @@ cudaError_t launch_norm(const NormArgs& p, cudaStream_t st) {
            : p.code_type == MOE_CODE_I8
                ? launch_early(rms_norm_wide_kernel<DT, MOE_CODE_I8>, p.T, kWide, 0, st, p)
                : launch_early(rms_norm_wide_kernel<DT, MOE_CODE_F8>, p.T, kWide, 0, st, p);
-  return by_width(p.H, [&](auto tpr, auto nv) {
+  return by_width_and_rows(p.H, p.T, [&](auto tpr, auto nv) {
     constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     constexpr int kBlock = block_threads(TPR), kRows = kBlock / TPR;
     const int64_t grid = (p.T + kRows - 1) / kRows;

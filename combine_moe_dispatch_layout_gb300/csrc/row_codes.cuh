@@ -43,6 +43,16 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t m) {
   return m;
 }
 
+// Two products in one instruction, each rounded once (no sum follows that the compiler
+// could merge it with).
+__device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 pa, pb, pd;\n\tmov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+      "mul.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // The block's scale, and what its values are multiplied by.
 struct F8Scale {
   float scale, inv;
@@ -57,10 +67,10 @@ __device__ __forceinline__ F8Scale f8_scale(uint32_t max_bits) {
 __device__ __forceinline__ uint2 f8_codes(const float (&y)[8], float inv) {
   uint16_t c[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(c[j])
-        : "f"(__fmul_rn(y[2 * j + 1], inv)), "f"(__fmul_rn(y[2 * j], inv)));
+  for (int j = 0; j < 4; ++j) {
+    const float2 q = mul_pair(make_float2(y[2 * j], y[2 * j + 1]), make_float2(inv, inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[j]) : "f"(q.y), "f"(q.x));
+  }
   return make_uint2(c[0] | uint32_t(c[1]) << 16, c[2] | uint32_t(c[3]) << 16);
 }
 
