@@ -44,7 +44,6 @@ constexpr int kEpiRegs = 216, kCtrlRegs = 72;
 static_assert(32 * (kEpiWarps * kEpiRegs + kCtrlWarps * kCtrlRegs) <= kThreads * 168,
               "no more registers than the launch has");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kAccCols = 256;   // column offset of the second accumulator
 constexpr int kTurn = 4;             // blocks per turn of a draining thread, see there
 constexpr int kMaxStages = 10;
 constexpr uint32_t kBoxBytes = 32 * 128;             // a warp's 32 rows of 128 output bytes
@@ -57,6 +56,9 @@ struct Maps {
 // NT: channels per tile.
 template <int NT>
 struct Stages {
+  // Accumulators: what TMEM holds.  (A block's way from its products' commit to the drain
+  // and back takes some 800 clocks, four times as long as a narrow tile's products.)
+  static constexpr int kAccs = kTmemCols / NT;
   static constexpr uint32_t kBytes = (TM + NT / CG) * BK;
   static constexpr uint32_t kBarBytes = 512;
   static size_t bytes(int stages, int G) {
@@ -95,12 +97,6 @@ __device__ __forceinline__ Tile decode_tile(int t, uint32_t goff, uint32_t tpre,
 }
 
 template <int OUT>
-__device__ __forceinline__ void store_one(void* c, int64_t at, float v) {
-  if constexpr (OUT == MOE_FP32) static_cast<float*>(c)[at] = v;
-  else static_cast<uint16_t*>(c)[at] = static_cast<uint16_t>(narrow_rn<OUT>(v));
-}
-
-template <int OUT>
 __device__ __forceinline__ uint32_t narrow_pair(float lo, float hi) {
   uint32_t h;
   if constexpr (OUT == MOE_BF16)
@@ -116,6 +112,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
                       int stages, int32_t* dev_status) {
   using St = Stages<NT>;
   constexpr int kCols = NT / (kEpiWarps / 4);          // columns per draining thread
+  constexpr int kAccs = St::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -126,10 +123,10 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   auto empty = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };  // multiplied
   constexpr int kT0 = 3 * kMaxStages;
   auto tfull = [&](int b) { return bars + 8 * (kT0 + b); };             // accumulator final
-  auto tempty = [&](int b) { return bars + 8 * (kT0 + 2 + b); };        // ... drained
-  const uint32_t tmem_slot = bars + 8 * (kT0 + 4), abort_flag = tmem_slot + 4;
+  auto tempty = [&](int b) { return bars + 8 * (kT0 + kAccs + b); };    // ... drained
+  const uint32_t tmem_slot = bars + 8 * (kT0 + 2 * kAccs), abort_flag = tmem_slot + 4;
   const uint32_t issued = abort_flag + 4;    // the pair's commits: of stages, of accumulators
-  static_assert(8 * (kT0 + 4) + 16 <= St::kBarBytes, "barriers fit");
+  static_assert(8 * (kT0 + 2 * kAccs) + 16 <= St::kBarBytes, "barriers fit");
   const uint32_t goff = bars + St::kBarBytes, tpre = goff + 4 * (p.G + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -154,7 +151,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       bar_init(peer(lane), 1);
       bar_init(empty(lane), 1);
     }
-    if (lane < 2) {
+    if (lane < kAccs) {
       bar_init(tfull(lane), 1);
       bar_init(tempty(lane), CG * kEpiWarps);
     }
@@ -192,8 +189,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
     for (uint32_t i = ncommit > ns ? ncommit - ns : 0; i < ncommit; ++i)
       ok &= bar_wait(empty(i % ns), (i / ns) & 1u);
 #pragma unroll 1
-    for (uint32_t i = nacc > 2 ? nacc - 2 : 0; i < nacc; ++i)
-      ok &= bar_wait(tfull(i & 1u), (i >> 1) & 1u);
+    for (uint32_t i = nacc > kAccs ? nacc - kAccs : 0; i < nacc; ++i)
+      ok &= bar_wait(tfull(i % kAccs), (i / kAccs) & 1u);
     if (!ok) set_status(dev_status, MOE_ERR_TIMEOUT);
   };
 
@@ -268,9 +265,9 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       bool ok = true;
       for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
-          const uint32_t b = nacc & 1u;
+          const uint32_t b = nacc % kAccs;
           if (!bar_wait(full(s), phase) || !bar_wait(peer(s), phase) ||
-              !bar_wait(tempty(b), ((nacc >> 1) & 1u) ^ 1u)) {
+              !bar_wait(tempty(b), ((nacc / kAccs) & 1u) ^ 1u)) {
             ok = false;
             break;
           }
@@ -278,7 +275,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
           if (issue) {
             const uint32_t st = sbase + s * St::kBytes;
             const uint64_t da = operand_desc(st), db = operand_desc(st + TM * BK);
-            const uint32_t d = tmem + b * kAccCols;
+            const uint32_t d = tmem + b * NT;
 #pragma unroll
             for (int kk = 0; kk < BK / 32; ++kk)     // + 32 bytes along K per step
               pair_mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk != 0);
@@ -363,8 +360,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
 #pragma unroll
         for (int turn = 0; turn < kTurn; ++turn) {
           if (kb + turn >= nk) break;
-          const uint32_t b = nacc & 1u;
-          ok = warp_bar_wait(tfull(b), (nacc >> 1) & 1u);
+          const uint32_t b = nacc % kAccs;
+          ok = warp_bar_wait(tfull(b), (nacc / kAccs) & 1u);
           if (!ok) break;
           ++nacc;
           tc_fence_after();
@@ -378,7 +375,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
             continue;
           }
           const float2 s2 = bcast2(sc[turn]);
-          const uint32_t from = base + b * kAccCols;
+          const uint32_t from = base + b * NT;
           constexpr int kParts = kCols / 8;
           float v[2][8];
           tmem_start8(from, v[0]);
@@ -401,63 +398,97 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
         break;
       }
       if (!work) continue;
-      const float* bias = p.bias ? p.bias + int64_t(tl.g) * p.N + n0 : nullptr;
-      auto value = [&](int j) {                // column j, which is one of the product's
-        const float v = j & 1 ? acc[j / 2].y : acc[j / 2].x;
-        return bias ? __fadd_rn(v, bias[j]) : v;
-      };
+      if (p.bias) {
+        const float* bias = p.bias + int64_t(tl.g) * p.N + n0;
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j) {
+          if (n0 + 2 * j < p.N) acc[j].x = __fadd_rn(acc[j].x, bias[2 * j]);
+          if (n0 + 2 * j + 1 < p.N) acc[j].y = __fadd_rn(acc[j].y, bias[2 * j + 1]);
+        }
+      }
       constexpr int kItem = OUT == MOE_FP32 ? 4 : 2, kVec = 16 / kItem;     // per 16 bytes
       auto piece = [&](int j) {                // columns j .. j + kVec - 1, narrowed
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
-        if (n0 + j < p.N) {
-          if constexpr (OUT == MOE_FP32)
-            o = make_uint4(__float_as_uint(value(j)), __float_as_uint(value(j + 1)),
-                           __float_as_uint(value(j + 2)), __float_as_uint(value(j + 3)));
-          else
-            o = make_uint4(narrow_pair<OUT>(value(j), value(j + 1)),
-                           narrow_pair<OUT>(value(j + 2), value(j + 3)),
-                           narrow_pair<OUT>(value(j + 4), value(j + 5)),
-                           narrow_pair<OUT>(value(j + 6), value(j + 7)));
-        }
-        return o;
+        if constexpr (OUT == MOE_FP32)
+          return make_uint4(__float_as_uint(acc[j / 2].x), __float_as_uint(acc[j / 2].y),
+                            __float_as_uint(acc[j / 2 + 1].x),
+                            __float_as_uint(acc[j / 2 + 1].y));
+        else
+          return make_uint4(narrow_pair<OUT>(acc[j / 2].x, acc[j / 2].y),
+                            narrow_pair<OUT>(acc[j / 2 + 1].x, acc[j / 2 + 1].y),
+                            narrow_pair<OUT>(acc[j / 2 + 2].x, acc[j / 2 + 2].y),
+                            narrow_pair<OUT>(acc[j / 2 + 3].x, acc[j / 2 + 3].y));
       };
-      constexpr int kBoxCols = 128 / kItem, kBoxes = kCols / kBoxCols;
-      if (kBoxes > 0 && p.N % kVec == 0 && rows >= 32) {
-        // 32 whole rows: 128 bytes of each at a time through shared memory (16-byte pieces
-        // swizzled as the copy reads them) and out by one tensor copy
+      constexpr int kBoxCols = kCols * kItem < 128 ? kCols : 128 / kItem;
+      constexpr int kBoxes = kCols / kBoxCols;
+      // kBoxCols columns of the warp's 32 rows into shared memory, 16-byte pieces swizzled as
+      // a tensor copy reads them
+      auto stage = [&](int j, uint32_t at) {
 #pragma unroll
-        for (int j = 0; j < kBoxes * kBoxCols; j += kBoxCols) {
-          const uint32_t at = box + (j / kBoxCols % 2) * kBoxBytes;
-          if (lane == 0) bulk_wait_read<kBoxes == 1 ? 0 : 1>();    // this buffer's last copy
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 o = piece(j + i * kVec);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                             at + lane * 128 + ((i ^ (lane & 7)) << 4)),
-                         "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w) : "memory");
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (n0 + j < p.N)
-              tensor_store_2d(&maps.c, (n0 + j) * kItem, first_row, at);
-            bulk_commit();
-          }
+        for (int i = 0; i < kBoxCols / kVec; ++i) {
+          const uint4 o = piece(j + i * kVec);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                           at + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                       "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w) : "memory");
         }
-      } else if (lane < rows) {
-        const int64_t at = (int64_t(first_row) + lane) * p.N + n0;
-        if (p.N % kVec == 0) {
+      };
+      if (p.N % kVec == 0) {
+        if (kBoxCols * kItem == 128 && rows >= 32) {       // whole rows: out by tensor copies
+#pragma unroll
+          for (int j = 0; j < kCols; j += kBoxCols) {
+            const uint32_t at = box + (j / kBoxCols % 2) * kBoxBytes;
+            if (lane == 0) bulk_wait_read<kBoxes == 1 ? 0 : 1>();    // this buffer's last copy
+            __syncwarp();
+            stage(j, at);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (n0 + j < p.N) tensor_store_2d(&maps.c, (n0 + j) * kItem, first_row, at);
+              bulk_commit();
+            }
+          }
+        } else if (lane < rows) {
+          const int64_t at = (int64_t(first_row) + lane) * p.N + n0;
 #pragma unroll
           for (int j = 0; j < kCols; j += kVec) {
             const uint4 o = piece(j);
             if (n0 + j < p.N)
               *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.c) + (at + j) * kItem) = o;
           }
-        } else {
+        }
+      } else {
+        // rows of c that do not start on 16 bytes: a row at a time by neighbouring lanes
+        // (a lane storing its own row by elements touches 32 lines an instruction: 197 x
+        // 1001 x 1992 in fp32 16.6 us, and 11.8 this way)
 #pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            if (n0 + j < p.N) store_one<OUT>(p.c, at + j, value(j));
+        for (int j = 0; j < kCols; j += kBoxCols) {
+          stage(j, box);
+          __syncwarp();
+          constexpr int kLanes = kBoxCols * kItem / 4;       // lanes per row, 4 bytes each
+          constexpr int kRows = 32 / kLanes, kBatch = 4;
+          const int word = lane % kLanes, n = n0 + j + word * (4 / kItem);
+          for (int r0 = lane / kLanes; r0 < min(rows, 32); r0 += kBatch * kRows) {
+            uint32_t v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int r = r0 + i * kRows;                  // (at most 31)
+              v[i] = static_cast<uint32_t>(
+                  smem_load(box + r * 128 + (((word >> 2) ^ (r & 7)) << 4) + (word & 3) * 4));
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int r = r0 + i * kRows;
+              if (r >= rows || n >= p.N) continue;
+              const int64_t to = int64_t(first_row + r) * p.N + n;
+              if constexpr (OUT == MOE_FP32) {
+                static_cast<uint32_t*>(p.c)[to] = v[i];
+              } else {
+                uint16_t* c = static_cast<uint16_t*>(p.c) + to;
+                c[0] = static_cast<uint16_t>(v[i]);
+                if (n + 1 < p.N) c[1] = static_cast<uint16_t>(v[i] >> 16);
+              }
+            }
+          }
+          __syncwarp();
         }
       }
       __syncwarp();
@@ -522,7 +553,17 @@ cudaError_t launch_nt(const Maps& maps, const LinearArgs& p, const Plan& plan,
 }
 
 // Whether the kernel that streams weights to the warps' own products is the faster one.
-bool use_few(const LinearArgs& p) { return p.a_rows <= 32 * int64_t(p.G); }
+// A few rows of a plain product: 16 rows of 4096 x 7168 take 14.3 us there and 24.4 here,
+// 64 rows 45 and 21.  A few per group on average: with 4, 64 groups of 4096 x 7168 take 299
+// and 322 us, 200 of 2048 x 512 58 and 74; with 6 335 and 334; with 8 389 and 336, 86 and
+// 76.  Small products, where this kernel's start (barriers, TMEM, clusters) is most of its
+// time: 256 x 512 x 512 4.8 and 6.3, 64 x 2048 x 2048 (at both limits) 9.1 and 10.1, 64 x
+// 7168 x 256 (past the first) 10.1 and 7.0.
+bool use_few(const LinearArgs& p) {
+  const int64_t outputs = p.a_rows * p.N;
+  return p.a_rows <= (p.G == 1 ? 16 : 6 * int64_t(p.G)) ||
+         (outputs <= (1 << 17) && outputs * p.K <= (1 << 28));
+}
 
 // The widest tile that gives every pair of SMs something to do.
 Plan make_plan(const LinearArgs& p, int sms) {

@@ -30,12 +30,11 @@
 namespace moe_ep {
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kChannels = 16;        // weight rows per warp
 constexpr int kStep = 256;           // codes of K per step: two blocks
 constexpr int kDepth = 3;            // steps in a warp's ring
 constexpr uint32_t kStepBytes = kChannels * kStep;
-constexpr size_t kRingBytes = size_t(kWarps) * kDepth * kStepBytes;
+constexpr size_t ring_bytes(int warps) { return size_t(warps) * kDepth * kStepBytes; }
 
 __device__ __forceinline__ void mma_f8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                        uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -81,9 +80,10 @@ struct Tokens {                      // a step as a lane holds it
 };
 
 // TB: tokens per block / 8.
-template <int TB>
-__global__ void __launch_bounds__(kThreads)
+template <int TB, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps)
 linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
+  constexpr int kThreads = 32 * kWarps;
   extern __shared__ __align__(16) uint8_t s_ring[];          // the rings, then the group tables
   __shared__ int64_t s_scan[kThreads * 12 / 8];
   __shared__ float s_sums[kWarps][8 * TB][kChannels];
@@ -95,7 +95,7 @@ linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
   const int ntn = (p.N + chans - 1) / chans;
   const int kblocks = code_blocks(p.K), nblocks = code_blocks(p.N);
   const int steps = (p.K + kStep - 1) / kStep;
-  const uint32_t goff = smem_addr(s_ring) + kRingBytes, tpre = goff + 4 * (p.G + 1);
+  const uint32_t goff = smem_addr(s_ring) + ring_bytes(kWarps), tpre = goff + 4 * (p.G + 1);
   const bool grouped = p.group_rows != nullptr;
   int tiles = row_blocks(static_cast<int>(p.a_rows), 8 * TB) * ntn;
   if (grouped) {
@@ -244,37 +244,48 @@ linear_f8_few_kernel(const LinearArgs p, int parts, int32_t* dev_status) {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int TB>
-cudaError_t launch_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
-  const size_t smem = kRingBytes + size_t(p.G + 1) * 8;
-  auto kernel = linear_f8_few_kernel<TB>;
+// Whether it was launched (parts of K: all kWarps of a CTA where `all`, which then has to
+// leave all CTAs running at once; else as many as that allows).
+template <int TB, int kWarps>
+cudaError_t launch_few(const LinearArgs& p, bool all, bool* done, int32_t* dev_status,
+                       cudaStream_t st) {
+  const size_t smem = ring_bytes(kWarps) + size_t(p.G + 1) * 8;
+  auto kernel = linear_f8_few_kernel<TB, kWarps>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   int dev = 0, sms = 0, per_sm = 0;
   cudaError_t e = current_device_sms(&dev, &sms);
-  if (e == cudaSuccess) e = kernel_blocks_per_sm(fn, kThreads, smem, &per_sm);
+  if (e == cudaSuccess) e = kernel_blocks_per_sm(fn, 32 * kWarps, smem, &per_sm);
   if (e != cudaSuccess) return e;
-  // Split K over more warps while all CTAs still run at once.
   const int64_t blocks = p.G == 1
                              ? (p.a_rows + 8 * TB - 1) / (8 * TB)
                              : p.a_rows / (8 * TB) + std::min<int64_t>(p.G, p.a_rows);
   const int64_t room = int64_t(std::max(1, per_sm)) * sms;
   const int pieces = (p.K + kStep - 1) / kStep;
-  int parts = 1;
   auto ctas = [&](int parts) {
     const int chans = kWarps / parts * kChannels;
     return blocks * ((p.N + chans - 1) / chans);
   };
+  int parts = 1;
   while (parts < kWarps && parts * 2 <= pieces && ctas(parts * 2) <= room) parts *= 2;
+  *done = !all || parts == kWarps;
+  if (!*done) return cudaSuccess;
   if (ctas(parts) > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_early(kernel, std::min(ctas(parts), room), kThreads, smem, st, p, parts,
+  return launch_early(kernel, std::min(ctas(parts), room), 32 * kWarps, smem, st, p, parts,
                       dev_status);
 }
 
 }  // namespace
 
+// Eight warps to a CTA where they can split K eight ways (one token by 4096 x 7168 7.4 us,
+// with four warps 8.5), else four (256 tokens over 256 experts the same, 100 rows in 200
+// groups of 300 x 300 7.9 and with eight 8.4).  More than 8 rows a group: two blocks of 8
+// share the weights' way (16 rows of 4096 x 7168 14.3 us).
 cudaError_t launch_linear_f8_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
-  const int64_t mean = (p.a_rows + p.G - 1) / p.G;
-  return mean <= 8 ? launch_few<1>(p, dev_status, st) : launch_few<2>(p, dev_status, st);
+  bool done = false;
+  if ((p.a_rows + p.G - 1) / p.G > 8) return launch_few<2, 4>(p, false, &done, dev_status, st);
+  const cudaError_t e = launch_few<1, 8>(p, true, &done, dev_status, st);
+  if (done || e != cudaSuccess) return e;
+  return launch_few<1, 4>(p, false, &done, dev_status, st);
 }
 
 }  // namespace moe_ep
