@@ -59,7 +59,10 @@ struct F8Scale {
 };
 __device__ __forceinline__ F8Scale f8_scale(uint32_t max_bits) {
   const float top = __uint_as_float(max(max_bits, __float_as_uint(kTinyMax)));
-  return {__fmul_rn(top, 1.0f / kF8Max), __fmul_rn(kF8Max, reciprocal(top))};
+  const float scale = __fmul_rn(top, 1.0f / kF8Max);
+  // (of the scale, whose reciprocal is a normal number for every finite block; that of a
+  // block's maximum beyond 2^126 is not, and would be 0)
+  return {scale, reciprocal(scale)};
 }
 
 // 8 values -> 8 e4m3 codes, nearest even (a product that rounding took past 448 is

@@ -9,19 +9,22 @@ synchronisation is needed between the stages.
 
 Around them: ``Routing`` / ``run_route`` (logits -> ids and weights), the
 gradients of a verbatim pipeline (``run_combine_backward``,
-``run_dispatch_backward``, ``run_route_backward``), and ``run_serve_moe``, an
-MoE layer from logits to output on 8-bit weights and activations.
+``run_dispatch_backward``, ``run_route_backward``), and MoE layers from logits to
+output on 8-bit weights and activations: ``run_serve_moe`` (INT8, a scale per
+row and channel) and, with the norm in front of it, ``run_norm_f8`` and
+``run_serve_moe_f8`` (e4m3, a scale per 128 values).
 """
 import torch
 
-from . import (fused_workspace_bytes, make_shape, layout_workspace_bytes,
+from . import (f8_row_bytes, fused_workspace_bytes, make_shape, layout_workspace_bytes,
                moe_codes_to_bf16, moe_combine, moe_combine_backward, moe_combine_f32,
                moe_combine_quant, moe_dispatch, moe_dispatch_expand, moe_dispatch_fused,
                moe_dispatch_layout, moe_group_offsets, moe_grouped_gemm_i8,
                moe_grouped_gemm_i8_dequant, moe_grouped_gemm_i8_swiglu,
-               moe_interleave_gate_up, moe_linear_i8, moe_notify_dispatch,
-               moe_quant_rows_bf16, moe_route, moe_route_backward,
-               moe_swiglu_quant_grouped, moe_swiglu_quant_grouped_bf16, recv_row_bytes)
+               moe_interleave_gate_up, moe_linear_f8, moe_linear_i8, moe_notify_dispatch,
+               moe_quant_rows_bf16, moe_rms_norm, moe_route, moe_route_backward,
+               moe_swiglu_f8, moe_swiglu_quant_grouped, moe_swiglu_quant_grouped_bf16,
+               recv_row_bytes)
 
 
 class PipelineBuffers:
@@ -295,3 +298,76 @@ def run_serve_moe(b, wts, routing, x, logits, stream=None):
                   (b.x2, _align32(I), b.x2.shape[1]), None, b.y2, b.dev_status, stream)
     moe_combine_f32(b.shape, b.y2, routing.topk_idx, routing.topk_weights, b.send_idx,
                     b.put_offset, b.rank_recv_base, b.out, b.dev_status, stream)
+
+
+# ---- the same in 8-bit floating point, from the residual stream on ------------------
+
+class Fp8MoeWeights:
+    """Expert weights as they are stored: w1 e4m3 [E, 2I, H] (gate rows, then up
+    rows), w2 e4m3 [E, H, I] and a fp32 scale per 128 x 128 block, s1 [E,
+    ceil(2I/128), ceil(H/128)] and s2 [E, ceil(H/128), ceil(I/128)]."""
+
+    def __init__(self, w1, s1, w2, s2):
+        E, N1, H = w1.shape
+        I = N1 // 2
+        if w2.shape != (E, H, I) or N1 % 2 or H % 16 or I % 16:
+            raise ValueError("w1 must be [E, 2I, H] and w2 [E, H, I], H and I multiples of 16")
+
+        def blocks(n):
+            return (n + 127) // 128
+
+        if s1.shape != (E, blocks(N1), blocks(H)) or s2.shape != (E, blocks(H), blocks(I)):
+            raise ValueError("s1 and s2 must hold a scale per 128 x 128 block")
+        self.E, self.H, self.I = E, H, I
+        self.w1, self.w2 = w1.contiguous(), w2.contiguous()
+        self.s1, self.s2 = s1.contiguous(), s2.contiguous()
+
+
+class ServeF8Buffers(PipelineBuffers):
+    """PipelineBuffers whose dispatch carries e4m3 row images verbatim (``shape`` is
+    that of the images as 16-bit rows), plus the norm's outputs (``sum``,
+    ``normed``, ``images``) and what the layer keeps between its stages: expert row
+    offsets, the gate/up products, the SwiGLU's row images and the experts'
+    outputs.  ``token_shape`` is the tokens' own."""
+
+    def __init__(self, R, bs, k, epr, H, I, dtype, device="cuda"):
+        row_bytes = f8_row_bytes(H)
+        super().__init__(R, bs, k, epr, row_bytes // 2, dtype, False, device)
+        T, P = R * bs, R * bs * k
+        self.H, self.I = H, I
+        self.token_shape = make_shape(R, bs, k, epr, H, dtype)
+        rows = dict(dtype=self.torch_dtype, device=device)
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.sum = torch.empty((T, H), **rows)
+        self.normed = torch.empty((T, H), **rows)
+        self.images = torch.empty((T, row_bytes), **u8)
+        self.group_off = torch.empty((R * epr + 1,), dtype=torch.int64, device=device)
+        self.h1 = torch.empty((P, 2 * I), **rows)
+        self.x2 = torch.empty((P, f8_row_bytes(I)), **u8)
+        self.y2 = torch.empty((P, H), **rows)
+        self.out = torch.empty((T, H), **rows)
+
+
+def run_norm_f8(b, x, residual, gamma, eps=1e-6, stream=None):
+    """The residual's addition (-> ``b.sum``; residual may be None) and the norm in
+    front of the layer: ``b.normed`` in the tokens' type, for the router, and
+    ``b.images`` in e4m3, for the products."""
+    moe_rms_norm(x, residual, gamma, eps, None if residual is None else b.sum, b.normed,
+                 b.images, None, b.dev_status, stream=stream)
+
+
+def run_serve_moe_f8(b, wts, routing, logits, stream=None):
+    """Route, dispatch of ``b.images`` (one launch, verbatim), gate/up product, SwiGLU
+    to e4m3, down product, weighted sum; the result is ``b.out``.  Logits as the
+    router makes them of ``b.normed``."""
+    H, I = b.H, b.I
+    run_route(b, routing, logits, stream)
+    run_dispatch_fused(b, b.images.view(b.torch_dtype), routing.topk_idx, stream)
+    moe_group_offsets(b.recv_per_expert, b.group_off, b.dev_status, stream)
+    moe_linear_f8(b.recv, wts.w1, H, b.recv_per_expert, wts.s1,
+                  (b.recv, _align32(H), b.row_bytes), None, b.h1, b.dev_status, stream)
+    moe_swiglu_f8(b.h1, b.group_off, b.x2, b.dev_status, stream)
+    moe_linear_f8(b.x2, wts.w2, I, b.recv_per_expert, wts.s2,
+                  (b.x2, _align32(I), b.x2.shape[1]), None, b.y2, b.dev_status, stream)
+    moe_combine(b.token_shape, b.y2, b.y2.shape[0], routing.topk_idx, routing.topk_weights,
+                b.send_idx, b.put_offset, b.rank_recv_base, b.out, b.dev_status, stream)
