@@ -31,6 +31,21 @@
 #include "tcgen05.cuh"
 
 namespace moe_ep {
+
+// linear_f8_polls.cu compiles this file a second time, for tests of the waits that run
+// out: with role waits of its own, and without the function that others call.
+#ifndef MOE_LINEAR_F8_POLLS
+namespace {
+// A role's wait for its next work; false after kGemmSpin polls.
+__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity) {
+  return bar_wait(bar, parity);
+}
+__device__ __forceinline__ bool warp_role_wait(uint32_t bar, uint32_t parity) {
+  return warp_bar_wait(bar, parity);
+}
+}  // namespace
+#endif
+
 namespace {
 
 constexpr int CG = 2;                // CTAs per tile (a pair)
@@ -208,7 +223,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
         const int wrow = tl.g * p.N + tl.n0 + rank * (NT / CG);
         const int arow = tl.row0 + rank * TM;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!bar_wait(empty(s), phase ^ 1u)) {
+          if (!role_wait(empty(s), phase ^ 1u)) {
             ok = false;
             break;
           }
@@ -241,7 +256,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       bool ok = true;
       for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
-          if (!bar_wait(full(s), phase) || smem_load(abort_flag)) {
+          if (!role_wait(full(s), phase) || smem_load(abort_flag)) {
             ok = false;
             break;
           }
@@ -266,8 +281,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
           const uint32_t b = nacc % kAccs;
-          if (!bar_wait(full(s), phase) || !bar_wait(peer(s), phase) ||
-              !bar_wait(tempty(b), ((nacc / kAccs) & 1u) ^ 1u)) {
+          if (!role_wait(full(s), phase) || !role_wait(peer(s), phase) ||
+              !role_wait(tempty(b), ((nacc / kAccs) & 1u) ^ 1u)) {
             ok = false;
             break;
           }
@@ -361,7 +376,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
         for (int turn = 0; turn < kTurn; ++turn) {
           if (kb + turn >= nk) break;
           const uint32_t b = nacc % kAccs;
-          ok = warp_bar_wait(tfull(b), (nacc / kAccs) & 1u);
+          ok = warp_role_wait(tfull(b), (nacc / kAccs) & 1u);
           if (!ok) break;
           ++nacc;
           tc_fence_after();
@@ -581,8 +596,23 @@ Plan make_plan(const LinearArgs& p, int sms) {
   return plan;
 }
 
+cudaError_t make_maps(const LinearArgs& p, Plan* plan, Maps* maps) {
+  cudaError_t e =
+      encode_bytes_2d(&maps->w, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, plan->nt / CG);
+  if (e == cudaSuccess) e = encode_bytes_2d(&maps->a, p.a, p.a_rows, p.K, p.a_stride, TM);
+  // (rows of c that do not start on 16 bytes are stored without the map)
+  const int64_t pitch = int64_t(p.N) * (p.c_dtype == MOE_FP32 ? 4 : 2);
+  maps->c = maps->a;
+  if (e == cudaSuccess && pitch % 16 == 0)
+    e = encode_bytes_2d(&maps->c, p.c, p.a_rows, pitch, pitch, 32);
+  plan->wide_scales = reinterpret_cast<uintptr_t>(p.row_scale) % 16 == 0 &&
+                      (p.a_rows == 1 || p.row_scale_stride % 16 == 0);
+  return e;
+}
+
 }  // namespace
 
+#ifndef MOE_LINEAR_F8_POLLS
 cudaError_t launch_linear_f8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
   if (use_few(p)) return launch_linear_f8_few(p, dev_status, st);
   int dev = 0, sms = 0, optin = 0;
@@ -592,19 +622,12 @@ cudaError_t launch_linear_f8(const LinearArgs& p, int32_t* dev_status, cudaStrea
   if (e != cudaSuccess) return e;
   Plan plan = make_plan(p, sms);
   Maps maps;
-  e = encode_bytes_2d(&maps.w, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, plan.nt / CG);
-  if (e == cudaSuccess) e = encode_bytes_2d(&maps.a, p.a, p.a_rows, p.K, p.a_stride, TM);
-  // (rows of c that do not start on 16 bytes are stored without the map)
-  const int64_t pitch = int64_t(p.N) * (p.c_dtype == MOE_FP32 ? 4 : 2);
-  maps.c = maps.a;
-  if (e == cudaSuccess && pitch % 16 == 0)
-    e = encode_bytes_2d(&maps.c, p.c, p.a_rows, pitch, pitch, 32);
-  plan.wide_scales = reinterpret_cast<uintptr_t>(p.row_scale) % 16 == 0 &&
-                     (p.a_rows == 1 || p.row_scale_stride % 16 == 0);
+  e = make_maps(p, &plan, &maps);
   if (e != cudaSuccess) return e;
   return plan.nt == 256   ? launch_nt<256>(maps, p, plan, dev_status, optin, st)
          : plan.nt == 128 ? launch_nt<128>(maps, p, plan, dev_status, optin, st)
                           : launch_nt<64>(maps, p, plan, dev_status, optin, st);
 }
+#endif
 
 }  // namespace moe_ep
