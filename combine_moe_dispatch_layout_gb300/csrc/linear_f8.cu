@@ -63,6 +63,7 @@ constexpr int kTurn = 4;             // blocks per turn of a draining thread, se
 constexpr int kMaxStages = 10;
 constexpr uint32_t kBoxBytes = 32 * 128;             // a warp's 32 rows of 128 output bytes
 constexpr uint32_t kOutBytes = kEpiWarps * 2 * kBoxBytes;
+constexpr int kMaxTable = 64;                        // a cluster's first tiles, decoded ahead
 
 struct Maps {
   CUtensorMap w, a, c;       // weights, token rows, the result
@@ -75,9 +76,10 @@ struct Stages {
   // and back takes some 800 clocks, four times as long as a narrow tile's products.)
   static constexpr int kAccs = kTmemCols / NT;
   static constexpr uint32_t kBytes = (TM + NT / CG) * BK;
-  static constexpr uint32_t kBarBytes = 512;
-  static size_t bytes(int stages, int G) {
-    return 1024 + size_t(stages) * kBytes + kOutBytes + kBarBytes + size_t(G + 1) * 8;
+  static constexpr uint32_t kBarBytes = 400;
+  static size_t bytes(int stages, int table, int G) {
+    return 1024 + size_t(stages) * kBytes + kOutBytes + kBarBytes + size_t(table) * 16 +
+           size_t(G + 1) * 8;
   }
 };
 
@@ -124,7 +126,7 @@ __device__ __forceinline__ uint32_t narrow_pair(float lo, float hi) {
 template <int NT, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, bool wide_scales,
-                      int stages, int32_t* dev_status) {
+                      int stages, int entries, int32_t* dev_status) {
   using St = Stages<NT>;
   constexpr int kCols = NT / (kEpiWarps / 4);          // columns per draining thread
   constexpr int kAccs = St::kAccs;
@@ -142,7 +144,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   const uint32_t tmem_slot = bars + 8 * (kT0 + 2 * kAccs), abort_flag = tmem_slot + 4;
   const uint32_t issued = abort_flag + 4;    // the pair's commits: of stages, of accumulators
   static_assert(8 * (kT0 + 2 * kAccs) + 16 <= St::kBarBytes, "barriers fit");
-  const uint32_t goff = bars + St::kBarBytes, tpre = goff + 4 * (p.G + 1);
+  const uint32_t table = bars + St::kBarBytes;
+  const uint32_t goff = table + entries * 16, tpre = goff + 4 * (p.G + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntn = (p.N + NT - 1) / NT;
@@ -184,6 +187,17 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
     __syncwarp();
     pair_tmem_alloc(tmem_slot, kTmemCols);
   }
+  __syncthreads();
+  if (tid >= kThreads - entries) {
+    const int i = tid - (kThreads - entries), t = cluster_id() + i * cluster_count();
+    if (t < smem_load(tpre + 4 * p.G)) {
+      const Tile tl = decode_tile<NT>(t, goff, tpre, p.G, ntn);
+      smem_store(table + i * 16, tl.g);
+      smem_store(table + i * 16 + 4, tl.n0);
+      smem_store(table + i * 16 + 8, tl.row0);
+      smem_store(table + i * 16 + 12, tl.rows);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   // The copies start at once; a role waits for the other CTA before it first reaches
@@ -193,6 +207,16 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
 
   // (each role reads what it needs: registers are short in some)
   auto tile_count = [&]() { return smem_load(tpre + 4 * p.G); };
+  // The cluster's i-th tile, t = cluster_id() + i * cluster_count().  (The search for its
+  // group and the divisions took some 400 clocks at the start of every tile.)
+  auto tile_at = [&](int i, int t) {
+    if (i >= entries) return decode_tile<NT>(t, goff, tpre, p.G, ntn);
+    Tile tl;
+    asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(tl.g), "=r"(tl.n0), "=r"(tl.row0), "=r"(tl.rows)
+                 : "r"(table + i * 16) : "memory");
+    return tl;
+  };
   // Waits for the last commit on each of this CTA's barriers, once all of them are
   // issued: ncommit of stages, nacc of accumulators.  A barrier's n-th commit is issued
   // only after this CTA's threads have seen its n-1-th, so at most one is outstanding and
@@ -218,8 +242,9 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       int s = 0;
       uint32_t phase = 0, nload = 0;
       bool ok = true;
-      for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
-        const Tile tl = decode_tile<NT>(t, goff, tpre, p.G, ntn);
+      int i = 0;
+      for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count(), ++i) {
+        const Tile tl = tile_at(i, t);
         const int wrow = tl.g * p.N + tl.n0 + rank * (NT / CG);
         const int arow = tl.row0 + rank * TM;
         for (int kb = 0; kb < nk; ++kb) {
@@ -329,41 +354,53 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
     const uint32_t box = outs + (warp - kCtrlWarps) * 2 * kBoxBytes;
     const int nblocks = code_blocks(p.N);
     cluster_wait_all();
+    // What the drain of a tile needs: its scales' places, and those of its first turn.
+    // kTurn blocks a turn, their scales loaded a turn ahead (the first ones before the tile
+    // ahead is stored): the token's 16 bytes at once (every load of a warp touches 32 lines,
+    // and takes as many of the L1 cycles that the products need to read shared memory:
+    // 8192 x 4096 x 7168 took 182 us by loads of 4 bytes, 174 by these, 197 with tensor
+    // copies of 128 x 16 bytes, which hold up the operands' copies, and 187 with a warp that
+    // loads for the others)
+    const unsigned char* as = nullptr;
+    const float* ws = nullptr;
+    bool work = false;
+    float ra[kTurn], rw[kTurn];
+    auto load_scales = [&](int kb) {
+      const float* from = reinterpret_cast<const float*>(as) + kb;
+      if (work && wide_scales && kb + kTurn <= nk) {
+        const float4 v = *reinterpret_cast<const float4*>(from);
+        ra[0] = v.x; ra[1] = v.y; ra[2] = v.z; ra[3] = v.w;
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) rw[i] = ws[kb + i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) {
+          const bool in = work && kb + i < nk;
+          ra[i] = in ? from[i] : 0.0f;
+          rw[i] = in ? ws[kb + i] : 0.0f;
+        }
+      }
+    };
+    auto aim = [&](const Tile& tl) {
+      const int row = tl.row0 + rank * TM + q * 32 + lane, n0 = tl.n0 + col0;
+      work = tl.rows > rank * TM + q * 32 && n0 < p.N;
+      as = p.row_scale + min(int64_t(row), p.a_rows - 1) * p.row_scale_stride;
+      ws = p.col_scale +
+           (int64_t(tl.g) * nblocks + min(n0 / kCodeBlock, nblocks - 1)) * nk;
+      load_scales(0);
+    };
     uint32_t nacc = 0;
     bool ok = true;
-    for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
-      const Tile tl = decode_tile<NT>(t, goff, tpre, p.G, ntn);
+    int index = 0, t = cluster_id();
+    Tile tl{};
+    if (t < tile_count()) {
+      tl = tile_at(0, t);
+      aim(tl);
+    }
+    while (ok && t < tile_count()) {
       const int first_row = tl.row0 + rank * TM + q * 32;   // of the warp; a lane's token is
       const int rows = tl.rows - rank * TM - q * 32;        // first_row + lane, rows there are
-      const int n0 = tl.n0 + col0;
-      const bool work = rows > 0 && n0 < p.N;
-      // kTurn blocks a turn, their scales loaded a turn ahead: the token's 16 bytes at once
-      // (every load of a warp touches 32 lines, and takes as many of the L1 cycles that the
-      // products need to read shared memory: 8192 x 4096 x 7168 took 182 us by loads of 4
-      // bytes, 174 by these, 197 with tensor copies of 128 x 16 bytes, which hold up the
-      // operands' copies, and 187 with a warp that loads for the others)
-      const unsigned char* as =
-          p.row_scale + min(int64_t(first_row) + lane, p.a_rows - 1) * p.row_scale_stride;
-      const float* ws = p.col_scale +
-                        (int64_t(tl.g) * nblocks + min(n0 / kCodeBlock, nblocks - 1)) * nk;
-      float ra[kTurn], rw[kTurn];
-      auto load_scales = [&](int kb) {
-        const float* from = reinterpret_cast<const float*>(as) + kb;
-        if (work && wide_scales && kb + kTurn <= nk) {
-          const float4 v = *reinterpret_cast<const float4*>(from);
-          ra[0] = v.x; ra[1] = v.y; ra[2] = v.z; ra[3] = v.w;
-#pragma unroll
-          for (int i = 0; i < kTurn; ++i) rw[i] = ws[kb + i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < kTurn; ++i) {
-            const bool in = work && kb + i < nk;
-            ra[i] = in ? from[i] : 0.0f;
-            rw[i] = in ? ws[kb + i] : 0.0f;
-          }
-        }
-      };
-      load_scales(0);
+      const int n0 = tl.n0 + col0, g = tl.g;
       float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
@@ -412,9 +449,14 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
         smem_store(abort_flag, 1);
         break;
       }
-      if (!work) continue;
+      t += cluster_count();
+      if (t < tile_count()) {
+        tl = tile_at(++index, t);
+        aim(tl);
+      }
+      if (rows <= 0 || n0 >= p.N) continue;
       if (p.bias) {
-        const float* bias = p.bias + int64_t(tl.g) * p.N + n0;
+        const float* bias = p.bias + int64_t(g) * p.N + n0;
 #pragma unroll
         for (int j = 0; j < kCols / 2; ++j) {
           if (n0 + 2 * j < p.N) acc[j].x = __fadd_rn(acc[j].x, bias[2 * j]);
@@ -536,8 +578,12 @@ cudaError_t launch_kernel(const Maps& maps, const LinearArgs& p, const Plan& pla
                           int32_t* dev_status, int optin, cudaStream_t st) {
   using S = Stages<NT>;
   int stages = kMaxStages;
-  while (stages > 2 && S::bytes(stages, p.G) > size_t(optin)) --stages;
-  const size_t smem = S::bytes(stages, p.G);
+  while (stages > 2 && S::bytes(stages, 0, p.G) > size_t(optin)) --stages;
+  // (a table in what the stages leave)
+  const int table = static_cast<int>(std::min<size_t>(
+      kMaxTable, (std::max(size_t(optin), S::bytes(stages, 0, p.G)) -
+                  S::bytes(stages, 0, p.G)) / 16));
+  const size_t smem = S::bytes(stages, table, p.G);
   auto kernel = linear_f8_tile_kernel<NT, OUT>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
@@ -554,7 +600,7 @@ cudaError_t launch_kernel(const Maps& maps, const LinearArgs& p, const Plan& pla
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, maps, p, plan.wide_scales, stages, dev_status);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p, plan.wide_scales, stages, table, dev_status);
 }
 
 template <int NT>
