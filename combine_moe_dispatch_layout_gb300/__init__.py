@@ -11,6 +11,7 @@ Stages (UMDK/CAM deep analysis v2, section 2 "EP Normal"):
 ``moe_dispatch`` (2.5, optional INT8 quantisation), ``moe_combine`` (2.6).
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -752,6 +753,7 @@ _F8_CODES = (torch.float8_e4m3fn, torch.uint8)
 _CODE = {"i8": MOE_CODE_I8, "f8": MOE_CODE_F8}
 
 
+@functools.lru_cache(maxsize=4096)
 def f8_row_bytes(H):
     """Bytes of an e4m3 row image of H codes: the codes, their scales from byte
     align32(H) on, each part padded to a multiple of 32."""
@@ -762,10 +764,16 @@ def _token_rows(t, name, dtype, T, H):
     """(pointer, row stride) of [T, H] rows of the token dtype (None: NULL)."""
     if t is None:
         return None, 0
-    p, stride, rows, cols = _rows(t, name, (dtype,))
-    if rows != T or cols != H:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != (T, H):
         raise ValueError("%s must be [%d, %d]" % (name, T, H))
-    return p, stride
+    stride, unit = t.stride()
+    if (unit != 1 and H > 1 and T > 0) or (T > 1 and stride < H):
+        raise ValueError("%s must be a matrix with contiguous rows" % name)
+    return t.data_ptr(), stride
 
 
 def _images(t, rows, row_bytes, name):
@@ -800,6 +808,7 @@ def moe_rms_norm(x, residual, gamma, eps, sum_out, out, codes, rstd, dev_status,
     return _check(st, "moe_rms_norm")
 
 
+@functools.lru_cache(maxsize=4096)
 def rms_norm_backward_workspace_bytes(T, H):
     return int(_lib.moe_rms_norm_backward_workspace_bytes(int(T), int(H)))
 
