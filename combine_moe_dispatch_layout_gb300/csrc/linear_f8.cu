@@ -13,8 +13,9 @@
 // of the weight rows.  Tokens are on the lanes so that a draining thread has one token:
 // its scale is one register, and the multiply-adds take two columns per instruction.
 // Warps of a CTA (one CTA per SM, persistent):
-//   warp 0   copies its 128 token rows and half of the weight rows, 128 bytes of each,
-//            into a ring of stages (tensor copies, 128-byte swizzle)
+//   warp 0   copies its 128 token rows, 128 bytes of each, into a ring of stages (tensor
+//            copies, 128-byte swizzle), and warp 2 its half of the weight rows (one warp
+//            for both took 400 clocks a stage, which shows in narrow tiles)
 //   warp 1   of the pair's first CTA: issues tcgen05.mma (K = 32), four per 128-code
 //            block, into one of two TMEM accumulators in turn; of its second CTA: tells
 //            the first which of its stages have landed
@@ -36,12 +37,16 @@ namespace moe_ep {
 // out: with role waits of its own, and without the function that others call.
 #ifndef MOE_LINEAR_F8_POLLS
 namespace {
-// A role's wait for its next work; false after kGemmSpin polls.
-__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity) {
-  return bar_wait(bar, parity);
-}
+// A role's waits for its next work; false after kGemmSpin polls.
 __device__ __forceinline__ bool warp_role_wait(uint32_t bar, uint32_t parity) {
   return warp_bar_wait(bar, parity);
+}
+__device__ __forceinline__ bool warp_role_wait2(uint32_t a, uint32_t b, uint32_t parity) {
+  return warp_bar_wait4(a, b, b, parity, a, parity);
+}
+__device__ __forceinline__ bool warp_role_wait4(uint32_t a, uint32_t b, uint32_t c,
+                                                uint32_t parity, uint32_t d, uint32_t pd) {
+  return warp_bar_wait4(a, b, c, parity, d, pd);
 }
 }  // namespace
 #endif
@@ -76,7 +81,7 @@ struct Stages {
   // and back takes some 800 clocks, four times as long as a narrow tile's products.)
   static constexpr int kAccs = kTmemCols / NT;
   static constexpr uint32_t kBytes = (TM + NT / CG) * BK;
-  static constexpr uint32_t kBarBytes = 400;
+  static constexpr uint32_t kBarBytes = 464;
   static size_t bytes(int stages, int table, int G) {
     return 1024 + size_t(stages) * kBytes + kOutBytes + kBarBytes + size_t(table) * 16 +
            size_t(G + 1) * 8;
@@ -135,10 +140,12 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
   const uint32_t outs = sbase + stages * St::kBytes, bars = outs + kOutBytes;
-  auto full = [&](int s) { return bars + 8 * s; };                      // this CTA's copies landed
-  auto peer = [&](int s) { return bars + 8 * (kMaxStages + s); };       // ... the other CTA's
-  auto empty = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };  // multiplied
-  constexpr int kT0 = 3 * kMaxStages;
+  // A stage's token rows (0) and weight rows (1) of this CTA landed: a barrier for each warp
+  // that copies, which after a timeout waits for its own copies whatever the other has done.
+  auto full = [&](int of, int s) { return bars + 8 * (of * kMaxStages + s); };
+  auto peer = [&](int s) { return bars + 8 * (2 * kMaxStages + s); };   // ... the other CTA's
+  auto empty = [&](int s) { return bars + 8 * (3 * kMaxStages + s); };  // multiplied
+  constexpr int kT0 = 4 * kMaxStages;
   auto tfull = [&](int b) { return bars + 8 * (kT0 + b); };             // accumulator final
   auto tempty = [&](int b) { return bars + 8 * (kT0 + kAccs + b); };    // ... drained
   const uint32_t tmem_slot = bars + 8 * (kT0 + 2 * kAccs), abort_flag = tmem_slot + 4;
@@ -165,7 +172,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   }
   if (warp == 0) {           // barriers: one lane each
     if (lane < stages) {
-      bar_init(full(lane), 1);
+      bar_init(full(0, lane), 1);
+      bar_init(full(1, lane), 1);
       bar_init(peer(lane), 1);
       bar_init(empty(lane), 1);
     }
@@ -202,7 +210,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   __syncthreads();
   // The copies start at once; a role waits for the other CTA before it first reaches
   // into it (its barriers must have been set up).
-  cluster_arrive_all();
+  cluster_arrive_all_relaxed();
   tc_fence_after();
 
   // (each role reads what it needs: registers are short in some)
@@ -236,27 +244,29 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   if (warp < kCtrlWarps) {
     regs_fewer<kCtrlRegs>();
     const int rank = crank(), nk = blocks_of_k();
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
       // ---- copies -------------------------------------------------------------------
       const bool issue = elect_one();
+      const int of = warp / 2;                 // 0: token rows, 1: weight rows
+      const uint32_t bytes = of ? (NT / CG) * BK : TM * BK;
+      const CUtensorMap* map = of ? &maps.w : &maps.a;
       int s = 0;
       uint32_t phase = 0, nload = 0;
       bool ok = true;
       int i = 0;
       for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count(), ++i) {
         const Tile tl = tile_at(i, t);
-        const int wrow = tl.g * p.N + tl.n0 + rank * (NT / CG);
-        const int arow = tl.row0 + rank * TM;
+        const int row = of ? tl.g * p.N + tl.n0 + rank * (NT / CG) : tl.row0 + rank * TM;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!role_wait(empty(s), phase ^ 1u)) {
+          // (the ring's first round finds it empty)
+          if (nload >= uint32_t(stages) && !warp_role_wait(empty(s), phase ^ 1u)) {
             ok = false;
             break;
           }
           if (issue) {
-            const uint32_t dst = sbase + s * St::kBytes;
-            bar_expect(full(s), St::kBytes);
-            tensor_load_2d(dst, &maps.a, kb * BK, arow, full(s));
-            tensor_load_2d(dst + TM * BK, &maps.w, kb * BK, wrow, full(s));
+            bar_expect(full(of, s), bytes);
+            tensor_load_2d(sbase + s * St::kBytes + of * (TM * BK), map, kb * BK, row,
+                           full(of, s));
           }
           ++nload;
           if (++s == stages) { s = 0; phase ^= 1u; }
@@ -271,7 +281,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       // nobody waited for)
       const uint32_t ns = stages;
       for (uint32_t i = nload > ns ? nload - ns : 0; issue && i < nload; ++i)
-        bar_wait(full(i % ns), (i / ns) & 1u);
+        bar_wait(full(of, i % ns), (i / ns) & 1u);
       cluster_wait_all();
     } else if (warp == 1 && rank == 1) {
       // ---- which stages of this CTA have landed ---------------------------------------
@@ -281,13 +291,14 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       bool ok = true;
       for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
-          if (!role_wait(full(s), phase) || smem_load(abort_flag)) {
+          if (!warp_role_wait2(full(0, s), full(1, s), phase)) {
             ok = false;
             break;
           }
-          if (lane == 0) cluster_arrive(cluster_addr(peer(s), 0));
+          cluster_arrive_if(lane == 0, cluster_addr(peer(s), 0));
           if (++s == stages) { s = 0; phase ^= 1u; }
         }
+        ok = ok && !smem_load(abort_flag);
       }
       if (!ok) {
         if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
@@ -306,8 +317,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
           const uint32_t b = nacc % kAccs;
-          if (!role_wait(full(s), phase) || !role_wait(peer(s), phase) ||
-              !role_wait(tempty(b), ((nacc / kAccs) & 1u) ^ 1u)) {
+          if (!warp_role_wait4(full(0, s), full(1, s), peer(s), phase, tempty(b),
+                               ((nacc / kAccs) & 1u) ^ 1u)) {
             ok = false;
             break;
           }
@@ -388,6 +399,10 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       ws = p.col_scale +
            (int64_t(tl.g) * nblocks + min(n0 / kCodeBlock, nblocks - 1)) * nk;
       load_scales(0);
+      // the tile's bias, which the store would otherwise wait for (197 x 1001 x 1992: 1 us)
+      if (p.bias && lane * 32 < kCols && n0 + lane * 32 < p.N)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias + int64_t(tl.g) * p.N + n0 +
+                                                      lane * 32));
     };
     uint32_t nacc = 0;
     bool ok = true;

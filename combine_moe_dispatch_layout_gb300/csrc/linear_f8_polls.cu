@@ -23,21 +23,22 @@ __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// As bar_wait and warp_bar_wait, with fewer polls (one at the least), which look and do
+// As warp_bar_wait and warp_bar_wait4, with fewer polls (one at the least), which look and do
 // not wait.
-__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity) {
-  uint32_t i = c_first;
-  do {
-    if (look(bar, parity)) return true;
-  } while (++i < kGemmSpin);
-  return false;
-}
 __device__ __forceinline__ bool warp_role_wait(uint32_t bar, uint32_t parity) {
   uint32_t i = c_first;
   do {
     if (__any_sync(0xffffffffu, look(bar, parity))) return true;
   } while (++i < kGemmSpin);
   return false;
+}
+__device__ __forceinline__ bool warp_role_wait2(uint32_t a, uint32_t b, uint32_t parity) {
+  return warp_role_wait(a, parity) && warp_role_wait(b, parity);
+}
+__device__ __forceinline__ bool warp_role_wait4(uint32_t a, uint32_t b, uint32_t c,
+                                                uint32_t parity, uint32_t d, uint32_t pd) {
+  return warp_role_wait(a, parity) && warp_role_wait(b, parity) && warp_role_wait(c, parity) &&
+         warp_role_wait(d, pd);
 }
 }  // namespace
 }  // namespace moe_ep

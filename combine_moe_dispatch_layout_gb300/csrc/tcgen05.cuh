@@ -55,6 +55,28 @@ __device__ __forceinline__ bool warp_bar_wait(uint32_t bar, uint32_t parity) {
     if (__any_sync(0xffffffffu, bar_poll(bar, parity))) return true;
   return false;
 }
+// Waits for phase `parity` of three barriers and `pd` of a fourth, a whole converged warp,
+// with their polls in flight together (one after the other they took 90 clocks each though
+// the phases were complete).
+__device__ __forceinline__ bool warp_bar_wait4(uint32_t a, uint32_t b, uint32_t c, uint32_t parity,
+                                               uint32_t d, uint32_t pd) {
+  for (uint32_t i = 0; i < kGemmSpin; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q, r, s;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %4;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q, [%2], %4;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 r, [%3], %4;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 s, [%5], %6;\n\t"
+        "and.pred p, p, q;\n\tand.pred r, r, s;\n\tand.pred p, p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(b), "r"(c), "r"(parity), "r"(d), "r"(pd)
+        : "memory");
+    if (__any_sync(0xffffffffu, ok != 0)) return true;
+  }
+  return false;
+}
 // 2-D tensor copy global -> shared, completion counted on `bar`.
 __device__ __forceinline__ void tensor_load_2d(uint32_t sdst, const CUtensorMap* map, int x,
                                                int y, uint32_t bar) {
@@ -151,6 +173,11 @@ __device__ __forceinline__ int cluster_count() {
 // CTA's shared memory) are visible after it.
 __device__ __forceinline__ void cluster_arrive_all() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+// The same without waiting for earlier writes: enough where all that the others need to see
+// is barriers set up before a fence_mbar_init().
+__device__ __forceinline__ void cluster_arrive_all_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait_all() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
