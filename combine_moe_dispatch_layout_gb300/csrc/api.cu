@@ -662,6 +662,7 @@ moe_status moe_swiglu_f8(const void* h, int32_t dtype, int64_t M, int32_t I, int
       M >= (int64_t(1) << 31) || I < 8 || I > MOE_EP_MAX_HIDDEN / 2 || I % 8 != 0 ||
       (group_off && (G < 1 || G > MOE_EP_MAX_EXPERTS)))
     return MOE_ERR_INVALID_ARG;
+  if (M * ((I + 511) / 512) > int64_t(INT32_MAX) * 16) return MOE_ERR_INVALID_ARG;   // the grid
   if (M == 0) return MOE_OK;
   if (!h || !codes || !valid_rows(h, M, 2 * int64_t(I), h_stride, dtype == MOE_FP32 ? 4 : 8) ||
       !aligned(codes, 16) || !aligned(group_off, 8))

@@ -17,11 +17,25 @@
 //            copies, 128-byte swizzle), and warp 2 its half of the weight rows (one warp
 //            for both took 400 clocks a stage, which shows in narrow tiles)
 //   warp 1   of the pair's first CTA: issues tcgen05.mma (K = 32), four per 128-code
-//            block, into one of two TMEM accumulators in turn; of its second CTA: tells
-//            the first which of its stages have landed
+//            block, into the TMEM accumulators in turn (two for 256 channels); of its
+//            second CTA: tells the first which of its stages have landed
 //   8 warps  drain a block's sums, scale and add them, and store the tile
 // Every wait is bounded: a timeout sets MOE_ERR_TIMEOUT, the CTA stops issuing work and
 // drains what is in flight.
+//
+// What bounds it.  A block of 128 codes is 512 clocks of products for a full tile (596 with
+// its copies, which share the shared memory's port), and its accumulator stays taken through
+// them, the commit's way to the draining warps, the drain (its 32,768 multiply-adds are 256
+// clocks of the SM's pipes; the last column is loaded some 350 after the first) and the
+// arrival's way back: with two accumulators 876 clocks a block (8192 x 4096 x 7168, ncu).
+// Looped for longer than 20 ms the board is at its power limit and lowers the clock, so
+// energy counts more than clocks: 166 us in bursts, 183 to 188 looped (a library product
+// without block scales 127 and 144).  Measured beside it: 32,768 x 7168 x 2048 in 32 uneven
+// groups 413 us, 1024 x 4096 x 4096 22.4, 8192 rows over 256 groups of 4096 x 7168 1425 to
+// 1530, 197 x 1001 x 1992 in fp32 10.8.  Slower for the first: four accumulators of 128
+// columns (the products read the token rows twice: 210), 16 draining warps (178), TMEM loads
+// of 4, 16 or 32 columns (198, 169, 210; of 8 here), scalar multiply-adds (215), single CTAs
+// instead of pairs (as many clocks, 3% more energy).
 #include <cuda.h>
 
 #include <algorithm>
@@ -64,7 +78,7 @@ constexpr int kEpiRegs = 216, kCtrlRegs = 72;
 static_assert(32 * (kEpiWarps * kEpiRegs + kCtrlWarps * kCtrlRegs) <= kThreads * 168,
               "no more registers than the launch has");
 constexpr uint32_t kTmemCols = 512;
-constexpr int kTurn = 4;             // blocks per turn of a draining thread, see there
+constexpr int kTurn = 4;             // blocks per turn of a draining thread, see load_scales
 constexpr int kMaxStages = 10;
 constexpr uint32_t kBoxBytes = 32 * 128;             // a warp's 32 rows of 128 output bytes
 constexpr uint32_t kOutBytes = kEpiWarps * 2 * kBoxBytes;

@@ -10,7 +10,9 @@
 // Both are bound by memory.  A row is read once, by TPR threads that keep it in
 // registers (16-bit, NV chunks of 8 values each) over the reduction; thread t holds
 // chunks t, t + TPR, ..., so every access of a warp is 512 consecutive bytes and a
-// half warp holds the 128 values of an e4m3 block.
+// half warp holds the 128 values of an e4m3 block.  Measured: 32,768 x 7168 with its residual
+// 271 us, 103% of a copy's rate, with codes too 319 (98%); 24,251 x 1000 to codes 17.3 (63%:
+// instructions, and one stream of loads a warp); the gradient of 32,768 x 7168 288 (97%).
 #include <algorithm>
 
 #include "row_codes.cuh"

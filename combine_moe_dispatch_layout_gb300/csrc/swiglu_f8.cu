@@ -6,7 +6,7 @@
 // 8 l of each, so all its loads are under way at once and its scales leave in one store.
 // Bound by memory, with the arithmetic close behind: at 31 instructions a value (IEEE
 // division and exponential, maxima of integers) the issue slots were 84% busy and 262,144 x
-// 2048 took 492 us.
+// 2048 took 492 us; as written here 391 to 408, 98 to 102% of a copy's rate.
 #include "row_codes.cuh"
 
 namespace moe_ep {

@@ -77,6 +77,7 @@ SWIGLU = dict(h=OK, dtype=0, M=4, I=64, stride=128, off=OK, G=2, codes=OK, st=OK
 
 @pytest.mark.parametrize("bad", [
     dict(h=None), dict(h=ODD), dict(dtype=3), dict(dtype=-1), dict(M=-1), dict(M=1 << 31),
+    dict(M=(1 << 31) - 1, I=32768, stride=65536),
     dict(I=0), dict(I=60), dict(I=32776), dict(stride=120), dict(stride=132), dict(off=OFF),
     dict(G=0), dict(G=4097), dict(codes=None), dict(codes=ODD), dict(st=None), dict(st=OFF)],
     ids=str)
