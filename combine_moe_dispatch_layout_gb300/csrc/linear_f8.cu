@@ -20,6 +20,9 @@
 //            block, into the TMEM accumulators in turn (two for 256 channels); of its
 //            second CTA: tells the first which of its stages have landed
 //   8 warps  drain a block's sums, scale and add them, and store the tile
+// Where there are few tiles a cluster of two pairs splits K: each pair sends its sums of one
+// half of a CTA's rows to the other one's shared memory, adds what it gets to its own sums of
+// the other half, and stores those.
 // Every wait is bounded: a timeout sets MOE_ERR_TIMEOUT, the CTA stops issuing work and
 // drains what is in flight.
 //
@@ -96,9 +99,11 @@ struct Stages {
   static constexpr int kAccs = kTmemCols / NT;
   static constexpr uint32_t kBytes = (TM + NT / CG) * BK;
   static constexpr uint32_t kBarBytes = 464;
-  static size_t bytes(int stages, int table, int G) {
-    return 1024 + size_t(stages) * kBytes + kOutBytes + kBarBytes + size_t(table) * 16 +
-           size_t(G + 1) * 8;
+  // the other pair's sums of half the rows
+  static constexpr uint32_t kSumBytes = TM / 2 * NT * 4;
+  static size_t bytes(int stages, int table, int G, bool split) {
+    return 1024 + size_t(stages) * kBytes + kOutBytes + (split ? kSumBytes : 0) + kBarBytes +
+           size_t(table) * 16 + size_t(G + 1) * 8;
   }
 };
 
@@ -142,7 +147,13 @@ __device__ __forceinline__ uint32_t narrow_pair(float lo, float hi) {
   return h;
 }
 
-template <int NT, int OUT>
+// Blocks of K of the first of two parts: whole turns of a draining thread.
+__host__ __device__ __forceinline__ int first_blocks(int K) {
+  return static_cast<int>(align_up((code_blocks(K) + 1) / 2, kTurn));
+}
+
+// SPLIT: two pairs to a cluster, which takes one tile.
+template <int NT, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, bool wide_scales,
                       int stages, int entries, int32_t* dev_status) {
@@ -153,7 +164,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
-  const uint32_t outs = sbase + stages * St::kBytes, bars = outs + kOutBytes;
+  const uint32_t outs = sbase + stages * St::kBytes, sums = outs + kOutBytes;
+  const uint32_t bars = sums + (SPLIT ? St::kSumBytes : 0);
   // A stage's token rows (0) and weight rows (1) of this CTA landed: a barrier for each warp
   // that copies, which after a timeout waits for its own copies whatever the other has done.
   auto full = [&](int of, int s) { return bars + 8 * (of * kMaxStages + s); };
@@ -170,8 +182,15 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ntn = (p.N + NT - 1) / NT;
-  auto crank = []() { return static_cast<int>(cluster_rank()); };
-  auto blocks_of_k = [&]() { return code_blocks(p.K); };
+  // rank in the pair; the pair's first CTA in the cluster; which part of K, and its blocks
+  auto pair_rank = []() { return static_cast<int>(cluster_rank() % CG); };
+  auto pair_leader = []() { return SPLIT ? static_cast<int>(cluster_rank() / CG * CG) : 0; };
+  auto k_part = []() { return SPLIT ? static_cast<int>(cluster_rank() / CG) : 0; };
+  auto first_part = [&]() { return first_blocks(p.K); };
+  auto blocks_of_k = [&]() {
+    const int all = code_blocks(p.K);
+    return !SPLIT ? all : k_part() ? all - first_part() : first_part();
+  };
 
   wait_for_stream();
   let_next_start();
@@ -257,13 +276,14 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
 
   if (warp < kCtrlWarps) {
     regs_fewer<kCtrlRegs>();
-    const int rank = crank(), nk = blocks_of_k();
+    const int rank = pair_rank(), nk = blocks_of_k();
     if (warp == 0 || warp == 2) {
       // ---- copies -------------------------------------------------------------------
       const bool issue = elect_one();
       const int of = warp / 2;                 // 0: token rows, 1: weight rows
       const uint32_t bytes = of ? (NT / CG) * BK : TM * BK;
       const CUtensorMap* map = of ? &maps.w : &maps.a;
+      const int kb0 = k_part() * first_part();
       int s = 0;
       uint32_t phase = 0, nload = 0;
       bool ok = true;
@@ -279,8 +299,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
           }
           if (issue) {
             bar_expect(full(of, s), bytes);
-            tensor_load_2d(sbase + s * St::kBytes + of * (TM * BK), map, kb * BK, row,
-                           full(of, s));
+            tensor_load_2d(sbase + s * St::kBytes + of * (TM * BK), map, (kb0 + kb) * BK,
+                           row, full(of, s));
           }
           ++nload;
           if (++s == stages) { s = 0; phase ^= 1u; }
@@ -309,7 +329,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
             ok = false;
             break;
           }
-          cluster_arrive_if(lane == 0, cluster_addr(peer(s), 0));
+          cluster_arrive_if(lane == 0, cluster_addr(peer(s), pair_leader()));
           if (++s == stages) { s = 0; phase ^= 1u; }
         }
         ok = ok && !smem_load(abort_flag);
@@ -344,8 +364,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
 #pragma unroll
             for (int kk = 0; kk < BK / 32; ++kk)     // + 32 bytes along K per step
               pair_mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk != 0);
-            pair_commit(tfull(b), uint16_t(3));
-            pair_commit(empty(s), uint16_t(3));
+            pair_commit(tfull(b), uint16_t(3 << pair_leader()));
+            pair_commit(empty(s), uint16_t(3 << pair_leader()));
           }
           ++nacc;
           if (++s == stages) { s = 0; phase ^= 1u; }
@@ -360,7 +380,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       // there were; it waits for them after the closing barrier
       if (issue) {
         await_commits(nacc, nacc);
-        const uint32_t to = cluster_addr(issued, 1);
+        const uint32_t to = cluster_addr(issued, pair_leader() + 1);
         cluster_store(to, nacc);
         cluster_store(to + 4, nacc);
       }
@@ -368,14 +388,15 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       cluster_wait_all();
     }
     __syncwarp();
+    if constexpr (SPLIT) cluster_sync();       // (the draining warps')
   } else {
     // ---- blocks' sums -> scaled sums -> stores --------------------------------------------
     regs_more<kEpiRegs>();
-    const int rank = crank(), nk = blocks_of_k();
+    const int rank = pair_rank(), nk = blocks_of_k();
     const int q = warp & 3;                  // TMEM lanes 32 q ..
     const int col0 = ((warp - kCtrlWarps) >> 2) * kCols;
     const uint32_t base = smem_load(tmem_slot) + (uint32_t(q * 32) << 16) + col0;
-    const uint32_t drained = cluster_addr(tempty(0), 0);
+    const uint32_t drained = cluster_addr(tempty(0), pair_leader());
     const uint32_t box = outs + (warp - kCtrlWarps) * 2 * kBoxBytes;
     const int nblocks = code_blocks(p.N);
     cluster_wait_all();
@@ -411,7 +432,11 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       work = tl.rows > rank * TM + q * 32 && n0 < p.N;
       as = p.row_scale + min(int64_t(row), p.a_rows - 1) * p.row_scale_stride;
       ws = p.col_scale +
-           (int64_t(tl.g) * nblocks + min(n0 / kCodeBlock, nblocks - 1)) * nk;
+           (int64_t(tl.g) * nblocks + min(n0 / kCodeBlock, nblocks - 1)) * code_blocks(p.K);
+      if constexpr (SPLIT) {
+        as += 4 * k_part() * first_part();
+        ws += k_part() * first_part();
+      }
       load_scales(0);
       // the tile's bias, which the store would otherwise wait for (197 x 1001 x 1992: 1 us)
       if (p.bias && lane * 32 < kCols && n0 + lane * 32 < p.N)
@@ -419,7 +444,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
                                                       lane * 32));
     };
     uint32_t nacc = 0;
-    bool ok = true;
+    bool ok = true, joined = false;          // the parts' sums
     int index = 0, t = cluster_id();
     Tile tl{};
     if (t < tile_count()) {
@@ -476,22 +501,58 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       if (!ok) {
         if (lane == 0) set_status(dev_status, MOE_ERR_TIMEOUT);
         smem_store(abort_flag, 1);
+        if (SPLIT) cluster_store(cluster_addr(abort_flag, (1 - k_part()) * CG + rank), 1);
         break;
       }
       t += cluster_count();
-      if (t < tile_count()) {
+      if (!SPLIT && t < tile_count()) {
         tl = tile_at(++index, t);
         aim(tl);
       }
-      if (rows <= 0 || n0 >= p.N) continue;
-      if (p.bias) {
+      auto add_bias = [&]() {
+        if (!p.bias) return;
         const float* bias = p.bias + int64_t(g) * p.N + n0;
 #pragma unroll
         for (int j = 0; j < kCols / 2; ++j) {
           if (n0 + 2 * j < p.N) acc[j].x = __fadd_rn(acc[j].x, bias[2 * j]);
           if (n0 + 2 * j + 1 < p.N) acc[j].y = __fadd_rn(acc[j].y, bias[2 * j + 1]);
         }
+      };
+      if constexpr (SPLIT) {
+        // Rows 0 .. 63 of a CTA are the first part's to finish, the others the second's: a
+        // thread sends its sums to the other part's, or adds those to its own.
+        const int part = q >> 1;
+        const uint32_t slot =
+            sums + ((((warp - kCtrlWarps) >> 2) * 2 + (q & 1)) * 32 + lane) * 16;
+        constexpr uint32_t kPitch = 32 * (kEpiWarps / 2) * 16;
+        const bool there = rows > 0 && n0 < p.N;
+        if (there && part != k_part()) {
+          const uint32_t to = cluster_addr(slot, part * CG + rank);
+#pragma unroll
+          for (int j = 0; j < kCols / 4; ++j)
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to + j * kPitch),
+                         "f"(acc[2 * j].x), "f"(acc[2 * j].y), "f"(acc[2 * j + 1].x),
+                         "f"(acc[2 * j + 1].y) : "memory");
+        } else if (there) {
+          add_bias();        // (the prefetch does not outlive the barrier: 0.8 us)
+        }
+        cluster_sync();
+        joined = true;
+        if (part != k_part() || smem_load(abort_flag)) break;    // (not all of them came)
+        if (there) {
+#pragma unroll
+          for (int j = 0; j < kCols / 4; ++j) {
+            float4 v;
+            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(slot + j * kPitch)
+                         : "memory");
+            acc[2 * j] = add2_rn(acc[2 * j], make_float2(v.x, v.y));
+            acc[2 * j + 1] = add2_rn(acc[2 * j + 1], make_float2(v.z, v.w));
+          }
+        }
       }
+      if (rows <= 0 || n0 >= p.N) continue;
+      if (!SPLIT) add_bias();
       constexpr int kItem = OUT == MOE_FP32 ? 4 : 2, kVec = 16 / kItem;     // per 16 bytes
       auto piece = [&](int j) {                // columns j .. j + kVec - 1, narrowed
         if constexpr (OUT == MOE_FP32)
@@ -550,7 +611,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
           stage(j, box);
           __syncwarp();
           constexpr int kLanes = kBoxCols * kItem / 4;       // lanes per row, 4 bytes each
-          constexpr int kRows = 32 / kLanes, kBatch = 4;
+          constexpr int kRows = 32 / kLanes, kBatch = 8;
           const int word = lane % kLanes, n = n0 + j + word * (4 / kItem);
           for (int r0 = lane / kLanes; r0 < min(rows, 32); r0 += kBatch * kRows) {
             uint32_t v[kBatch];
@@ -579,6 +640,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       }
       __syncwarp();
     }
+    if (SPLIT && !joined) cluster_sync();      // a timeout, or no tile: the others wait
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
   }
@@ -598,32 +660,34 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
 
 struct Plan {
   int nt;          // channels per tile
+  bool split;      // two pairs for a tile's K
   int clusters;
   bool wide_scales;          // every row's scales start on 16 bytes
 };
 
-template <int NT, int OUT>
+template <int NT, int OUT, bool SPLIT>
 cudaError_t launch_kernel(const Maps& maps, const LinearArgs& p, const Plan& plan,
                           int32_t* dev_status, int optin, cudaStream_t st) {
   using S = Stages<NT>;
   int stages = kMaxStages;
-  while (stages > 2 && S::bytes(stages, 0, p.G) > size_t(optin)) --stages;
+  while (stages > 2 && S::bytes(stages, 0, p.G, SPLIT) > size_t(optin)) --stages;
   // (a table in what the stages leave)
-  const int table = static_cast<int>(std::min<size_t>(
-      kMaxTable, (std::max(size_t(optin), S::bytes(stages, 0, p.G)) -
-                  S::bytes(stages, 0, p.G)) / 16));
-  const size_t smem = S::bytes(stages, table, p.G);
-  auto kernel = linear_f8_tile_kernel<NT, OUT>;
+  const size_t least = S::bytes(stages, 0, p.G, SPLIT);
+  const int table = static_cast<int>(
+      std::min<size_t>(kMaxTable, (std::max(size_t(optin), least) - least) / 16));
+  const size_t smem = S::bytes(stages, table, p.G, SPLIT);
+  auto kernel = linear_f8_tile_kernel<NT, OUT, SPLIT>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
+  const unsigned size = SPLIT ? 2 * CG : CG;       // of a cluster
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters * CG));
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters) * size);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.x = size;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;      // see launch_early
   at[1].val.programmaticStreamSerializationAllowed = 1;
@@ -632,13 +696,13 @@ cudaError_t launch_kernel(const Maps& maps, const LinearArgs& p, const Plan& pla
   return cudaLaunchKernelEx(&cfg, kernel, maps, p, plan.wide_scales, stages, table, dev_status);
 }
 
-template <int NT>
-cudaError_t launch_nt(const Maps& maps, const LinearArgs& p, const Plan& plan,
-                      int32_t* dev_status, int optin, cudaStream_t st) {
+template <int NT, bool SPLIT>
+cudaError_t launch_out(const Maps& maps, const LinearArgs& p, const Plan& plan,
+                       int32_t* dev_status, int optin, cudaStream_t st) {
   switch (p.c_dtype) {
-    case MOE_BF16: return launch_kernel<NT, MOE_BF16>(maps, p, plan, dev_status, optin, st);
-    case MOE_FP16: return launch_kernel<NT, MOE_FP16>(maps, p, plan, dev_status, optin, st);
-    default: return launch_kernel<NT, MOE_FP32>(maps, p, plan, dev_status, optin, st);
+    case MOE_BF16: return launch_kernel<NT, MOE_BF16, SPLIT>(maps, p, plan, dev_status, optin, st);
+    case MOE_FP16: return launch_kernel<NT, MOE_FP16, SPLIT>(maps, p, plan, dev_status, optin, st);
+    default: return launch_kernel<NT, MOE_FP32, SPLIT>(maps, p, plan, dev_status, optin, st);
   }
 }
 
@@ -655,19 +719,45 @@ bool use_few(const LinearArgs& p) {
          (outputs <= (1 << 17) && outputs * p.K <= (1 << 28));
 }
 
-// The widest tile that gives every pair of SMs something to do.
+// The form that is expected to take the least time: rounds of tiles over the pairs of SMs,
+// each of so many clocks a block of K (0.24 us at 128 channels, 0.40 at 256), its start and
+// store as three blocks more.  K in two parts costs 2 us for the exchange and a second pair's
+// start; 36 clusters of four CTAs run at once on 152 SMs (with a 37th 256 x 4736 x 4096 takes
+// 21.7 us).  Measured in us at 128 and 256 channels whole, 64 and 128 in parts:
+//    33 x 4096 x 1024    7.9   8.4     -   8.4      256 x 1024 x 7168   18.3  26.1  13.7  14.7
+//    64 x 4096 x 4096   12.8  16.9     -  11.6      256 x 4096 x 7168   19.3  26.9     -  16.4
+//   512 x 4096 x 7168   20.5  27.2     -     -     1024 x 4096 x 7168   34.2  28.6     -     -
+//  1280 x 4096 x 7168   47.3  50.3     -     -     2048 x 4096 x 7168   62.7  52.5     -     -
+//  16 groups' 2048 rows of 1032 x 1100  13.5  16.8; 200 groups' 6400 of 512 x 512  26.0  24.0.
+// (64 channels whole: 9.9, 18.9, 14.0, 20.3, 32.3, 56.4, 68.2, 94.4, 18.8 and 35.2: more of
+// the clusters read the same rows.)
 Plan make_plan(const LinearArgs& p, int sms) {
-  const int64_t pairs = std::max(1, sms / CG);
-  // at most this many, for any group sizes
-  const int64_t blocks = p.G == 1 ? (p.a_rows + CG * TM - 1) / (CG * TM)
-                                  : p.a_rows / (CG * TM) + std::min<int64_t>(p.G, p.a_rows);
+  const int64_t pairs = std::max(1, sms / CG), fours = sms * 36 / 152, kb = code_blocks(p.K);
+  auto blocks_of = [&](int64_t rows) { return (rows + CG * TM - 1) / (CG * TM); };
+  // at most this many for any group sizes, and with even ones
+  const int64_t most = p.G == 1 ? blocks_of(p.a_rows)
+                                : p.a_rows / (CG * TM) + std::min<int64_t>(p.G, p.a_rows);
+  const int64_t even = std::min<int64_t>(most, p.G * blocks_of((p.a_rows + p.G - 1) / p.G));
+  auto columns = [&](int nt) { return (p.N + nt - 1) / nt; };
   Plan plan{};
-  for (int nt : {256, 128, 64}) {
-    const int64_t tiles = blocks * ((p.N + nt - 1) / nt);
+  int64_t least = INT64_MAX;             // 1/100 us
+  auto take = [&](int nt, bool split, int64_t cost, int64_t clusters) {
+    if (cost >= least) return;
+    least = cost;
     plan.nt = nt;
-    plan.clusters = static_cast<int>(std::min(tiles, pairs));
-    if (tiles >= pairs) break;
+    plan.split = split;
+    plan.clusters = static_cast<int>(clusters);
+  };
+  for (int nt : {128, 256}) {
+    const int64_t rounds = (even * columns(nt) + pairs - 1) / pairs;
+    take(nt, false, 480 + rounds * (kb + 3) * (nt == 128 ? 24 : 40),
+         std::min(most * columns(nt), pairs));
   }
+  const int64_t first = first_blocks(p.K);
+  if (p.G == 1 && kb - first >= kTurn)
+    for (int nt : {64, 128})
+      if (most * columns(nt) <= fours)
+        take(nt, true, 680 + (first + 3) * (nt == 64 ? 22 : 24), most * columns(nt));
   return plan;
 }
 
@@ -699,9 +789,11 @@ cudaError_t launch_linear_f8(const LinearArgs& p, int32_t* dev_status, cudaStrea
   Maps maps;
   e = make_maps(p, &plan, &maps);
   if (e != cudaSuccess) return e;
-  return plan.nt == 256   ? launch_nt<256>(maps, p, plan, dev_status, optin, st)
-         : plan.nt == 128 ? launch_nt<128>(maps, p, plan, dev_status, optin, st)
-                          : launch_nt<64>(maps, p, plan, dev_status, optin, st);
+  if (plan.split)
+    return plan.nt == 128 ? launch_out<128, true>(maps, p, plan, dev_status, optin, st)
+                          : launch_out<64, true>(maps, p, plan, dev_status, optin, st);
+  return plan.nt == 256 ? launch_out<256, false>(maps, p, plan, dev_status, optin, st)
+                        : launch_out<128, false>(maps, p, plan, dev_status, optin, st);
 }
 #endif
 

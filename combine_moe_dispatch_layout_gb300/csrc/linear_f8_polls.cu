@@ -47,7 +47,8 @@ __device__ __forceinline__ bool warp_role_wait4(uint32_t a, uint32_t b, uint32_t
 #include "linear_f8.cu"
 
 // What moe_linear_f8 does with a problem on a GPU of `sms` SMs: plan[0] = channels per
-// tile of the kernel it takes (0: the kernel for few rows), plan[1] = clusters.  Host only.
+// tile of the kernel it takes (0: the kernel for few rows), plan[1] = clusters, plan[2] =
+// pairs that share a tile's K.  Host only.
 extern "C" void moe_test_linear_f8_plan(int64_t a_rows, int32_t G, int32_t N, int32_t K,
                                         int32_t sms, int32_t* plan) {
   moe_ep::LinearArgs p{};
@@ -55,20 +56,21 @@ extern "C" void moe_test_linear_f8_plan(int64_t a_rows, int32_t G, int32_t N, in
   p.G = G;
   p.N = N;
   p.K = K;
-  plan[0] = plan[1] = 0;
+  plan[0] = plan[1] = plan[2] = 0;
   if (moe_ep::use_few(p)) return;
   const moe_ep::Plan best = moe_ep::make_plan(p, sms);
   plan[0] = best.nt;
   plan[1] = best.clusters;
+  plan[2] = best.split ? 2 : 1;
 }
 
-// moe_linear_f8's tile kernel of nt channels with fp32 results and roles that wait for at
-// most `polls` looks at a barrier (other arguments as there; the caller keeps the limits).
+// moe_linear_f8's tile kernel with fp32 results and roles that wait for at most `polls`
+// looks at a barrier (arguments as there; the caller keeps the limits).
 extern "C" moe_status moe_test_linear_f8_polls(const void* a, int64_t a_rows, int64_t a_stride,
                                                const void* w, int64_t w_stride, int32_t G,
                                                int32_t N, int32_t K, const int32_t* group_rows,
                                                const float* w_scale, const void* a_scale,
-                                               int64_t a_scale_stride, float* c, int32_t nt,
+                                               int64_t a_scale_stride, float* c,
                                                uint32_t polls, int32_t* dev_status,
                                                void* stream) {
   using namespace moe_ep;
@@ -85,12 +87,14 @@ extern "C" moe_status moe_test_linear_f8_polls(const void* a, int64_t a_rows, in
     e = cudaMemcpyToSymbolAsync(c_first, &from, sizeof(from), 0, cudaMemcpyHostToDevice, st);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   Plan plan = make_plan(p, sms);
-  plan.nt = nt;
   Maps maps;
   e = make_maps(p, &plan, &maps);
   if (e == cudaSuccess)
-    e = nt == 256   ? launch_kernel<256, MOE_FP32>(maps, p, plan, dev_status, optin, st)
-        : nt == 128 ? launch_kernel<128, MOE_FP32>(maps, p, plan, dev_status, optin, st)
-                    : launch_kernel<64, MOE_FP32>(maps, p, plan, dev_status, optin, st);
+    e = plan.split
+            ? (plan.nt == 128
+                   ? launch_kernel<128, MOE_FP32, true>(maps, p, plan, dev_status, optin, st)
+                   : launch_kernel<64, MOE_FP32, true>(maps, p, plan, dev_status, optin, st))
+        : plan.nt == 256 ? launch_kernel<256, MOE_FP32, false>(maps, p, plan, dev_status, optin, st)
+                         : launch_kernel<128, MOE_FP32, false>(maps, p, plan, dev_status, optin, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

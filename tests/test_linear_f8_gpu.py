@@ -171,6 +171,52 @@ def test_bad_counts(ep, sizes):
     p.check()
 
 
+# sizes whose K two pairs of SMs share: whole tiles, a tile that ends in either half of either
+# SM's rows, groups of fewer rows than the buffer (and clusters without a tile), uneven parts
+@pytest.mark.parametrize("rows,extra,N,K", [
+    (256, 0, 1024, 2048), (30, 226, 1000, 3000), (70, 0, 1500, 3500), (130, 0, 4096, 4000),
+    (200, 312, 1032, 2600), (17, 1, 4600, 4500), (321, 0, 72, 16000), (512, 0, 2304, 7168)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_parts_of_k(ep, rows, extra, N, K, dtype):
+    for bias, images in ((False, True), (True, False)):
+        p = Problem(ep, [rows], N, K, dtype, bias=bias, images=images, extra=extra)
+        p.run()
+        p.check()
+
+
+def test_parts_of_k_and_bad_counts(ep):
+    for rows, N, K in ((300, 1000, 2000), (40, 4096, 3500)):
+        p = Problem(ep, [rows], N, K, extra=20)
+        for count, status in ((rows + 21, ep.MOE_ERR_CAPACITY), (-1, ep.MOE_ERR_INVALID_ARG), (0, 0)):
+            p.group_rows[0] = count
+            p.st.zero_()
+            p.run()
+            torch.cuda.synchronize()
+            assert int(p.st.item()) == status
+            assert bool((p.c.contiguous().view(torch.uint8) == 0xA5).all())
+        p.group_rows[0] = rows
+        p.st.zero_()
+        p.run()
+        p.check()
+
+
+def test_parts_of_k_and_codes_that_are_no_numbers(ep):
+    """In either part, of either half of the rows."""
+    rows, N, K = 256, 1024, 2048
+    for row, col, k in ((3, 7, 5), (100, 600, 2000), (200, 1023, 1023), (255, 64, 1024)):
+        p, clean = Problem(ep, [rows], N, K), Problem(ep, [rows], N, K)
+        p.a[row, k] = 0x7F
+        p.w[0, col, k] = 0xFF
+        clean.run()
+        p.run()
+        torch.cuda.synchronize()
+        assert bool(p.c[row].isnan().all()) and bool(p.c[:, col].isnan().all())
+        keep = torch.ones_like(p.c, dtype=torch.bool)
+        keep[row] = False
+        keep[:, col] = False
+        assert torch.equal(p.c[keep], clean.c[keep])
+
+
 def test_the_same_bits_every_time(ep):
     for sizes, N, K in (([1], 4096, 7168), ([3] * 30, 512, 2048), ([500], 1000, 4096),
                         ([90, 300, 7], 700, 1500)):
@@ -216,7 +262,7 @@ def test_far_weights(ep):
 @pytest.mark.parametrize("sizes,N,K,calls", [
     ([1], 4096, 4096, 200), ([5, 0, 3, 8], 512, 4096, 200), ([600], 1000, 4096, 200),
     ([24576], 64, 2048, 200), ([700, 0, 2500, 130, 1000, 300], 500, 2992, 200),
-    ([197], 1001, 1992, 200), ([90] * 12, 700, 2100, 200)],
+    ([197], 1001, 1992, 200), ([90] * 12, 700, 2100, 200), ([100], 4096, 4096, 200)],
     ids=lambda v: str(v).replace(" ", "")[:30])
 def test_rows_written_just_before(ep, sizes, N, K, calls):
     """Operands that arrive late and out of order: rows written just before by a copy,

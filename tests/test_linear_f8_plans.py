@@ -18,14 +18,17 @@ import plain_f8 as P
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PKG = os.path.join(ROOT, "combine_moe_dispatch_layout_gb300")
 SMS = 152
-PLANS = {  # channels per tile: sizes, N, K
-    256: [((24576,), 72, 700), ((5000,), 1000, 1300), ((100, 900, 0, 1200, 300, 1, 400, 99) * 4,
-                                                      1032, 1100)],
-    128: [((3000,), 800, 1000), ((600, 0, 300, 256, 1), 2000, 500)],
-    64: [((300,), 1000, 2000), ((40,), 4096, 1500), ((60, 2, 90), 1032, 4000)],
-    0: [((1,), 4096, 7168), ((16,), 7168, 512), ((6,) * 40, 512, 512), ((256,), 512, 1024)],
+PLANS = {  # channels per tile, pairs that share a tile: sizes, N, K
+    (256, 1): [((3000,), 800, 1000), ((8192,), 1000, 1000), ((5, 0, 1157, 40, 1), 2000, 500),
+               ((100, 900, 0, 1200, 300, 1, 400, 99) * 4, 1275, 1100)],
+    (128, 1): [((24576,), 72, 700), ((5000,), 1000, 1300), ((300,), 1000, 1025),
+               ((130, 126, 0, 256) * 4, 1032, 1100), ((60, 2, 90), 1032, 4000)],
+    (128, 2): [((40,), 4096, 3500), ((700,), 1001, 3073), ((256,), 4601, 7168)],
+    (64, 2): [((300,), 1000, 2000), ((197,), 1001, 1992), ((256,), 72, 16384)],
+    (0, 0): [((1,), 4096, 7168), ((16,), 7168, 512), ((6,) * 40, 512, 512),
+             ((256,), 512, 1024)],
 }
-TILES = [(nt, *s) for nt, some in PLANS.items() if nt for s in some]
+TILES = [s for form, some in PLANS.items() if form[0] for s in some]
 
 
 def _ids(v):
@@ -44,12 +47,12 @@ def test_the_shapes_take_every_form():
     i32 = ctypes.c_int32
     fn.argtypes = [ctypes.c_int64, i32, i32, i32, i32, ctypes.c_void_p]
     fn.restype = None
-    for nt, shapes in PLANS.items():
+    for form, shapes in PLANS.items():
         for sizes, N, K in shapes:
-            plan = (i32 * 2)()
+            plan = (i32 * 3)()
             fn(sum(sizes), len(sizes), N, K, SMS, plan)
-            assert plan[0] == nt, (sizes, N, K, tuple(plan))
-            assert 2 * plan[1] <= SMS
+            assert (plan[0], plan[2]) == form, (sizes, N, K, tuple(plan))
+            assert 2 * plan[1] * plan[2] <= SMS
 
 
 def test_registers_cover_the_split():
@@ -64,7 +67,7 @@ def test_registers_cover_the_split():
     epi, ctrl = constant("kEpiWarps"), constant("kCtrlWarps")
     threads = 32 * (epi + ctrl)
     split = 32 * (epi * constant("kEpiRegs") + ctrl * constant("kCtrlRegs"))
-    for unit, kernels in (("linear_f8", 9), ("linear_f8_polls", 3)):
+    for unit, kernels in (("linear_f8", 12), ("linear_f8_polls", 4)):
         report = open(os.path.join(PKG, "_build", unit + ".ptxas.txt")).read()
         used = [int(m) for m in re.findall(r"linear_f8_tile_kernel.*?Used (\d+) registers", report,
                                            re.S)]
@@ -80,7 +83,7 @@ def ep():
     import combine_moe_dispatch_layout_gb300 as ep
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     fn = ep.lib().moe_test_linear_f8_polls
-    fn.argtypes = [vp, i64, i64, vp, i64, i32, i32, i32, vp, vp, vp, i64, vp, i32,
+    fn.argtypes = [vp, i64, i64, vp, i64, i32, i32, i32, vp, vp, vp, i64, vp,
                    ctypes.c_uint32, vp, vp]
     fn.restype = ctypes.c_int
     return ep
@@ -122,32 +125,32 @@ class Problem:
         assert bool(((got - want).abs() <= P.linear_bound(want, mag, self.K,
                                                           torch.float32)).all())
 
-    def hook(self, nt, polls):
+    def hook(self, polls):
         a, w, s = self.a, self.w, self.scale
         return self.ep.lib().moe_test_linear_f8_polls(
             a.data_ptr(), a.shape[0], a.shape[1], w.data_ptr(), w.shape[2], len(self.sizes),
             self.N, self.K, self.counts.data_ptr(), self.w_scale.data_ptr(), s.data_ptr(),
-            4 * s.shape[1], self.c.data_ptr(), nt, polls, self.st.data_ptr(),
+            4 * s.shape[1], self.c.data_ptr(), polls, self.st.data_ptr(),
             torch.cuda.current_stream().cuda_stream)
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("nt,sizes,N,K", TILES, ids=_ids)
-def test_every_form(ep, nt, sizes, N, K):
+@pytest.mark.parametrize("sizes,N,K", TILES, ids=_ids)
+def test_every_form(ep, sizes, N, K):
     Problem(ep, sizes, N, K).check()
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("nt,sizes,N,K", TILES, ids=_ids)
+@pytest.mark.parametrize("sizes,N,K", TILES, ids=_ids)
 @pytest.mark.parametrize("polls", [1, 3, 30, 300, 3000])
-def test_waits_that_run_out(ep, nt, sizes, N, K, polls):
+def test_waits_that_run_out(ep, sizes, N, K, polls):
     p = Problem(ep, sizes, N, K)
     want = p.run()
     ended = 0
     for _ in range(3):
         p.raw.fill_(-7.0)
         p.st.zero_()
-        assert p.hook(nt, polls) == 0
+        assert p.hook(polls) == 0
         torch.cuda.synchronize()
         status = int(p.st.item())
         assert status in (0, ep.MOE_ERR_TIMEOUT)
