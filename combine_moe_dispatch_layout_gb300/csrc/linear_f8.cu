@@ -34,11 +34,11 @@
 // Looped for longer than 20 ms the board is at its power limit and lowers the clock, so
 // energy counts more than clocks: 166 us in bursts, 183 to 188 looped (a library product
 // without block scales 127 and 144).  Measured beside it: 32,768 x 7168 x 2048 in 32 uneven
-// groups 413 us, 1024 x 4096 x 4096 22.4, 8192 rows over 256 groups of 4096 x 7168 1425 to
-// 1530, 197 x 1001 x 1992 in fp32 10.8.  Slower for the first: four accumulators of 128
-// columns (the products read the token rows twice: 210), 16 draining warps (178), TMEM loads
-// of 4, 16 or 32 columns (198, 169, 210; of 8 here), scalar multiply-adds (215), single CTAs
-// instead of pairs (as many clocks, 3% more energy).
+// groups 413 us, 1024 x 4096 x 4096 19.5, 256 x 4096 x 7168 16.0, 8192 rows over 256 groups
+// of 4096 x 7168 1425 to 1530, 197 x 1001 x 1992 in fp32 10.6.  Slower for the first: four
+// accumulators of 128 columns (the products read the token rows twice: 210), 16 draining
+// warps (178), TMEM loads of 4, 16 or 32 columns (198, 169, 210; of 8 here), scalar
+// multiply-adds (215), single CTAs instead of pairs (as many clocks, 3% more energy).
 #include <cuda.h>
 
 #include <algorithm>
@@ -707,30 +707,41 @@ cudaError_t launch_out(const Maps& maps, const LinearArgs& p, const Plan& plan,
 }
 
 // Whether the kernel that streams weights to the warps' own products is the faster one.
-// A few rows of a plain product: 16 rows of 4096 x 7168 take 14.3 us there and 24.4 here,
-// 64 rows 45 and 21.  A few per group on average: with 4, 64 groups of 4096 x 7168 take 299
-// and 322 us, 200 of 2048 x 512 58 and 74; with 6 335 and 334; with 8 389 and 336, 86 and
-// 76.  Small products, where this kernel's start (barriers, TMEM, clusters) is most of its
-// time: 256 x 512 x 512 4.8 and 6.3, 64 x 2048 x 2048 (at both limits) 9.1 and 10.1, 64 x
-// 7168 x 256 (past the first) 10.1 and 7.0.
+// A few rows of a plain product: up to 8 a weight byte meets one instruction (8 rows of 4096 x
+// 7168 take 8.0 us there and 18.6 here), up to 16 two, which bound it (16 rows of 4096 x 7168
+// 14.4 and 15 to 19, of 16,384 x 4096 29.9 and 21.4; 20 rows 23.9 and 15.1).  A few per group
+// on average: with 6, 40 groups of 512 x 512 7.5 and 11.0, 40 of 2048 x 2048 41.6 and 42.6,
+// 64 of 4096 x 7168 334 and 324; with 10, 8 of 4096 x 4096 57.2 and 34.4.  Small products,
+// where this kernel's start (barriers, TMEM, clusters) is most of its time: 256 x 512 x 512
+// 4.8 and 5.8, 128 x 1024 x 2048 (at both limits) 9.1 and 9.2, 64 x 7168 x 256 (past the
+// first) 10.1 and 7.0.
 bool use_few(const LinearArgs& p) {
   const int64_t outputs = p.a_rows * p.N;
-  return p.a_rows <= (p.G == 1 ? 16 : 6 * int64_t(p.G)) ||
-         (outputs <= (1 << 17) && outputs * p.K <= (1 << 28));
+  const int64_t rows = p.G > 1 ? 6 * int64_t(p.G) : int64_t(p.N) * p.K <= 1 << 25 ? 16 : 8;
+  return p.a_rows <= rows || (outputs <= (1 << 17) && outputs * p.K <= (1 << 28));
 }
 
 // The form that is expected to take the least time: rounds of tiles over the pairs of SMs,
-// each of so many clocks a block of K (0.24 us at 128 channels, 0.40 at 256), its start and
-// store as three blocks more.  K in two parts costs 2 us for the exchange and a second pair's
-// start; 36 clusters of four CTAs run at once on 152 SMs (with a 37th 256 x 4736 x 4096 takes
-// 21.7 us).  Measured in us at 128 and 256 channels whole, 64 and 128 in parts:
-//    33 x 4096 x 1024    7.9   8.4     -   8.4      256 x 1024 x 7168   18.3  26.1  13.7  14.7
-//    64 x 4096 x 4096   12.8  16.9     -  11.6      256 x 4096 x 7168   19.3  26.9     -  16.4
-//   512 x 4096 x 7168   20.5  27.2     -     -     1024 x 4096 x 7168   34.2  28.6     -     -
-//  1280 x 4096 x 7168   47.3  50.3     -     -     2048 x 4096 x 7168   62.7  52.5     -     -
-//  16 groups' 2048 rows of 1032 x 1100  13.5  16.8; 200 groups' 6400 of 512 x 512  26.0  24.0.
-// (64 channels whole: 9.9, 18.9, 14.0, 20.3, 32.3, 56.4, 68.2, 94.4, 18.8 and 35.2: more of
-// the clusters read the same rows.)
+// each of so much a block of K (0.26, 0.24 and 0.40 us at 64, 128 and 256 channels) with its
+// start as three blocks more, and the store, which is long where it is not by tensor copies of
+// 16-bit values.  K in two parts costs 2 us for the exchange and a second pair's start; 36
+// clusters of four CTAs run at once on 152 SMs (with a 37th 256 x 4736 x 4096 takes
+// 21.7 us).  Measured in us at 64, 128 and 256 channels whole, 64 and 128 in parts:
+//   bf16    33 x 4096 x 1024    9.9   7.9   8.4     -   8.4
+//           64 x 4096 x 4096   14.0  12.8  16.9     -  11.6
+//          256 x 1024 x 7168   18.9  18.3  26.1  13.7  14.7
+//          256 x 4096 x 7168   20.3  19.3  26.9     -  16.4
+//          512 x 4096 x 7168   32.3  20.5  27.2     -     -
+//         1024 x 4096 x 7168   56.4  34.2  28.6     -     -
+//         1280 x 4096 x 7168   68.2  47.3  50.3     -     -
+//         2048 x 4096 x 7168   94.4  62.7  52.5     -     -
+//         2048 rows in 16 groups of 1032 x 1100       18.8  13.5  16.8
+//         6400 rows in 200 groups of 512 x 512        35.2  26.0  24.0
+//          129 x 1500 x  700    7.5   9.0  12.6     -     -
+//   fp32   300 x 1000 x 1025    8.9   9.7  13.3     -     -
+//          197 x 1001 x 1992   10.6  12.5     -  10.6  13.1
+//          512 x 4096 x 4096   22.1  16.9  23.2     -     -
+//         4096 x 4096 x 4096    113  77.4  81.7     -     -
 Plan make_plan(const LinearArgs& p, int sms) {
   const int64_t pairs = std::max(1, sms / CG), fours = sms * 36 / 152, kb = code_blocks(p.K);
   auto blocks_of = [&](int64_t rows) { return (rows + CG * TM - 1) / (CG * TM); };
@@ -738,7 +749,7 @@ Plan make_plan(const LinearArgs& p, int sms) {
   const int64_t most = p.G == 1 ? blocks_of(p.a_rows)
                                 : p.a_rows / (CG * TM) + std::min<int64_t>(p.G, p.a_rows);
   const int64_t even = std::min<int64_t>(most, p.G * blocks_of((p.a_rows + p.G - 1) / p.G));
-  auto columns = [&](int nt) { return (p.N + nt - 1) / nt; };
+  const bool long_store = p.c_dtype == MOE_FP32 || p.N % 8 != 0;
   Plan plan{};
   int64_t least = INT64_MAX;             // 1/100 us
   auto take = [&](int nt, bool split, int64_t cost, int64_t clusters) {
@@ -748,16 +759,17 @@ Plan make_plan(const LinearArgs& p, int sms) {
     plan.split = split;
     plan.clusters = static_cast<int>(clusters);
   };
-  for (int nt : {128, 256}) {
-    const int64_t rounds = (even * columns(nt) + pairs - 1) / pairs;
-    take(nt, false, 480 + rounds * (kb + 3) * (nt == 128 ? 24 : 40),
-         std::min(most * columns(nt), pairs));
+  for (int nt : {128, 256, 64}) {
+    const int64_t columns = (p.N + nt - 1) / nt, first = first_blocks(p.K);
+    const int64_t block = nt == 256 ? 40 : nt == 128 ? 24 : 26;
+    const int64_t store = !long_store ? 0 : nt == 256 ? 450 : nt == 128 ? 200 : 60;
+    const int64_t joined = !long_store ? 0 : nt == 128 ? 200 : 130;       // by half the warps
+    const int64_t rounds = (even * columns + pairs - 1) / pairs;
+    take(nt, false, (nt == 64 ? 570 : 480) + rounds * ((kb + 3) * block + store),
+         std::min(most * columns, pairs));
+    if (nt <= 128 && p.G == 1 && kb - first >= kTurn && most * columns <= fours)
+      take(nt, true, (nt == 64 ? 650 : 680) + (first + 3) * 24 + joined, most * columns);
   }
-  const int64_t first = first_blocks(p.K);
-  if (p.G == 1 && kb - first >= kTurn)
-    for (int nt : {64, 128})
-      if (most * columns(nt) <= fours)
-        take(nt, true, 680 + (first + 3) * (nt == 64 ? 22 : 24), most * columns(nt));
   return plan;
 }
 
@@ -792,8 +804,9 @@ cudaError_t launch_linear_f8(const LinearArgs& p, int32_t* dev_status, cudaStrea
   if (plan.split)
     return plan.nt == 128 ? launch_out<128, true>(maps, p, plan, dev_status, optin, st)
                           : launch_out<64, true>(maps, p, plan, dev_status, optin, st);
-  return plan.nt == 256 ? launch_out<256, false>(maps, p, plan, dev_status, optin, st)
-                        : launch_out<128, false>(maps, p, plan, dev_status, optin, st);
+  return plan.nt == 256   ? launch_out<256, false>(maps, p, plan, dev_status, optin, st)
+         : plan.nt == 128 ? launch_out<128, false>(maps, p, plan, dev_status, optin, st)
+                          : launch_out<64, false>(maps, p, plan, dev_status, optin, st);
 }
 #endif
 

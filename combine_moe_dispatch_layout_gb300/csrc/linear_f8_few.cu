@@ -39,7 +39,9 @@ constexpr int kChannels = 16;        // weight rows per warp
 constexpr int kStep = 256;           // codes of K per step: two blocks
 constexpr int kDepth = 3;            // steps in a warp's ring
 constexpr uint32_t kStepBytes = kChannels * kStep;
-__host__ __device__ constexpr size_t ring_bytes(int warps) { return size_t(warps) * kDepth * kStepBytes; }
+__host__ __device__ constexpr size_t ring_bytes(int warps) {
+  return size_t(warps) * kDepth * kStepBytes;
+}
 
 __device__ __forceinline__ void mma_f8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                        uint32_t a3, uint32_t b0, uint32_t b1) {

@@ -46,7 +46,7 @@ __device__ __forceinline__ bool warp_role_wait4(uint32_t a, uint32_t b, uint32_t
 #define MOE_LINEAR_F8_POLLS
 #include "linear_f8.cu"
 
-// What moe_linear_f8 does with a problem on a GPU of `sms` SMs: plan[0] = channels per
+// What moe_linear_f8 does with a problem (c in fp32) on a GPU of `sms` SMs: plan[0] = channels per
 // tile of the kernel it takes (0: the kernel for few rows), plan[1] = clusters, plan[2] =
 // pairs that share a tile's K.  Host only.
 extern "C" void moe_test_linear_f8_plan(int64_t a_rows, int32_t G, int32_t N, int32_t K,
@@ -56,6 +56,7 @@ extern "C" void moe_test_linear_f8_plan(int64_t a_rows, int32_t G, int32_t N, in
   p.G = G;
   p.N = N;
   p.K = K;
+  p.c_dtype = MOE_FP32;
   plan[0] = plan[1] = plan[2] = 0;
   if (moe_ep::use_few(p)) return;
   const moe_ep::Plan best = moe_ep::make_plan(p, sms);
@@ -90,11 +91,14 @@ extern "C" moe_status moe_test_linear_f8_polls(const void* a, int64_t a_rows, in
   Maps maps;
   e = make_maps(p, &plan, &maps);
   if (e == cudaSuccess)
-    e = plan.split
-            ? (plan.nt == 128
-                   ? launch_kernel<128, MOE_FP32, true>(maps, p, plan, dev_status, optin, st)
-                   : launch_kernel<64, MOE_FP32, true>(maps, p, plan, dev_status, optin, st))
-        : plan.nt == 256 ? launch_kernel<256, MOE_FP32, false>(maps, p, plan, dev_status, optin, st)
-                         : launch_kernel<128, MOE_FP32, false>(maps, p, plan, dev_status, optin, st);
+    e = plan.split && plan.nt == 64
+            ? launch_kernel<64, MOE_FP32, true>(maps, p, plan, dev_status, optin, st)
+        : plan.split
+            ? launch_kernel<128, MOE_FP32, true>(maps, p, plan, dev_status, optin, st)
+        : plan.nt == 64
+            ? launch_kernel<64, MOE_FP32, false>(maps, p, plan, dev_status, optin, st)
+        : plan.nt == 128
+            ? launch_kernel<128, MOE_FP32, false>(maps, p, plan, dev_status, optin, st)
+            : launch_kernel<256, MOE_FP32, false>(maps, p, plan, dev_status, optin, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

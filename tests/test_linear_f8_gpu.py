@@ -187,7 +187,8 @@ def test_parts_of_k(ep, rows, extra, N, K, dtype):
 def test_parts_of_k_and_bad_counts(ep):
     for rows, N, K in ((300, 1000, 2000), (40, 4096, 3500)):
         p = Problem(ep, [rows], N, K, extra=20)
-        for count, status in ((rows + 21, ep.MOE_ERR_CAPACITY), (-1, ep.MOE_ERR_INVALID_ARG), (0, 0)):
+        for count, status in ((rows + 21, ep.MOE_ERR_CAPACITY), (-1, ep.MOE_ERR_INVALID_ARG),
+                              (0, 0)):
             p.group_rows[0] = count
             p.st.zero_()
             p.run()
