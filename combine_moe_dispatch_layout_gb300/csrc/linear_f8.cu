@@ -20,7 +20,8 @@
 //            block, into the TMEM accumulators in turn (two for 256 channels); of its
 //            second CTA: tells the first which of its stages have landed
 //   8 warps  drain a block's sums, scale and add them, and store the tile
-// Where there are few tiles a cluster of two pairs splits K: each pair sends its sums of one
+// (kPair.)  Groups of few rows are taken by CTAs by themselves, 128 tokens x 256 channels
+// (kSingle).  Where there are few tiles a cluster of two pairs splits K (kHalves): each pair sends its sums of one
 // half of a CTA's rows to the other one's shared memory, adds what it gets to its own sums of
 // the other half, and stores those.
 // Every wait is bounded: a timeout sets MOE_ERR_TIMEOUT, the CTA stops issuing work and
@@ -70,7 +71,10 @@ __device__ __forceinline__ bool warp_role_wait4(uint32_t a, uint32_t b, uint32_t
 
 namespace {
 
-constexpr int CG = 2;                // CTAs per tile (a pair)
+enum Form { kPair, kHalves, kSingle };       // two CTAs to a tile, two pairs, one CTA
+__host__ __device__ constexpr int ctas_of(int form) {        // that multiply together
+  return form == kSingle ? 1 : 2;
+}
 constexpr int TM = 128;              // tokens per CTA
 constexpr int BK = kCodeBlock;       // codes per stage: one 128-byte row
 constexpr int kRasterTokens = 8;     // token blocks per raster band (weights reused from L2)
@@ -84,7 +88,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kTurn = 4;             // blocks per turn of a draining thread, see load_scales
 constexpr int kMaxStages = 10;
 constexpr uint32_t kBoxBytes = 32 * 128;             // a warp's 32 rows of 128 output bytes
-constexpr uint32_t kOutBytes = kEpiWarps * 2 * kBoxBytes;
+// (a CTA by itself has the second box's memory for another stage)
+__host__ __device__ constexpr int boxes_of(int form) { return form == kSingle ? 1 : 2; }
 constexpr int kMaxTable = 64;                        // a cluster's first tiles, decoded ahead
 
 struct Maps {
@@ -92,17 +97,18 @@ struct Maps {
 };
 
 // NT: channels per tile.
-template <int NT>
+template <int NT, int FORM>
 struct Stages {
   // Accumulators: what TMEM holds.  (A block's way from its products' commit to the drain
   // and back takes some 800 clocks, four times as long as a narrow tile's products.)
   static constexpr int kAccs = kTmemCols / NT;
-  static constexpr uint32_t kBytes = (TM + NT / CG) * BK;
+  static constexpr uint32_t kBytes = (TM + NT / ctas_of(FORM)) * BK;
+  static constexpr uint32_t kOutBytes = kEpiWarps * boxes_of(FORM) * kBoxBytes;
   static constexpr uint32_t kBarBytes = 464;
   // the other pair's sums of half the rows
-  static constexpr uint32_t kSumBytes = TM / 2 * NT * 4;
-  static size_t bytes(int stages, int table, int G, bool split) {
-    return 1024 + size_t(stages) * kBytes + kOutBytes + (split ? kSumBytes : 0) + kBarBytes +
+  static constexpr uint32_t kSumBytes = FORM == kHalves ? TM / 2 * NT * 4 : 0;
+  static size_t bytes(int stages, int table, int G) {
+    return 1024 + size_t(stages) * kBytes + kOutBytes + kSumBytes + kBarBytes +
            size_t(table) * 16 + size_t(G + 1) * 8;
   }
 };
@@ -111,11 +117,12 @@ struct Tile {
   int g;           // group
   int n0;          // first output channel
   int row0;        // first token row
-  int rows;        // tokens of the group from there on, at most CG * TM
+  int rows;        // tokens of the group from there on, at most a tile's
 };
 
-template <int NT>
+template <int NT, int FORM>
 __device__ __forceinline__ Tile decode_tile(int t, uint32_t goff, uint32_t tpre, int G, int ntn) {
+  constexpr int CG = ctas_of(FORM);
   const int lo = group_of_tile(t, tpre, G);
   const int off = smem_load(goff + 4 * lo);
   const int cnt = smem_load(goff + 4 * lo + 4) - off;
@@ -152,20 +159,21 @@ __host__ __device__ __forceinline__ int first_blocks(int K) {
   return static_cast<int>(align_up((code_blocks(K) + 1) / 2, kTurn));
 }
 
-// SPLIT: two pairs to a cluster, which takes one tile.
-template <int NT, int OUT, bool SPLIT>
+template <int NT, int OUT, int FORM>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, bool wide_scales,
                       int stages, int entries, int32_t* dev_status) {
-  using St = Stages<NT>;
+  using St = Stages<NT, FORM>;
+  constexpr int CG = ctas_of(FORM);
+  constexpr bool SPLIT = FORM == kHalves;      // two pairs to a cluster, which takes one tile
   constexpr int kCols = NT / (kEpiWarps / 4);          // columns per draining thread
   constexpr int kAccs = St::kAccs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
-  const uint32_t outs = sbase + stages * St::kBytes, sums = outs + kOutBytes;
-  const uint32_t bars = sums + (SPLIT ? St::kSumBytes : 0);
+  const uint32_t outs = sbase + stages * St::kBytes, sums = outs + St::kOutBytes;
+  const uint32_t bars = sums + St::kSumBytes;
   // A stage's token rows (0) and weight rows (1) of this CTA landed: a barrier for each warp
   // that copies, which after a timeout waits for its own copies whatever the other has done.
   auto full = [&](int of, int s) { return bars + 8 * (of * kMaxStages + s); };
@@ -226,13 +234,14 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   }
   if (warp == 1) {
     __syncwarp();
-    pair_tmem_alloc(tmem_slot, kTmemCols);
+    if constexpr (CG == 2) pair_tmem_alloc(tmem_slot, kTmemCols);
+    else tmem_alloc(tmem_slot, kTmemCols);
   }
   __syncthreads();
   if (tid >= kThreads - entries) {
     const int i = tid - (kThreads - entries), t = cluster_id() + i * cluster_count();
     if (t < smem_load(tpre + 4 * p.G)) {
-      const Tile tl = decode_tile<NT>(t, goff, tpre, p.G, ntn);
+      const Tile tl = decode_tile<NT, FORM>(t, goff, tpre, p.G, ntn);
       smem_store(table + i * 16, tl.g);
       smem_store(table + i * 16 + 4, tl.n0);
       smem_store(table + i * 16 + 8, tl.row0);
@@ -251,7 +260,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   // The cluster's i-th tile, t = cluster_id() + i * cluster_count().  (The search for its
   // group and the divisions took some 400 clocks at the start of every tile.)
   auto tile_at = [&](int i, int t) {
-    if (i >= entries) return decode_tile<NT>(t, goff, tpre, p.G, ntn);
+    if (i >= entries) return decode_tile<NT, FORM>(t, goff, tpre, p.G, ntn);
     Tile tl;
     asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(tl.g), "=r"(tl.n0), "=r"(tl.row0), "=r"(tl.rows)
@@ -317,7 +326,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       for (uint32_t i = nload > ns ? nload - ns : 0; issue && i < nload; ++i)
         bar_wait(full(of, i % ns), (i / ns) & 1u);
       cluster_wait_all();
-    } else if (warp == 1 && rank == 1) {
+    } else if (CG == 2 && warp == 1 && rank == 1) {
       // ---- which stages of this CTA have landed ---------------------------------------
       cluster_wait_all();
       int s = 0;
@@ -351,7 +360,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
           const uint32_t b = nacc % kAccs;
-          if (!warp_role_wait4(full(0, s), full(1, s), peer(s), phase, tempty(b),
+          if (!warp_role_wait4(full(0, s), full(1, s), CG == 2 ? peer(s) : full(1, s), phase, tempty(b),
                                ((nacc / kAccs) & 1u) ^ 1u)) {
             ok = false;
             break;
@@ -362,10 +371,17 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
             const uint64_t da = operand_desc(st), db = operand_desc(st + TM * BK);
             const uint32_t d = tmem + b * NT;
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)     // + 32 bytes along K per step
-              pair_mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk != 0);
-            pair_commit(tfull(b), uint16_t(3 << pair_leader()));
-            pair_commit(empty(s), uint16_t(3 << pair_leader()));
+            for (int kk = 0; kk < BK / 32; ++kk) {   // + 32 bytes along K per step
+              if constexpr (CG == 2) pair_mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk != 0);
+              else mma_f8(d, da + 2 * kk, db + 2 * kk, idesc, kk != 0);
+            }
+            if constexpr (CG == 2) {
+              pair_commit(tfull(b), uint16_t(3 << pair_leader()));
+              pair_commit(empty(s), uint16_t(3 << pair_leader()));
+            } else {
+              mma_commit(tfull(b));
+              mma_commit(empty(s));
+            }
           }
           ++nacc;
           if (++s == stages) { s = 0; phase ^= 1u; }
@@ -380,9 +396,11 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       // there were; it waits for them after the closing barrier
       if (issue) {
         await_commits(nacc, nacc);
-        const uint32_t to = cluster_addr(issued, pair_leader() + 1);
-        cluster_store(to, nacc);
-        cluster_store(to + 4, nacc);
+        if constexpr (CG == 2) {
+          const uint32_t to = cluster_addr(issued, pair_leader() + 1);
+          cluster_store(to, nacc);
+          cluster_store(to + 4, nacc);
+        }
       }
     } else {
       cluster_wait_all();
@@ -397,7 +415,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
     const int col0 = ((warp - kCtrlWarps) >> 2) * kCols;
     const uint32_t base = smem_load(tmem_slot) + (uint32_t(q * 32) << 16) + col0;
     const uint32_t drained = cluster_addr(tempty(0), pair_leader());
-    const uint32_t box = outs + (warp - kCtrlWarps) * 2 * kBoxBytes;
+    constexpr int kWarpBoxes = boxes_of(FORM);
+    const uint32_t box = outs + (warp - kCtrlWarps) * kWarpBoxes * kBoxBytes;
     const int nblocks = code_blocks(p.N);
     cluster_wait_all();
     // What the drain of a tile needs: its scales' places, and those of its first turn.
@@ -582,8 +601,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
         if (kBoxCols * kItem == 128 && rows >= 32) {       // whole rows: out by tensor copies
 #pragma unroll
           for (int j = 0; j < kCols; j += kBoxCols) {
-            const uint32_t at = box + (j / kBoxCols % 2) * kBoxBytes;
-            if (lane == 0) bulk_wait_read<kBoxes == 1 ? 0 : 1>();    // this buffer's last copy
+            const uint32_t at = box + (j / kBoxCols % kWarpBoxes) * kBoxBytes;
+            if (lane == 0) bulk_wait_read<kBoxes == 1 || kWarpBoxes == 1 ? 0 : 1>();    // this buffer's last copy
             __syncwarp();
             stage(j, at);
             fence_proxy_async_smem();
@@ -654,32 +673,33 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
     await_commits(smem_load(issued), smem_load(issued + 4));
     __syncwarp();
     tc_fence_after();
-    pair_tmem_free(smem_load(tmem_slot), kTmemCols);
+    if constexpr (CG == 2) pair_tmem_free(smem_load(tmem_slot), kTmemCols);
+    else tmem_free(smem_load(tmem_slot), kTmemCols);
   }
 }
 
 struct Plan {
   int nt;          // channels per tile
-  bool split;      // two pairs for a tile's K
+  Form form;
   int clusters;
   bool wide_scales;          // every row's scales start on 16 bytes
 };
 
-template <int NT, int OUT, bool SPLIT>
+template <int NT, int OUT, Form FORM>
 cudaError_t launch_kernel(const Maps& maps, const LinearArgs& p, const Plan& plan,
                           int32_t* dev_status, int optin, cudaStream_t st) {
-  using S = Stages<NT>;
+  using S = Stages<NT, FORM>;
   int stages = kMaxStages;
-  while (stages > 2 && S::bytes(stages, 0, p.G, SPLIT) > size_t(optin)) --stages;
+  while (stages > 2 && S::bytes(stages, 0, p.G) > size_t(optin)) --stages;
   // (a table in what the stages leave)
-  const size_t least = S::bytes(stages, 0, p.G, SPLIT);
+  const size_t least = S::bytes(stages, 0, p.G);
   const int table = static_cast<int>(
       std::min<size_t>(kMaxTable, (std::max(size_t(optin), least) - least) / 16));
-  const size_t smem = S::bytes(stages, table, p.G, SPLIT);
-  auto kernel = linear_f8_tile_kernel<NT, OUT, SPLIT>;
+  const size_t smem = S::bytes(stages, table, p.G);
+  auto kernel = linear_f8_tile_kernel<NT, OUT, FORM>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  const unsigned size = SPLIT ? 2 * CG : CG;       // of a cluster
+  const unsigned size = FORM == kSingle ? 1 : FORM == kPair ? 2 : 4;       // of a cluster
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan.clusters) * size);
   cfg.blockDim = dim3(kThreads);
@@ -696,29 +716,43 @@ cudaError_t launch_kernel(const Maps& maps, const LinearArgs& p, const Plan& pla
   return cudaLaunchKernelEx(&cfg, kernel, maps, p, plan.wide_scales, stages, table, dev_status);
 }
 
-template <int NT, bool SPLIT>
+template <int NT, Form FORM>
 cudaError_t launch_out(const Maps& maps, const LinearArgs& p, const Plan& plan,
                        int32_t* dev_status, int optin, cudaStream_t st) {
   switch (p.c_dtype) {
-    case MOE_BF16: return launch_kernel<NT, MOE_BF16, SPLIT>(maps, p, plan, dev_status, optin, st);
-    case MOE_FP16: return launch_kernel<NT, MOE_FP16, SPLIT>(maps, p, plan, dev_status, optin, st);
-    default: return launch_kernel<NT, MOE_FP32, SPLIT>(maps, p, plan, dev_status, optin, st);
+    case MOE_BF16: return launch_kernel<NT, MOE_BF16, FORM>(maps, p, plan, dev_status, optin, st);
+    case MOE_FP16: return launch_kernel<NT, MOE_FP16, FORM>(maps, p, plan, dev_status, optin, st);
+    default: return launch_kernel<NT, MOE_FP32, FORM>(maps, p, plan, dev_status, optin, st);
   }
 }
+
+// Blocks of `rows` token rows: at most so many for any group sizes, and with even ones.
+int64_t most_blocks(const LinearArgs& p, int rows) {
+  return p.G == 1 ? (p.a_rows + rows - 1) / rows
+                  : p.a_rows / rows + std::min<int64_t>(p.G, p.a_rows);
+}
+int64_t even_blocks(const LinearArgs& p, int rows) {
+  return std::min(most_blocks(p, rows), p.G * (((p.a_rows + p.G - 1) / p.G + rows - 1) / rows));
+}
+// Tiles of a CTA by itself.
+int64_t single_tiles(const LinearArgs& p) { return even_blocks(p, TM) * ((p.N + 255) / 256); }
 
 // Whether the kernel that streams weights to the warps' own products is the faster one.
 // A few rows of a plain product: up to 8 a weight byte meets one instruction (8 rows of 4096 x
 // 7168 take 8.0 us there and 18.6 here), up to 16 two, which bound it (16 rows of 4096 x 7168
-// 14.4 and 15 to 19, of 16,384 x 4096 29.9 and 21.4; 20 rows 23.9 and 15.1).  A few per group
-// on average: with 6, 40 groups of 512 x 512 7.5 and 11.0, 40 of 2048 x 2048 41.6 and 42.6,
-// 64 of 4096 x 7168 334 and 324; with 10, 8 of 4096 x 4096 57.2 and 34.4.  Small products,
-// where this kernel's start (barriers, TMEM, clusters) is most of its time: 256 x 512 x 512
-// 4.8 and 5.8, 128 x 1024 x 2048 (at both limits) 9.1 and 9.2, 64 x 7168 x 256 (past the
-// first) 10.1 and 7.0.
-bool use_few(const LinearArgs& p) {
+// 14.4 and 15 to 19, of 16,384 x 4096 29.9 and 21.4; 20 rows 23.9 and 15.1).  A few rows of
+// few groups, which have not a tile for every SM: 16 rows in 8 groups of 4096 x 4096 27.4 and
+// 30.3, 64 in 32 of 1024 x 1024 9.7 and 11.5, but 48 in 8 of 4096 x 4096 34.3 and 28.0; with
+// more tiles 256 in 256 of 4096 x 7168 733 and 721, 1024 uneven ones 1105 and 854, 80 in 40
+// of 2048 x 2048 31.8 and 29.7.  Small products, where this kernel's start (barriers, TMEM,
+// clusters) is most of its time: 256 x 512 x 512 4.8 and 5.8, 128 x 1024 x 2048 (at both
+// limits) 9.1 and 9.2, 64 x 7168 x 256 (past the first) 10.1 and 7.0, 240 rows in 40 groups of
+// 512 x 512 7.5 and 7.3.
+bool use_few(const LinearArgs& p, int sms) {
   const int64_t outputs = p.a_rows * p.N;
-  const int64_t rows = p.G > 1 ? 6 * int64_t(p.G) : int64_t(p.N) * p.K <= 1 << 25 ? 16 : 8;
-  return p.a_rows <= rows || (outputs <= (1 << 17) && outputs * p.K <= (1 << 28));
+  const bool few = p.G > 1 ? p.a_rows <= 3 * int64_t(p.G) && single_tiles(p) < sms
+                           : p.a_rows <= (int64_t(p.N) * p.K <= 1 << 25 ? 16 : 8);
+  return few || (outputs <= (1 << 17) && outputs * p.K <= (1 << 28));
 }
 
 // The form that is expected to take the least time: rounds of tiles over the pairs of SMs,
@@ -735,28 +769,38 @@ bool use_few(const LinearArgs& p) {
 //         1024 x 4096 x 7168   56.4  34.2  28.6     -     -
 //         1280 x 4096 x 7168   68.2  47.3  50.3     -     -
 //         2048 x 4096 x 7168   94.4  62.7  52.5     -     -
-//         2048 rows in 16 groups of 1032 x 1100       18.8  13.5  16.8
-//         6400 rows in 200 groups of 512 x 512        35.2  26.0  24.0
 //          129 x 1500 x  700    7.5   9.0  12.6     -     -
 //   fp32   300 x 1000 x 1025    8.9   9.7  13.3     -     -
 //          197 x 1001 x 1992   10.6  12.5     -  10.6  13.1
 //          512 x 4096 x 4096   22.1  16.9  23.2     -     -
 //         4096 x 4096 x 4096    113  77.4  81.7     -     -
+// Groups of up to 512 rows that have enough tiles: CTAs by themselves (256 channels).  For a
+// tile of up to 128 rows both a pair's SMs would multiply rows that do not count, and two
+// tiles' weights are on their way where the pair's SMs have one's: in pairs and singly 2048 or
+// 8192 rows of 256 groups of 4096 x 7168 1456 and 1104, 1494 and 1123 (6.8 TB/s), 32,768 1580
+// and 1375; 4096 of 8 groups (512 each) 152 and 120; 2048 of 16 groups of 1032 x 1100 (80
+// tiles) 14.6 and 12.1; 8192 of 8 (1024 each) 195 and 203, 65,536 of 32 of 2048 x 2048 238 and
+// 268.  With a tile for fewer than all SMs a long K waits for its few stages: 1000 rows of 8
+// groups of 4096 x 7168 57 and 63.
 Plan make_plan(const LinearArgs& p, int sms) {
-  const int64_t pairs = std::max(1, sms / CG), fours = sms * 36 / 152, kb = code_blocks(p.K);
-  auto blocks_of = [&](int64_t rows) { return (rows + CG * TM - 1) / (CG * TM); };
-  // at most this many for any group sizes, and with even ones
-  const int64_t most = p.G == 1 ? blocks_of(p.a_rows)
-                                : p.a_rows / (CG * TM) + std::min<int64_t>(p.G, p.a_rows);
-  const int64_t even = std::min<int64_t>(most, p.G * blocks_of((p.a_rows + p.G - 1) / p.G));
+  const int64_t pairs = std::max(1, sms / 2), fours = sms * 36 / 152, kb = code_blocks(p.K);
   const bool long_store = p.c_dtype == MOE_FP32 || p.N % 8 != 0;
   Plan plan{};
+  const int64_t tiles = single_tiles(p);
+  if (p.G > 1 && p.a_rows <= 512 * int64_t(p.G) &&
+      (tiles >= sms || (2 * tiles >= sms && p.a_rows * kb <= 2048 * int64_t(p.G)))) {
+    plan.nt = 256;
+    plan.form = kSingle;
+    plan.clusters = static_cast<int>(
+        std::min<int64_t>(most_blocks(p, TM) * ((p.N + 255) / 256), sms));
+    return plan;
+  }
   int64_t least = INT64_MAX;             // 1/100 us
-  auto take = [&](int nt, bool split, int64_t cost, int64_t clusters) {
+  auto take = [&](int nt, Form form, int64_t cost, int64_t clusters) {
     if (cost >= least) return;
     least = cost;
     plan.nt = nt;
-    plan.split = split;
+    plan.form = form;
     plan.clusters = static_cast<int>(clusters);
   };
   for (int nt : {128, 256, 64}) {
@@ -764,18 +808,20 @@ Plan make_plan(const LinearArgs& p, int sms) {
     const int64_t block = nt == 256 ? 40 : nt == 128 ? 24 : 26;
     const int64_t store = !long_store ? 0 : nt == 256 ? 450 : nt == 128 ? 200 : 60;
     const int64_t joined = !long_store ? 0 : nt == 128 ? 200 : 130;       // by half the warps
-    const int64_t rounds = (even * columns + pairs - 1) / pairs;
-    take(nt, false, (nt == 64 ? 570 : 480) + rounds * ((kb + 3) * block + store),
-         std::min(most * columns, pairs));
-    if (nt <= 128 && p.G == 1 && kb - first >= kTurn && most * columns <= fours)
-      take(nt, true, (nt == 64 ? 650 : 680) + (first + 3) * 24 + joined, most * columns);
+    const int64_t most = most_blocks(p, 2 * TM) * columns;
+    const int64_t rounds = (even_blocks(p, 2 * TM) * columns + pairs - 1) / pairs;
+    take(nt, kPair, (nt == 64 ? 570 : 480) + rounds * ((kb + 3) * block + store),
+         std::min(most, pairs));
+    if (nt <= 128 && p.G == 1 && kb - first >= kTurn && most <= fours)
+      take(nt, kHalves, (nt == 64 ? 650 : 680) + (first + 3) * 24 + joined, most);
   }
   return plan;
 }
 
 cudaError_t make_maps(const LinearArgs& p, Plan* plan, Maps* maps) {
   cudaError_t e =
-      encode_bytes_2d(&maps->w, p.w, int64_t(p.G) * p.N, p.K, p.w_stride, plan->nt / CG);
+      encode_bytes_2d(&maps->w, p.w, int64_t(p.G) * p.N, p.K, p.w_stride,
+                      plan->nt / ctas_of(plan->form));
   if (e == cudaSuccess) e = encode_bytes_2d(&maps->a, p.a, p.a_rows, p.K, p.a_stride, TM);
   // (rows of c that do not start on 16 bytes are stored without the map)
   const int64_t pitch = int64_t(p.N) * (p.c_dtype == MOE_FP32 ? 4 : 2);
@@ -791,22 +837,23 @@ cudaError_t make_maps(const LinearArgs& p, Plan* plan, Maps* maps) {
 
 #ifndef MOE_LINEAR_F8_POLLS
 cudaError_t launch_linear_f8(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
-  if (use_few(p)) return launch_linear_f8_few(p, dev_status, st);
   int dev = 0, sms = 0, optin = 0;
   cudaError_t e = current_device_sms(&dev, &sms);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e != cudaSuccess) return e;
+  if (use_few(p, sms)) return launch_linear_f8_few(p, dev_status, st);
+  e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
   Plan plan = make_plan(p, sms);
   Maps maps;
   e = make_maps(p, &plan, &maps);
   if (e != cudaSuccess) return e;
-  if (plan.split)
-    return plan.nt == 128 ? launch_out<128, true>(maps, p, plan, dev_status, optin, st)
-                          : launch_out<64, true>(maps, p, plan, dev_status, optin, st);
-  return plan.nt == 256   ? launch_out<256, false>(maps, p, plan, dev_status, optin, st)
-         : plan.nt == 128 ? launch_out<128, false>(maps, p, plan, dev_status, optin, st)
-                          : launch_out<64, false>(maps, p, plan, dev_status, optin, st);
+  if (plan.form == kSingle) return launch_out<256, kSingle>(maps, p, plan, dev_status, optin, st);
+  if (plan.form == kHalves)
+    return plan.nt == 128 ? launch_out<128, kHalves>(maps, p, plan, dev_status, optin, st)
+                          : launch_out<64, kHalves>(maps, p, plan, dev_status, optin, st);
+  return plan.nt == 256   ? launch_out<256, kPair>(maps, p, plan, dev_status, optin, st)
+         : plan.nt == 128 ? launch_out<128, kPair>(maps, p, plan, dev_status, optin, st)
+                          : launch_out<64, kPair>(maps, p, plan, dev_status, optin, st);
 }
 #endif
 

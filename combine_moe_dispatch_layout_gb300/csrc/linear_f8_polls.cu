@@ -48,7 +48,7 @@ __device__ __forceinline__ bool warp_role_wait4(uint32_t a, uint32_t b, uint32_t
 
 // What moe_linear_f8 does with a problem (c in fp32) on a GPU of `sms` SMs: plan[0] = channels per
 // tile of the kernel it takes (0: the kernel for few rows), plan[1] = clusters, plan[2] =
-// pairs that share a tile's K.  Host only.
+// CTAs of a cluster.  Host only.
 extern "C" void moe_test_linear_f8_plan(int64_t a_rows, int32_t G, int32_t N, int32_t K,
                                         int32_t sms, int32_t* plan) {
   moe_ep::LinearArgs p{};
@@ -58,11 +58,11 @@ extern "C" void moe_test_linear_f8_plan(int64_t a_rows, int32_t G, int32_t N, in
   p.K = K;
   p.c_dtype = MOE_FP32;
   plan[0] = plan[1] = plan[2] = 0;
-  if (moe_ep::use_few(p)) return;
+  if (moe_ep::use_few(p, sms)) return;
   const moe_ep::Plan best = moe_ep::make_plan(p, sms);
   plan[0] = best.nt;
   plan[1] = best.clusters;
-  plan[2] = best.split ? 2 : 1;
+  plan[2] = best.form == moe_ep::kSingle ? 1 : best.form == moe_ep::kPair ? 2 : 4;
 }
 
 // moe_linear_f8's tile kernel with fp32 results and roles that wait for at most `polls`
@@ -91,14 +91,16 @@ extern "C" moe_status moe_test_linear_f8_polls(const void* a, int64_t a_rows, in
   Maps maps;
   e = make_maps(p, &plan, &maps);
   if (e == cudaSuccess)
-    e = plan.split && plan.nt == 64
-            ? launch_kernel<64, MOE_FP32, true>(maps, p, plan, dev_status, optin, st)
-        : plan.split
-            ? launch_kernel<128, MOE_FP32, true>(maps, p, plan, dev_status, optin, st)
+    e = plan.form == kSingle
+            ? launch_kernel<256, MOE_FP32, kSingle>(maps, p, plan, dev_status, optin, st)
+        : plan.form == kHalves && plan.nt == 64
+            ? launch_kernel<64, MOE_FP32, kHalves>(maps, p, plan, dev_status, optin, st)
+        : plan.form == kHalves
+            ? launch_kernel<128, MOE_FP32, kHalves>(maps, p, plan, dev_status, optin, st)
         : plan.nt == 64
-            ? launch_kernel<64, MOE_FP32, false>(maps, p, plan, dev_status, optin, st)
+            ? launch_kernel<64, MOE_FP32, kPair>(maps, p, plan, dev_status, optin, st)
         : plan.nt == 128
-            ? launch_kernel<128, MOE_FP32, false>(maps, p, plan, dev_status, optin, st)
-            : launch_kernel<256, MOE_FP32, false>(maps, p, plan, dev_status, optin, st);
+            ? launch_kernel<128, MOE_FP32, kPair>(maps, p, plan, dev_status, optin, st)
+            : launch_kernel<256, MOE_FP32, kPair>(maps, p, plan, dev_status, optin, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
