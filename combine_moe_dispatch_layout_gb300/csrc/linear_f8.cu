@@ -21,9 +21,9 @@
 //            second CTA: tells the first which of its stages have landed
 //   8 warps  drain a block's sums, scale and add them, and store the tile
 // (kPair.)  Groups of few rows are taken by CTAs by themselves, 128 tokens x 256 channels
-// (kSingle).  Where there are few tiles a cluster of two pairs splits K (kHalves): each pair sends its sums of one
-// half of a CTA's rows to the other one's shared memory, adds what it gets to its own sums of
-// the other half, and stores those.
+// (kSingle).  Where there are few tiles a cluster of two pairs splits K (kHalves): each pair
+// sends its sums of one half of a CTA's rows to the other one's shared memory, adds what it
+// gets to its own sums of the other half, and stores those.
 // Every wait is bounded: a timeout sets MOE_ERR_TIMEOUT, the CTA stops issuing work and
 // drains what is in flight.
 //
@@ -36,9 +36,9 @@
 // energy counts more than clocks: 166 us in bursts, 183 to 188 looped (a library product
 // without block scales 127 and 144).  Measured beside it: 32,768 x 7168 x 2048 in 32 uneven
 // groups 413 us, 1024 x 4096 x 4096 19.5, 256 x 4096 x 7168 16.0, 8192 rows over 256 groups
-// of 4096 x 7168 1425 to 1530, 197 x 1001 x 1992 in fp32 10.6.  Slower for the first: four
-// accumulators of 128 columns (the products read the token rows twice: 210), 16 draining
-// warps (178), TMEM loads of 4, 16 or 32 columns (198, 169, 210; of 8 here), scalar
+// of 4096 x 7168 1116 (6.85 TB/s, kSingle), 197 x 1001 x 1992 in fp32 10.6.  Slower for the
+// first: four accumulators of 128 columns (the products read the token rows twice: 210), 16
+// draining warps (178), TMEM loads of 4, 16 or 32 columns (198, 169, 210; of 8 here), scalar
 // multiply-adds (215), single CTAs instead of pairs (as many clocks, 3% more energy).
 #include <cuda.h>
 
@@ -360,7 +360,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
       for (int t = cluster_id(); ok && t < tile_count(); t += cluster_count()) {
         for (int kb = 0; kb < nk; ++kb) {
           const uint32_t b = nacc % kAccs;
-          if (!warp_role_wait4(full(0, s), full(1, s), CG == 2 ? peer(s) : full(1, s), phase, tempty(b),
+          const uint32_t other = CG == 2 ? peer(s) : full(1, s);
+          if (!warp_role_wait4(full(0, s), full(1, s), other, phase, tempty(b),
                                ((nacc / kAccs) & 1u) ^ 1u)) {
             ok = false;
             break;
@@ -602,7 +603,8 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
 #pragma unroll
           for (int j = 0; j < kCols; j += kBoxCols) {
             const uint32_t at = box + (j / kBoxCols % kWarpBoxes) * kBoxBytes;
-            if (lane == 0) bulk_wait_read<kBoxes == 1 || kWarpBoxes == 1 ? 0 : 1>();    // this buffer's last copy
+            // (this buffer's last copy)
+            if (lane == 0) bulk_wait_read<kBoxes == 1 || kWarpBoxes == 1 ? 0 : 1>();
             __syncwarp();
             stage(j, at);
             fence_proxy_async_smem();

@@ -19,8 +19,8 @@
 //
 // Measured (in a graph): one token by 4096 x 7168 7.1 us (29 MB, 4.3 us at a copy's rate; the
 // rest is the launch, the first bytes' way and the sums), 256 tokens over 256 experts of 4096
-// x 7168 734 us, 6.5 TB/s, 4 rows each of 64 groups 300 (6.3 TB/s); with 8 rows each, 389, the
-// tokens' way through L1 is the longer one and the tile kernel the faster.
+// x 7168 734 us, 6.5 TB/s (in tiles 721), 4 rows each of 64 groups 300 (in tiles 275); with 8
+// rows each, 389, the tokens' way through L1 is the longer one.
 //
 // A warp takes 16 channels and up to 8 TB tokens; `parts` warps of a CTA split K where
 // there are too few channels to fill the GPU (their sums are added in order).  A
