@@ -18,6 +18,18 @@
 #include "row_codes.cuh"
 
 namespace moe_ep {
+
+// rms_norm_polls.cu compiles the gradient's kernel a second time, for tests of the waits that
+// run out: with a wait of its own, and without the functions that others call.
+#ifndef MOE_RMS_NORM_POLLS
+namespace {
+// A thread's wait for its team's next row; false after kGemmSpin polls.
+__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity) {
+  return mbar_wait_bounded(bar, parity, kGemmSpin);
+}
+}  // namespace
+#endif
+
 namespace {
 
 constexpr int kNoCodes = -1;
@@ -179,7 +191,8 @@ rms_norm_kernel(const NormArgs p) {
 // of x and of d_sum) come by bulk copies into a ring of `depth` rows a team of TPR threads,
 // so that the next rows are on their way while one is reduced and written; both passes over
 // a row read it from there.  (By loads into registers a CTA waited for every row: 32,768 x
-// 7168 440 us.)
+// 7168 440 us.)  Where a wait runs out in any thread its team does not write that row, asks
+// for no further one, and leaves once the copies on their way have landed.
 constexpr int kMaxDepth = 4;
 __host__ __device__ constexpr int backward_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 
@@ -190,7 +203,9 @@ rms_norm_backward_kernel(const NormBackwardArgs p, int depth) {
   constexpr bool kKeepGamma = NV < 4;            // in registers
   extern __shared__ __align__(16) uint8_t s_ring[];
   __shared__ __align__(8) uint64_t s_full[kRows][kMaxDepth];
-  __shared__ float s_part[2][TPR > 32 ? TPR / 32 : 1];
+  // a reduction's sums; behind them, read along, 1 where a thread's wait ran out
+  constexpr int kGaveUp = TPR / 32;
+  __shared__ __align__(16) float s_part[2][kGaveUp + 4];
   wait_for_stream();
   let_next_start();
   const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
@@ -199,6 +214,7 @@ rms_norm_backward_kernel(const NormBackwardArgs p, int depth) {
   uint8_t* ring = s_ring + size_t(slot) * depth * parts * row_bytes;
   uint64_t* full = s_full[slot];
   if (t == 0) {
+    if constexpr (TPR > 32) s_part[0][kGaveUp] = s_part[1][kGaveUp] = 0.0f;
     for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
@@ -241,12 +257,18 @@ rms_norm_backward_kernel(const NormBackwardArgs p, int depth) {
     for (int i = 0; i < depth; ++i) fetch(first + i * stride, i);
   int at = 0, turn = 0;
   uint32_t phase = 0;
-  bool ok = true;                     // a wait that ran out: no further one
+  bool ok = true;                     // the team's: no wait ran out
   float rstd_next = first < p.T ? p.rstd[first] : 0.0f;
-  for (int64_t row = first; row < p.T; row += stride, turn ^= 1) {
+  int64_t row = first;
+  for (; row < p.T; row += stride, turn ^= 1) {
     const float rstd = rstd_next;
     if (row + stride < p.T) rstd_next = p.rstd[row + stride];
-    if (ok) ok = mbar_wait_bounded(&full[at], phase, kGemmSpin);
+    ok = row_wait(&full[at], phase);
+    if constexpr (TPR == 32) {
+      ok = __all_sync(kAll, ok);
+    } else if (!ok) {
+      s_part[turn][kGaveUp] = 1.0f;    // (the others learn of it behind the next barrier)
+    }
     const uint4* dv = reinterpret_cast<const uint4*>(ring + size_t(at) * parts * row_bytes);
     const uint4 *xv = dv + chunks, *sv = xv + chunks;
     float dot = 0.0f;
@@ -266,6 +288,8 @@ rms_norm_backward_kernel(const NormBackwardArgs p, int depth) {
       }
     }
     const float mean = __fdiv_rn(row_reduce<TPR>(dot, s_part[turn], t, Add()), float(p.H));
+    if constexpr (TPR > 32) ok = s_part[turn][kGaveUp] == 0.0f;
+    if (!ok) break;
     // every thread is done with the row before this one: its place is free
     if (TPR == 32) __syncwarp();
     if (t == 0 && row != first) {
@@ -296,11 +320,16 @@ rms_norm_backward_kernel(const NormBackwardArgs p, int depth) {
     }
   }
   if (!ok) {
-    // no copy may land once the CTA has gone
     set_status(p.dev_status, MOE_ERR_TIMEOUT);
-    for (int i = 0; i < depth; ++i) {
-      mbar_wait_bounded(&full[i], 0, kGemmSpin);
-      mbar_wait_bounded(&full[i], 1, kGemmSpin);
+    // No copy may land once the CTA has gone: the rows asked for from this one on, one fewer
+    // than the ring holds behind the first.
+    for (int left = row == first ? depth : depth - 1; left > 0 && row < p.T;
+         --left, row += stride) {
+      mbar_wait_bounded(&full[at], phase, kGemmSpin);
+      if (++at == depth) {
+        at = 0;
+        phase ^= 1u;
+      }
     }
   }
   float* part = p.parts + int64_t(blockIdx.x) * p.H;
@@ -615,6 +644,7 @@ cudaError_t launch_backward(const NormBackwardArgs& p, int parts, cudaStream_t s
 
 }  // namespace
 
+#ifndef MOE_RMS_NORM_POLLS
 cudaError_t launch_rms_norm(const NormArgs& p, cudaStream_t st) {
   return p.dtype == MOE_BF16 ? launch_norm<MOE_BF16>(p, st) : launch_norm<MOE_FP16>(p, st);
 }
@@ -632,5 +662,6 @@ cudaError_t launch_rms_norm_backward(const NormBackwardArgs& p, float* d_gamma,
   return launch_early(rms_norm_columns_kernel, (p.H + kSumCols - 1) / kSumCols,
                       kSumCols * kSumGroups, 0, st, p.parts, parts, p.H, d_gamma);
 }
+#endif
 
 }  // namespace moe_ep

@@ -677,8 +677,9 @@ size_t moe_rms_norm_backward_workspace_bytes(int64_t T, int32_t H);
  *   rstd                   fp32 [T] (read)
  *   d_gamma                fp32 [H] (written; zeros with T == 0)
  *   workspace              16-byte aligned
- * Limits as moe_rms_norm; a wait that ran out sets MOE_ERR_TIMEOUT.  Two launches
- * (three with H > 16384). */
+ * Limits as moe_rms_norm; a wait that ran out sets MOE_ERR_TIMEOUT (the rows of d_x that
+ * were not reached stay as they were, d_gamma means nothing).  Two launches (three with
+ * H > 16384). */
 moe_status moe_rms_norm_backward(const void* d_out, int32_t dtype, int64_t T, int32_t H,
                                  int64_t d_out_stride, const void* x, int64_t x_stride,
                                  const float* gamma, const float* rstd, const void* d_sum,
