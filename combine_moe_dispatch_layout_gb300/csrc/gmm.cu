@@ -295,6 +295,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
       r += c;
       tt += static_cast<int32_t>((c + BM - 1) / BM) * ntn;
     }
+    fence_proxy_async_smem();      // the scan lies where copies will write
   }
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {

@@ -32,7 +32,8 @@ __device__ __forceinline__ void smem_store(uint32_t a, int v) {
 // goff[g] = first row of group g, tpre[g] = tiles before it (shared-memory
 // addresses of G + 1 words each; the last ones are the totals), a group having
 // row_blocks(rows, block) * ntn tiles.  More rows than the buffer holds set
-// MOE_ERR_CAPACITY and leave no tiles.  s_scan: 12 * THREADS bytes, 8-aligned.
+// MOE_ERR_CAPACITY and leave no tiles.  s_scan: 12 * THREADS bytes, 8-aligned (a caller whose
+// bulk or tensor copies write there later fences the proxies first, in every thread).
 // All THREADS threads take part; the tables are ready after the caller's next
 // __syncthreads().
 template <int THREADS>

@@ -204,6 +204,7 @@ linear_f8_tile_kernel(const __grid_constant__ Maps maps, const LinearArgs p, boo
   let_next_start();
   if (p.group_rows) {        // the scan borrows the stages, which are not in use yet
     build_group_tables<kThreads>(p, CG * TM, ntn, smem, goff, tpre, dev_status);
+    fence_proxy_async_smem();      // (before the copies that write there)
   } else if (tid == 64) {
     const int rows = static_cast<int>(p.a_rows);
     smem_store(goff, 0);
