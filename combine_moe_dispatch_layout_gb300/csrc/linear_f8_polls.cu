@@ -28,7 +28,7 @@ __device__ __forceinline__ bool look(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool warp_role_wait(uint32_t bar, uint32_t parity) {
   uint32_t i = c_first;
   do {
-    if (__any_sync(0xffffffffu, look(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, look(bar, parity))) return true;
   } while (++i < kGemmSpin);
   return false;
 }

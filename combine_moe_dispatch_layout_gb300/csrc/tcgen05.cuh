@@ -49,10 +49,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 // The same for a whole converged warp, which stays so (a lane's own loop made the compiler
-// guard every wait against divergence, and spill what it keeps for that).
+// guard every wait against divergence, and spill what it keeps for that).  Every lane has to
+// see the phase itself: one that has not has acquired nothing of what lies behind it.
 __device__ __forceinline__ bool warp_bar_wait(uint32_t bar, uint32_t parity) {
   for (uint32_t i = 0; i < kGemmSpin; ++i)
-    if (__any_sync(0xffffffffu, bar_poll(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, bar_poll(bar, parity))) return true;
   return false;
 }
 // Waits for phase `parity` of three barriers and `pd` of a fourth, a whole converged warp,
@@ -73,7 +74,7 @@ __device__ __forceinline__ bool warp_bar_wait4(uint32_t a, uint32_t b, uint32_t 
         : "=r"(ok)
         : "r"(a), "r"(b), "r"(c), "r"(parity), "r"(d), "r"(pd)
         : "memory");
-    if (__any_sync(0xffffffffu, ok != 0)) return true;
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
   }
   return false;
 }
