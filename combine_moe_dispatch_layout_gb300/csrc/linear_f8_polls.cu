@@ -46,23 +46,28 @@ __device__ __forceinline__ bool warp_role_wait4(uint32_t a, uint32_t b, uint32_t
 #define MOE_LINEAR_F8_POLLS
 #include "linear_f8.cu"
 
-// What moe_linear_f8 does with a problem (c in fp32) on a GPU of `sms` SMs: plan[0] = channels per
-// tile of the kernel it takes (0: the kernel for few rows), plan[1] = clusters, plan[2] =
-// CTAs of a cluster.  Host only.
-extern "C" void moe_test_linear_f8_plan(int64_t a_rows, int32_t G, int32_t N, int32_t K,
-                                        int32_t sms, int32_t* plan) {
+// What moe_linear_f8 does with a problem on a GPU of `sms` SMs: plan[0] = channels per tile of
+// the kernel it takes (0: the kernel for few rows), plan[1] = clusters, plan[2] = CTAs of a
+// cluster.  Host only.
+extern "C" void moe_test_linear_f8_plan_of(int64_t a_rows, int32_t G, int32_t N, int32_t K,
+                                           int32_t c_dtype, int32_t sms, int32_t* plan) {
   moe_ep::LinearArgs p{};
   p.a_rows = a_rows;
   p.G = G;
   p.N = N;
   p.K = K;
-  p.c_dtype = MOE_FP32;
+  p.c_dtype = c_dtype;
   plan[0] = plan[1] = plan[2] = 0;
   if (moe_ep::use_few(p, sms)) return;
   const moe_ep::Plan best = moe_ep::make_plan(p, sms);
   plan[0] = best.nt;
   plan[1] = best.clusters;
   plan[2] = best.form == moe_ep::kSingle ? 1 : best.form == moe_ep::kPair ? 2 : 4;
+}
+// The same with fp32 results.
+extern "C" void moe_test_linear_f8_plan(int64_t a_rows, int32_t G, int32_t N, int32_t K,
+                                        int32_t sms, int32_t* plan) {
+  moe_test_linear_f8_plan_of(a_rows, G, N, K, MOE_FP32, sms, plan);
 }
 
 // moe_linear_f8's tile kernel with fp32 results and roles that wait for at most `polls`

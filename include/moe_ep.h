@@ -708,8 +708,9 @@ moe_status moe_swiglu_f8(const void* h, int32_t dtype, int64_t M, int32_t I, int
  *             (+ bias[g][n])
  * with the inner sums on the tensor cores (fp32), the scales' product rounded to fp32
  * once and every further step one fp32 operation; then c rounded to c_dtype.  The order
- * of the sums depends on the sizes alone.  Codes of NaN and scales of any value take part
- * as such.
+ * of the sums over b depends on a_rows, G, N, K, c_dtype and the GPU, and on nothing else: the
+ * same call gives the same bits every time, but a result in another type need not be the same
+ * sums rounded another way.  Codes of NaN and scales of any value take part as such.
  *   a        [a_rows], rows a_stride bytes apart: e4m3 row images, or codes alone
  *   w        [G][N], rows w_stride bytes apart (w[g] N rows after w[g-1])
  *   w_scale  fp32 [G][ceil(N/128)][ceil(K/128)]
