@@ -37,7 +37,8 @@ struct Raw8 {                           // 8 values as they lie in memory
 };
 
 // 1 / (1 + exp(-x)): the exponential as 2^(-x log2 e), within 2^-21 and |x| 2^-23 of itself
-// (the argument's rounding); from x = -87 on down the divisor leaves fp32 and the result is 0.
+// (the argument's rounding).  From x = -126 ln 2, about -87.34, on down the divisor passes 2^126:
+// its reciprocal would be subnormal, and is 0.
 __device__ __forceinline__ float sigmoid(float x) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(x, -1.44269504f)));

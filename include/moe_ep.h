@@ -688,15 +688,16 @@ moe_status moe_rms_norm_backward(const void* d_out, int32_t dtype, int64_t T, in
                                  void* stream);
 
 /* The step between an e4m3 layer's two products: rows [gate | up] of 2I values ->
- * e4m3 row images of h = gate / (1 + exp(-gate)) * up (fp32, within 2^-16 of itself; from
- * gate = -87 on down h is 0).
+ * e4m3 row images of h = gate / (1 + exp(-gate)) * up (fp32, within 2^-16 of itself; where
+ * 1 + exp(-gate) passes 2^126, from about gate = -87.34 on down, h is 0).
  *   h          [M] rows of 2I elements of dtype (MOE_BF16, MOE_FP16 or MOE_FP32),
  *              h_stride elements apart (at least 2I; not looked at with M <= 1),
  *              16-byte aligned, the stride too
  *   group_off  int64 [G+1] (moe_group_offsets) or NULL: rows at or past group_off[G]
  *              are not written; an offset past M sets MOE_ERR_CAPACITY
  *   codes      moe_f8_row_bytes(I) apart, 16-byte aligned, apart from h
- * 0 <= M < 2^31, 8 <= I <= MOE_EP_MAX_HIDDEN / 2, I % 8 == 0.  One launch. */
+ * 0 <= M < 2^31, 8 <= I <= MOE_EP_MAX_HIDDEN / 2, I % 8 == 0, M * ceil(I / 512) <= 16 *
+ * (2^31 - 1) (the launch's blocks).  One launch. */
 moe_status moe_swiglu_f8(const void* h, int32_t dtype, int64_t M, int32_t I, int64_t h_stride,
                          const int64_t* group_off, int32_t G, void* codes,
                          int32_t* dev_status, void* stream);
