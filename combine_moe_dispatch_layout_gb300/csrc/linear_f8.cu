@@ -35,8 +35,8 @@
 // Looped for longer than 20 ms the board is at its power limit and lowers the clock, so
 // energy counts more than clocks: 166 us in bursts, 183 to 188 looped (a library product
 // without block scales 127 and 144).  Measured beside it: 32,768 x 7168 x 2048 in 32 uneven
-// groups 413 us, 1024 x 4096 x 4096 19.5, 256 x 4096 x 7168 16.0, 8192 rows over 256 groups
-// of 4096 x 7168 1116 (6.85 TB/s, kSingle), 197 x 1001 x 1992 in fp32 10.6.  Slower for the
+// groups 417 us, 1024 x 4096 x 4096 19.8, 256 x 4096 x 7168 16.1, 8192 rows over 256 groups
+// of 4096 x 7168 1111 (6.85 TB/s, kSingle), 197 x 1001 x 1992 in fp32 10.6 to 12.  Slower for the
 // first: four accumulators of 128 columns (the products read the token rows twice: 210), 16
 // draining warps (178), TMEM loads of 4, 16 or 32 columns (198, 169, 210; of 8 here), scalar
 // multiply-adds (215), single CTAs instead of pairs (as many clocks, 3% more energy).
@@ -747,7 +747,8 @@ int64_t single_tiles(const LinearArgs& p) { return even_blocks(p, TM) * ((p.N + 
 // few groups, which have not a tile for every SM: 16 rows in 8 groups of 4096 x 4096 27.4 and
 // 30.3, 64 in 32 of 1024 x 1024 9.7 and 11.5, but 48 in 8 of 4096 x 4096 34.3 and 28.0; with
 // more tiles 256 in 256 of 4096 x 7168 733 and 721, 1024 uneven ones 1105 and 854, 80 in 40
-// of 2048 x 2048 31.8 and 29.7.  Small products, where this kernel's start (barriers, TMEM,
+// of 2048 x 2048 31.8 and 29.7, and with a K of one block 80 in 138 of 4096 x 64 24.3 and
+// 16.6, 512 in 256 of 2048 x 64 46.4 and 23.5.  Small products, where this kernel's start (barriers, TMEM,
 // clusters) is most of its time: 256 x 512 x 512 4.8 and 5.8, 128 x 1024 x 2048 (at both
 // limits) 9.1 and 9.2, 64 x 7168 x 256 (past the first) 10.1 and 7.0, 240 rows in 40 groups of
 // 512 x 512 7.5 and 7.3.

@@ -14,13 +14,13 @@
 // rows, copied asynchronously into a ring of kDepth steps of its own in shared memory (no
 // barrier but the warp's own stands between copy and use), four CTAs to an SM.  The ring
 // runs on over tile ends.  Tokens and scales come through L1, a step ahead, in registers.
-// (With the weights a block ahead in registers too, 32 groups of 8 rows of 4096 x 7168
-// took 282 us at 3.3 TB/s.)
+// (With the weights a block ahead in registers too they came at 3.3 TB/s.)
 //
-// Measured (in a graph): one token by 4096 x 7168 7.1 us (29 MB, 4.3 us at a copy's rate; the
-// rest is the launch, the first bytes' way and the sums), 256 tokens over 256 experts of 4096
-// x 7168 734 us, 6.5 TB/s (in tiles 721), 4 rows each of 64 groups 300 (in tiles 275); with 8
-// rows each, 389, the tokens' way through L1 is the longer one.
+// Measured (in a graph): one token by 4096 x 7168 7.1 to 7.5 us (29 MB, 4.3 us at a copy's
+// rate; the rest is the launch, the first bytes' way and the sums), 8 tokens 8.4, 16 tokens
+// 14.2 (each weight byte meets two instructions), 16 in 8 groups of 4096 x 4096 27.5.  Many
+// groups are linear_f8.cu's: 256 tokens over 256 experts of 4096 x 7168 take 734 us here and
+// 721 there; with 8 rows a group the tokens' way through L1 is the longer one.
 //
 // A warp takes 16 channels and up to 8 TB tokens; `parts` warps of a CTA split K where
 // there are too few channels to fill the GPU (their sums are added in order).  A
@@ -284,9 +284,9 @@ cudaError_t launch_few(const LinearArgs& p, bool all, bool* done, int32_t* dev_s
 }  // namespace
 
 // Eight warps to a CTA where they can split K eight ways (one token by 4096 x 7168 7.4 us,
-// with four warps 8.5), else four (256 tokens over 256 experts the same, 100 rows in 200
-// groups of 300 x 300 7.9 and with eight 8.4).  More than 8 rows a group: two blocks of 8
-// share the weights' way (16 rows of 4096 x 7168 14.3 us).
+// with four warps 8.5), else four (100 rows in 200 groups of 300 x 300 7.9 and with eight
+// 8.4).  More than 8 rows a group: two blocks of 8 share the weights' way (16 rows of 4096 x
+// 7168 14.3 us).
 cudaError_t launch_linear_f8_few(const LinearArgs& p, int32_t* dev_status, cudaStream_t st) {
   bool done = false;
   if ((p.a_rows + p.G - 1) / p.G > 8) return launch_few<2, 4>(p, false, &done, dev_status, st);

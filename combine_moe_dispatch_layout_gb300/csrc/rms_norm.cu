@@ -12,7 +12,9 @@
 // chunks t, t + TPR, ..., so every access of a warp is 512 consecutive bytes and a
 // half warp holds the 128 values of an e4m3 block.  Measured: 32,768 x 7168 with its residual
 // 271 us, 103% of a copy's rate, with codes too 319 (98%); 24,251 x 1000 to codes 17.3 (63%:
-// instructions, and one stream of loads a warp); the gradient of 32,768 x 7168 288 (97%).
+// instructions, and one stream of loads a warp); the gradient of 32,768 x 7168 290 (97%).
+// INT8 codes wait for a second reduction, the row's maximum: 330 us for the first (95%), 20.0
+// for the narrow rows.
 #include <algorithm>
 
 #include "row_codes.cuh"
@@ -591,7 +593,7 @@ cudaError_t launch_norm(const NormArgs& p, cudaStream_t st) {
 
 // CTAs that an SM's shared memory and registers are shared by: two, so that one's
 // reductions overlap the other's; rows of which two do not fit twice have an SM alone.
-// (32,768 x 7168 with one CTA an SM and twice its ring 326 us, with two 288.)
+// (32,768 x 7168 with one CTA an SM and twice its ring 326 us, with two 288 to 290.)
 template <int TPR, int NV>
 constexpr int kCtasPerSm = TPR * NV <= 1024 ? 2 : 1;
 template <int TPR, int NV>

@@ -722,7 +722,11 @@ moe_status moe_swiglu_f8(const void* h, int32_t dtype, int64_t M, int32_t I, int
  *            groups' total are not written
  * group_rows, alignments, limits and what is read of rows past K: as moe_linear_i8, with
  * a_scale_stride >= 4 ceil(K/128) (not looked at with a_rows <= 1).  Errors found on the
- * device as there.  One launch. */
+ * device as there.  One launch.
+ * How it runs is chosen by a_rows, as the counts are known to the device alone: of a buffer
+ * made for many more rows than come the results are right and slower to have (2048 rows of
+ * 256 groups of 4096 x 7168 take 1.10 ms in a buffer of 2048 or 32,768 rows, 1.45 in one of
+ * 262,144). */
 moe_status moe_linear_f8(const void* a, int64_t a_rows, int64_t a_stride, const void* w,
                          int64_t w_stride, int32_t G, int32_t N, int32_t K,
                          const int32_t* group_rows, const float* w_scale,
